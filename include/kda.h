@@ -1,7 +1,9 @@
 /*
  * kda.h -- C ABI of the GB300 (sm_103a) KDA decode / speculative-verify step,
- * its record replay (kda_recover) and the output-projection consumer epilogue
- * that follows the attention layer (kda_oproj, declared at the end).
+ * its record replay (kda_recover), the output-projection consumer epilogue
+ * that follows the attention layer (kda_oproj), linear attention with one
+ * decay per head (kda_lin_prompt, kda_lin_step) and snapshots of state pages
+ * in 8 or 4 bits (kda_snapshot_save, kda_snapshot_load).
  *
  * The operation is the one defined by the vLLM API page
  *   "vllm.models.kimi_k3.nvidia.specialized_decode.cutedsl.kda.wide"
@@ -34,7 +36,8 @@
  *
  * Ownership and threading: the caller owns every buffer; every pointer is a
  * DEVICE pointer of the current device.  The library allocates nothing,
- * never synchronises, and enqueues exactly one kernel on `stream` per call.
+ * never synchronises, and enqueues exactly one kernel on `stream` per call
+ * (kda_lin_prompt: up to three).
  * Calls are reentrant and may come from several host threads at once (the
  * first call on a device reads its attributes and configures the kernel
  * under a lock); two calls that write the same pool regions must be ordered
@@ -72,7 +75,8 @@ enum {
                               /* tokens, or an item count beyond 2^31-1        */
   KDA_ERR_DEVICE = 9,         /* no usable device, or not an sm_103 device     */
   KDA_ERR_LAUNCH = 10,        /* the kernel launch failed (CUDA error)         */
-  KDA_ERR_PATH = 11           /* path outside 0..2                             */
+  KDA_ERR_PATH = 11,          /* path outside 0..2                             */
+  KDA_ERR_WORKSPACE = 12      /* kda_lin_prompt: workspace missing or too small */
 };
 
 /* Device-side error flags, OR-ed into *err when err != NULL.  An item that
@@ -81,8 +85,11 @@ enum {
   KDA_DEVERR_SLOT = 1,        /* slot, conv slot or a write target >= num_slots,
                                  or a conv slot <= 0 on a live verify item     */
   KDA_DEVERR_ACCEPTED = 2,    /* accepted[r] outside 1..tokens                 */
-  KDA_DEVERR_TIMEOUT = 4      /* an on-chip copy wait ran out (the kernel      */
+  KDA_DEVERR_TIMEOUT = 4,     /* an on-chip copy wait ran out (the kernel      */
                               /* stopped early; outputs are incomplete)        */
+  KDA_DEVERR_SEQ = 8          /* kda_lin_prompt: seq_starts out of order or     */
+                              /* outside 0..tokens, or a sequence longer than  */
+                              /* max_seq                                       */
 };
 
 /* Arguments of one step.  Layouts are row-major; dim = heads * 128.
@@ -263,6 +270,126 @@ typedef struct kda_oproj_args {
  * outside the ranges above), KDA_ERR_ALIGNMENT, KDA_ERR_DEVICE,
  * KDA_ERR_LAUNCH; nothing is launched on error.  One kernel on `stream`. */
 int kda_oproj(const kda_oproj_args *args, void *stream);
+
+/* ---- Linear attention with one decay per head -------------------------------
+ *
+ * The companion of the KDA step for layers whose state decays by one factor
+ * per head instead of one per key and takes no delta correction.  Per head,
+ * on the same 128x128 FP32 page [value row i][key j]:
+ *     S_t = exp(g_t) S_{t-1} + v_t k_t^T,      o_t = scale * S_t q_t.
+ * q and k have qk_heads heads, v and o heads; value head h reads query and key
+ * head h / (heads / qk_heads).  g (`decay`) is the logarithm of the decay, <= 0:
+ * f32 [heads] (decay_rows 0) or one per token, f32 [rows, heads] contiguous
+ * (decay_rows 1); -inf is a reset (the factor 0).  Rows of q, k, v and output
+ * are BF16 [head][128] and may be slices of wider rows: row t starts at
+ * t * stride elements, strides are multiples of 8 and at least the row's own
+ * width; q, k, v, output and state are 16-byte aligned, the other arrays 4. */
+
+/* Arguments of one prompt call (kda_lin_prompt). */
+typedef struct kda_lin_prompt_args {
+  int32_t seqs;             /* sequences (0 is a no-op)                        */
+  int32_t heads;            /* value heads H (0 is a no-op)                    */
+  int32_t qk_heads;         /* query / key heads, a divisor of heads           */
+  int32_t tokens;           /* rows of q, k, v and output                      */
+  int32_t max_seq;          /* no sequence is longer than this                 */
+  int32_t num_slots;        /* slots of `state` (ignored without slots)        */
+  int32_t decay_rows;       /* 0: decay is [heads]; 1: [tokens, heads]         */
+  int32_t path;             /* 0 = automatic; 1 = recurrent (token by token);  */
+                            /* 2 = chunked (128 tokens at a time)              */
+  int64_t q_stride, k_stride, v_stride, o_stride;   /* elements between rows   */
+  const void *q;            /* bf16 [tokens, qk_heads * 128]                   */
+  const void *k;            /* bf16 [tokens, qk_heads * 128]                   */
+  const void *v;            /* bf16 [tokens, heads * 128]                      */
+  const float *decay;       /* f32: see decay_rows                             */
+  const int32_t *seq_starts;/* i32 [seqs + 1]: sequence r is rows              */
+                            /* seq_starts[r] .. seq_starts[r + 1] - 1          */
+  const int32_t *src_slots; /* i32 [seqs] or NULL: page a sequence starts from;*/
+                            /* <= 0 (or NULL): from zeros.  May be shared      */
+  const int32_t *dst_slots; /* i32 [seqs] or NULL: page its last state goes to;*/
+                            /* <= 0 (or NULL): dropped.  Distinct, and no      */
+                            /* other sequence's src; may be its own src        */
+  float *state;             /* f32 [num_slots, heads, 128, 128] (with slots)   */
+  void *output;             /* bf16 [tokens, heads * 128]                      */
+  float scale;              /* of the output                                   */
+  int32_t *err;             /* optional device word for KDA_DEVERR_* flags     */
+  void *workspace;          /* 256-byte aligned; NULL when none is needed      */
+  int64_t workspace_bytes;  /* at least kda_lin_prompt_workspace(args)         */
+} kda_lin_prompt_args;
+
+/* Bytes of workspace that kda_lin_prompt needs for these sizes (`seqs`,
+ * `heads`, `tokens`, `max_seq`, `path` are read), 0 for none or for sizes that
+ * it refuses; -1 when args is NULL.  The workspace holds nothing between
+ * calls; calls that may run at the same time need their own. */
+int64_t kda_lin_prompt_workspace(const kda_lin_prompt_args *args);
+
+/* Prompt form over ragged sequences, chunked: a sequence's outputs and last
+ * state from its first state.  Rows that no sequence covers are left as they
+ * are; a sequence without tokens copies its first state.  A sequence with a
+ * flagged slot (KDA_DEVERR_SLOT) or range (KDA_DEVERR_SEQ) writes nothing.
+ * Sequences must not overlap.  A non-finite value in a live row may reach
+ * every output of its 128-token chunk and what follows it; rows outside the
+ * sequence reach nothing.  Up to three kernels on `stream`, in order. */
+int kda_lin_prompt(const kda_lin_prompt_args *args, void *stream);
+
+/* Arguments of one single-token step (kda_lin_step). */
+typedef struct kda_lin_step_args {
+  int32_t batch;            /* requests, one row each (0 is a no-op)           */
+  int32_t heads;            /* value heads H (0 is a no-op)                    */
+  int32_t qk_heads;         /* query / key heads, a divisor of heads           */
+  int32_t num_slots;
+  int32_t decay_rows;       /* 0: decay is [heads]; 1: [batch, heads]          */
+  int64_t q_stride, k_stride, v_stride, o_stride;   /* elements between rows   */
+  const void *q, *k, *v;    /* bf16 [batch, qk_heads (v: heads) * 128]         */
+  const float *decay;
+  const int32_t *slots;     /* i32 [batch]: the page, updated in place; <= 0 = */
+                            /* padding (a row of zeros, nothing else written)  */
+  float *state;             /* f32 [num_slots, heads, 128, 128]       in/out   */
+  void *output;             /* bf16 [batch, heads * 128]                       */
+  float scale;
+  int32_t *err;             /* optional device word for KDA_DEVERR_* flags     */
+} kda_lin_step_args;
+
+/* Recurrent form, one token per request.  Live requests have distinct slots.
+ * A slot >= num_slots raises KDA_DEVERR_SLOT and is handled as padding.  One
+ * kernel on `stream`. */
+int kda_lin_step(const kda_lin_step_args *args, void *stream);
+
+/* ---- Snapshots: state pages kept in 8 or 4 bits ------------------------------
+ *
+ * A snapshot keeps one slot's pages (of the KDA step or of the linear
+ * attention above) for later: a prefix cache, a request to fork.  Codes are
+ * whole numbers -L .. L, L = 127 (bits 8) or 7 (bits 4), with one FP32 scale
+ * for a group of keys of one value row (bits 8: the row's 128 keys; bits 4: 32
+ * keys).  With m the group's largest magnitude: scale = m / L rounded to FP32
+ * and code = x / scale to the nearest whole number, ties to even, decided as
+ * in exact arithmetic.  Groups with m < 2^-118 are kept as zeros (scale 0);
+ * groups with an infinity or NaN are kept as NaN (scale NaN, codes 0).  Reading
+ * gives code * scale in FP32.  Two 4-bit codes share a byte: key 2j in the low
+ * half, 2j + 1 in the high half, in two's complement. */
+typedef struct kda_snapshot_args {
+  int32_t count;            /* entries (0 is a no-op)                          */
+  int32_t heads;            /* H heads (0 is a no-op)                          */
+  int32_t num_slots;        /* slots of `state`                                */
+  int32_t num_snaps;        /* rows of `codes` and `scales`                    */
+  int32_t bits;             /* 8 or 4                                          */
+  const int32_t *slots;     /* i32 [count]: pool slot; <= 0 = padding          */
+  const int32_t *snaps;     /* i32 [count]: snapshot; <= 0 = padding           */
+  float *state;             /* f32 [num_slots, heads, 128, 128]                */
+  void *codes;              /* bits 8: i8 [num_snaps, heads, 128, 128];        */
+                            /* bits 4: u8 [num_snaps, heads, 128, 64]          */
+  float *scales;            /* f32 [num_snaps, heads, 128 (bits 4: , 4)]       */
+  int32_t *err;             /* optional device word for KDA_DEVERR_* flags     */
+} kda_snapshot_args;
+
+/* Quantises state[slots[i]] into snapshot snaps[i], all heads.  The snapshots
+ * written are distinct.  Pointers to state, codes and scales are 16-byte
+ * aligned.  A slot or snapshot past its pool raises KDA_DEVERR_SLOT and the
+ * entry writes nothing.  One kernel on `stream`. */
+int kda_snapshot_save(const kda_snapshot_args *args, void *stream);
+
+/* Reads snapshot snaps[i] back into state[slots[i]], all heads; the slots
+ * written are distinct, a snapshot may be read into several.  Rules as above. */
+int kda_snapshot_load(const kda_snapshot_args *args, void *stream);
 
 /* Self-test of the bounded on-chip waits that every kernel above uses: one
  * CTA waits on an mbarrier that nothing completes; the wait gives up after

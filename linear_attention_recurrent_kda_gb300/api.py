@@ -293,3 +293,194 @@ def kda_oproj(*, partials, prefix, output, out_norm, blocks=None, norm=None,
         rc = _lib.call("kda_oproj", a, s.cuda_stream)
     if rc != _lib.KDA_SUCCESS:
         raise _lib.KdaError(rc, _lib.strerror(rc))
+
+
+# ------------------------------------ linear attention with one decay per head
+
+def _rows(name, t, width):
+    """A BF16 CUDA tensor [rows, width] whose rows may be slices of wider rows:
+    elements of a row adjacent, any row stride that the library takes."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 2 or (width is not None and t.shape[1] != width):
+        raise ValueError(f"{name} must be [rows, {'width' if width is None else width}], "
+                         f"got {tuple(t.shape)}")
+    stride = t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+    if t.shape[1] and (t.stride(1) != 1 or stride % 8 or stride < t.shape[1]):
+        raise ValueError(f"{name}: the elements of a row must be adjacent and rows a multiple "
+                         f"of 8 elements apart, got strides {tuple(t.stride())}")
+    return stride
+
+
+def _lin_rows(q, k, v, output, decay):
+    """Shapes of the linear-attention rows: (rows, heads, qk_heads, strides)."""
+    vs = _rows("v", v, None)
+    qs = _rows("q", q, None)
+    rows, width = v.shape
+    if width % DK or q.shape[1] % DK or not q.shape[1]:
+        raise ValueError("q, k and v rows must be whole heads of 128")
+    H, Hk = width // DK, q.shape[1] // DK
+    if H % Hk:
+        raise ValueError(f"{H} value heads are not a multiple of {Hk} query heads")
+    ks = _rows("k", k, q.shape[1])
+    os_ = _rows("output", output, width)
+    for name, t in (("q", q), ("k", k), ("output", output)):
+        if t.shape[0] != rows:
+            raise ValueError(f"{name} must have {rows} rows, got {t.shape[0]}")
+    _check("decay", decay, torch.float32)
+    if tuple(decay.shape) not in ((H,), (rows, H)):
+        raise ValueError(f"decay must be [{H}] or [{rows}, {H}], got {tuple(decay.shape)}")
+    return rows, H, Hk, (qs, ks, vs, os_)
+
+
+def _lin_state(state, H):
+    _check("state", state, torch.float32)
+    if state.dim() != 4 or tuple(state.shape[1:]) != (H, DK, DK):
+        raise ValueError("state must be [num_slots, heads, 128, 128]")
+    return state.shape[0]
+
+
+def _run(entry, args, dev, stream):
+    with torch.cuda.device(dev):
+        s = stream if stream is not None else torch.cuda.current_stream(dev)
+        rc = _lib.call(entry, args, s.cuda_stream)
+    if rc != _lib.KDA_SUCCESS:
+        raise _lib.KdaError(rc, _lib.strerror(rc))
+
+
+def kda_lin_prompt(*, q, k, v, decay, seq_starts, output, scale: float, state=None,
+                   src_slots=None, dst_slots=None, max_seq: Optional[int] = None, err=None,
+                   path: int = 0, workspace=None,
+                   stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Linear attention with one decay per head over ragged prompts
+    (include/kda.h ``kda_lin_prompt``).
+
+    ``q``, ``k`` bf16 [tokens, qk_heads * 128], ``v``, ``output`` bf16 [tokens,
+    heads * 128] (each may be a slice of wider rows); ``decay`` f32, the
+    logarithm of the decay, [heads] or [tokens, heads]; ``seq_starts`` i32 [seqs
+    + 1]; ``state`` f32 [num_slots, heads, 128, 128] with ``src_slots`` (the
+    pages the sequences start from) and ``dst_slots`` (where their last states
+    go), i32 [seqs] each or None.  ``max_seq``: no sequence is longer (default:
+    ``tokens``; the tighter, the better the work is laid out).  ``workspace``: a
+    CUDA uint8 tensor of at least ``kda_lin_prompt_workspace`` bytes; by default
+    allocated for the call, on the stream it runs on."""
+    i32 = torch.int32
+    rows, H, Hk, strides = _lin_rows(q, k, v, output, decay)
+    _check("seq_starts", seq_starts, i32)
+    if seq_starts.dim() != 1 or seq_starts.shape[0] < 1:
+        raise ValueError("seq_starts must be [seqs + 1]")
+    B = seq_starts.shape[0] - 1
+    _check("src_slots", src_slots, i32, (B,), allow_none=True)
+    _check("dst_slots", dst_slots, i32, (B,), allow_none=True)
+    if state is None and (src_slots is not None or dst_slots is not None):
+        raise ValueError("state is required with src_slots or dst_slots")
+    num_slots = 0 if state is None else _lin_state(state, H)
+    _check("err", err, i32, allow_none=True)
+    dev = v.device
+    _same_device(dev, q=q, k=k, output=output, decay=decay, seq_starts=seq_starts, state=state,
+                 src_slots=src_slots, dst_slots=dst_slots, err=err, workspace=workspace)
+    a = _lib.KdaLinPromptArgs()
+    a.seqs, a.heads, a.qk_heads, a.tokens = B, H, Hk, rows
+    a.max_seq = rows if max_seq is None else min(int(max_seq), rows)
+    a.num_slots, a.decay_rows, a.path = num_slots, int(decay.dim() == 2), int(path)
+    a.q_stride, a.k_stride, a.v_stride, a.o_stride = strides
+    a.q, a.k, a.v, a.decay = _ptr(q), _ptr(k), _ptr(v), _ptr(decay)
+    a.seq_starts, a.src_slots, a.dst_slots = _ptr(seq_starts), _ptr(src_slots), _ptr(dst_slots)
+    a.state, a.output, a.scale, a.err = _ptr(state), _ptr(output), float(scale), _ptr(err)
+    need = _lib.prompt_workspace(a)
+    if workspace is not None:
+        _check("workspace", workspace, torch.uint8)
+        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
+    elif need > 0:
+        # from the pool of the stream that uses it: freed behind its kernels
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        a.workspace, a.workspace_bytes = _ptr(workspace), need
+    _run("kda_lin_prompt", a, dev, stream)
+
+
+class KdaLinStep:
+    """A prepared single-token step of linear attention with one decay per head
+    (include/kda.h ``kda_lin_step``) over fixed device tensors.
+
+    ``q``, ``k`` bf16 [batch, qk_heads * 128], ``v``, ``output`` bf16 [batch,
+    heads * 128]; ``decay`` f32 [heads] or [batch, heads]; ``slots`` i32 [batch]
+    (<= 0: padding); ``state`` f32 [num_slots, heads, 128, 128], updated in
+    place.  Validates once and launches with ``__call__(stream)``; the tensors'
+    contents may change between calls, their storage may not."""
+
+    def __init__(self, *, q, k, v, decay, slots, state, output, scale: float, err=None):
+        rows, H, Hk, strides = _lin_rows(q, k, v, output, decay)
+        _check("slots", slots, torch.int32, (rows,))
+        num_slots = _lin_state(state, H)
+        _check("err", err, torch.int32, allow_none=True)
+        self.device = v.device
+        _same_device(v.device, q=q, k=k, output=output, decay=decay, slots=slots, state=state,
+                     err=err)
+        a = _lib.KdaLinStepArgs()
+        a.batch, a.heads, a.qk_heads, a.num_slots = rows, H, Hk, num_slots
+        a.decay_rows = int(decay.dim() == 2)
+        a.q_stride, a.k_stride, a.v_stride, a.o_stride = strides
+        a.q, a.k, a.v, a.decay, a.slots = _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(slots)
+        a.state, a.output, a.scale, a.err = _ptr(state), _ptr(output), float(scale), _ptr(err)
+        self.args = a
+        self._keep = (q, k, v, decay, slots, state, output, err)
+
+    def __call__(self, stream: Optional[torch.cuda.Stream] = None) -> None:
+        _run("kda_lin_step", self.args, self.device, stream)
+
+
+def kda_lin_step(stream: Optional[torch.cuda.Stream] = None, **kw) -> None:
+    """One single-token step on ``stream``; see ``KdaLinStep``."""
+    KdaLinStep(**kw)(stream)
+
+
+# ------------------------------------------------- snapshots of state pages
+
+def _snapshot(entry, state, slots, codes, scales, snaps, err, stream):
+    _check("state", state, torch.float32)
+    if state.dim() != 4 or tuple(state.shape[2:]) != (DK, DK):
+        raise ValueError("state must be [num_slots, heads, 128, 128]")
+    H = state.shape[1]
+    if not isinstance(codes, torch.Tensor) or codes.dtype not in (torch.int8, torch.uint8):
+        raise TypeError("codes must be an int8 (8 bits) or uint8 (4 bits) tensor")
+    bits = 8 if codes.dtype == torch.int8 else 4
+    _check("codes", codes, codes.dtype)
+    if codes.dim() != 4 or tuple(codes.shape[1:]) != (H, DK, DK * bits // 8):
+        raise ValueError(f"codes of {bits} bits must be [num_snaps, {H}, 128, {DK * bits // 8}]")
+    n = codes.shape[0]
+    _check("scales", scales, torch.float32, (n, H, DK) if bits == 8 else (n, H, DK, 4))
+    _check("slots", slots, torch.int32)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [count]")
+    _check("snaps", snaps, torch.int32, tuple(slots.shape))
+    _check("err", err, torch.int32, allow_none=True)
+    _same_device(state.device, codes=codes, scales=scales, slots=slots, snaps=snaps, err=err)
+    a = _lib.KdaSnapshotArgs()
+    a.count, a.heads, a.num_slots, a.num_snaps, a.bits = slots.shape[0], H, state.shape[0], n, bits
+    a.slots, a.snaps, a.state = _ptr(slots), _ptr(snaps), _ptr(state)
+    a.codes, a.scales, a.err = _ptr(codes), _ptr(scales), _ptr(err)
+    _run(entry, a, state.device, stream)
+
+
+def kda_snapshot_save(*, state, slots, codes, scales, snaps, err=None,
+                      stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Keep the pages ``state[slots[i]]`` as snapshots ``snaps[i]`` in 8 or 4
+    bits (include/kda.h ``kda_snapshot_save``).
+
+    ``state`` f32 [num_slots, heads, 128, 128]; ``codes`` int8 [num_snaps, heads,
+    128, 128] (8 bits) or uint8 [num_snaps, heads, 128, 64] (4 bits); ``scales``
+    f32 [num_snaps, heads, 128] or [num_snaps, heads, 128, 4]; ``slots`` and
+    ``snaps`` i32 [count], an entry with either <= 0 is skipped."""
+    _snapshot("kda_snapshot_save", state, slots, codes, scales, snaps, err, stream)
+
+
+def kda_snapshot_load(*, codes, scales, snaps, state, slots, err=None,
+                      stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Read the snapshots ``snaps[i]`` back into ``state[slots[i]]``; see
+    ``kda_snapshot_save``."""
+    _snapshot("kda_snapshot_load", state, slots, codes, scales, snaps, err, stream)

@@ -1,8 +1,8 @@
 """Build the in-tree CUDA libraries for sm_103a.
 
 ``libkda_gb300.so``: the translation units of the step and its companions
-(the step, split, replay, output-projection and self-test kernels; the C ABI
-of include/kda.h).  ``libkda_probe_gb300.so``: the measurement probe of
+(the step, split, replay, output-projection, linear-attention, snapshot and
+self-test kernels; the C ABI of include/kda.h).  ``libkda_probe_gb300.so``: the measurement probe of
 include/kda_probe.h, a bench instrument kept out of the product library.
 Every translation unit is compiled by its own nvcc process, in parallel, with
 a single ``-gencode arch=compute_103a,code=sm_103a``; each library is linked
@@ -23,10 +23,12 @@ LIB_PATH = os.path.join(HERE, "libkda_gb300.so")
 PROBE_LIB_PATH = os.path.join(HERE, "libkda_probe_gb300.so")
 SOURCES = [os.path.join(CSRC, n) for n in ("kda_step.cu", "kda_split.cu",
                                             "kda_recover.cu", "kda_oproj.cu",
+                                            "kda_lin.cu", "kda_snapshot.cu",
                                             "kda_selftest.cu")]
 PROBE_SOURCES = [os.path.join(CSRC, "kda_probe.cu")]
 HEADERS = [os.path.join(INCLUDE, "kda.h"), os.path.join(INCLUDE, "kda_probe.h"),
-           os.path.join(CSRC, "kda_device.cuh"), os.path.join(CSRC, "kda_host.h")]
+           os.path.join(CSRC, "kda_device.cuh"), os.path.join(CSRC, "kda_lin.cuh"),
+           os.path.join(CSRC, "kda_host.h")]
 LIBS = ((LIB_PATH, SOURCES), (PROBE_LIB_PATH, PROBE_SOURCES))
 
 NVCC_FLAGS = [

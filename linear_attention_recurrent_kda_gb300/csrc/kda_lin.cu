@@ -1,0 +1,263 @@
+// Linear attention with one decay per head: the single-token step, the
+// token-by-token prompt form, and the checks and dispatch of both calls.
+//
+// Both forms keep a page slice in registers: a warp holds 16 value rows, lane
+// l the keys 4l .. 4l+3 of each (a row is one 512-byte access of the warp), so
+// that S q needs one 16-shuffle reduce-scatter for 16 rows.  A product v k is
+// rounded before it joins the decayed state: both are exact BF16 values, so it
+// is exact in FP32.
+//
+// The step is HBM-bound (a page read and written per item, 128 KiB against
+// 160 kflop).  CTAs of two warps, a quarter page each: all 16 loads of a thread
+// are in flight at once and the many small CTAs of an SM keep its memory
+// queue full without a pipeline; a batch of few requests still spreads over
+// the SMs.
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "../../include/kda.h"
+#include "kda_device.cuh"
+#include "kda_host.h"
+#include "kda_lin.cuh"
+
+namespace kda {
+namespace lin {
+
+constexpr int kWarps = 2;                               // of a CTA (recurrent forms)
+constexpr int kParts = kDim / (kWarps * kRows);         // CTAs of a page
+
+struct StepParams {
+  int batch, heads, group, num_slots, decay_rows;
+  int64_t q_stride, k_stride, v_stride, o_stride;
+  const __nv_bfloat16 *q, *k, *v;
+  const float *decay;
+  const int32_t *slots;
+  float *state;
+  __nv_bfloat16 *output;
+  float scale;
+  int32_t *err;
+};
+
+__global__ void __launch_bounds__(kWarps * 32) step_kernel(const __grid_constant__ StepParams p) {
+  const int part = blockIdx.x % kParts, item = blockIdx.x / kParts;
+  const int r = item / p.heads, h = item % p.heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row0 = (part * kWarps + warp) * kRows;
+  __nv_bfloat16 *out = p.output + r * p.o_stride + h * kDim + row0;
+  const int slot = __ldg(p.slots + r);
+  if (slot <= 0 || slot >= p.num_slots) {
+    if (lane < kRows) out[lane] = __float2bfloat16_rn(0.0f);
+    if (slot >= p.num_slots && p.err && threadIdx.x == 0) atomicOr(p.err, KDA_DEVERR_SLOT);
+    return;
+  }
+  float4 *page = reinterpret_cast<float4 *>(page_of(p.state, slot, p.heads, h) + row0 * kDim) + lane;
+  float4 s[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) s[i] = __ldcs(page + i * 32);
+  float k[4], q[4];
+  unpack4(__ldg(reinterpret_cast<const uint2 *>(p.k + r * p.k_stride + h / p.group * kDim) + lane), k);
+  unpack4(__ldg(reinterpret_cast<const uint2 *>(p.q + r * p.q_stride + h / p.group * kDim) + lane), q);
+  const float v = __bfloat162float(p.v[r * p.v_stride + h * kDim + row0 + (lane & (kRows - 1))]);
+  const float d =
+      expf(__ldg(p.decay + (p.decay_rows ? static_cast<int64_t>(r) * p.heads : 0) + h));
+  const float o = token_step(s, d, k, q, v, lane);
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) __stcs(page + i * 32, s[i]);
+  if ((lane & 1) == 0) out[lane >> 1] = __float2bfloat16_rn(p.scale * o);
+}
+
+// Token by token over a sequence: the operands of token t + 1 are loaded while
+// token t is computed.
+__global__ void __launch_bounds__(kWarps * 32)
+    recurrent_kernel(const __grid_constant__ PromptParams p) {
+  const int part = blockIdx.x % kParts, item = blockIdx.x / kParts;
+  const int b = item / p.heads, h = item % p.heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row0 = (part * kWarps + warp) * kRows;
+  Seq seq;
+  if (const int bad = resolve_seq(p, b, &seq)) {
+    if (p.err && threadIdx.x == 0) atomicOr(p.err, bad);
+    return;
+  }
+  float4 s[kRows];
+  if (seq.src) {
+    const float4 *page =
+        reinterpret_cast<const float4 *>(page_of(p.state, seq.src, p.heads, h) + row0 * kDim) + lane;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) s[i] = page[i * 32];
+  } else {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) s[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  const uint2 *kp =
+      reinterpret_cast<const uint2 *>(p.k + seq.start * p.k_stride + h / p.group * kDim) + lane;
+  const uint2 *qp =
+      reinterpret_cast<const uint2 *>(p.q + seq.start * p.q_stride + h / p.group * kDim) + lane;
+  const __nv_bfloat16 *vp =
+      p.v + seq.start * p.v_stride + h * kDim + row0 + (lane & (kRows - 1));
+  const float *gp = p.decay + (p.decay_rows ? static_cast<int64_t>(seq.start) * p.heads : 0) + h;
+  const int64_t g_step = p.decay_rows ? p.heads : 0;
+  __nv_bfloat16 *out = p.output + seq.start * p.o_stride + h * kDim + row0 + (lane >> 1);
+  uint2 kn = make_uint2(0, 0), qn = kn;
+  __nv_bfloat16 vn = __float2bfloat16_rn(0.0f);
+  float gn = 0.0f;
+  for (int t = 0; t <= seq.len; ++t) {
+    const uint2 kc = kn, qc = qn;
+    const float v = __bfloat162float(vn), d = expf(gn);
+    if (t < seq.len) {
+      kn = __ldg(kp);
+      qn = __ldg(qp);
+      vn = *vp;
+      gn = __ldg(gp);
+      kp += p.k_stride / 4;
+      qp += p.q_stride / 4;
+      vp += p.v_stride;
+      gp += g_step;
+    }
+    if (t == 0) continue;
+    float k[4], q[4];
+    unpack4(kc, k);
+    unpack4(qc, q);
+    const float o = token_step(s, d, k, q, v, lane);
+    if ((lane & 1) == 0) *out = __float2bfloat16_rn(p.scale * o);
+    out += p.o_stride;
+  }
+  if (seq.dst) {
+    float4 *page =
+        reinterpret_cast<float4 *>(page_of(p.state, seq.dst, p.heads, h) + row0 * kDim) + lane;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) __stcs(page + i * 32, s[i]);
+  }
+}
+
+static bool aligned(const void *q, uintptr_t to) {
+  return (reinterpret_cast<uintptr_t>(q) & (to - 1)) == 0;
+}
+
+// Row strides: multiples of 8 elements (16 bytes), no shorter than the row and
+// short enough for a tensor map (2^40 bytes).
+static bool stride_ok(int64_t stride, int64_t width) {
+  return stride % 8 == 0 && stride >= width && stride < (int64_t(1) << 38);
+}
+
+template <class Args>
+static int check_common(const Args *a, int64_t count) {
+  if (count < 0 || a->heads < 0 || a->qk_heads < 1 || a->heads % a->qk_heads != 0)
+    return KDA_ERR_SHAPE;
+  if (a->decay_rows != 0 && a->decay_rows != 1) return KDA_ERR_SHAPE;
+  if (count * a->heads * kParts > 0x7fffffffll) return KDA_ERR_SHAPE;
+  const int64_t kw = int64_t(a->qk_heads) * kDim, vw = int64_t(a->heads) * kDim;
+  if (!stride_ok(a->q_stride, kw) || !stride_ok(a->k_stride, kw) || !stride_ok(a->v_stride, vw) ||
+      !stride_ok(a->o_stride, vw))
+    return KDA_ERR_SHAPE;
+  return KDA_SUCCESS;
+}
+
+template <class Args>
+static bool rows_aligned(const Args *a) {
+  return aligned(a->q, 16) && aligned(a->k, 16) && aligned(a->v, 16) && aligned(a->output, 16) &&
+         aligned(a->state, 16) && aligned(a->decay, 4) && aligned(a->err, 4);
+}
+
+static int run_step(const kda_lin_step_args *a, cudaStream_t stream) {
+  if (!a) return KDA_ERR_NULL_ARGS;
+  if (const int rc = check_common(a, a->batch)) return rc;
+  if (a->num_slots < 1) return KDA_ERR_SHAPE;
+  if (a->batch == 0 || a->heads == 0) return KDA_SUCCESS;
+  if (!a->q || !a->k || !a->v || !a->decay || !a->slots || !a->state || !a->output)
+    return KDA_ERR_NULL_POINTER;
+  if (!rows_aligned(a) || !aligned(a->slots, 4)) return KDA_ERR_ALIGNMENT;
+  int dev = 0;
+  DeviceFacts df;
+  if (!current_device(&dev, &df)) return KDA_ERR_DEVICE;
+  StepParams p;
+  p.batch = a->batch;
+  p.heads = a->heads;
+  p.group = a->heads / a->qk_heads;
+  p.num_slots = a->num_slots;
+  p.decay_rows = a->decay_rows;
+  p.q_stride = a->q_stride;
+  p.k_stride = a->k_stride;
+  p.v_stride = a->v_stride;
+  p.o_stride = a->o_stride;
+  p.q = static_cast<const __nv_bfloat16 *>(a->q);
+  p.k = static_cast<const __nv_bfloat16 *>(a->k);
+  p.v = static_cast<const __nv_bfloat16 *>(a->v);
+  p.decay = a->decay;
+  p.slots = a->slots;
+  p.state = a->state;
+  p.output = static_cast<__nv_bfloat16 *>(a->output);
+  p.scale = a->scale;
+  p.err = a->err;
+  step_kernel<<<a->batch * a->heads * kParts, kWarps * 32, 0, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
+}
+
+// The sizes' part of the checks, and the plan: 1 = recurrent, 2 = chunked.
+static int plan_prompt(const kda_lin_prompt_args *a, int *path) {
+  if (const int rc = check_common(a, a->seqs)) return rc;
+  if (a->tokens < 0 || a->max_seq < 0 || (a->state && a->num_slots < 1)) return KDA_ERR_SHAPE;
+  if (a->path < 0 || a->path > 2) return KDA_ERR_PATH;
+  *path = 1;
+  return KDA_SUCCESS;
+}
+
+static int run_prompt(const kda_lin_prompt_args *a, cudaStream_t stream) {
+  if (!a) return KDA_ERR_NULL_ARGS;
+  int path = 0;
+  if (const int rc = plan_prompt(a, &path)) return rc;
+  if (a->seqs == 0 || a->heads == 0) return KDA_SUCCESS;
+  if (!a->seq_starts || !a->decay) return KDA_ERR_NULL_POINTER;
+  if (a->tokens > 0 && (!a->q || !a->k || !a->v || !a->output)) return KDA_ERR_NULL_POINTER;
+  if ((a->src_slots || a->dst_slots) && !a->state) return KDA_ERR_NULL_POINTER;
+  if (!rows_aligned(a) || !aligned(a->seq_starts, 4) || !aligned(a->src_slots, 4) ||
+      !aligned(a->dst_slots, 4))
+    return KDA_ERR_ALIGNMENT;
+  int dev = 0;
+  DeviceFacts df;
+  if (!current_device(&dev, &df)) return KDA_ERR_DEVICE;
+  PromptParams p = {};
+  p.seqs = a->seqs;
+  p.heads = a->heads;
+  p.group = a->heads / a->qk_heads;
+  p.tokens = a->tokens;
+  p.max_seq = a->max_seq;
+  p.num_slots = a->num_slots;
+  p.decay_rows = a->decay_rows;
+  p.segs = 1;
+  p.seg_len = a->max_seq;
+  p.q_stride = a->q_stride;
+  p.k_stride = a->k_stride;
+  p.v_stride = a->v_stride;
+  p.o_stride = a->o_stride;
+  p.q = static_cast<const __nv_bfloat16 *>(a->q);
+  p.k = static_cast<const __nv_bfloat16 *>(a->k);
+  p.v = static_cast<const __nv_bfloat16 *>(a->v);
+  p.decay = a->decay;
+  p.seq_starts = a->seq_starts;
+  p.src_slots = a->src_slots;
+  p.dst_slots = a->dst_slots;
+  p.state = a->state;
+  p.output = static_cast<__nv_bfloat16 *>(a->output);
+  p.scale = a->scale;
+  p.err = a->err;
+  recurrent_kernel<<<a->seqs * a->heads * kParts, kWarps * 32, 0, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
+}
+
+}  // namespace lin
+}  // namespace kda
+
+extern "C" int kda_lin_step(const kda_lin_step_args *args, void *stream) {
+  return kda::lin::run_step(args, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int kda_lin_prompt(const kda_lin_prompt_args *args, void *stream) {
+  return kda::lin::run_prompt(args, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int64_t kda_lin_prompt_workspace(const kda_lin_prompt_args *args) {
+  if (!args) return -1;
+  return 0;
+}

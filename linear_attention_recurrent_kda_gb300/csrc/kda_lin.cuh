@@ -1,0 +1,94 @@
+// Shared by the linear-attention kernels (one decay per head): the prompt
+// call's parameters, the resolution of one sequence, and the slice of a state
+// page that a warp keeps in registers in the recurrent forms.
+//
+// Per head, page S [value row i][key j] in FP32:
+//   S_t = exp(g_t) S_{t-1} + v_t k_t^T,   o_t = scale * S_t q_t.
+#pragma once
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "../../include/kda.h"
+#include "kda_device.cuh"
+
+namespace kda {
+namespace lin {
+
+constexpr int kDim = 128;                 // keys and value rows of a page
+constexpr int kPage = kDim * kDim;        // floats of a page
+constexpr int kRows = 16;                 // value rows a warp holds (recurrent forms)
+
+struct PromptParams {
+  int seqs, heads, group, tokens, max_seq, num_slots, decay_rows;  // group = heads / qk_heads
+  int segs, seg_len;      // segments a sequence may be split into (1: not split), their tokens
+  int64_t q_stride, k_stride, v_stride, o_stride;
+  const __nv_bfloat16 *q, *k, *v;
+  const float *decay;
+  const int32_t *seq_starts, *src_slots, *dst_slots;
+  float *state;
+  __nv_bfloat16 *output;
+  float scale;
+  int32_t *err;
+  float *ws_state;        // [seqs][segs][heads][128 * 128] when segs > 1
+  float *ws_decay;        // [seqs][segs][heads]
+};
+
+// One sequence of a prompt call: its rows and slots (0: none).
+struct Seq {
+  int start, len, src, dst;
+};
+
+// Resolves sequence b.  Returns the KDA_DEVERR_* flags it raises; a flagged
+// sequence is skipped.
+__device__ __forceinline__ int resolve_seq(const PromptParams &p, int b, Seq *s) {
+  const int lo = __ldg(p.seq_starts + b), hi = __ldg(p.seq_starts + b + 1);
+  int bad = 0;
+  if (lo < 0 || hi < lo || hi > p.tokens || hi - lo > p.max_seq) bad |= KDA_DEVERR_SEQ;
+  const int src = p.src_slots ? __ldg(p.src_slots + b) : 0;
+  const int dst = p.dst_slots ? __ldg(p.dst_slots + b) : 0;
+  if (src >= p.num_slots && src > 0) bad |= KDA_DEVERR_SLOT;
+  if (dst >= p.num_slots && dst > 0) bad |= KDA_DEVERR_SLOT;
+  s->start = lo;
+  s->len = hi - lo;
+  s->src = src > 0 ? src : 0;
+  s->dst = dst > 0 ? dst : 0;
+  return bad;
+}
+
+__device__ __forceinline__ float *page_of(float *state, int slot, int heads, int h) {
+  return state + (static_cast<int64_t>(slot) * heads + h) * kPage;
+}
+
+__device__ __forceinline__ void unpack4(const uint2 &u, float (&f)[4]) {
+  f[0] = __uint_as_float(u.x << 16);
+  f[1] = __uint_as_float(u.x & 0xFFFF0000u);
+  f[2] = __uint_as_float(u.y << 16);
+  f[3] = __uint_as_float(u.y & 0xFFFF0000u);
+}
+
+// One token on a warp's kRows value rows: lane l holds keys 4l .. 4l+3 of each
+// row.  vrow: lane r < kRows holds v of row r.  Returns S q of row lane / 2
+// (FP32, unscaled).
+__device__ __forceinline__ float token_step(float4 (&s)[kRows], float d, const float (&k)[4],
+                                            const float (&q)[4], float vrow, int lane) {
+  float dot[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const float v = __shfl_sync(0xffffffffu, vrow, r);
+    s[r].x = __fmaf_rn(s[r].x, d, v * k[0]);
+    s[r].y = __fmaf_rn(s[r].y, d, v * k[1]);
+    s[r].z = __fmaf_rn(s[r].z, d, v * k[2]);
+    s[r].w = __fmaf_rn(s[r].w, d, v * k[3]);
+    dot[r] = __fmaf_rn(s[r].w, q[3],
+                       __fmaf_rn(s[r].z, q[2], __fmaf_rn(s[r].y, q[1], s[r].x * q[0])));
+  }
+  return warp_reduce_scatter<kRows>(dot, lane);
+}
+
+// The chunked form (kda_lin_prompt.cu): enqueues its kernels for checked
+// parameters.  Returns a KDA_* code.
+int launch_chunked(const PromptParams &p, int qk_heads, int sms, cudaStream_t stream);
+
+}  // namespace lin
+}  // namespace kda

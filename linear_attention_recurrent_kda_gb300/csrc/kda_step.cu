@@ -1390,6 +1390,7 @@ const char *kda_strerror(int code) {
     case KDA_ERR_DEVICE: return "no usable sm_103 device";
     case KDA_ERR_LAUNCH: return "kernel launch failed";
     case KDA_ERR_PATH: return "path must be 0, 1 or 2";
+    case KDA_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     default: return "unknown error code";
   }
 }

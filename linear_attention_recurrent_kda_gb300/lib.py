@@ -26,12 +26,16 @@ KDA_ERR_SHAPE = 8
 KDA_ERR_DEVICE = 9
 KDA_ERR_LAUNCH = 10
 KDA_ERR_PATH = 11
+KDA_ERR_WORKSPACE = 12
 KDA_PATH_AUTO, KDA_PATH_PERSISTENT, KDA_PATH_SPLIT = 0, 1, 2
 KDA_DEVERR_SLOT = 1
 KDA_DEVERR_ACCEPTED = 2
 KDA_DEVERR_TIMEOUT = 4
+KDA_DEVERR_SEQ = 8
 
 EXPORTED = ("kda_decode", "kda_verify", "kda_step_noalloc", "kda_recover", "kda_oproj",
+            "kda_lin_prompt_workspace", "kda_lin_prompt", "kda_lin_step",
+            "kda_snapshot_save", "kda_snapshot_load",
             "kda_selftest_wait_timeout", "kda_strerror", "kda_abi_version")
 
 
@@ -78,6 +82,46 @@ class KdaOprojArgs(ctypes.Structure):
     ]
 
 
+class KdaLinPromptArgs(ctypes.Structure):
+    """Mirror of ``struct kda_lin_prompt_args``."""
+    _fields_ = [
+        ("seqs", ctypes.c_int32), ("heads", ctypes.c_int32),
+        ("qk_heads", ctypes.c_int32), ("tokens", ctypes.c_int32),
+        ("max_seq", ctypes.c_int32), ("num_slots", ctypes.c_int32),
+        ("decay_rows", ctypes.c_int32), ("path", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64), ("o_stride", ctypes.c_int64),
+        ("q", _P), ("k", _P), ("v", _P), ("decay", _P), ("seq_starts", _P),
+        ("src_slots", _P), ("dst_slots", _P), ("state", _P), ("output", _P),
+        ("scale", ctypes.c_float), ("err", _P), ("workspace", _P),
+        ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
+class KdaLinStepArgs(ctypes.Structure):
+    """Mirror of ``struct kda_lin_step_args``."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("heads", ctypes.c_int32),
+        ("qk_heads", ctypes.c_int32), ("num_slots", ctypes.c_int32),
+        ("decay_rows", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64), ("o_stride", ctypes.c_int64),
+        ("q", _P), ("k", _P), ("v", _P), ("decay", _P), ("slots", _P),
+        ("state", _P), ("output", _P), ("scale", ctypes.c_float), ("err", _P),
+    ]
+
+
+class KdaSnapshotArgs(ctypes.Structure):
+    """Mirror of ``struct kda_snapshot_args``."""
+    _fields_ = [
+        ("count", ctypes.c_int32), ("heads", ctypes.c_int32),
+        ("num_slots", ctypes.c_int32), ("num_snaps", ctypes.c_int32),
+        ("bits", ctypes.c_int32),
+        ("slots", _P), ("snaps", _P), ("state", _P), ("codes", _P), ("scales", _P),
+        ("err", _P),
+    ]
+
+
 class KdaError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"KDA error {code}: {msg}")
@@ -106,6 +150,17 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.kda_recover.restype = ctypes.c_int
     lib.kda_oproj.argtypes = [ctypes.POINTER(KdaOprojArgs), ctypes.c_void_p]
     lib.kda_oproj.restype = ctypes.c_int
+    for name, args, res in (("kda_lin_prompt_workspace", [ctypes.POINTER(KdaLinPromptArgs)],
+                             ctypes.c_int64),
+                            ("kda_lin_prompt", [ctypes.POINTER(KdaLinPromptArgs), _P],
+                             ctypes.c_int),
+                            ("kda_lin_step", [ctypes.POINTER(KdaLinStepArgs), _P], ctypes.c_int),
+                            ("kda_snapshot_save", [ctypes.POINTER(KdaSnapshotArgs), _P],
+                             ctypes.c_int),
+                            ("kda_snapshot_load", [ctypes.POINTER(KdaSnapshotArgs), _P],
+                             ctypes.c_int)):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, res
     lib.kda_selftest_wait_timeout.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     lib.kda_selftest_wait_timeout.restype = ctypes.c_int
     lib.kda_strerror.argtypes = [ctypes.c_int]
@@ -125,3 +180,8 @@ def call(entry: str, args, stream_handle: int) -> int:
     """Raw call: returns the library's code without raising."""
     fn = getattr(load(), entry)
     return int(fn(ctypes.byref(args), ctypes.c_void_p(stream_handle or None)))
+
+
+def prompt_workspace(args) -> int:
+    """Bytes of workspace that ``kda_lin_prompt`` needs for these sizes."""
+    return int(load().kda_lin_prompt_workspace(ctypes.byref(args)))

@@ -1,0 +1,327 @@
+"""GPU tests of the linear attention with one decay per head (kda_lin_prompt,
+kda_lin_step) against the recurrence in 64 bits; bounds from tests/linref.py."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from linear_attention_recurrent_kda_gb300 import lib as kl
+from linear_attention_recurrent_kda_gb300.api import KdaLinStep, kda_lin_prompt, kda_lin_step
+from tests import linref
+
+pytestmark = pytest.mark.gpu
+D = 128
+bf16 = torch.bfloat16
+
+
+def rows(g, n, heads, unit=False):
+    x = torch.randn(n, heads, D, generator=g)
+    if unit:
+        x = x / x.norm(dim=-1, keepdim=True)
+    return x.view(n, heads * D).to(bf16)
+
+
+def make(lens, H, Hk, *, per_token=True, slots=0, seed=1, behind=0, scale_g=1.0):
+    """Inputs on the CPU; `behind` rows follow the last sequence."""
+    g = torch.Generator().manual_seed(seed)
+    n = sum(lens) + behind
+    starts = [0]
+    for x in lens:
+        starts.append(starts[-1] + x)
+    decay = -scale_g * torch.rand(*((n, H) if per_token else (H,)), generator=g)
+    return dict(q=rows(g, n, Hk, True), k=rows(g, n, Hk, True), v=rows(g, n, H), decay=decay,
+                starts=starts,
+                state=torch.randn(slots, H, D, D, generator=g) * 0.3 if slots else None)
+
+
+def launch(inp, *, src=None, dst=None, path=0, max_seq=None, stream=None, fill=float("nan"),
+           scale=0.5, err=None, **over):
+    """One call on device copies; returns (output, state) on the CPU."""
+    dev = {n: inp[n].cuda() for n in ("q", "k", "v", "decay")}
+    dev.update(over)
+    state = inp["state"].cuda() if inp["state"] is not None else None
+    out = torch.full((inp["v"].shape[0], inp["v"].shape[1]), fill, dtype=bf16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    kda_lin_prompt(**dev, seq_starts=torch.tensor(inp["starts"], **i32), output=out, scale=scale,
+                   state=state, src_slots=None if src is None else torch.tensor(src, **i32),
+                   dst_slots=None if dst is None else torch.tensor(dst, **i32), path=path,
+                   max_seq=max_seq, stream=stream, err=err)
+    torch.cuda.synchronize()
+    return out.cpu(), None if state is None else state.cpu()
+
+
+def verify(inp, got, path, src=None, dst=None, scale=0.5):
+    out, state = got
+    starts = inp["starts"]
+    ref, mag, S, M = linref.prompt(inp["q"], inp["k"], inp["v"], inp["decay"], starts, scale,
+                                   inp["state"], src)
+    for r in range(len(starts) - 1):
+        a, b = starts[r], starts[r + 1]
+        bound = linref.out_bound(ref[a:b], mag[a:b], b - a, path != 1)
+        off = (out[a:b].double() - ref[a:b]).abs()
+        assert torch.all(off <= bound), (r, a, b, float((off / bound).max()))
+        if dst is not None and dst[r] > 0:
+            off = (state[dst[r]].double() - S[r]).abs()
+            bound = linref.state_bound(M[r], b - a)
+            assert torch.all(off <= bound), (r, float((off / bound.clamp_min(1e-30)).max()))
+    # rows behind the last sequence and pages nobody writes stay as they were
+    assert torch.all(torch.isnan(out[starts[-1]:]))
+    if state is not None:
+        written = {s for s in dst or [] if s > 0}
+        for s in range(state.shape[0]):
+            if s not in written:
+                assert torch.equal(state[s], inp["state"][s]), s
+
+
+PATHS = [1, 2]
+LENS = [[1], [2, 1], [5, 0, 3], [127], [128], [129, 1], [31, 32, 33, 64, 65], [255, 256, 257],
+        [400, 7, 0, 130]]
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("lens", LENS, ids=lambda v: "-".join(map(str, v)))
+@pytest.mark.parametrize("H,Hk,per_token", [(2, 2, True), (4, 1, False), (3, 3, True)])
+def test_prompt(lens, H, Hk, per_token, path):
+    B = len(lens)
+    inp = make(lens, H, Hk, per_token=per_token, slots=2 * B + 2, seed=sum(lens) + H, behind=5)
+    # every other sequence starts from a page, the last one's state is dropped
+    src = [r + 1 if r % 2 == 0 else 0 for r in range(B)]
+    dst = [B + 1 + r for r in range(B)]
+    if B > 1:
+        dst[-1] = 0
+    verify(inp, launch(inp, src=src, dst=dst, path=path), path, src, dst)
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_without_a_state(path):
+    inp = make([3, 140], 2, 2, seed=5)
+    verify(inp, launch(inp, path=path), path)
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_page_in_place_and_shared(path):
+    """A sequence may write the page it starts from; two may start from one page."""
+    inp = make([150, 33, 70], 2, 1, slots=5, seed=6)
+    src, dst = [1, 4, 4], [1, 2, 3]
+    verify(inp, launch(inp, src=src, dst=dst, path=path), path, src, dst)
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("how", ["reset", "none", "strong", "mixed"])
+def test_decays(path, how):
+    """Decays of -inf (a reset), 0 (none) and far below the smallest factor."""
+    inp = make([300, 40], 2, 2, slots=4, seed=7)
+    g = inp["decay"]
+    if how == "reset":
+        g[torch.randperm(340, generator=torch.Generator().manual_seed(1))[:20], 0] = -float("inf")
+        g[150:155] = -float("inf")
+    elif how == "none":
+        g.zero_()
+    elif how == "strong":
+        g.mul_(60.0)
+    else:
+        g[::7] *= 200.0
+        g[::3] = 0.0
+    src, dst = [1, 0], [2, 3]
+    verify(inp, launch(inp, src=src, dst=dst, path=path), path, src, dst)
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_rows_outside_a_sequence_reach_nothing(path, bad):
+    """Non-finite rows behind the last sequence, and of another sequence, leave
+    the others' outputs and pages as they are without them."""
+    inp = make([70, 130, 9], 2, 2, slots=5, seed=8, behind=140)
+    src, dst = [1, 0, 0], [2, 3, 4]
+    clean = launch(inp, src=src, dst=dst, path=path)
+    dirty = {n: t.clone() if isinstance(t, torch.Tensor) else t for n, t in inp.items()}
+    for n in ("q", "k", "v", "decay"):
+        dirty[n][209:] = bad
+        dirty[n][70:200] = bad
+    got = launch(dirty, src=src, dst=dst, path=path)
+    for a, b in ((0, 70), (200, 209)):
+        assert torch.equal(got[0][a:b], clean[0][a:b])
+    assert torch.equal(got[1][2], clean[1][2]) and torch.equal(got[1][4], clean[1][4])
+    assert torch.all(torch.isnan(got[0][209:]))
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_slices_of_wider_rows(path):
+    """q, k and v as column slices of one projection, the output as a slice too."""
+    inp = make([200, 37], 2, 2, slots=3, seed=9)
+    x = torch.full((237, 3 * 256 + 40), float("nan"), dtype=bf16)
+    for i, n in enumerate("qkv"):
+        x[:, 8 + 256 * i:8 + 256 * (i + 1)] = inp[n]
+    x = x.cuda()
+    out = torch.full((237, 512), float("nan"), dtype=bf16, device="cuda")
+    state = inp["state"].cuda()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    kda_lin_prompt(q=x[:, 8:264], k=x[:, 264:520], v=x[:, 520:776], decay=inp["decay"].cuda(),
+                   seq_starts=torch.tensor(inp["starts"], **i32), output=out[:, 128:384],
+                   scale=0.5, state=state, dst_slots=torch.tensor([2, 1], **i32), path=path)
+    torch.cuda.synchronize()
+    verify(inp, (out[:, 128:384].cpu(), state.cpu()), path, None, [2, 1])
+    assert torch.all(torch.isnan(out[:, :128])) and torch.all(torch.isnan(out[:, 384:]))
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_flagged_sequences_write_nothing(path):
+    inp = make([40, 50, 60, 70], 2, 2, slots=6, seed=10)
+    good = launch(inp, src=[1, 0, 0, 0], dst=[2, 3, 4, 5], path=path)
+
+    def check(src, dst, starts, flag, bad, max_seq=None):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = launch(dict(inp, starts=starts), src=src, dst=dst, path=path, err=err,
+                     max_seq=max_seq)
+        assert int(err) == flag
+        for r in range(4):
+            a, b = inp["starts"][r], inp["starts"][r + 1]
+            if r in bad:
+                assert torch.all(torch.isnan(got[0][a:b])), r
+                assert torch.equal(got[1][r + 2], inp["state"][r + 2])
+            else:
+                assert torch.equal(got[0][a:b], good[0][a:b]), r
+                assert torch.equal(got[1][r + 2], good[1][r + 2])
+
+    starts = inp["starts"]
+    check([1, 6, 0, 0], [2, 3, 4, 5], starts, kl.KDA_DEVERR_SLOT, {1})
+    check([1, 0, 0, 0], [2, 3, 99, 5], starts, kl.KDA_DEVERR_SLOT, {2})
+    check([1, 0, 0, 0], [2, 3, 4, 5], starts[:4] + [221], kl.KDA_DEVERR_SEQ, {3})
+    check([1, 0, 0, 0], [2, 3, 4, 5], [-1] + starts[1:], kl.KDA_DEVERR_SEQ, {0})
+    check([1, 0, 0, 0], [2, 3, 4, 5], starts, kl.KDA_DEVERR_SEQ, {3}, max_seq=60)
+    check([1, 0, 0, 0], [2, 3, 4, 5], [0, 40, 30, 150, 220], kl.KDA_DEVERR_SEQ, {1, 2},
+          max_seq=70)
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_other_stream_and_graph(path):
+    inp = make([260, 33], 2, 2, slots=5, seed=11)
+    src, dst = [1, 0], [3, 4]
+    want = launch(inp, src=src, dst=dst, path=path)
+    s = torch.cuda.Stream()
+    got = launch(inp, src=src, dst=dst, path=path, stream=s)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    dev = {n: inp[n].cuda() for n in ("q", "k", "v", "decay", "state")}
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = torch.zeros(293, 256, dtype=bf16, device="cuda")
+    kw = dict(dev, seq_starts=torch.tensor(inp["starts"], **i32), output=out, scale=0.5,
+              src_slots=torch.tensor(src, **i32), dst_slots=torch.tensor(dst, **i32), path=path)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kda_lin_prompt(**kw)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(want[0], out.cpu())
+    assert torch.equal(want[1], dev["state"].cpu())
+
+
+# ------------------------------------------------------------------------- step
+
+def step_ref(inp, state, slots, scale):
+    """Values and magnitudes of one step per live request."""
+    B = len(slots)
+    return linref.prompt(inp["q"], inp["k"], inp["v"], inp["decay"], list(range(B + 1)), scale,
+                         state, slots)
+
+
+@pytest.mark.parametrize("B,H,Hk,per_token", [(1, 1, 1, True), (7, 2, 1, False), (33, 5, 5, True),
+                                              (3, 64, 8, True)])
+def test_step(B, H, Hk, per_token):
+    inp = make([1] * B, H, Hk, per_token=per_token, slots=B + 3, seed=B)
+    g = torch.Generator().manual_seed(B)
+    slots = (torch.randperm(B + 2, generator=g)[:B] + 1).to(torch.int32)
+    if B > 2:
+        slots[1], slots[2] = 0, -4
+    state = inp["state"].cuda()
+    out = torch.full((B, H * D), float("nan"), dtype=bf16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = {n: inp[n].cuda() for n in ("q", "k", "v", "decay")}
+    kda_lin_step(**kw, slots=slots.cuda(), state=state, output=out, scale=0.7, err=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    sl = slots.tolist()
+    ref, mag, S, M = step_ref(inp, inp["state"], sl, 0.7)
+    for r, s in enumerate(sl):
+        if s <= 0:
+            assert torch.all(out[r].cpu().view(torch.int16) == 0)
+            continue
+        off = (out[r].cpu().double() - ref[r]).abs()
+        assert torch.all(off <= linref.out_bound(ref[r], mag[r], 1, False))
+        off = (state[s].cpu().double() - S[r]).abs()
+        assert torch.all(off <= 5 * linref.U32 * M[r])
+    for s in set(range(B + 3)) - set(sl):
+        assert torch.equal(state[s].cpu(), inp["state"][s])
+
+
+def test_step_flags_a_slot_past_the_pool():
+    inp = make([1] * 3, 2, 2, slots=4, seed=3)
+    kw = {n: inp[n].cuda() for n in ("q", "k", "v", "decay", "state")}
+    out = torch.full((3, 256), float("nan"), dtype=bf16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kda_lin_step(**kw, slots=torch.tensor([1, 4, 2], dtype=torch.int32).cuda(), output=out,
+                 scale=1.0, err=err)
+    assert int(err) == kl.KDA_DEVERR_SLOT
+    assert torch.all(out[1].view(torch.int16) == 0) and torch.isfinite(out).all()
+    assert torch.equal(kw["state"][3].cpu(), inp["state"][3])
+
+
+def test_steps_from_a_page_past_32_bit_offsets():
+    """The last pages of a pool of more than 2^31 floats (prompt and step)."""
+    H, slots = 64, 2 ** 31 // (64 * D * D) + 3
+    state = torch.zeros(slots, H, D, D, device="cuda")
+    inp = make([140], H, H, seed=4)
+    kw = {n: inp[n].cuda() for n in ("q", "k", "v", "decay")}
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = torch.zeros(140, H * D, dtype=bf16, device="cuda")
+    small = torch.zeros(3, H, D, D, device="cuda")
+    for pool, last in ((state, slots - 1), (small, 2)):
+        for path in PATHS:
+            kda_lin_prompt(**kw, seq_starts=torch.tensor([0, 140], **i32), output=out, scale=1.0,
+                           state=pool, dst_slots=torch.tensor([last - (path == 1)], **i32),
+                           path=path)
+        one = {n: t[:1] if t.dim() == 2 else t for n, t in kw.items()}
+        o = torch.zeros(1, H * D, dtype=bf16, device="cuda")
+        kda_lin_step(**one, slots=torch.tensor([last], **i32), state=pool, output=o, scale=1.0)
+    assert torch.equal(state[slots - 2:], small[1:])
+
+
+def test_prepared_step_repeats_and_replays():
+    """KdaLinStep over changing contents, eagerly and from a graph: the same bits."""
+    inp = make([1] * 6, 4, 2, slots=8, seed=12)
+    kw = {n: inp[n].cuda() for n in ("q", "k", "v", "decay")}
+    slots = torch.tensor([3, 1, 0, 7, 5, 2], dtype=torch.int32, device="cuda")
+    res = []
+    for mode in ("eager", "graph"):
+        state, out = inp["state"].cuda(), torch.zeros(6, 512, dtype=bf16, device="cuda")
+        x = {n: t.clone() for n, t in kw.items()}
+        step = KdaLinStep(**x, slots=slots, state=state, output=out, scale=0.3)
+        if mode == "graph":
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step()
+        outs = []
+        for t in range(4):
+            for n in "qkv":
+                x[n].copy_(kw[n].roll(t, 0))
+            graph.replay() if mode == "graph" else step()
+            outs.append(out.clone())
+        torch.cuda.synchronize()
+        res.append((torch.stack(outs), state))
+    assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
+
+
+def test_prompt_recurrent_form_equals_steps_bitwise():
+    """The recurrent prompt form is the step token by token: the same bits."""
+    inp = make([11], 3, 3, slots=3, seed=13)
+    out, state = launch(inp, src=[1], dst=[2], path=1)
+    st = inp["state"].cuda()
+    kw = {n: inp[n].cuda() for n in ("q", "k", "v", "decay")}
+    for t in range(11):
+        o = torch.zeros(1, 384, dtype=bf16, device="cuda")
+        kda_lin_step(**{n: x[t:t + 1].contiguous() for n, x in kw.items()},
+                     slots=torch.tensor([1], dtype=torch.int32, device="cuda"), state=st,
+                     output=o, scale=0.5)
+        assert torch.equal(o[0].cpu(), out[t])
+    assert torch.equal(st[1].cpu(), state[2])
