@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(HERE, "libkda_gb300.so")
 PROBE_LIB_PATH = os.path.join(HERE, "libkda_probe_gb300.so")
 SOURCES = [os.path.join(CSRC, n) for n in ("kda_step.cu", "kda_split.cu",
                                             "kda_recover.cu", "kda_oproj.cu",
-                                            "kda_lin.cu", "kda_snapshot.cu",
+                                            "kda_lin.cu", "kda_lin_prompt.cu", "kda_snapshot.cu",
                                             "kda_selftest.cu")]
 PROBE_SOURCES = [os.path.join(CSRC, "kda_probe.cu")]
 HEADERS = [os.path.join(INCLUDE, "kda.h"), os.path.join(INCLUDE, "kda_probe.h"),

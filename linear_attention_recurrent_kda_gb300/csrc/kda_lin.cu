@@ -194,19 +194,46 @@ static int run_step(const kda_lin_step_args *a, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
 }
 
-// The sizes' part of the checks, and the plan: 1 = recurrent, 2 = chunked.
-static int plan_prompt(const kda_lin_prompt_args *a, int *path) {
+// How a prompt call runs.
+struct Plan {
+  bool chunked;
+  int segs, seg_len;      // segments of a sequence, their tokens
+  int64_t workspace;      // bytes
+};
+
+constexpr int kRecurrentMost = 16;
+constexpr int kShares = 152;            // SMs that the work is shared among
+constexpr int kShortestSegment = 512;
+
+// The sizes' part of the checks, and the plan.
+static int plan_prompt(const kda_lin_prompt_args *a, Plan *plan) {
   if (const int rc = check_common(a, a->seqs)) return rc;
   if (a->tokens < 0 || a->max_seq < 0 || (a->state && a->num_slots < 1)) return KDA_ERR_SHAPE;
   if (a->path < 0 || a->path > 2) return KDA_ERR_PATH;
-  *path = 1;
+  const int64_t longest = a->max_seq < a->tokens ? a->max_seq : a->tokens;
+  plan->chunked = longest > 0 && (a->path == 2 || (a->path == 0 && longest > kRecurrentMost));
+  plan->segs = 1;
+  plan->seg_len = longest > 0 ? static_cast<int>(longest) : 1;
+  plan->workspace = 0;
+  if (plan->chunked) {
+    // an SM's share of all tokens x heads, in whole chunks
+    int64_t len = (static_cast<int64_t>(a->tokens) * a->heads / kShares + 127) / 128 * 128;
+    if (len < kShortestSegment) len = kShortestSegment;
+    if (longest > len) {
+      plan->seg_len = static_cast<int>(len);
+      plan->segs = static_cast<int>((longest + len - 1) / len);
+      if (static_cast<int64_t>(a->seqs) * plan->segs * a->heads > 0x7fffffffll)
+        return KDA_ERR_SHAPE;
+      plan->workspace = ws_pages(a->tokens, len, a->heads) * (kPage + 1) * 4;
+    }
+  }
   return KDA_SUCCESS;
 }
 
 static int run_prompt(const kda_lin_prompt_args *a, cudaStream_t stream) {
   if (!a) return KDA_ERR_NULL_ARGS;
-  int path = 0;
-  if (const int rc = plan_prompt(a, &path)) return rc;
+  Plan plan;
+  if (const int rc = plan_prompt(a, &plan)) return rc;
   if (a->seqs == 0 || a->heads == 0) return KDA_SUCCESS;
   if (!a->seq_starts || !a->decay) return KDA_ERR_NULL_POINTER;
   if (a->tokens > 0 && (!a->q || !a->k || !a->v || !a->output)) return KDA_ERR_NULL_POINTER;
@@ -214,6 +241,9 @@ static int run_prompt(const kda_lin_prompt_args *a, cudaStream_t stream) {
   if (!rows_aligned(a) || !aligned(a->seq_starts, 4) || !aligned(a->src_slots, 4) ||
       !aligned(a->dst_slots, 4))
     return KDA_ERR_ALIGNMENT;
+  if (plan.workspace > 0 && (!a->workspace || !aligned(a->workspace, 256) ||
+                             a->workspace_bytes < plan.workspace))
+    return KDA_ERR_WORKSPACE;
   int dev = 0;
   DeviceFacts df;
   if (!current_device(&dev, &df)) return KDA_ERR_DEVICE;
@@ -222,11 +252,11 @@ static int run_prompt(const kda_lin_prompt_args *a, cudaStream_t stream) {
   p.heads = a->heads;
   p.group = a->heads / a->qk_heads;
   p.tokens = a->tokens;
-  p.max_seq = a->max_seq;
+  p.max_seq = a->max_seq < a->tokens ? a->max_seq : a->tokens;
   p.num_slots = a->num_slots;
   p.decay_rows = a->decay_rows;
-  p.segs = 1;
-  p.seg_len = a->max_seq;
+  p.segs = plan.segs;
+  p.seg_len = plan.seg_len;
   p.q_stride = a->q_stride;
   p.k_stride = a->k_stride;
   p.v_stride = a->v_stride;
@@ -242,6 +272,13 @@ static int run_prompt(const kda_lin_prompt_args *a, cudaStream_t stream) {
   p.output = static_cast<__nv_bfloat16 *>(a->output);
   p.scale = a->scale;
   p.err = a->err;
+  if (plan.chunked) {
+    if (plan.workspace > 0) {
+      p.ws_state = static_cast<float *>(a->workspace);
+      p.ws_decay = p.ws_state + ws_pages(p.tokens, p.seg_len, p.heads) * kPage;
+    }
+    return launch_chunked(p, a->qk_heads, dev, df.sms, stream);
+  }
   recurrent_kernel<<<a->seqs * a->heads * kParts, kWarps * 32, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
 }
@@ -259,5 +296,6 @@ extern "C" int kda_lin_prompt(const kda_lin_prompt_args *args, void *stream) {
 
 extern "C" int64_t kda_lin_prompt_workspace(const kda_lin_prompt_args *args) {
   if (!args) return -1;
-  return 0;
+  kda::lin::Plan plan;
+  return kda::lin::plan_prompt(args, &plan) ? 0 : plan.workspace;
 }

@@ -30,8 +30,8 @@ struct PromptParams {
   __nv_bfloat16 *output;
   float scale;
   int32_t *err;
-  float *ws_state;        // [seqs][segs][heads][128 * 128] when segs > 1
-  float *ws_decay;        // [seqs][segs][heads]
+  float *ws_state;        // pages of the segments when segs > 1 (kda_lin_prompt.cu)
+  float *ws_decay;        // their total decays
 };
 
 // One sequence of a prompt call: its rows and slots (0: none).
@@ -86,9 +86,14 @@ __device__ __forceinline__ float token_step(float4 (&s)[kRows], float d, const f
   return warp_reduce_scatter<kRows>(dot, lane);
 }
 
+// Pages of workspace of the chunked form with these segments.
+inline int64_t ws_pages(int64_t tokens, int64_t seg_len, int64_t heads) {
+  return 2 * (tokens / seg_len + 1) * heads;
+}
+
 // The chunked form (kda_lin_prompt.cu): enqueues its kernels for checked
 // parameters.  Returns a KDA_* code.
-int launch_chunked(const PromptParams &p, int qk_heads, int sms, cudaStream_t stream);
+int launch_chunked(const PromptParams &p, int qk_heads, int dev, int sms, cudaStream_t stream);
 
 }  // namespace lin
 }  // namespace kda

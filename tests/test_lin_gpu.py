@@ -92,6 +92,22 @@ def test_prompt(lens, H, Hk, per_token, path):
     verify(inp, launch(inp, src=src, dst=dst, path=path), path, src, dst)
 
 
+@pytest.mark.parametrize("lens", [[1300], [1, 1536, 513, 512, 40], [600, 1024, 1025]],
+                         ids=lambda v: "-".join(map(str, v)))
+@pytest.mark.parametrize("H,Hk,per_token", [(2, 1, True), (1, 1, False)])
+def test_long_sequences_in_segments(lens, H, Hk, per_token):
+    """Few heads and long sequences: the chunked form splits them into segments."""
+    B = len(lens)
+    inp = make(lens, H, Hk, per_token=per_token, slots=2 * B + 1, seed=sum(lens), behind=3,
+               scale_g=0.05)
+    assert kl.prompt_workspace(kl.KdaLinPromptArgs(
+        seqs=B, heads=H, qk_heads=Hk, tokens=sum(lens) + 3, max_seq=max(lens), q_stride=Hk * D,
+        k_stride=Hk * D, v_stride=H * D, o_stride=H * D)) > 0
+    src = [r + 1 if r % 2 == 0 else 0 for r in range(B)]
+    dst = [r + 1 for r in range(B)]                     # in place, where carried
+    verify(inp, launch(inp, src=src, dst=dst, max_seq=max(lens)), 2, src, dst)
+
+
 @pytest.mark.parametrize("path", PATHS)
 def test_without_a_state(path):
     inp = make([3, 140], 2, 2, seed=5)
