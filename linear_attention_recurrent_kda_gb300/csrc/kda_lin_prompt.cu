@@ -8,11 +8,16 @@
 // Four products of 128^3 a chunk, one unit (sequence or segment of it, head)
 // after the other per CTA, one CTA per SM.
 //
-// Factors.  Exponents are differences of sums; they are formed without
-// cancellation from sums inside 32-token blocks: bl (prefix), f = 2^(suffix)
-// and the blocks' totals.  Off the diagonal 2^(b_i - b_j) is a row factor times
-// f_j, both <= 1; on it 2^(bl_i - bl_j).  Logarithms below -160 (in powers of
-// two) count as -160: the factor is 0 in FP32 either way, and a reset of -inf
+// Factors.  K'' takes its exponents from sums inside 32-token blocks (f =
+// 2^(sum of the tokens behind, in the block)) and the totals of the blocks
+// behind: sums of numbers of one sign, nothing cancels.  P: in a chunk whose
+// decay is above 2^-128 ("mild"), O = 2^(b_i - r) (Q (2^r S)^T + P' V) with
+// P'_ij = A_ij 2^(r - b_j), r half the chunk's logarithm rounded to a whole
+// number: every factor is within 2^+-64, one product per element of A and one per
+// element of O.  Stronger decays take a row factor times f_j off the diagonal
+// blocks, both <= 1, 2^(bl_i - bl_j) on them (bl: prefix sums in the block), and
+// O = Q S^T is scaled by rows before P V joins it.  Logarithms below -160 (base
+// 2) count as -160: the factor is 0 in FP32 either way, and a reset of -inf
 // stays a number.
 //
 // Precision.  The page stays in FP32 registers.  K'' = factor * key is the one
@@ -22,11 +27,12 @@
 // Q S^T are rounded to BF16 once: they only feed an output that is itself
 // rounded to BF16, and the FP32 sum keeps their errors at that size.
 //
-// Roles (512 threads, 16 warps): TMA loads (warp 0), MMA issue (1), decay
-// tables (2), output stores (3); three warpgroups: P and O (4-7), K'' (8-11),
-// the page (12-15).  K'' is built transposed (lanes = keys) by transposing
-// shared-memory matrix loads straight into TMEM, as the A operand: no shared
-// memory is written for it.  P is written over A in TMEM.
+// Roles (512 threads, 16 warps): TMA loads (warp 0), MMA issue for the page
+// (U, Q S^T; warp 1) and for the outputs (A, P V; warp 3), the work and its decay
+// tables (warp 2); three warpgroups: P and O (4-7), K'' (8-11), the page
+// (12-15).  K'' is built transposed (lanes = keys) by transposing shared-memory
+// matrix loads straight into TMEM, as the A operand: no shared memory is
+// written for it.  P is written over A in TMEM.
 //   TMEM columns: A / P 0, O 128, U (the update) 256, K'' 384 (2 x 48).
 //   Shared memory: Q, K, V double-buffered (32 KiB tiles, 128-byte swizzle) and
 //   the page's BF16 copy; O leaves through Q's tile.
@@ -49,23 +55,39 @@ constexpr int kHalf = 128 * 128;                 // bytes of a [128][64] BF16 ti
 constexpr int kTile = 2 * kHalf;                 // bytes of a [128][128] BF16 tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -160.0f;               // of a decay's base-2 logarithm
+constexpr float kMild = -128.0f;                 // a chunk's, for the one-factor form of P
 
 constexpr uint32_t kColA = 0, kColO = 128, kColU = 256, kColK = 384, kColsK = 48;
 
 struct Table {
-  float bl[kChunk];    // prefix sums inside 32-token blocks (base-2 logarithms)
-  float f[kChunk];     // 2^(sum of the tokens behind, in the block)
-  float total[4];      // block totals
+  float f[kChunk];     // 2^(sum of the tokens behind, in the 32-token block)
+  float x[kChunk];     // mild: 2^(ref - b); else bl, prefix sums in the block
+  float total[4];      // the blocks' logarithms
+  float sum;           // the chunk's
+  float ref;           // mild: r, else 0
+  uint32_t mild, pad;
 };
+
+// One chunk of the CTA's work, as the table warp hands it to the other roles.
+struct Info {
+  int rows;            // tokens; 0: a unit without tokens, -1: no more
+  int row, head;
+  int first, last;     // of its unit
+  const float *from;   // first: the page it starts from (NULL: zeros)
+  float *to, *decay;   // last: where the page, and the unit's logarithm, go (or NULL)
+};
+
+constexpr int kInfos = 4;
 
 struct Ctrl {
   Table tab[2];
+  Info info[kInfos];
+  uint64_t info_full[kInfos], info_empty[kInfos];
   uint64_t full_q[2], full_k[2], full_v[2];      // TMA landed
   uint64_t empty_q[2], empty_k[2], empty_v[2];
   uint64_t tab_full[2], tab_empty[2];
   uint64_t kq_full[2], kq_empty[2];              // K'' quarters in TMEM
   uint64_t v_ok[2];                              // V's rows behind the end are zeros
-  uint64_t st_full[2];                           // O staged in Q's tile (or written)
   uint64_t a_full, p_full, qs_full, o_full, o_empty, u_full, u_empty, s_full;
   uint32_t tmem, abort;
 };
@@ -86,6 +108,64 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
           smem_addr(bar))
       : "memory");
+}
+// Waits for the phase of `parity`, in a dozen instructions (the roles' loops
+// share the instruction cache, and their code is what fills it).  Each try may
+// sleep for a microsecond; after 2^21 tries, or when another thread raised
+// `abort`, the wait gives up, raises it and returns false.
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, uint32_t *abort) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .u32 n, a;\n mov.u32 n, 2097152;\n"
+      "again:\n"
+      " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, 1000;\n"
+      " @p bra.uni done;\n"
+      " ld.volatile.shared.u32 a, [%3];\n"
+      " sub.u32 n, n, 1;\n"
+      " setp.ne.u32 q, n, 0;\n"
+      " setp.eq.and.u32 q, a, 0, q;\n"
+      " @q bra again;\n"
+      " st.volatile.shared.u32 [%3], 1;\n"
+      "done:\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(smem_addr(abort))
+      : "memory");
+  return ok != 0;
+}
+
+// Two FP32 values in one 64-bit register pair.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(f32x2 v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(r));
+  return r != 0;
 }
 __device__ __forceinline__ void tc_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -110,39 +190,20 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       : "memory");
 }
 
-// Loads 32 columns of this warp's 32 lanes (and waits for them).
-__device__ __forceinline__ void tc_ld32(uint32_t addr, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+// Loads of N columns of this warp's 32 lanes; the registers hold them after the
+// wait.
+__device__ __forceinline__ void tc_ld(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(addr)
+               : "memory");
 }
-
-__device__ __forceinline__ void tc_st32(uint32_t addr, const float (&v)[32]) {
-  uint32_t r[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31]), "r"(addr)
-      : "memory");
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+               : "memory");
 }
 
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
@@ -199,6 +260,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// BF16 of both halves: low in the low half.
+__device__ __forceinline__ uint32_t pack2(f32x2 v) {
+  float lo, hi;
+  unpair(v, lo, hi);
+  return pack2(lo, hi);
+}
 __device__ __forceinline__ float low_half(uint32_t r) { return __uint_as_float(r << 16); }
 __device__ __forceinline__ float high_half(uint32_t r) { return __uint_as_float(r & 0xFFFF0000u); }
 
@@ -214,6 +281,48 @@ __device__ __forceinline__ uint32_t tile_at(int row, int group) {
   return static_cast<uint32_t>((group >> 3) * kHalf + row * 128 + (((group & 7) ^ (row & 7)) << 4));
 }
 
+__device__ __forceinline__ uint32_t upper_halves(f32x2 v) {
+  return __byte_perm(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32), 0x7632);
+}
+__device__ __forceinline__ f32x2 raw_pair(uint32_t lo, uint32_t hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+
+// P of a chunk with strong decays, a row of a warp's 32 at a time: a row factor
+// times f off the diagonal block, 2^(bl_i - bl_j) on it.  bl: this row's prefix
+// sum in its block.  Returns the row's factor of Q S^T.
+__device__ __forceinline__ float strong_rows(const Table &tab, uint32_t col_a, int w4, int lane,
+                                             float bl) {
+  uint32_t a[32], r[16];
+#pragma unroll 1
+  for (int J = 0; J <= w4; ++J) {
+    tc_ld(col_a + 32 * J, a);
+    tc_wait_ld(a);
+    if (J < w4) {
+      float sum = bl;                                   // and the blocks between
+      for (int m = J + 1; m < w4; ++m) sum += tab.total[m];
+      const float row = exp2_approx(sum);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        r[j] = pack2(__uint_as_float(a[2 * j]) * (row * tab.f[32 * J + 2 * j]),
+                     __uint_as_float(a[2 * j + 1]) * (row * tab.f[32 * J + 2 * j + 1]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float x = __uint_as_float(a[2 * j]) * exp2_approx(bl - tab.x[32 * J + 2 * j]);
+        const float y = __uint_as_float(a[2 * j + 1]) * exp2_approx(bl - tab.x[32 * J + 2 * j + 1]);
+        r[j] = pack2(2 * j <= lane ? x : 0.0f, 2 * j + 1 <= lane ? y : 0.0f);
+      }
+    }
+    tc_st16(col_a + 16 * J, r);
+  }
+  float sum = bl;
+  for (int m = 0; m < w4; ++m) sum += tab.total[m];
+  return exp2_approx(sum);
+}
+
 // -------------------------------------------------------------- units, chunks
 
 struct Unit {
@@ -222,23 +331,21 @@ struct Unit {
   int src, dst;
 };
 
-// Walks the chunks of this CTA's units, the same way in every role.
+// Walks this CTA's units.
 template <bool kOut>
 struct Walk {
   const PromptParams &p;
   int64_t u;
   Unit unit;
-  int chunk, chunks;       // of the unit
 
-  __device__ explicit Walk(const PromptParams &p_) : p(p_), u(blockIdx.x), chunk(0), chunks(0) {
-    u -= gridDim.x;
-  }
+  __device__ explicit Walk(const PromptParams &p_) : p(p_), u(blockIdx.x) {}
   // The next unit that has work for this kernel.
-  __device__ bool next_unit(bool report) {
+  __device__ bool next(bool report) {
     const int64_t units = static_cast<int64_t>(p.seqs) * p.segs * p.heads;
-    for (u += gridDim.x; u < units; u += gridDim.x) {
-      const int rest = static_cast<int>(u / p.heads);
-      unit.h = static_cast<int>(u - static_cast<int64_t>(rest) * p.heads);
+    for (; u < units; u += gridDim.x) {
+      const uint32_t at = static_cast<uint32_t>(u);      // units < 2^31
+      const uint32_t rest = at / p.heads;
+      unit.h = at - rest * p.heads;
       unit.b = rest / p.segs;
       unit.seg = rest - unit.b * p.segs;
       Seq s;
@@ -253,25 +360,11 @@ struct Walk {
       unit.n = left < p.seg_len ? left : p.seg_len;
       unit.src = s.src;
       unit.dst = s.dst;
-      chunk = -1;
-      chunks = (unit.n + kChunk - 1) / kChunk;
+      u += gridDim.x;
       return true;
     }
     return false;
   }
-  __device__ bool next_chunk() { return ++chunk < chunks; }
-  // The next chunk of this or a later unit.
-  __device__ bool next() {
-    while (true) {
-      if (chunks && next_chunk()) return true;
-      if (!next_unit(false)) return false;
-    }
-  }
-  __device__ int rows() const {
-    const int left = unit.n - chunk * kChunk;
-    return left < kChunk ? left : kChunk;
-  }
-  __device__ int first_row() const { return unit.row + chunk * kChunk; }
 };
 
 // A segment's page in the workspace.  All segments but a sequence's last have
@@ -284,6 +377,18 @@ __device__ __forceinline__ int64_t ws_index(const PromptParams &p, int first_row
 }
 __device__ __forceinline__ int64_t ws_index(const PromptParams &p, const Unit &u) {
   return ws_index(p, u.row, u.seg == u.segs - 1, u.h);
+}
+
+// The next chunk of a role (a whole warp; m counts them).  False: no more.
+__device__ __forceinline__ bool next_chunk(Ctrl &c, uint32_t &m, Info &info, int lane) {
+  const uint32_t at = m % kInfos;
+  if (!__all_sync(0xffffffffu, wait_phase(&c.info_full[at], (m / kInfos) & 1, &c.abort)))
+    return false;
+  info = c.info[at];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&c.info_empty[at]);
+  ++m;
+  return info.rows >= 0;
 }
 
 // -------------------------------------------------------------------- kernel
@@ -312,19 +417,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     c.abort = 0;
+    for (int i = 0; i < kInfos; ++i) {
+      mbar_init(&c.info_full[i], 1);
+      mbar_init(&c.info_empty[i], kOut ? 15 : 10);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.full_q[i], 1);
       mbar_init(&c.full_k[i], 1);
       mbar_init(&c.full_v[i], 1);
       mbar_init(&c.empty_q[i], 1);
       mbar_init(&c.empty_k[i], kOut ? 5 : 4);
-      mbar_init(&c.empty_v[i], 1);
+      mbar_init(&c.empty_v[i], kOut ? 2 : 1);
       mbar_init(&c.tab_full[i], 1);
       mbar_init(&c.tab_empty[i], kOut ? 12 : 8);
       mbar_init(&c.kq_full[i], 4);
       mbar_init(&c.kq_empty[i], 1);
       mbar_init(&c.v_ok[i], 4);
-      mbar_init(&c.st_full[i], 4);
     }
     mbar_init(&c.a_full, 1);
     mbar_init(&c.p_full, 4);
@@ -344,134 +452,167 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = c.tmem;
 
 // A wait that ran out leaves the role's loop; whole warps leave together.
-#define KDA_WAIT(bar, parity) \
-  if (!mbar_wait(&(bar), (parity), abort_flag)) break
-#define KDA_WAIT_WARP(bar, parity) \
-  if (!__all_sync(0xffffffffu, mbar_wait(&(bar), (parity), abort_flag))) break
+#define KDA_WAIT(bar, parity)                        \
+  if (!wait_phase(&(bar), (parity), &c.abort)) break
+#define KDA_WAIT_WARP(bar, parity)                                                \
+  if (!__all_sync(0xffffffffu, wait_phase(&(bar), (parity), &c.abort))) break
 
   if (*abort_flag) {
     // nothing runs
   } else if (warp < 4) {
     regs_dec<80>();
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ------------------------------------------------------------ TMA loads
-      Walk<kOut> it(p);
-      for (uint32_t n = 0; it.next(); ++n) {
-        const int buf = n & 1, boxes = (it.rows() + 31) >> 5, y = it.first_row();
+      Info info;
+      uint32_t m = 0, n = 0;
+      while (next_chunk(c, m, info, lane)) {
+        if (info.rows == 0) continue;
+        const int buf = n & 1, boxes = (info.rows + 31) >> 5;
         const uint32_t parity = ((n >> 1) & 1) ^ 1;
-        const int xk = it.unit.h / p.group * kDim, xv = it.unit.h * kDim;
-        KDA_WAIT(c.empty_k[buf], parity);
-        mbar_arrive_expect_tx(&c.full_k[buf], boxes * 8192);
-        for (int i = 0; i < boxes; ++i)
-          for (int t = 0; t < 2; ++t)
-            tma_load(sk + buf * kTile + t * kHalf + i * 4096, &map_k, xk + 64 * t, y + 32 * i,
-                     &c.full_k[buf]);
+        const int xk = info.head / p.group * kDim, xv = info.head * kDim;
+        // boxes of 32 rows x 64 columns, one a lane
+        auto load = [&](uint8_t *tile, const CUtensorMap *map, int x, uint64_t *bar) {
+          if (lane == 0) mbar_arrive_expect_tx(bar, boxes * 8192);
+          __syncwarp();
+          const int i = lane >> 1, t = lane & 1;
+          if (i < boxes)
+            tma_load(tile + buf * kTile + t * kHalf + i * 4096, map, x + 64 * t, info.row + 32 * i,
+                     bar);
+        };
+        KDA_WAIT_WARP(c.empty_k[buf], parity);
+        load(sk, &map_k, xk, &c.full_k[buf]);
+        KDA_WAIT_WARP(c.empty_v[buf], parity);
+        load(sv, &map_v, xv, &c.full_v[buf]);
         if (kOut) {
-          KDA_WAIT(c.empty_q[buf], parity);
-          mbar_arrive_expect_tx(&c.full_q[buf], boxes * 8192);
-          for (int i = 0; i < boxes; ++i)
-            for (int t = 0; t < 2; ++t)
-              tma_load(sq + buf * kTile + t * kHalf + i * 4096, &map_q, xk + 64 * t, y + 32 * i,
-                       &c.full_q[buf]);
+          KDA_WAIT_WARP(c.empty_q[buf], parity);
+          load(sq, &map_q, xk, &c.full_q[buf]);
         }
-        KDA_WAIT(c.empty_v[buf], parity);
-        mbar_arrive_expect_tx(&c.full_v[buf], boxes * 8192);
-        for (int i = 0; i < boxes; ++i)
-          for (int t = 0; t < 2; ++t)
-            tma_load(sv + buf * kTile + t * kHalf + i * 4096, &map_v, xv + 64 * t, y + 32 * i,
-                     &c.full_v[buf]);
+        ++n;
       }
-    } else if (warp == 1 && lane == 0) {
-      // ------------------------------------------------------------ MMA issue
-      Walk<kOut> it(p);
-      bool more = it.next();
+    } else if (warp == 1) {
+      // ------------------------------------------- MMA issue: U and Q S^T
+      // The warp walks and waits as one; one elected thread issues.  Descriptors
+      // are sums of a base and constants (addresses count 16 bytes).
       uint32_t quarter = 0;
-      auto issue_qk = [&](int buf) {
-        const uint32_t q = smem_addr(sq + buf * kTile), k = smem_addr(sk + buf * kTile);
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t off = (j >> 2) * kHalf + (j & 3) * 32;
-          tc_mma_ss(tmem + kColA, desc_k_major(q + off), desc_k_major(k + off), kIdesc, j > 0);
-        }
-      };
-      if (kOut && more) {
-        do {
-          KDA_WAIT(c.full_k[0], 0);
-          KDA_WAIT(c.full_q[0], 0);
-          tc_fence_after();
-          issue_qk(0);
-          tc_commit(&c.a_full);
-          tc_commit(&c.empty_k[0]);
-        } while (false);
-      }
-      for (uint32_t n = 0; more; ++n) {
-        const int buf = n & 1, quarters = (it.rows() + 31) >> 5;
+      const uint64_t q0 = desc_k_major(smem_addr(sq)), v0 = desc_mn_major(smem_addr(sv)),
+                     s0 = desc_mn_major(smem_addr(ss));
+      Info info;
+      uint32_t m = 0, n = 0;
+      while (next_chunk(c, m, info, lane)) {
+        if (info.rows == 0) continue;
+        const int buf = n & 1, quarters = (info.rows + 31) >> 5;
         const uint32_t one = n & 1, two = (n >> 1) & 1;
-        const uint32_t v = smem_addr(sv + buf * kTile);
-        if (kOut) {
-          // O = Q S^T (unscaled)
-          KDA_WAIT(c.s_full, one);
-          if (n > 0) KDA_WAIT(c.o_empty, one ^ 1);
-          tc_fence_after();
-          const uint32_t q = smem_addr(sq + buf * kTile), s = smem_addr(ss);
-          for (int j = 0; j < 8; ++j)
-            tc_mma_ss(tmem + kColO, desc_k_major(q + (j >> 2) * kHalf + (j & 3) * 32),
-                      desc_mn_major(s + j * 2048), kIdescBmn, j > 0);
-          tc_commit(&c.qs_full);
-        }
         // U = K''^T V, quarter by quarter of 32 tokens
-        KDA_WAIT(c.full_v[buf], two);
-        KDA_WAIT(c.v_ok[buf], two);
-        if (n > 0) KDA_WAIT(c.u_empty, one ^ 1);
+        KDA_WAIT_WARP(c.full_v[buf], two);
+        KDA_WAIT_WARP(c.v_ok[buf], two);
+        if (n > 0) KDA_WAIT_WARP(c.u_empty, one ^ 1);
         int i = 0;
         for (; i < quarters; ++i, ++quarter) {
           const int kb = quarter & 1;
-          KDA_WAIT(c.kq_full[kb], (quarter >> 1) & 1);
+          KDA_WAIT_WARP(c.kq_full[kb], (quarter >> 1) & 1);
           tc_fence_after();
-          for (int part = 0; part < 3; ++part)
-            for (int j = 0; j < 2; ++j)
-              tc_mma_ts(tmem + kColU, tmem + kColK + kb * kColsK + part * 16 + j * 8,
-                        desc_mn_major(v + (2 * i + j) * 2048), kIdescBmn, i + part + j > 0);
-          tc_commit(&c.kq_empty[kb]);
+          if (elect_one()) {
+            const uint32_t a = tmem + kColK + kb * kColsK;
+            const uint64_t v = v0 + buf * (kTile >> 4) + i * (4096 >> 4);
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                tc_mma_ts(tmem + kColU, a + part * 16 + j * 8, v + j * (2048 >> 4), kIdescBmn,
+                          i + part + j > 0);
+            tc_commit(&c.kq_empty[kb]);
+            if (i == quarters - 1) {
+              tc_commit(&c.u_full);
+              tc_commit(&c.empty_v[buf]);
+            }
+          }
+          __syncwarp();
         }
         if (i < quarters) break;
-        tc_commit(&c.u_full);
         if (kOut) {
-          // O += P V
-          KDA_WAIT(c.p_full, one);
+          // O = Q S^T
+          KDA_WAIT_WARP(c.s_full, one);
+          KDA_WAIT_WARP(c.full_q[buf], two);
+          if (n > 0) KDA_WAIT_WARP(c.o_empty, one ^ 1);
           tc_fence_after();
-          for (int j = 0; j < 2 * quarters; ++j)
-            tc_mma_ts(tmem + kColO, tmem + kColA + j * 8, desc_mn_major(v + j * 2048), kIdescBmn, 1);
-          tc_commit(&c.o_full);
+          if (elect_one()) {
+            const uint64_t q = q0 + buf * (kTile >> 4);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              tc_mma_ss(tmem + kColO, q + (((j >> 2) * kHalf + (j & 3) * 32) >> 4),
+                        s0 + j * (2048 >> 4), kIdescBmn, j > 0);
+            tc_commit(&c.qs_full);
+          }
+          __syncwarp();
         }
-        tc_commit(&c.empty_v[buf]);
-        more = it.next();
-        if (kOut && more) {
-          const int nb = (n + 1) & 1;
-          const uint32_t np = ((n + 1) >> 1) & 1;
-          KDA_WAIT(c.full_k[nb], np);
-          KDA_WAIT(c.full_q[nb], np);
-          tc_fence_after();
-          issue_qk(nb);
-          tc_commit(&c.a_full);
-          tc_commit(&c.empty_k[nb]);
-        }
+        ++n;
       }
     } else if (warp == 2) {
-      // --------------------------------------------------------- decay tables
+      // -------------------------------------- the work, and its decay tables
       Walk<kOut> it(p);
-      for (uint32_t n = 0; it.next(); ++n) {
-        const int buf = n & 1, rows = it.rows();
+      Info next;
+      int t = 0;                                           // tokens of the unit handed out
+      bool unit = false;
+      // the next chunk into `next`, and its decays (4 a lane)
+      auto look = [&](float (&g)[4]) {
+        if (!unit) {
+          if (!it.next(lane == 0)) {
+            next.rows = -1;
+            return;
+          }
+          const Unit &u = it.unit;
+          next.head = u.h;
+          next.from = nullptr;
+          next.to = next.decay = nullptr;
+          if (!kOut || u.segs > 1) {
+            float *page = p.ws_state + ws_index(p, u) * kPage;
+            if (kOut) {
+              next.from = page;
+            } else {
+              next.to = page;
+              next.decay = p.ws_decay + ws_index(p, u);
+            }
+          } else if (u.src) {
+            next.from = page_of(p.state, u.src, p.heads, u.h);
+          }
+          if (kOut && u.seg == u.segs - 1 && u.dst) next.to = page_of(p.state, u.dst, p.heads, u.h);
+          t = 0;
+        }
+        const int left = it.unit.n - t;
+        next.row = it.unit.row + t;
+        next.rows = left < kChunk ? left : kChunk;
+        next.first = t == 0;
+        next.last = left <= kChunk;
+        t += kChunk;
+        unit = !next.last;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int x = 4 * lane + j;
+          const int64_t at = p.decay_rows ? static_cast<int64_t>(next.row + x) * p.heads : 0;
+          g[j] = x < next.rows ? __ldg(p.decay + at + next.head) : 0.0f;
+        }
+      };
+      float ahead[4] = {};
+      look(ahead);
+      uint32_t m = 0, n = 0;
+      while (true) {
+        KDA_WAIT_WARP(c.info_empty[m % kInfos], ((m / kInfos) & 1) ^ 1);
+        if (lane == 0) {
+          c.info[m % kInfos] = next;
+          mbar_arrive(&c.info_full[m % kInfos]);
+        }
+        __syncwarp();
+        ++m;
+        const int rows = next.rows, buf = n & 1;
+        if (rows < 0) break;
         float g[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int t = 4 * lane + j;
-          g[j] = 0.0f;
-          if (t < rows) {
-            const int64_t at = p.decay_rows ? static_cast<int64_t>(it.first_row() + t) * p.heads : 0;
-            g[j] = __ldg(p.decay + at + it.unit.h) * kLog2e;
-            if (g[j] < kLowest) g[j] = kLowest;
-          }
+          g[j] = ahead[j] * kLog2e;
+          if (g[j] < kLowest) g[j] = kLowest;
         }
+        look(ahead);
+        if (rows == 0) continue;
         const float sum = (g[0] + g[1]) + (g[2] + g[3]);
         // sums of the lanes before and behind this one in its block of 8 lanes
         float before = sum, behind = sum;
@@ -487,149 +628,217 @@ __global__ void __launch_bounds__(kThreads, 1)
         behind = __shfl_down_sync(0xffffffffu, behind, 1, 8);
         if ((lane & 7) == 0) before = 0.0f;
         if ((lane & 7) == 7) behind = 0.0f;
-        KDA_WAIT_WARP(c.tab_empty[buf], ((n >> 1) & 1) ^ 1);
-        Table &tab = c.tab[buf];
-        float4 bl, f;
-        bl.x = before + g[0];
-        bl.y = bl.x + g[1];
-        bl.z = bl.y + g[2];
-        bl.w = bl.z + g[3];
+        const float t0 = __shfl_sync(0xffffffffu, total, 0), t1 = __shfl_sync(0xffffffffu, total, 8),
+                    t2 = __shfl_sync(0xffffffffu, total, 16), t3 = __shfl_sync(0xffffffffu, total, 24);
+        const float all = (t0 + t1) + (t2 + t3);
+        const bool mild = all >= kMild && all <= 0.0f;
+        const float ref = mild ? floorf(0.5f * all) : 0.0f;
+        float4 x, f;
+        x.x = before + g[0];
+        x.y = x.x + g[1];
+        x.z = x.y + g[2];
+        x.w = x.z + g[3];
+        if (mild) {
+          const float base = ref - (lane < 8 ? 0.0f : lane < 16 ? t0 : lane < 24 ? t0 + t1 : t0 + t1 + t2);
+          x.x = exp2_approx(base - x.x);
+          x.y = exp2_approx(base - x.y);
+          x.z = exp2_approx(base - x.z);
+          x.w = exp2_approx(base - x.w);
+        }
         const float s3 = behind, s2 = s3 + g[3], s1 = s2 + g[2], s0 = s1 + g[1];
         f.x = exp2_approx(s0);
         f.y = exp2_approx(s1);
         f.z = exp2_approx(s2);
         f.w = exp2_approx(s3);
-        reinterpret_cast<float4 *>(tab.bl)[lane] = bl;
+        KDA_WAIT_WARP(c.tab_empty[buf], ((n >> 1) & 1) ^ 1);
+        Table &tab = c.tab[buf];
+        reinterpret_cast<float4 *>(tab.x)[lane] = x;
         reinterpret_cast<float4 *>(tab.f)[lane] = f;
         if ((lane & 7) == 0) tab.total[lane >> 3] = total;
+        if (lane == 1) {
+          tab.sum = all;
+          tab.ref = ref;
+          tab.mild = mild;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&c.tab_full[buf]);
+        ++n;
       }
-    } else if (kOut && warp == 3 && lane == 0) {
-      // -------------------------------------------------------- output stores
-      Walk<kOut> it(p);
-      for (uint32_t n = 0; it.next(); ++n) {
-        const int buf = n & 1;
-        KDA_WAIT(c.st_full[buf], (n >> 1) & 1);
-        if (it.rows() == kChunk) {
-          for (int t = 0; t < 2; ++t)
-            tma_store(&map_o, it.unit.h * kDim + 64 * t, it.first_row(), sq + buf * kTile + t * kHalf);
-          bulk_commit();
-          bulk_wait_read(0);
+    } else if (kOut && warp == 3) {
+      // ------------------------------------------- MMA issue: A and P V
+      const uint64_t q0 = desc_k_major(smem_addr(sq)), k0 = desc_k_major(smem_addr(sk)),
+                     v0 = desc_mn_major(smem_addr(sv));
+      Info info;
+      uint32_t m = 0, n = 0;
+      while (next_chunk(c, m, info, lane)) {
+        if (info.rows == 0) continue;
+        const int buf = n & 1, quarters = (info.rows + 31) >> 5;
+        const uint32_t one = n & 1, two = (n >> 1) & 1;
+        // A = Q K^T, over the P that the products before it have read
+        KDA_WAIT_WARP(c.full_k[buf], two);
+        KDA_WAIT_WARP(c.full_q[buf], two);
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t q = q0 + buf * (kTile >> 4), k = k0 + buf * (kTile >> 4);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t off = ((j >> 2) * kHalf + (j & 3) * 32) >> 4;
+            tc_mma_ss(tmem + kColA, q + off, k + off, kIdesc, j > 0);
+          }
+          tc_commit(&c.a_full);
+          tc_commit(&c.empty_k[buf]);
         }
-        mbar_arrive(&c.empty_q[buf]);
+        __syncwarp();
+        // O += P V
+        KDA_WAIT_WARP(c.full_v[buf], two);
+        KDA_WAIT_WARP(c.v_ok[buf], two);
+        KDA_WAIT_WARP(c.qs_full, one);
+        KDA_WAIT_WARP(c.p_full, one);
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t v = v0 + buf * (kTile >> 4);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < 2 * quarters)
+              tc_mma_ts(tmem + kColO, tmem + kColA + j * 8, v + j * (2048 >> 4), kIdescBmn, 1);
+          tc_commit(&c.o_full);
+          tc_commit(&c.empty_v[buf]);
+        }
+        __syncwarp();
+        ++n;
       }
-      bulk_wait_all();
     }
     __syncwarp();
   } else if (warp < 8) {
     // ------------------------------------------------------------------ P, O
     if (kOut) {
-      Walk<kOut> it(p);
+      Info info;
+      uint32_t m = 0, n = 0;
       const int i = 32 * w4 + lane;                       // row of the chunk
       const uint32_t lanes = static_cast<uint32_t>(32 * w4) << 16;
-      for (uint32_t n = 0; it.next(); ++n) {
-        const int buf = n & 1, rows = it.rows();
+      const uint32_t col_a = tmem + lanes + kColA, col_o = tmem + lanes + kColO;
+      while (next_chunk(c, m, info, lane)) {
+        if (info.rows == 0) continue;
+        const int buf = n & 1, rows = info.rows;
         const uint32_t one = n & 1;
         const Table &tab = c.tab[buf];
+        uint32_t a[32], r[16];
+        float of;                                         // O's factor
         KDA_WAIT_WARP(c.tab_full[buf], (n >> 1) & 1);
         KDA_WAIT_WARP(c.a_full, one);
         tc_fence_after();
-        const float bl = tab.bl[i];
-        float sum = bl;                                   // logarithm of the row factor
-        // blocks J = w4 .. 0 need row factors from near to far; P is written
-        // over A, so they go 0 .. w4: sum over the blocks between first
-        for (int m = 1; m < w4; ++m) sum += tab.total[m];
-        float v[32];
-        uint32_t r[16];
-        for (int J = 0; J < w4; ++J) {
-          const float row = exp2_approx(sum);
-          tc_ld32(tmem + lanes + kColA + 32 * J, v);
+        const float xi = tab.x[i];
+        const bool mild = tab.mild;
+        if (mild) {
+          of = p.scale * rcp_approx(xi);
+          // blocks of 32 columns up to the diagonal one; P is written over A
+          // (block J over half of block J / 2, which is read)
+#pragma unroll 1
+          for (int J = 0; J <= w4; ++J) {
+            tc_ld(col_a + 32 * J, a);
+            const ulonglong2 *f = reinterpret_cast<const ulonglong2 *>(tab.x + 32 * J);
+            tc_wait_ld(a);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 f = reinterpret_cast<const float4 *>(tab.f + 32 * J)[j];
-            r[2 * j] = pack2(v[4 * j] * (row * f.x), v[4 * j + 1] * (row * f.y));
-            r[2 * j + 1] = pack2(v[4 * j + 2] * (row * f.z), v[4 * j + 3] * (row * f.w));
+            for (int j = 0; j < 8; ++j) {
+              const ulonglong2 ff = f[j];
+              r[2 * j] = pack2(mul2(raw_pair(a[4 * j], a[4 * j + 1]), ff.x));
+              r[2 * j + 1] = pack2(mul2(raw_pair(a[4 * j + 2], a[4 * j + 3]), ff.y));
+            }
+            if (J == w4) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                r[j] &= 2 * j + 1 <= lane ? 0xFFFFFFFFu : 2 * j <= lane ? 0xFFFFu : 0u;
+            }
+            tc_st16(col_a + 16 * J, r);
           }
-          tc_st16(tmem + lanes + kColA + 16 * J, r);
-          // next: one block fewer between
-          sum = bl;
-          for (int m = J + 2; m < w4; ++m) sum += tab.total[m];
-        }
-        tc_ld32(tmem + lanes + kColA + 32 * w4, v);
+        } else {
+          of = p.scale;
+          const float e = strong_rows(tab, col_a, w4, lane, xi);
+          // O = E (Q S^T)
+          KDA_WAIT_WARP(c.qs_full, one);
+          tc_fence_after();
+#pragma unroll 1
+          for (int j = 0; j < 4; ++j) {
+            tc_ld(col_o + 32 * j, a);
+            tc_wait_ld(a);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float4 o = reinterpret_cast<const float4 *>(tab.bl + 32 * w4)[j];
-          float x[4] = {exp2_approx(bl - o.x), exp2_approx(bl - o.y), exp2_approx(bl - o.z),
-                        exp2_approx(bl - o.w)};
-#pragma unroll
-          for (int m = 0; m < 4; ++m) x[m] = 4 * j + m <= lane ? v[4 * j + m] * x[m] : 0.0f;
-          r[2 * j] = pack2(x[0], x[1]);
-          r[2 * j + 1] = pack2(x[2], x[3]);
+            for (int m = 0; m < 32; ++m) a[m] = __float_as_uint(__uint_as_float(a[m]) * e);
+            tc_st32(col_o + 32 * j, a);
+          }
         }
-        tc_st16(tmem + lanes + kColA + 16 * w4, r);
+        // (columns of later blocks are zeros)
 #pragma unroll
         for (int j = 0; j < 16; ++j) r[j] = 0;
-        for (int J = w4 + 1; J < 4; ++J) tc_st16(tmem + lanes + kColA + 16 * J, r);
-        sum = bl;
-        for (int m = 0; m < w4; ++m) sum += tab.total[m];
-        const float e = exp2_approx(sum);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.tab_empty[buf]);
-        // O = E (Q S^T)
-        KDA_WAIT_WARP(c.qs_full, one);
-        tc_fence_after();
-        for (int j = 0; j < 4; ++j) {
-          tc_ld32(tmem + lanes + kColO + 32 * j, v);
-#pragma unroll
-          for (int m = 0; m < 32; ++m) v[m] *= e;
-          tc_st32(tmem + lanes + kColO + 32 * j, v);
-        }
+#pragma unroll 1
+        for (int J = w4 + 1; J < 4; ++J) tc_st16(col_a + 16 * J, r);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c.p_full);
-        // the chunk's outputs
+        if (lane == 0) {
+          mbar_arrive(&c.p_full);
+          mbar_arrive(&c.tab_empty[buf]);
+        }
+        // the chunk's outputs: through Q's tile, or by rows where it is not full
         KDA_WAIT_WARP(c.o_full, one);
         tc_fence_after();
-        uint4 out[16];
-#pragma unroll
+        const bool full = rows == kChunk;
+        const uint32_t tile = smem_addr(sq + buf * kTile) + i * 128;
+        __nv_bfloat16 *to = p.output + (info.row + i) * p.o_stride + info.head * kDim;
+        const f32x2 of2 = pair(of, of);
+#pragma unroll 1
         for (int j = 0; j < 4; ++j) {
-          tc_ld32(tmem + lanes + kColO + 32 * j, v);
+          tc_ld(col_o + 32 * j, a);
+          tc_wait_ld(a);
 #pragma unroll
-          for (int m = 0; m < 4; ++m)
-            out[4 * j + m] = make_uint4(
-                pack2(p.scale * v[8 * m], p.scale * v[8 * m + 1]),
-                pack2(p.scale * v[8 * m + 2], p.scale * v[8 * m + 3]),
-                pack2(p.scale * v[8 * m + 4], p.scale * v[8 * m + 5]),
-                pack2(p.scale * v[8 * m + 6], p.scale * v[8 * m + 7]));
+          for (int m = 0; m < 16; ++m) r[m] = pack2(mul2(raw_pair(a[2 * m], a[2 * m + 1]), of2));
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint4 v = make_uint4(r[4 * m], r[4 * m + 1], r[4 * m + 2], r[4 * m + 3]);
+            if (full) {
+              const uint32_t at =
+                  tile + (j >> 1) * kHalf + ((((j & 1) * 4 + m) ^ (lane & 7)) << 4);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y),
+                           "r"(v.z), "r"(v.w)
+                           : "memory");
+            } else if (i < rows) {
+              reinterpret_cast<uint4 *>(to)[4 * j + m] = v;
+            }
+          }
         }
         tc_fence_before();
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&c.o_empty);
-        if (rows == kChunk) {
-          uint8_t *tile = sq + buf * kTile;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) *reinterpret_cast<uint4 *>(tile + tile_at(i, j)) = out[j];
-          fence_proxy_async_smem();
-        } else if (i < rows) {
-          uint4 *to = reinterpret_cast<uint4 *>(
-              p.output + (it.first_row() + i) * p.o_stride + it.unit.h * kDim);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) to[j] = out[j];
+        if (full) {
+          // the four warps' rows are staged: one thread stores the tile
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          if (threadIdx.x == 128) {
+            const uint8_t *q = sq + buf * kTile;
+            tma_store(&map_o, info.head * kDim, info.row, q);
+            tma_store(&map_o, info.head * kDim + 64, info.row, q + kHalf);
+            bulk_commit();
+            bulk_wait_read(0);
+            mbar_arrive(&c.empty_q[buf]);
+          }
+        } else if (threadIdx.x == 128) {
+          mbar_arrive(&c.empty_q[buf]);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c.st_full[buf]);
+        ++n;
       }
+      if (threadIdx.x == 128) bulk_wait_all();
     }
     __syncwarp();
   } else if (warp < 12) {
     regs_dec<96>();
     // ------------------------------------------------------------------- K''
-    Walk<kOut> it(p);
-    uint32_t quarter = 0;
-    for (uint32_t n = 0; it.next(); ++n) {
-      const int buf = n & 1, rows = it.rows(), quarters = (rows + 31) >> 5;
+    Info info;
+    uint32_t m = 0, n = 0, quarter = 0;
+    // rows and column groups of the matrices that a lane addresses
+    const int m_row = 8 * (lane >> 4) + (lane & 7), m_group = (lane >> 3) & 1;
+    while (next_chunk(c, m, info, lane)) {
+      if (info.rows == 0) continue;
+      const int buf = n & 1, rows = info.rows, quarters = (rows + 31) >> 5;
       const uint32_t two = (n >> 1) & 1;
       const Table &tab = c.tab[buf];
       KDA_WAIT_WARP(c.full_v[buf], two);
@@ -654,46 +863,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         float sum = 0.0f;
         for (int m = i + 1; m < 4; ++m) sum += tab.total[m];
         const float block = exp2_approx(sum);
-        float2 f[4];
+        f32x2 f[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f[j] = reinterpret_cast<const float2 *>(tab.f + 32 * i + 8 * j)[lane & 3];
-          f[j].x *= block;
-          f[j].y *= block;
-        }
-        const int valid = rows - 32 * i - 2 * (lane & 3);   // token 8 j + e is live below it
-        KDA_WAIT_WARP(c.kq_empty[kb], ((quarter >> 1) & 1) ^ 1);
-        tc_fence_after();
+        for (int j = 0; j < 4; ++j)
+          f[j] = mul2(reinterpret_cast<const f32x2 *>(tab.f + 32 * i + 8 * j)[lane & 3],
+                      pair(block, block));
+        const int valid = rows - 32 * i - 2 * (lane & 3);  // tokens behind it: any keys
+        bool gone = false;
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-          const int d0 = 32 * w4 + 16 * half;
-          uint32_t hi[8], mid[8], lo[8];
+          uint32_t raw[8], hi[8], mid[8], lo[8];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             uint32_t r[4];
-            const int m = lane >> 3;
-            ldmatrix_x4_trans(
-                k + tile_at(32 * i + 16 * x + 8 * (m >> 1) + (lane & 7), d0 / 8 + (m & 1)), r);
+            ldmatrix_x4_trans(k + tile_at(32 * i + 16 * x + m_row, 4 * w4 + 2 * half + m_group), r);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int j = 2 * x + (y >> 1);
-              float a = 8 * j < valid ? low_half(r[y]) * f[j].x : 0.0f;
-              float b = 8 * j + 1 < valid ? high_half(r[y]) * f[j].y : 0.0f;
-              const uint32_t h = pack2(a, b);
-              a -= low_half(h);
-              b -= high_half(h);
-              const uint32_t s = pack2(a, b);
-              a -= low_half(s);
-              b -= high_half(s);
-              hi[4 * x + y] = h;
-              mid[4 * x + y] = s;
-              lo[4 * x + y] = pack2(a, b);
+            for (int y = 0; y < 4; ++y) raw[4 * x + y] = r[y];
+          }
+          if (32 * i + 32 > rows) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const int j = y >> 1;
+              raw[y] &= 8 * j + 1 < valid ? 0xFFFFFFFFu : 8 * j < valid ? 0xFFFFu : 0u;
             }
           }
-          const uint32_t at = tmem + (static_cast<uint32_t>(d0) << 16) + kColK + kb * kColsK;
+          // three parts by truncation: 8 + 8 + 8 bits hold all 24
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const f32x2 v = mul2(raw_pair(raw[y] << 16, raw[y] & 0xFFFF0000u), f[y >> 1]);
+            const f32x2 v1 = sub2(v, v & 0xFFFF0000FFFF0000ull);
+            const f32x2 v2 = sub2(v1, v1 & 0xFFFF0000FFFF0000ull);
+            hi[y] = upper_halves(v);
+            mid[y] = upper_halves(v1);
+            lo[y] = upper_halves(v2);
+          }
+          if (half == 0) {
+            gone = !__all_sync(0xffffffffu, wait_phase(&c.kq_empty[kb], ((quarter >> 1) & 1) ^ 1,
+                                                       &c.abort));
+            if (gone) break;
+            tc_fence_after();
+          }
+          const uint32_t at =
+              tmem + (static_cast<uint32_t>(32 * w4 + 16 * half) << 16) + kColK + kb * kColsK;
           tc_st_16x128(at, hi);
           tc_st_16x128(at + 16, mid);
           tc_st_16x128(at + 32, lo);
         }
+        if (gone) break;
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -705,79 +921,80 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&c.empty_k[buf]);
         mbar_arrive(&c.tab_empty[buf]);
       }
+      ++n;
     }
     __syncwarp();
   } else {
     regs_inc<208>();
     // -------------------------------------------------------------- the page
-    Walk<kOut> it(p);
+    Info info;
+    uint32_t m = 0, n = 0;
     const int d = 32 * w4 + lane;                          // key
-    const uint32_t lanes = static_cast<uint32_t>(32 * w4) << 16;
-    uint32_t n = 0;
-    bool ok = true;
-    while (ok && it.next_unit(threadIdx.x == 384)) {
-      float s[kDim];
-      const float *from = nullptr;
-      if (kOut) {
-        if (it.unit.segs > 1)
-          from = p.ws_state + ws_index(p, it.unit) * kPage;
-        else if (it.unit.src)
-          from = page_of(p.state, it.unit.src, p.heads, it.unit.h);
-      }
-      if (from) {
+    const uint32_t col_u = tmem + (static_cast<uint32_t>(32 * w4) << 16) + kColU;
+    f32x2 s[kDim / 2];                                     // value rows 2 i, 2 i + 1
+    float all = 0.0f;                                      // the unit's decay (logarithm)
+    while (next_chunk(c, m, info, lane)) {
+      if (info.first) {
+        all = 0.0f;
+        if (info.from) {
 #pragma unroll
-        for (int i = 0; i < kDim; ++i) s[i] = from[i * kDim + d];
-      } else {
+          for (int i = 0; i < kDim / 2; ++i)
+            s[i] = pair(info.from[2 * i * kDim + d], info.from[(2 * i + 1) * kDim + d]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kDim; ++i) s[i] = 0.0f;
+          for (int i = 0; i < kDim / 2; ++i) s[i] = 0;
+        }
       }
-      float all = 0.0f;                                    // the unit's decay (logarithm)
-      for (; it.next_chunk(); ++n) {
-        ok = false;
+      if (info.rows > 0) {
         const int buf = n & 1;
         const uint32_t one = n & 1;
         const Table &tab = c.tab[buf];
+        KDA_WAIT_WARP(c.tab_full[buf], (n >> 1) & 1);
+        const float total = tab.sum, ref = tab.ref;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.tab_empty[buf]);
         if (kOut) {
+          // the page's copy for Q S^T; the product before has read the last one
+          if (n > 0) KDA_WAIT_WARP(c.qs_full, one ^ 1);
+          const float e = exp2_approx(ref);
+          const f32x2 e2 = pair(e, e);
 #pragma unroll
           for (int g = 0; g < 16; ++g)
             *reinterpret_cast<uint4 *>(ss + tile_at(d, g)) =
-                make_uint4(pack2(s[8 * g], s[8 * g + 1]), pack2(s[8 * g + 2], s[8 * g + 3]),
-                           pack2(s[8 * g + 4], s[8 * g + 5]), pack2(s[8 * g + 6], s[8 * g + 7]));
+                make_uint4(pack2(mul2(s[4 * g], e2)), pack2(mul2(s[4 * g + 1], e2)),
+                           pack2(mul2(s[4 * g + 2], e2)), pack2(mul2(s[4 * g + 3], e2)));
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&c.s_full);
         }
-        KDA_WAIT_WARP(c.tab_full[buf], (n >> 1) & 1);
-        const float total = (tab.total[0] + tab.total[1]) + (tab.total[2] + tab.total[3]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.tab_empty[buf]);
         const float keep = exp2_approx(total);
+        const f32x2 keep2 = pair(keep, keep);
         all += total;
         KDA_WAIT_WARP(c.u_full, one);
         tc_fence_after();
+        uint32_t u[32];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float v[32];
-          tc_ld32(tmem + lanes + kColU + 32 * j, v);
+          tc_ld(col_u + 32 * j, u);
+          tc_wait_ld(u);
 #pragma unroll
-          for (int m = 0; m < 32; ++m) s[32 * j + m] = __fmaf_rn(s[32 * j + m], keep, v[m]);
+          for (int m = 0; m < 16; ++m)
+            s[16 * j + m] = fma2(s[16 * j + m], keep2, raw_pair(u[2 * m], u[2 * m + 1]));
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&c.u_empty);
-        ok = true;
+        ++n;
       }
-      if (!ok) break;
-      float *to = nullptr;
-      if (!kOut) {
-        to = p.ws_state + ws_index(p, it.unit) * kPage;
-        if (threadIdx.x == 384) p.ws_decay[ws_index(p, it.unit)] = all;
-      } else if (it.unit.seg == it.unit.segs - 1 && it.unit.dst) {
-        to = page_of(p.state, it.unit.dst, p.heads, it.unit.h);
-      }
-      if (to) {
+      if (info.last && info.to) {
 #pragma unroll
-        for (int i = 0; i < kDim; ++i) to[i * kDim + d] = s[i];
+        for (int i = 0; i < kDim / 2; ++i) {
+          float x, y;
+          unpair(s[i], x, y);
+          info.to[2 * i * kDim + d] = x;
+          info.to[(2 * i + 1) * kDim + d] = y;
+        }
+        if (!kOut && threadIdx.x == 384) *info.decay = all;
       }
     }
     __syncwarp();
