@@ -27,13 +27,13 @@
 // Q S^T are rounded to BF16 once: they only feed an output that is itself
 // rounded to BF16, and the FP32 sum keeps their errors at that size.
 //
-// Roles (512 threads, 16 warps): TMA loads (warp 0), MMA issue for the page
+// Roles (768 threads, 24 warps): TMA loads and stores (warp 0), MMA issue for the page
 // (U, Q S^T; warp 1) and for the outputs (A, P V; warp 3), the work and its decay
-// tables (warp 2); three warpgroups: P and O (4-7), K'' (8-11), the page
-// (12-15).  K'' is built transposed (lanes = keys) by transposing shared-memory
+// tables (warp 2); five warpgroups: P and O (4-11, 64 columns a
+// warp), K'' (12-19, 16 keys a warp), the page (20-23).  K'' is built transposed (lanes = keys) by transposing shared-memory
 // matrix loads straight into TMEM, as the A operand: no shared memory is
 // written for it.  P is written over A in TMEM.
-//   TMEM columns: A / P 0, O 128, U (the update) 256, K'' 384 (2 x 48).
+//   TMEM columns: A / P 0 (P's halves at 0 and 64), O 128, U (the update) 256, K'' 384 (2 x 48).
 //   Shared memory: Q, K, V double-buffered (32 KiB tiles, 128-byte swizzle) and
 //   the page's BF16 copy; O leaves through Q's tile.
 #include <cuda.h>
@@ -50,7 +50,7 @@ namespace kda {
 namespace lin {
 
 constexpr int kChunk = 128;
-constexpr int kThreads = 512;
+constexpr int kThreads = 768;
 constexpr int kHalf = 128 * 128;                 // bytes of a [128][64] BF16 tile
 constexpr int kTile = 2 * kHalf;                 // bytes of a [128][128] BF16 tile
 constexpr float kLog2e = 1.4426950408889634f;
@@ -84,10 +84,10 @@ struct Ctrl {
   Info info[kInfos];
   uint64_t info_full[kInfos], info_empty[kInfos];
   uint64_t full_q[2], full_k[2], full_v[2];      // TMA landed
-  uint64_t empty_q[2], empty_k[2], empty_v[2];
+  uint64_t empty_k[2], empty_v[2];
+  uint64_t st_full[2];                           // O staged in Q's tile (or written)
   uint64_t tab_full[2], tab_empty[2];
   uint64_t kq_full[2], kq_empty[2];              // K'' quarters in TMEM
-  uint64_t v_ok[2];                              // V's rows behind the end are zeros
   uint64_t a_full, p_full, qs_full, o_full, o_empty, u_full, u_empty, s_full;
   uint32_t tmem, abort;
 };
@@ -290,15 +290,16 @@ __device__ __forceinline__ f32x2 raw_pair(uint32_t lo, uint32_t hi) {
   return r;
 }
 
-// P of a chunk with strong decays, a row of a warp's 32 at a time: a row factor
-// times f off the diagonal block, 2^(bl_i - bl_j) on it.  bl: this row's prefix
-// sum in its block.  Returns the row's factor of Q S^T.
-__device__ __forceinline__ float strong_rows(const Table &tab, uint32_t col_a, int w4, int lane,
-                                             float bl) {
+// P of a chunk with strong decays, 64 columns (`side`) of a warp's 32 rows: a row
+// factor times f off the diagonal block, 2^(bl_i - bl_j) on it, zeros behind.
+// bl: this row's prefix sum in its block.  Returns the row's factor of Q S^T.
+__device__ __forceinline__ float strong_rows(const Table &tab, uint32_t col_a, int side, int w4,
+                                             int lane, float bl) {
   uint32_t a[32], r[16];
 #pragma unroll 1
-  for (int J = 0; J <= w4; ++J) {
-    tc_ld(col_a + 32 * J, a);
+  for (int z = 0; z < 2; ++z) {
+    const int J = 2 * side + z;
+    tc_ld(col_a + 32 * z, a);
     tc_wait_ld(a);
     if (J < w4) {
       float sum = bl;                                   // and the blocks between
@@ -309,14 +310,15 @@ __device__ __forceinline__ float strong_rows(const Table &tab, uint32_t col_a, i
         r[j] = pack2(__uint_as_float(a[2 * j]) * (row * tab.f[32 * J + 2 * j]),
                      __uint_as_float(a[2 * j + 1]) * (row * tab.f[32 * J + 2 * j + 1]));
     } else {
+      const int to = J == w4 ? lane : -1;               // the last column to keep
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const float x = __uint_as_float(a[2 * j]) * exp2_approx(bl - tab.x[32 * J + 2 * j]);
         const float y = __uint_as_float(a[2 * j + 1]) * exp2_approx(bl - tab.x[32 * J + 2 * j + 1]);
-        r[j] = pack2(2 * j <= lane ? x : 0.0f, 2 * j + 1 <= lane ? y : 0.0f);
+        r[j] = pack2(2 * j <= to ? x : 0.0f, 2 * j + 1 <= to ? y : 0.0f);
       }
     }
-    tc_st16(col_a + 16 * J, r);
+    tc_st16(col_a + 16 * z, r);
   }
   float sum = bl;
   for (int m = 0; m < w4; ++m) sum += tab.total[m];
@@ -419,26 +421,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     c.abort = 0;
     for (int i = 0; i < kInfos; ++i) {
       mbar_init(&c.info_full[i], 1);
-      mbar_init(&c.info_empty[i], kOut ? 15 : 10);
+      mbar_init(&c.info_empty[i], kOut ? 23 : 14);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.full_q[i], 1);
       mbar_init(&c.full_k[i], 1);
       mbar_init(&c.full_v[i], 1);
-      mbar_init(&c.empty_q[i], 1);
-      mbar_init(&c.empty_k[i], kOut ? 5 : 4);
+      mbar_init(&c.st_full[i], 8);
+      mbar_init(&c.empty_k[i], kOut ? 9 : 8);
       mbar_init(&c.empty_v[i], kOut ? 2 : 1);
       mbar_init(&c.tab_full[i], 1);
-      mbar_init(&c.tab_empty[i], kOut ? 12 : 8);
-      mbar_init(&c.kq_full[i], 4);
+      mbar_init(&c.tab_empty[i], kOut ? 20 : 12);
+      mbar_init(&c.kq_full[i], 8);
       mbar_init(&c.kq_empty[i], 1);
-      mbar_init(&c.v_ok[i], 4);
     }
     mbar_init(&c.a_full, 1);
-    mbar_init(&c.p_full, 4);
+    mbar_init(&c.p_full, 8);
     mbar_init(&c.qs_full, 1);
     mbar_init(&c.o_full, 1);
-    mbar_init(&c.o_empty, 4);
+    mbar_init(&c.o_empty, 8);
     mbar_init(&c.u_full, 1);
     mbar_init(&c.u_empty, 4);
     mbar_init(&c.s_full, 4);
@@ -460,13 +461,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (*abort_flag) {
     // nothing runs
   } else if (warp < 4) {
-    regs_dec<80>();
+    regs_dec<56>();
     if (warp == 0) {
-      // ------------------------------------------------------------ TMA loads
+      // ------------------------------------------------- TMA loads and stores
       Info info;
-      uint32_t m = 0, n = 0;
+      uint32_t m = 0, n = 0, stored = 0;
+      int row1 = 0, row2 = 0, head1 = 0, head2 = 0, rows1 = 0, rows2 = 0;  // the last two chunks
+      // the stored-th chunk's outputs leave Q's tile, which is then free
+      auto store = [&](int row, int head, int rows) {
+        const int buf = stored & 1;
+        if (!__all_sync(0xffffffffu, wait_phase(&c.st_full[buf], (stored >> 1) & 1, &c.abort)))
+          return false;
+        if (lane == 0 && rows == kChunk) {
+          const uint8_t *tile = sq + buf * kTile;
+          tma_store(&map_o, head * kDim, row, tile);
+          tma_store(&map_o, head * kDim + 64, row, tile + kHalf);
+          bulk_commit();
+          bulk_wait_read(0);
+        }
+        __syncwarp();
+        ++stored;
+        return true;
+      };
+      bool ok = true;
       while (next_chunk(c, m, info, lane)) {
         if (info.rows == 0) continue;
+        ok = false;
         const int buf = n & 1, boxes = (info.rows + 31) >> 5;
         const uint32_t parity = ((n >> 1) & 1) ^ 1;
         const int xk = info.head / p.group * kDim, xv = info.head * kDim;
@@ -484,16 +504,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         KDA_WAIT_WARP(c.empty_v[buf], parity);
         load(sv, &map_v, xv, &c.full_v[buf]);
         if (kOut) {
-          KDA_WAIT_WARP(c.empty_q[buf], parity);
+          if (n >= 2 && !store(row2, head2, rows2)) break;
           load(sq, &map_q, xk, &c.full_q[buf]);
+          row2 = row1, head2 = head1, rows2 = rows1;
+          row1 = info.row, head1 = info.head, rows1 = info.rows;
         }
         ++n;
+        ok = true;
       }
+      if (kOut && ok) {
+        if (stored + 2 == n) ok = store(row2, head2, rows2);
+        if (ok && stored < n) store(row1, head1, rows1);
+      }
+      if (lane == 0) bulk_wait_all();
     } else if (warp == 1) {
       // ------------------------------------------- MMA issue: U and Q S^T
       // The warp walks and waits as one; one elected thread issues.  Descriptors
       // are sums of a base and constants (addresses count 16 bytes).
       uint32_t quarter = 0;
+      const bool leader = elect_one();
       const uint64_t q0 = desc_k_major(smem_addr(sq)), v0 = desc_mn_major(smem_addr(sv)),
                      s0 = desc_mn_major(smem_addr(ss));
       Info info;
@@ -503,15 +532,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int buf = n & 1, quarters = (info.rows + 31) >> 5;
         const uint32_t one = n & 1, two = (n >> 1) & 1;
         // U = K''^T V, quarter by quarter of 32 tokens
-        KDA_WAIT_WARP(c.full_v[buf], two);
-        KDA_WAIT_WARP(c.v_ok[buf], two);
+        // (the first K'' also says that V is there)
         if (n > 0) KDA_WAIT_WARP(c.u_empty, one ^ 1);
         int i = 0;
         for (; i < quarters; ++i, ++quarter) {
           const int kb = quarter & 1;
           KDA_WAIT_WARP(c.kq_full[kb], (quarter >> 1) & 1);
           tc_fence_after();
-          if (elect_one()) {
+          if (leader) {
             const uint32_t a = tmem + kColK + kb * kColsK;
             const uint64_t v = v0 + buf * (kTile >> 4) + i * (4096 >> 4);
 #pragma unroll
@@ -535,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           KDA_WAIT_WARP(c.full_q[buf], two);
           if (n > 0) KDA_WAIT_WARP(c.o_empty, one ^ 1);
           tc_fence_after();
-          if (elect_one()) {
+          if (leader) {
             const uint64_t q = q0 + buf * (kTile >> 4);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -666,6 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (kOut && warp == 3) {
       // ------------------------------------------- MMA issue: A and P V
+      const bool leader = elect_one();
       const uint64_t q0 = desc_k_major(smem_addr(sq)), k0 = desc_k_major(smem_addr(sk)),
                      v0 = desc_mn_major(smem_addr(sv));
       Info info;
@@ -678,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         KDA_WAIT_WARP(c.full_k[buf], two);
         KDA_WAIT_WARP(c.full_q[buf], two);
         tc_fence_after();
-        if (elect_one()) {
+        if (leader) {
           const uint64_t q = q0 + buf * (kTile >> 4), k = k0 + buf * (kTile >> 4);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -690,17 +719,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         // O += P V
-        KDA_WAIT_WARP(c.full_v[buf], two);
-        KDA_WAIT_WARP(c.v_ok[buf], two);
-        KDA_WAIT_WARP(c.qs_full, one);
+        KDA_WAIT_WARP(c.qs_full, one);                     // (and V is there)
         KDA_WAIT_WARP(c.p_full, one);
         tc_fence_after();
-        if (elect_one()) {
+        if (leader) {
           const uint64_t v = v0 + buf * (kTile >> 4);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             if (j < 2 * quarters)
-              tc_mma_ts(tmem + kColO, tmem + kColA + j * 8, v + j * (2048 >> 4), kIdescBmn, 1);
+              tc_mma_ts(tmem + kColO, tmem + kColA + (j >> 2) * 64 + (j & 3) * 8, v + j * (2048 >> 4), kIdescBmn, 1);
           tc_commit(&c.o_full);
           tc_commit(&c.empty_v[buf]);
         }
@@ -709,14 +736,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp < 8) {
+  } else if (warp < 12) {
+    regs_dec<64>();
     // ------------------------------------------------------------------ P, O
     if (kOut) {
       Info info;
       uint32_t m = 0, n = 0;
       const int i = 32 * w4 + lane;                       // row of the chunk
+      const int side = (warp - 4) >> 2;                   // columns 64 side .. of P and O
       const uint32_t lanes = static_cast<uint32_t>(32 * w4) << 16;
-      const uint32_t col_a = tmem + lanes + kColA, col_o = tmem + lanes + kColO;
+      const uint32_t col_a = tmem + lanes + kColA + 64 * side,
+                     col_o = tmem + lanes + kColO + 64 * side;
       while (next_chunk(c, m, info, lane)) {
         if (info.rows == 0) continue;
         const int buf = n & 1, rows = info.rows;
@@ -731,12 +761,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool mild = tab.mild;
         if (mild) {
           of = p.scale * rcp_approx(xi);
-          // blocks of 32 columns up to the diagonal one; P is written over A
-          // (block J over half of block J / 2, which is read)
+          // 32 columns at a time; P is written over the A that is read
 #pragma unroll 1
-          for (int J = 0; J <= w4; ++J) {
-            tc_ld(col_a + 32 * J, a);
+          for (int z = 0; z < 2; ++z) {
+            const int J = 2 * side + z;                   // block of 32 columns
             const ulonglong2 *f = reinterpret_cast<const ulonglong2 *>(tab.x + 32 * J);
+            tc_ld(col_a + 32 * z, a);
             tc_wait_ld(a);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -744,21 +774,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               r[2 * j] = pack2(mul2(raw_pair(a[4 * j], a[4 * j + 1]), ff.x));
               r[2 * j + 1] = pack2(mul2(raw_pair(a[4 * j + 2], a[4 * j + 3]), ff.y));
             }
-            if (J == w4) {
+            if (J >= w4) {
+              const int to = J == w4 ? lane : -1;         // the last column to keep
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                r[j] &= 2 * j + 1 <= lane ? 0xFFFFFFFFu : 2 * j <= lane ? 0xFFFFu : 0u;
+                r[j] &= 2 * j + 1 <= to ? 0xFFFFFFFFu : 2 * j <= to ? 0xFFFFu : 0u;
             }
-            tc_st16(col_a + 16 * J, r);
+            tc_st16(col_a + 16 * z, r);
           }
         } else {
           of = p.scale;
-          const float e = strong_rows(tab, col_a, w4, lane, xi);
+          const float e = strong_rows(tab, col_a, side, w4, lane, xi);
           // O = E (Q S^T)
           KDA_WAIT_WARP(c.qs_full, one);
           tc_fence_after();
 #pragma unroll 1
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 2; ++j) {
             tc_ld(col_o + 32 * j, a);
             tc_wait_ld(a);
 #pragma unroll
@@ -766,11 +797,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_st32(col_o + 32 * j, a);
           }
         }
-        // (columns of later blocks are zeros)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) r[j] = 0;
-#pragma unroll 1
-        for (int J = w4 + 1; J < 4; ++J) tc_st16(col_a + 16 * J, r);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -782,81 +808,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         KDA_WAIT_WARP(c.o_full, one);
         tc_fence_after();
         const bool full = rows == kChunk;
-        const uint32_t tile = smem_addr(sq + buf * kTile) + i * 128;
-        __nv_bfloat16 *to = p.output + (info.row + i) * p.o_stride + info.head * kDim;
+        const uint32_t tile = smem_addr(sq + buf * kTile + side * kHalf) + i * 128;
+        __nv_bfloat16 *to = p.output + (info.row + i) * p.o_stride + info.head * kDim + 64 * side;
         const f32x2 of2 = pair(of, of);
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2; ++j) {
           tc_ld(col_o + 32 * j, a);
           tc_wait_ld(a);
 #pragma unroll
-          for (int m = 0; m < 16; ++m) r[m] = pack2(mul2(raw_pair(a[2 * m], a[2 * m + 1]), of2));
-#pragma unroll
           for (int m = 0; m < 4; ++m) {
-            const uint4 v = make_uint4(r[4 * m], r[4 * m + 1], r[4 * m + 2], r[4 * m + 3]);
+            uint32_t v[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              v[z] = pack2(mul2(raw_pair(a[8 * m + 2 * z], a[8 * m + 2 * z + 1]), of2));
             if (full) {
-              const uint32_t at =
-                  tile + (j >> 1) * kHalf + ((((j & 1) * 4 + m) ^ (lane & 7)) << 4);
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y),
-                           "r"(v.z), "r"(v.w)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               tile + (((4 * j + m) ^ (lane & 7)) << 4)),
+                           "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
                            : "memory");
             } else if (i < rows) {
-              reinterpret_cast<uint4 *>(to)[4 * j + m] = v;
+              reinterpret_cast<uint4 *>(to)[4 * j + m] = make_uint4(v[0], v[1], v[2], v[3]);
             }
           }
         }
         tc_fence_before();
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c.o_empty);
-        if (full) {
-          // the four warps' rows are staged: one thread stores the tile
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-          if (threadIdx.x == 128) {
-            const uint8_t *q = sq + buf * kTile;
-            tma_store(&map_o, info.head * kDim, info.row, q);
-            tma_store(&map_o, info.head * kDim + 64, info.row, q + kHalf);
-            bulk_commit();
-            bulk_wait_read(0);
-            mbar_arrive(&c.empty_q[buf]);
-          }
-        } else if (threadIdx.x == 128) {
-          mbar_arrive(&c.empty_q[buf]);
+        if (lane == 0) {
+          mbar_arrive(&c.o_empty);
+          mbar_arrive(&c.st_full[buf]);
         }
-        __syncwarp();
         ++n;
       }
-      if (threadIdx.x == 128) bulk_wait_all();
     }
     __syncwarp();
-  } else if (warp < 12) {
-    regs_dec<96>();
+  } else if (warp < 20) {
+    regs_dec<56>();
     // ------------------------------------------------------------------- K''
     Info info;
     uint32_t m = 0, n = 0, quarter = 0;
-    // rows and column groups of the matrices that a lane addresses
-    const int m_row = 8 * (lane >> 4) + (lane & 7), m_group = (lane >> 3) & 1;
+    const int half = (warp - 12) >> 2;                     // which 16 of the 32 keys
+    // this lane's row of the matrices that it addresses (token, 16-byte group)
+    const uint32_t at_k =
+        smem_addr(sk) + tile_at(8 * (lane >> 4) + (lane & 7), 4 * w4 + 2 * half + ((lane >> 3) & 1));
+    const uint32_t at_t = tmem + (static_cast<uint32_t>(32 * w4 + 16 * half) << 16) + kColK;
     while (next_chunk(c, m, info, lane)) {
       if (info.rows == 0) continue;
       const int buf = n & 1, rows = info.rows, quarters = (rows + 31) >> 5;
       const uint32_t two = (n >> 1) & 1;
       const Table &tab = c.tab[buf];
-      KDA_WAIT_WARP(c.full_v[buf], two);
-      if (rows < 32 * quarters) {
-        // rows behind the sequence's end become zeros: they are other rows of
-        // the tensor (or stale), and 0 * NaN is not 0
-        const int at = threadIdx.x & 127;
-        for (int x = at; x < (32 * quarters - rows) * 16; x += 128)
-          *reinterpret_cast<uint4 *>(sv + buf * kTile + tile_at(rows + (x >> 4), x & 15)) =
-              make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
+      if (half == 0) {
+        KDA_WAIT_WARP(c.full_v[buf], two);
+        if (rows < 32 * quarters) {
+          // rows behind the sequence's end become zeros: they are other rows of
+          // the tensor (or stale), and 0 * NaN is not 0
+          const int at = threadIdx.x & 127;
+#pragma unroll 1
+          for (int x = at; x < (32 * quarters - rows) * 16; x += 128)
+            *reinterpret_cast<uint4 *>(sv + buf * kTile + tile_at(rows + (x >> 4), x & 15)) =
+                make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c.v_ok[buf]);
       KDA_WAIT_WARP(c.tab_full[buf], two);
       KDA_WAIT_WARP(c.full_k[buf], two);
-      const uint32_t k = smem_addr(sk + buf * kTile);
       int i = 0;
+#pragma unroll 1
       for (; i < quarters; ++i, ++quarter) {
         const int kb = quarter & 1;
         // factors of the 8 tokens a lane sees: 8 j + 2 (lane % 4) + {0, 1}
@@ -868,48 +885,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 4; ++j)
           f[j] = mul2(reinterpret_cast<const f32x2 *>(tab.f + 32 * i + 8 * j)[lane & 3],
                       pair(block, block));
-        const int valid = rows - 32 * i - 2 * (lane & 3);  // tokens behind it: any keys
-        bool gone = false;
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          uint32_t raw[8], hi[8], mid[8], lo[8];
+        uint32_t raw[8], hi[8], mid[8], lo[8];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t r[4];
-            ldmatrix_x4_trans(k + tile_at(32 * i + 16 * x + m_row, 4 * w4 + 2 * half + m_group), r);
+        for (int x = 0; x < 2; ++x) {
+          uint32_t r[4];
+          ldmatrix_x4_trans(at_k + buf * kTile + i * 4096 + x * 2048, r);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) raw[4 * x + y] = r[y];
-          }
-          if (32 * i + 32 > rows) {
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              const int j = y >> 1;
-              raw[y] &= 8 * j + 1 < valid ? 0xFFFFFFFFu : 8 * j < valid ? 0xFFFFu : 0u;
-            }
-          }
-          // three parts by truncation: 8 + 8 + 8 bits hold all 24
+          for (int y = 0; y < 4; ++y) raw[4 * x + y] = r[y];
+        }
+        if (32 * i + 32 > rows) {
+          const int valid = rows - 32 * i - 2 * (lane & 3);  // tokens behind it: any keys
 #pragma unroll
           for (int y = 0; y < 8; ++y) {
-            const f32x2 v = mul2(raw_pair(raw[y] << 16, raw[y] & 0xFFFF0000u), f[y >> 1]);
-            const f32x2 v1 = sub2(v, v & 0xFFFF0000FFFF0000ull);
-            const f32x2 v2 = sub2(v1, v1 & 0xFFFF0000FFFF0000ull);
-            hi[y] = upper_halves(v);
-            mid[y] = upper_halves(v1);
-            lo[y] = upper_halves(v2);
+            const int j = y >> 1;
+            raw[y] &= 8 * j + 1 < valid ? 0xFFFFFFFFu : 8 * j < valid ? 0xFFFFu : 0u;
           }
-          if (half == 0) {
-            gone = !__all_sync(0xffffffffu, wait_phase(&c.kq_empty[kb], ((quarter >> 1) & 1) ^ 1,
-                                                       &c.abort));
-            if (gone) break;
-            tc_fence_after();
-          }
-          const uint32_t at =
-              tmem + (static_cast<uint32_t>(32 * w4 + 16 * half) << 16) + kColK + kb * kColsK;
-          tc_st_16x128(at, hi);
-          tc_st_16x128(at + 16, mid);
-          tc_st_16x128(at + 32, lo);
         }
-        if (gone) break;
+        // three parts by truncation: 8 + 8 + 8 bits hold all 24
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          const f32x2 v = mul2(raw_pair(raw[y] << 16, raw[y] & 0xFFFF0000u), f[y >> 1]);
+          const f32x2 v1 = sub2(v, v & 0xFFFF0000FFFF0000ull);
+          const f32x2 v2 = sub2(v1, v1 & 0xFFFF0000FFFF0000ull);
+          hi[y] = upper_halves(v);
+          mid[y] = upper_halves(v1);
+          lo[y] = upper_halves(v2);
+        }
+        KDA_WAIT_WARP(c.kq_empty[kb], ((quarter >> 1) & 1) ^ 1);
+        tc_fence_after();
+        tc_st_16x128(at_t + kb * kColsK, hi);
+        tc_st_16x128(at_t + kb * kColsK + 16, mid);
+        tc_st_16x128(at_t + kb * kColsK + 32, lo);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -925,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    regs_inc<208>();
+    regs_inc<184>();
     // -------------------------------------------------------------- the page
     Info info;
     uint32_t m = 0, n = 0;
@@ -994,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           info.to[2 * i * kDim + d] = x;
           info.to[(2 * i + 1) * kDim + d] = y;
         }
-        if (!kOut && threadIdx.x == 384) *info.decay = all;
+        if (!kOut && threadIdx.x == 640) *info.decay = all;
       }
     }
     __syncwarp();
