@@ -296,58 +296,91 @@ def kda_oproj(*, partials, prefix, output, out_norm, blocks=None, norm=None,
 
 
 # ------------------------------------ linear attention with one decay per head
+#
+# These calls are short, so their host side is too: one look at each tensor, and
+# the general checks (with their messages) only where that look fails.
 
-def _rows(name, t, width):
-    """A BF16 CUDA tensor [rows, width] whose rows may be slices of wider rows:
-    elements of a row adjacent, any row stride that the library takes."""
+def _want(name, t, dtype, shape, index):
+    """The address of a contiguous CUDA tensor of this type, shape (None: any)
+    and device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous()
+            and t.get_device() == index and (shape is None or t.shape == shape)):
+        _check(name, t, dtype, shape)
+        _same_device(torch.device("cuda", index), **{name: t})
+    return t.data_ptr()
+
+
+def _maybe(name, t, dtype, shape, index):
+    return None if t is None else _want(name, t, dtype, shape, index)
+
+
+def _cuda_index(name, t):
+    """Index of the CUDA device of a tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    if t.dtype != torch.bfloat16:
+    return t.get_device()
+
+
+def _rows(name, t, rows, width, index):
+    """(address, row stride) of a BF16 CUDA tensor [rows, width] whose rows may be
+    slices of wider rows: elements of a row adjacent, any row stride that the
+    library takes."""
+    if _cuda_index(name, t) != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 2 or (width is not None and t.shape[1] != width):
-        raise ValueError(f"{name} must be [rows, {'width' if width is None else width}], "
-                         f"got {tuple(t.shape)}")
-    stride = t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
-    if t.shape[1] and (t.stride(1) != 1 or stride % 8 or stride < t.shape[1]):
-        raise ValueError(f"{name}: the elements of a row must be adjacent and rows a multiple "
-                         f"of 8 elements apart, got strides {tuple(t.stride())}")
-    return stride
+    if t.shape != (rows, width):
+        raise ValueError(f"{name} must have shape {(rows, width)}, got {tuple(t.shape)}")
+    step, one = t.stride()
+    if rows <= 1:
+        step = width
+    if one != 1 or step % 8 or step < width:
+        if width:
+            raise ValueError(f"{name}: the elements of a row must be adjacent and rows a "
+                             f"multiple of 8 elements apart, got strides {tuple(t.stride())}")
+    return t.data_ptr(), step
 
 
-def _lin_rows(q, k, v, output, decay):
-    """Shapes of the linear-attention rows: (rows, heads, qk_heads, strides)."""
-    vs = _rows("v", v, None)
-    qs = _rows("q", q, None)
+def _lin_shape(q, v):
+    """(device index, rows, heads, qk_heads) of linear-attention rows."""
+    index = _cuda_index("v", v)
+    _cuda_index("q", q)
+    if v.dim() != 2 or q.dim() != 2 or v.shape[1] % DK or q.shape[1] % DK or not q.shape[1]:
+        raise ValueError("q, k and v must be rows of whole heads of 128")
     rows, width = v.shape
-    if width % DK or q.shape[1] % DK or not q.shape[1]:
-        raise ValueError("q, k and v rows must be whole heads of 128")
     H, Hk = width // DK, q.shape[1] // DK
     if H % Hk:
         raise ValueError(f"{H} value heads are not a multiple of {Hk} query heads")
-    ks = _rows("k", k, q.shape[1])
-    os_ = _rows("output", output, width)
-    for name, t in (("q", q), ("k", k), ("output", output)):
-        if t.shape[0] != rows:
-            raise ValueError(f"{name} must have {rows} rows, got {t.shape[0]}")
-    _check("decay", decay, torch.float32)
-    if tuple(decay.shape) not in ((H,), (rows, H)):
-        raise ValueError(f"decay must be [{H}] or [{rows}, {H}], got {tuple(decay.shape)}")
-    return rows, H, Hk, (qs, ks, vs, os_)
+    return index, rows, H, Hk
 
 
-def _lin_state(state, H):
-    _check("state", state, torch.float32)
-    if state.dim() != 4 or tuple(state.shape[1:]) != (H, DK, DK):
-        raise ValueError("state must be [num_slots, heads, 128, 128]")
-    return state.shape[0]
+def _decay(decay, rows, H, index):
+    per_row = isinstance(decay, torch.Tensor) and decay.dim() == 2
+    return _want("decay", decay, torch.float32, (rows, H) if per_row else (H,), index), int(per_row)
 
 
-def _run(entry, args, dev, stream):
-    with torch.cuda.device(dev):
-        s = stream if stream is not None else torch.cuda.current_stream(dev)
-        rc = _lib.call(entry, args, s.cuda_stream)
+def _state(state, H, index):
+    ptr = _want("state", state, torch.float32, None, index)
+    if state.dim() != 4 or state.shape[1:] != (H, DK, DK):
+        raise ValueError(f"state must be [num_slots, {H}, 128, 128], got {tuple(state.shape)}")
+    return ptr, state.shape[0]
+
+
+def _run(entry, args, index, stream):
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device_index != index:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, expected cuda:{index}")
+    else:
+        handle = stream.cuda_stream
+    # the library launches on the current device: make it the tensors' one
+    if torch._C._cuda_getDevice() == index:
+        rc = _lib.call(entry, args, handle)
+    else:
+        with torch.cuda.device(index):
+            rc = _lib.call(entry, args, handle)
     if rc != _lib.KDA_SUCCESS:
         raise _lib.KdaError(rc, _lib.strerror(rc))
 
@@ -366,41 +399,42 @@ def kda_lin_prompt(*, q, k, v, decay, seq_starts, output, scale: float, state=No
     pages the sequences start from) and ``dst_slots`` (where their last states
     go), i32 [seqs] each or None.  ``max_seq``: no sequence is longer (default:
     ``tokens``; the tighter, the better the work is laid out).  ``workspace``: a
-    CUDA uint8 tensor of at least ``kda_lin_prompt_workspace`` bytes; by default
+    CUDA uint8 tensor of at least ``lib.prompt_workspace`` bytes; by default
     allocated for the call, on the stream it runs on."""
     i32 = torch.int32
-    rows, H, Hk, strides = _lin_rows(q, k, v, output, decay)
-    _check("seq_starts", seq_starts, i32)
+    index, rows, H, Hk = _lin_shape(q, v)
+    qp, qs = _rows("q", q, rows, Hk * DK, index)
+    kp, ks = _rows("k", k, rows, Hk * DK, index)
+    vp, vs = _rows("v", v, rows, H * DK, index)
+    op, os_ = _rows("output", output, rows, H * DK, index)
+    dp, per_row = _decay(decay, rows, H, index)
+    sp = _want("seq_starts", seq_starts, i32, None, index)
     if seq_starts.dim() != 1 or seq_starts.shape[0] < 1:
         raise ValueError("seq_starts must be [seqs + 1]")
     B = seq_starts.shape[0] - 1
-    _check("src_slots", src_slots, i32, (B,), allow_none=True)
-    _check("dst_slots", dst_slots, i32, (B,), allow_none=True)
-    if state is None and (src_slots is not None or dst_slots is not None):
-        raise ValueError("state is required with src_slots or dst_slots")
-    num_slots = 0 if state is None else _lin_state(state, H)
-    _check("err", err, i32, allow_none=True)
-    dev = v.device
-    _same_device(dev, q=q, k=k, output=output, decay=decay, seq_starts=seq_starts, state=state,
-                 src_slots=src_slots, dst_slots=dst_slots, err=err, workspace=workspace)
-    a = _lib.KdaLinPromptArgs()
-    a.seqs, a.heads, a.qk_heads, a.tokens = B, H, Hk, rows
-    a.max_seq = rows if max_seq is None else min(int(max_seq), rows)
-    a.num_slots, a.decay_rows, a.path = num_slots, int(decay.dim() == 2), int(path)
-    a.q_stride, a.k_stride, a.v_stride, a.o_stride = strides
-    a.q, a.k, a.v, a.decay = _ptr(q), _ptr(k), _ptr(v), _ptr(decay)
-    a.seq_starts, a.src_slots, a.dst_slots = _ptr(seq_starts), _ptr(src_slots), _ptr(dst_slots)
-    a.state, a.output, a.scale, a.err = _ptr(state), _ptr(output), float(scale), _ptr(err)
-    need = _lib.prompt_workspace(a)
+    src = _maybe("src_slots", src_slots, i32, (B,), index)
+    dst = _maybe("dst_slots", dst_slots, i32, (B,), index)
+    if state is None:
+        if src_slots is not None or dst_slots is not None:
+            raise ValueError("state is required with src_slots or dst_slots")
+        state_p, num_slots = None, 0
+    else:
+        state_p, num_slots = _state(state, H, index)
+    a = _lib.KdaLinPromptArgs(
+        B, H, Hk, rows, rows if max_seq is None else min(int(max_seq), rows), num_slots, per_row,
+        int(path), qs, ks, vs, os_, qp, kp, vp, dp, sp, src, dst, state_p, op, float(scale),
+        _maybe("err", err, i32, None, index))
     if workspace is not None:
-        _check("workspace", workspace, torch.uint8)
-        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
-    elif need > 0:
-        # from the pool of the stream that uses it: freed behind its kernels
-        with torch.cuda.device(dev), torch.cuda.stream(stream):
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        a.workspace, a.workspace_bytes = _ptr(workspace), need
-    _run("kda_lin_prompt", a, dev, stream)
+        a.workspace = _want("workspace", workspace, torch.uint8, None, index)
+        a.workspace_bytes = workspace.numel()
+    else:
+        need = _lib.prompt_workspace(a)
+        if need > 0:
+            # from the pool of the stream that uses it: freed behind its kernels
+            with torch.cuda.device(index), torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
+            a.workspace, a.workspace_bytes = workspace.data_ptr(), need
+    _run("kda_lin_prompt", a, index, stream)
 
 
 class KdaLinStep:
@@ -414,24 +448,22 @@ class KdaLinStep:
     contents may change between calls, their storage may not."""
 
     def __init__(self, *, q, k, v, decay, slots, state, output, scale: float, err=None):
-        rows, H, Hk, strides = _lin_rows(q, k, v, output, decay)
-        _check("slots", slots, torch.int32, (rows,))
-        num_slots = _lin_state(state, H)
-        _check("err", err, torch.int32, allow_none=True)
-        self.device = v.device
-        _same_device(v.device, q=q, k=k, output=output, decay=decay, slots=slots, state=state,
-                     err=err)
-        a = _lib.KdaLinStepArgs()
-        a.batch, a.heads, a.qk_heads, a.num_slots = rows, H, Hk, num_slots
-        a.decay_rows = int(decay.dim() == 2)
-        a.q_stride, a.k_stride, a.v_stride, a.o_stride = strides
-        a.q, a.k, a.v, a.decay, a.slots = _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(slots)
-        a.state, a.output, a.scale, a.err = _ptr(state), _ptr(output), float(scale), _ptr(err)
-        self.args = a
+        self.index, rows, H, Hk = index, rows, H, Hk = _lin_shape(q, v)
+        qp, qs = _rows("q", q, rows, Hk * DK, index)
+        kp, ks = _rows("k", k, rows, Hk * DK, index)
+        vp, vs = _rows("v", v, rows, H * DK, index)
+        op, os_ = _rows("output", output, rows, H * DK, index)
+        dp, per_row = _decay(decay, rows, H, index)
+        sp = _want("slots", slots, torch.int32, (rows,), index)
+        state_p, num_slots = _state(state, H, index)
+        self.args = _lib.KdaLinStepArgs(
+            rows, H, Hk, num_slots, per_row, qs, ks, vs, os_, qp, kp, vp, dp, sp, state_p, op,
+            float(scale), _maybe("err", err, torch.int32, None, index))
+        # keep the tensors alive as long as the prepared step
         self._keep = (q, k, v, decay, slots, state, output, err)
 
     def __call__(self, stream: Optional[torch.cuda.Stream] = None) -> None:
-        _run("kda_lin_step", self.args, self.device, stream)
+        _run("kda_lin_step", self.args, self.index, stream)
 
 
 def kda_lin_step(stream: Optional[torch.cuda.Stream] = None, **kw) -> None:
@@ -442,29 +474,28 @@ def kda_lin_step(stream: Optional[torch.cuda.Stream] = None, **kw) -> None:
 # ------------------------------------------------- snapshots of state pages
 
 def _snapshot(entry, state, slots, codes, scales, snaps, err, stream):
-    _check("state", state, torch.float32)
-    if state.dim() != 4 or tuple(state.shape[2:]) != (DK, DK):
+    index = _cuda_index("state", state)
+    if state.dim() != 4:
         raise ValueError("state must be [num_slots, heads, 128, 128]")
-    H = state.shape[1]
-    if not isinstance(codes, torch.Tensor) or codes.dtype not in (torch.int8, torch.uint8):
+    num_slots, H = state.shape[:2]
+    _want("state", state, torch.float32, (num_slots, H, DK, DK), index)
+    if _cuda_index("codes", codes) == index and codes.dtype is torch.int8:
+        bits, width, groups = 8, DK, (DK,)
+    elif codes.dtype is torch.uint8:
+        bits, width, groups = 4, DK // 2, (DK, 4)
+    else:
         raise TypeError("codes must be an int8 (8 bits) or uint8 (4 bits) tensor")
-    bits = 8 if codes.dtype == torch.int8 else 4
-    _check("codes", codes, codes.dtype)
-    if codes.dim() != 4 or tuple(codes.shape[1:]) != (H, DK, DK * bits // 8):
-        raise ValueError(f"codes of {bits} bits must be [num_snaps, {H}, 128, {DK * bits // 8}]")
-    n = codes.shape[0]
-    _check("scales", scales, torch.float32, (n, H, DK) if bits == 8 else (n, H, DK, 4))
-    _check("slots", slots, torch.int32)
-    if slots.dim() != 1:
-        raise ValueError("slots must be [count]")
-    _check("snaps", snaps, torch.int32, tuple(slots.shape))
-    _check("err", err, torch.int32, allow_none=True)
-    _same_device(state.device, codes=codes, scales=scales, slots=slots, snaps=snaps, err=err)
-    a = _lib.KdaSnapshotArgs()
-    a.count, a.heads, a.num_slots, a.num_snaps, a.bits = slots.shape[0], H, state.shape[0], n, bits
-    a.slots, a.snaps, a.state = _ptr(slots), _ptr(snaps), _ptr(state)
-    a.codes, a.scales, a.err = _ptr(codes), _ptr(scales), _ptr(err)
-    _run(entry, a, state.device, stream)
+    n = codes.shape[0] if codes.dim() else 0
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be an int32 tensor [count]")
+    i32, count = torch.int32, slots.shape[0]
+    a = _lib.KdaSnapshotArgs(
+        count, H, num_slots, n, bits, _want("slots", slots, i32, None, index),
+        _want("snaps", snaps, i32, (count,), index), state.data_ptr(),
+        _want("codes", codes, codes.dtype, (n, H, DK, width), index),
+        _want("scales", scales, torch.float32, (n, H) + groups, index),
+        _maybe("err", err, i32, None, index))
+    _run(entry, a, index, stream)
 
 
 def kda_snapshot_save(*, state, slots, codes, scales, snaps, err=None,

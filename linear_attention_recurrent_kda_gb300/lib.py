@@ -178,10 +178,9 @@ def strerror(code: int) -> str:
 
 def call(entry: str, args, stream_handle: int) -> int:
     """Raw call: returns the library's code without raising."""
-    fn = getattr(load(), entry)
-    return int(fn(ctypes.byref(args), ctypes.c_void_p(stream_handle or None)))
+    return getattr(_lib or load(), entry)(args, stream_handle or None)
 
 
 def prompt_workspace(args) -> int:
     """Bytes of workspace that ``kda_lin_prompt`` needs for these sizes."""
-    return int(load().kda_lin_prompt_workspace(ctypes.byref(args)))
+    return (_lib or load()).kda_lin_prompt_workspace(args)

@@ -341,3 +341,65 @@ def test_prompt_recurrent_form_equals_steps_bitwise():
                      output=o, scale=0.5)
         assert torch.equal(o[0].cpu(), out[t])
     assert torch.equal(st[1].cpu(), state[2])
+
+
+# --------------------------------------------------------------------- refusals
+
+def test_refusals_of_the_binding():
+    inp = make([40, 8], 4, 2, slots=3, seed=14)
+    dev = {n: inp[n].cuda() for n in ("q", "k", "v", "decay", "state")}
+    i32 = dict(dtype=torch.int32, device="cuda")
+    base = dict(dev, seq_starts=torch.tensor(inp["starts"], **i32), scale=1.0,
+                output=torch.full((48, 512), 7.0, dtype=bf16, device="cuda"),
+                dst_slots=torch.tensor([1, 2], **i32))
+    wide = torch.zeros(48, 600, dtype=bf16, device="cuda")
+    for kw, error in [
+            (dict(q=dev["q"].float()), TypeError),
+            (dict(q=dev["q"][:, :128 + 64]), ValueError),
+            (dict(k=dev["k"][:47]), ValueError),
+            (dict(k=dev["k"][:, :128]), ValueError),
+            (dict(v=torch.zeros(48, 3 * 128, dtype=bf16, device="cuda")), ValueError),
+            (dict(v=wide.t()[:512].t()), None),                  # a slice of wider rows
+            (dict(v=torch.zeros(48, 516, dtype=bf16, device="cuda")[:, :512]), ValueError),
+            (dict(v=torch.zeros(512, 48, dtype=bf16, device="cuda").t()), ValueError),
+            (dict(v=wide[:, 4:516]), kl.KDA_ERR_ALIGNMENT),
+            (dict(output=dev["v"].cpu()), ValueError),
+            (dict(decay=dev["decay"].double()), TypeError),
+            (dict(decay=dev["decay"][:, :3].contiguous()), ValueError),
+            (dict(decay=dev["decay"].t()), ValueError),
+            (dict(seq_starts=base["seq_starts"].long()), TypeError),
+            (dict(seq_starts=torch.zeros(2, 2, **i32)), ValueError),
+            (dict(dst_slots=torch.tensor([1], **i32)), ValueError),
+            (dict(state=None), ValueError),
+            (dict(state=dev["state"][:, :2].contiguous()), ValueError),
+            (dict(state=dev["state"].half()), TypeError),
+            (dict(path=3), kl.KDA_ERR_PATH),
+            (dict(err=torch.zeros(1, device="cuda")), TypeError)]:
+        if error is None:
+            kda_lin_prompt(**dict(base, **kw))
+            base["output"].fill_(7.0)
+        elif isinstance(error, int):
+            with pytest.raises(kl.KdaError) as e:
+                kda_lin_prompt(**dict(base, **kw))
+            assert e.value.code == error
+        else:
+            with pytest.raises(error):
+                kda_lin_prompt(**dict(base, **kw))
+    torch.cuda.synchronize()
+    assert torch.all(base["output"] == 7.0)
+
+
+def test_workspace_of_the_caller():
+    """The caller's workspace gives the same bits; one too small is refused."""
+    inp = make([1400], 2, 2, slots=3, seed=15)
+    want = launch(inp, dst=[2], max_seq=1400)
+    need = kl.prompt_workspace(kl.KdaLinPromptArgs(
+        seqs=1, heads=2, qk_heads=2, tokens=1400, max_seq=1400, q_stride=256, k_stride=256,
+        v_stride=256, o_stride=256))
+    assert need > 0
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")      # (NaN bits)
+    got = launch(inp, dst=[2], max_seq=1400, workspace=ws)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1][2], got[1][2])
+    with pytest.raises(kl.KdaError) as e:
+        launch(inp, dst=[2], max_seq=1400, workspace=ws[:-1].clone())
+    assert e.value.code == kl.KDA_ERR_WORKSPACE

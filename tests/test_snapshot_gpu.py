@@ -236,3 +236,27 @@ def test_prefix_cache_run(bits, path):
     end = state.cpu()
     for r in range(2):
         assert torch.all((end[3 + r].double() - S[r]).abs() <= 5 * linref.U32 * M[r])
+
+
+def test_refusals_of_the_binding():
+    state = torch.zeros(4, 2, D, D, device="cuda")
+    codes, scales = pools(3, 2, 8)
+    base = dict(state=state, slots=i32([1, 2]), codes=codes, scales=scales, snaps=i32([1, 2]))
+    for kw, error in [
+            (dict(state=state.double()), TypeError),
+            (dict(state=state[:, :, :64].contiguous()), ValueError),
+            (dict(state=state.transpose(2, 3)), ValueError),
+            (dict(codes=codes.short()), TypeError),
+            (dict(codes=codes[:, :1].contiguous()), ValueError),
+            (dict(codes=codes.view(torch.uint8)), ValueError),
+            (dict(codes=codes[:2].contiguous()), ValueError),
+            (dict(scales=scales[:, :, :64].contiguous()), ValueError),
+            (dict(slots=i32([1])), ValueError),
+            (dict(snaps=base["snaps"].long()), TypeError),
+            (dict(slots=i32([[1, 2]])), ValueError),
+            (dict(scales=scales.cpu()), ValueError)]:
+        for f in (kda_snapshot_save, kda_snapshot_load):
+            with pytest.raises(error):
+                f(**dict(base, **kw))
+    torch.cuda.synchronize()
+    assert torch.all(codes == 85) and torch.all(state == 0)
