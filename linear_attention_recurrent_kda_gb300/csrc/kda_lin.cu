@@ -203,7 +203,7 @@ struct Plan {
 
 constexpr int kRecurrentMost = 16;
 constexpr int kShares = 152;            // SMs that the work is shared among
-constexpr int kShortestSegment = 512;
+constexpr int kShortestSegment = 256;
 
 // The sizes' part of the checks, and the plan.
 static int plan_prompt(const kda_lin_prompt_args *a, Plan *plan) {
@@ -216,10 +216,12 @@ static int plan_prompt(const kda_lin_prompt_args *a, Plan *plan) {
   plan->seg_len = longest > 0 ? static_cast<int>(longest) : 1;
   plan->workspace = 0;
   if (plan->chunked) {
-    // an SM's share of all tokens x heads, in whole chunks
-    int64_t len = (static_cast<int64_t>(a->tokens) * a->heads / kShares + 127) / 128 * 128;
+    // A sequence much longer than an SM's share of all tokens x heads would keep
+    // its SM busy alone: it is split, into segments of a quarter share.
+    const int64_t share = static_cast<int64_t>(a->tokens) * a->heads / kShares;
+    int64_t len = (share / 4 + 127) / 128 * 128;
     if (len < kShortestSegment) len = kShortestSegment;
-    if (longest > len) {
+    if (longest > share * 8 / 5 && longest > 2 * len) {
       plan->seg_len = static_cast<int>(len);
       plan->segs = static_cast<int>((longest + len - 1) / len);
       if (static_cast<int64_t>(a->seqs) * plan->segs * a->heads > 0x7fffffffll)

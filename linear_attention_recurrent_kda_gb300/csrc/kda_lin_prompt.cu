@@ -28,7 +28,7 @@
 // rounded to BF16, and the FP32 sum keeps their errors at that size.
 //
 // Roles (768 threads, 24 warps): TMA loads and stores (warp 0), MMA issue for the page
-// (U, Q S^T; warp 1) and for the outputs (A, P V; warp 3), the work and its decay
+// (U; warp 1) and for the outputs (A, Q S^T, P V; warp 3), the work and its decay
 // tables (warp 2); five warpgroups: P and O (4-11, 64 columns a
 // warp), K'' (12-19, 16 keys a warp), the page (20-23).  K'' is built transposed (lanes = keys) by transposing shared-memory
 // matrix loads straight into TMEM, as the A operand: no shared memory is
@@ -59,15 +59,6 @@ constexpr float kMild = -128.0f;                 // a chunk's, for the one-facto
 
 constexpr uint32_t kColA = 0, kColO = 128, kColU = 256, kColK = 384, kColsK = 48;
 
-struct Table {
-  float f[kChunk];     // 2^(sum of the tokens behind, in the 32-token block)
-  float x[kChunk];     // mild: 2^(ref - b); else bl, prefix sums in the block
-  float total[4];      // the blocks' logarithms
-  float sum;           // the chunk's
-  float ref;           // mild: r, else 0
-  uint32_t mild, pad;
-};
-
 // One chunk of the CTA's work, as the table warp hands it to the other roles.
 struct Info {
   int rows;            // tokens; 0: a unit without tokens, -1: no more
@@ -77,23 +68,55 @@ struct Info {
   float *to, *decay;   // last: where the page, and the unit's logarithm, go (or NULL)
 };
 
+// The chunk with its factors, for the roles that compute.
+struct Table {
+  float f[kChunk];     // 2^(sum of the tokens behind, in the 32-token block)
+  float x[kChunk];     // mild: 2^(ref - b); else bl, prefix sums in the block
+  float total[4];      // the blocks' logarithms
+  float sum;           // the chunk's
+  float ref;           // mild: r, else 0
+  uint32_t mild, pad;
+  Info info;
+};
+static_assert(sizeof(Table) % 16 == 0, "vector loads");
+
+// The chunk for the roles that move data and issue.
+struct Move {
+  int rows, row, head;
+};
+
 constexpr int kInfos = 4;
+constexpr int kList = 16;      // units of a CTA that can be put in order
 
 struct Ctrl {
   Table tab[2];
-  Info info[kInfos];
-  uint64_t info_full[kInfos], info_empty[kInfos];
+  Move move[kInfos];
+  uint64_t move_full[kInfos], move_empty[kInfos];
   uint64_t full_q[2], full_k[2], full_v[2];      // TMA landed
   uint64_t empty_k[2], empty_v[2];
   uint64_t st_full[2];                           // O staged in Q's tile (or written)
   uint64_t tab_full[2], tab_empty[2];
-  uint64_t kq_full[2], kq_empty[2];              // K'' quarters in TMEM
-  uint64_t a_full, p_full, qs_full, o_full, o_empty, u_full, u_empty, s_full;
+  uint64_t v_ok[2];                              // V there, zeros behind the end
+  uint64_t kq_full[4], kq_empty[4];              // K'' quarters in TMEM
+  uint64_t u_full[2], u_empty[2];
+  uint64_t a_full, p_full, qs_full, o_full, o_empty, s_full;
+  uint32_t list[kList];                          // the CTA's units, where sorted
   uint32_t tmem, abort;
 };
 
 constexpr int kSmem = 7 * kTile + sizeof(Ctrl);
 static_assert(kSmem <= 232448, "shared memory of one CTA");
+
+// Without outputs A's and O's columns are free: the update has two accumulators
+// and K'' four buffers.
+template <bool kOut>
+struct Cols {
+  static constexpr uint32_t kU = kOut ? 1 : 2, kKq = kOut ? 2 : 4;
+  __device__ static uint32_t u(uint32_t n) { return kOut || (n & 1) == 0 ? kColU : kColA; }
+  __device__ static uint32_t kq(uint32_t b) {
+    return b < 2 ? kColK + b * kColsK : kColO + (b - 2) * kColsK;
+  }
+};
 
 // ------------------------------------------------------------------- tcgen05
 
@@ -333,19 +356,65 @@ struct Unit {
   int src, dst;
 };
 
+// A unit's segment: whether it has work in this kernel, and which rows.
+template <bool kOut>
+__device__ __forceinline__ bool segment_of(const PromptParams &p, const Seq &s, int seg, int *segs,
+                                           int *n) {
+  *segs = s.len > p.seg_len ? (s.len + p.seg_len - 1) / p.seg_len : 1;
+  const int left = s.len - seg * p.seg_len;
+  *n = left < p.seg_len ? left : p.seg_len;
+  return seg < (kOut ? *segs : *segs - 1);
+}
+
+// Puts this CTA's units in order: all units by length, the longest first, dealt
+// to the CTAs forth and back, so that each gets long and short ones (256 ragged
+// sequences: 12% less time than every grid-th unit).  Units of a sequence's
+// segment follow one another (heads).  One thread a segment ranks it by counting
+// the longer ones; `keys` is scratch.  All threads call it.
+template <bool kOut>
+__device__ __forceinline__ void order_units(const PromptParams &p, int *keys, uint32_t *list) {
+  const int pairs = p.seqs * p.segs, i = threadIdx.x;
+  int key = -1;
+  if (i < pairs) {
+    Seq s;
+    int segs, n;
+    if (!resolve_seq(p, i / p.segs, &s) && segment_of<kOut>(p, s, i % p.segs, &segs, &n)) key = n;
+    keys[i] = key;
+  }
+  __syncthreads();
+  if (i < pairs) {
+    uint32_t rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < pairs; ++j) rank += keys[j] > key || (keys[j] == key && j < i);
+    const uint32_t lo = rank * p.heads, units = static_cast<uint32_t>(pairs) * p.heads;
+    for (uint32_t k = 0, base = 0; k < kList && base < units; ++k, base += gridDim.x) {
+      const uint32_t r = base + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      if (r - lo < static_cast<uint32_t>(p.heads)) list[k] = i * p.heads + (r - lo);
+    }
+  }
+  fence_proxy_async_smem();
+}
+
 // Walks this CTA's units.
 template <bool kOut>
 struct Walk {
   const PromptParams &p;
-  int64_t u;
+  const uint32_t *list;    // NULL: every grid-th unit
+  uint32_t k;
   Unit unit;
 
-  __device__ explicit Walk(const PromptParams &p_) : p(p_), u(blockIdx.x) {}
+  __device__ Walk(const PromptParams &p_, const uint32_t *list_) : p(p_), list(list_), k(0) {}
   // The next unit that has work for this kernel.
   __device__ bool next(bool report) {
-    const int64_t units = static_cast<int64_t>(p.seqs) * p.segs * p.heads;
-    for (; u < units; u += gridDim.x) {
-      const uint32_t at = static_cast<uint32_t>(u);      // units < 2^31
+    const int64_t units = static_cast<int64_t>(p.seqs) * p.segs * p.heads;   // < 2^31
+    while (true) {
+      const int64_t place = static_cast<int64_t>(k) * gridDim.x +
+                            (list && (k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      // (forth and back: the last round may pass over this CTA)
+      if (static_cast<int64_t>(k) * gridDim.x >= units) return false;
+      const uint32_t at = list ? list[k % kList] : static_cast<uint32_t>(place);
+      ++k;
+      if (place >= units) continue;
       const uint32_t rest = at / p.heads;
       unit.h = at - rest * p.heads;
       unit.b = rest / p.segs;
@@ -355,17 +424,12 @@ struct Walk {
         if (report && p.err) atomicOr(p.err, bad);
         continue;
       }
-      unit.segs = s.len > p.seg_len ? (s.len + p.seg_len - 1) / p.seg_len : 1;
-      if (unit.seg >= (kOut ? unit.segs : unit.segs - 1)) continue;
+      if (!segment_of<kOut>(p, s, unit.seg, &unit.segs, &unit.n)) continue;
       unit.row = s.start + unit.seg * p.seg_len;
-      const int left = s.len - unit.seg * p.seg_len;
-      unit.n = left < p.seg_len ? left : p.seg_len;
       unit.src = s.src;
       unit.dst = s.dst;
-      u += gridDim.x;
       return true;
     }
-    return false;
   }
 };
 
@@ -382,15 +446,20 @@ __device__ __forceinline__ int64_t ws_index(const PromptParams &p, const Unit &u
 }
 
 // The next chunk of a role (a whole warp; m counts them).  False: no more.
-__device__ __forceinline__ bool next_chunk(Ctrl &c, uint32_t &m, Info &info, int lane) {
+__device__ __forceinline__ bool next_move(Ctrl &c, uint32_t &m, Move &move, int lane) {
   const uint32_t at = m % kInfos;
-  if (!__all_sync(0xffffffffu, wait_phase(&c.info_full[at], (m / kInfos) & 1, &c.abort)))
+  if (!__all_sync(0xffffffffu, wait_phase(&c.move_full[at], (m / kInfos) & 1, &c.abort)))
     return false;
-  info = c.info[at];
+  move = c.move[at];
   __syncwarp();
-  if (lane == 0) mbar_arrive(&c.info_empty[at]);
+  if (lane == 0) mbar_arrive(&c.move_empty[at]);
   ++m;
-  return info.rows >= 0;
+  return move.rows >= 0;
+}
+// The same with its factors: the table of chunk m, whose user gives it back.
+__device__ __forceinline__ bool next_table(Ctrl &c, uint32_t m) {
+  return __all_sync(0xffffffffu, wait_phase(&c.tab_full[m & 1], (m >> 1) & 1, &c.abort)) &&
+         c.tab[m & 1].info.rows >= 0;
 }
 
 // -------------------------------------------------------------------- kernel
@@ -407,6 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *sq = smem, *sk = smem + 2 * kTile, *sv = smem + 4 * kTile, *ss = smem + 6 * kTile;
   Ctrl &c = *reinterpret_cast<Ctrl *>(smem + 7 * kTile);
+  using C = Cols<kOut>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w4 = warp & 3;                           // TMEM lanes 32 w4 .. of this warp
   volatile uint32_t *abort_flag = &c.abort;
@@ -420,33 +490,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     c.abort = 0;
     for (int i = 0; i < kInfos; ++i) {
-      mbar_init(&c.info_full[i], 1);
-      mbar_init(&c.info_empty[i], kOut ? 23 : 14);
+      mbar_init(&c.move_full[i], 1);
+      mbar_init(&c.move_empty[i], kOut ? 3 : 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.full_q[i], 1);
       mbar_init(&c.full_k[i], 1);
       mbar_init(&c.full_v[i], 1);
       mbar_init(&c.st_full[i], 8);
-      mbar_init(&c.empty_k[i], kOut ? 9 : 8);
+      mbar_init(&c.v_ok[i], 4);
+      mbar_init(&c.empty_k[i], kOut ? 9 : 16);
       mbar_init(&c.empty_v[i], kOut ? 2 : 1);
       mbar_init(&c.tab_full[i], 1);
-      mbar_init(&c.tab_empty[i], kOut ? 20 : 12);
-      mbar_init(&c.kq_full[i], 8);
-      mbar_init(&c.kq_empty[i], 1);
+      mbar_init(&c.tab_empty[i], 20);
+      mbar_init(&c.u_full[i], 1);
+      mbar_init(&c.u_empty[i], 4);
     }
     mbar_init(&c.a_full, 1);
     mbar_init(&c.p_full, 8);
     mbar_init(&c.qs_full, 1);
     mbar_init(&c.o_full, 1);
     mbar_init(&c.o_empty, 8);
-    mbar_init(&c.u_full, 1);
-    mbar_init(&c.u_empty, 4);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&c.kq_full[i], 8);
+      mbar_init(&c.kq_empty[i], 1);
+    }
     mbar_init(&c.s_full, 4);
     // a tile base that breaks the swizzle's 1024 bytes would give wrong data
     if (smem_addr(smem) & 1023u) c.abort = 1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  const int64_t all_units = static_cast<int64_t>(p.seqs) * p.segs * p.heads;
+  const bool sorted = all_units > gridDim.x && p.seqs * static_cast<int64_t>(p.segs) <= kThreads &&
+                      all_units <= static_cast<int64_t>(gridDim.x) * kList;
+  if (sorted) order_units<kOut>(p, reinterpret_cast<int *>(sq), c.list);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -464,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_dec<56>();
     if (warp == 0) {
       // ------------------------------------------------- TMA loads and stores
-      Info info;
+      Move info;
       uint32_t m = 0, n = 0, stored = 0;
       int row1 = 0, row2 = 0, head1 = 0, head2 = 0, rows1 = 0, rows2 = 0;  // the last two chunks
       // the stored-th chunk's outputs leave Q's tile, which is then free
@@ -484,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       bool ok = true;
-      while (next_chunk(c, m, info, lane)) {
+      while (next_move(c, m, info, lane)) {
         if (info.rows == 0) continue;
         ok = false;
         const int buf = n & 1, boxes = (info.rows + 31) >> 5;
@@ -518,66 +595,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (lane == 0) bulk_wait_all();
     } else if (warp == 1) {
-      // ------------------------------------------- MMA issue: U and Q S^T
+      // ------------------------------------------------------- MMA issue: U
       // The warp walks and waits as one; one elected thread issues.  Descriptors
       // are sums of a base and constants (addresses count 16 bytes).
       uint32_t quarter = 0;
       const bool leader = elect_one();
-      const uint64_t q0 = desc_k_major(smem_addr(sq)), v0 = desc_mn_major(smem_addr(sv)),
-                     s0 = desc_mn_major(smem_addr(ss));
-      Info info;
+      const uint64_t v0 = desc_mn_major(smem_addr(sv));
+      Move info;
       uint32_t m = 0, n = 0;
-      while (next_chunk(c, m, info, lane)) {
+      while (next_move(c, m, info, lane)) {
         if (info.rows == 0) continue;
         const int buf = n & 1, quarters = (info.rows + 31) >> 5;
         const uint32_t one = n & 1, two = (n >> 1) & 1;
         // U = K''^T V, quarter by quarter of 32 tokens
         // (the first K'' also says that V is there)
-        if (n > 0) KDA_WAIT_WARP(c.u_empty, one ^ 1);
+        const uint32_t ub = n % C::kU, ur = n / C::kU & 1;
+        KDA_WAIT_WARP(c.u_empty[ub], ur ^ 1);
         int i = 0;
         for (; i < quarters; ++i, ++quarter) {
-          const int kb = quarter & 1;
-          KDA_WAIT_WARP(c.kq_full[kb], (quarter >> 1) & 1);
+          const uint32_t kb = quarter % C::kKq;
+          KDA_WAIT_WARP(c.kq_full[kb], quarter / C::kKq & 1);
           tc_fence_after();
           if (leader) {
-            const uint32_t a = tmem + kColK + kb * kColsK;
+            const uint32_t a = tmem + C::kq(kb), u = tmem + C::u(n);
             const uint64_t v = v0 + buf * (kTile >> 4) + i * (4096 >> 4);
 #pragma unroll
             for (int part = 0; part < 3; ++part)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                tc_mma_ts(tmem + kColU, a + part * 16 + j * 8, v + j * (2048 >> 4), kIdescBmn,
+                tc_mma_ts(u, a + part * 16 + j * 8, v + j * (2048 >> 4), kIdescBmn,
                           i + part + j > 0);
             tc_commit(&c.kq_empty[kb]);
             if (i == quarters - 1) {
-              tc_commit(&c.u_full);
+              tc_commit(&c.u_full[ub]);
               tc_commit(&c.empty_v[buf]);
             }
           }
           __syncwarp();
         }
         if (i < quarters) break;
-        if (kOut) {
-          // O = Q S^T
-          KDA_WAIT_WARP(c.s_full, one);
-          KDA_WAIT_WARP(c.full_q[buf], two);
-          if (n > 0) KDA_WAIT_WARP(c.o_empty, one ^ 1);
-          tc_fence_after();
-          if (leader) {
-            const uint64_t q = q0 + buf * (kTile >> 4);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              tc_mma_ss(tmem + kColO, q + (((j >> 2) * kHalf + (j & 3) * 32) >> 4),
-                        s0 + j * (2048 >> 4), kIdescBmn, j > 0);
-            tc_commit(&c.qs_full);
-          }
-          __syncwarp();
-        }
         ++n;
       }
     } else if (warp == 2) {
       // -------------------------------------- the work, and its decay tables
-      Walk<kOut> it(p);
+      Walk<kOut> it(p, sorted ? c.list : nullptr);
       Info next;
       int t = 0;                                           // tokens of the unit handed out
       bool unit = false;
@@ -585,7 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto look = [&](float (&g)[4]) {
         if (!unit) {
           if (!it.next(lane == 0)) {
-            next.rows = -1;
+            next = Info{-1};
+            g[0] = g[1] = g[2] = g[3] = 0.0f;
             return;
           }
           const Unit &u = it.unit;
@@ -622,25 +684,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       float ahead[4] = {};
       look(ahead);
-      uint32_t m = 0, n = 0;
+      uint32_t m = 0;
       while (true) {
-        KDA_WAIT_WARP(c.info_empty[m % kInfos], ((m / kInfos) & 1) ^ 1);
+        KDA_WAIT_WARP(c.move_empty[m % kInfos], ((m / kInfos) & 1) ^ 1);
         if (lane == 0) {
-          c.info[m % kInfos] = next;
-          mbar_arrive(&c.info_full[m % kInfos]);
+          c.move[m % kInfos] = Move{next.rows, next.row, next.head};
+          mbar_arrive(&c.move_full[m % kInfos]);
         }
         __syncwarp();
+        const Info info = next;
+        const int rows = info.rows, buf = m & 1;
+        const uint32_t round = (m >> 1) & 1;
         ++m;
-        const int rows = next.rows, buf = n & 1;
-        if (rows < 0) break;
         float g[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           g[j] = ahead[j] * kLog2e;
           if (g[j] < kLowest) g[j] = kLowest;
         }
-        look(ahead);
-        if (rows == 0) continue;
+        if (rows >= 0) look(ahead);
         const float sum = (g[0] + g[1]) + (g[2] + g[3]);
         // sums of the lanes before and behind this one in its block of 8 lanes
         float before = sum, behind = sum;
@@ -678,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         f.y = exp2_approx(s1);
         f.z = exp2_approx(s2);
         f.w = exp2_approx(s3);
-        KDA_WAIT_WARP(c.tab_empty[buf], ((n >> 1) & 1) ^ 1);
+        KDA_WAIT_WARP(c.tab_empty[buf], round ^ 1);
         Table &tab = c.tab[buf];
         reinterpret_cast<float4 *>(tab.x)[lane] = x;
         reinterpret_cast<float4 *>(tab.f)[lane] = f;
@@ -687,19 +749,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           tab.sum = all;
           tab.ref = ref;
           tab.mild = mild;
+          tab.info = info;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&c.tab_full[buf]);
-        ++n;
+        if (rows < 0) break;
       }
     } else if (kOut && warp == 3) {
-      // ------------------------------------------- MMA issue: A and P V
+      // ----------------------------------------- MMA issue: A, Q S^T and P V
       const bool leader = elect_one();
       const uint64_t q0 = desc_k_major(smem_addr(sq)), k0 = desc_k_major(smem_addr(sk)),
-                     v0 = desc_mn_major(smem_addr(sv));
-      Info info;
+                     v0 = desc_mn_major(smem_addr(sv)), s0 = desc_mn_major(smem_addr(ss));
+      Move info;
       uint32_t m = 0, n = 0;
-      while (next_chunk(c, m, info, lane)) {
+      while (next_move(c, m, info, lane)) {
         if (info.rows == 0) continue;
         const int buf = n & 1, quarters = (info.rows + 31) >> 5;
         const uint32_t one = n & 1, two = (n >> 1) & 1;
@@ -718,8 +781,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_commit(&c.empty_k[buf]);
         }
         __syncwarp();
+        // O = Q S^T
+        KDA_WAIT_WARP(c.s_full, one);
+        KDA_WAIT_WARP(c.o_empty, one ^ 1);
+        tc_fence_after();
+        if (leader) {
+          const uint64_t q = q0 + buf * (kTile >> 4);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            tc_mma_ss(tmem + kColO, q + (((j >> 2) * kHalf + (j & 3) * 32) >> 4),
+                      s0 + j * (2048 >> 4), kIdescBmn, j > 0);
+          tc_commit(&c.qs_full);
+        }
+        __syncwarp();
         // O += P V
-        KDA_WAIT_WARP(c.qs_full, one);                     // (and V is there)
+        KDA_WAIT_WARP(c.v_ok[buf], two);
         KDA_WAIT_WARP(c.p_full, one);
         tc_fence_after();
         if (leader) {
@@ -736,25 +812,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp < 12) {
+  } else if (kOut && warp < 12) {
     regs_dec<64>();
     // ------------------------------------------------------------------ P, O
-    if (kOut) {
-      Info info;
+    {
       uint32_t m = 0, n = 0;
       const int i = 32 * w4 + lane;                       // row of the chunk
       const int side = (warp - 4) >> 2;                   // columns 64 side .. of P and O
       const uint32_t lanes = static_cast<uint32_t>(32 * w4) << 16;
       const uint32_t col_a = tmem + lanes + kColA + 64 * side,
                      col_o = tmem + lanes + kColO + 64 * side;
-      while (next_chunk(c, m, info, lane)) {
-        if (info.rows == 0) continue;
-        const int buf = n & 1, rows = info.rows;
+      for (; next_table(c, m); ++m) {
+        const Table &tab = c.tab[m & 1];
+        const int rows = tab.info.rows, row = tab.info.row, head = tab.info.head;
+        if (rows == 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c.tab_empty[m & 1]);
+          continue;
+        }
+        const int buf = n & 1;
         const uint32_t one = n & 1;
-        const Table &tab = c.tab[buf];
         uint32_t a[32], r[16];
         float of;                                         // O's factor
-        KDA_WAIT_WARP(c.tab_full[buf], (n >> 1) & 1);
         KDA_WAIT_WARP(c.a_full, one);
         tc_fence_after();
         const float xi = tab.x[i];
@@ -765,20 +844,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int z = 0; z < 2; ++z) {
             const int J = 2 * side + z;                   // block of 32 columns
-            const ulonglong2 *f = reinterpret_cast<const ulonglong2 *>(tab.x + 32 * J);
-            tc_ld(col_a + 32 * z, a);
-            tc_wait_ld(a);
+            if (J <= w4) {
+              const ulonglong2 *f = reinterpret_cast<const ulonglong2 *>(tab.x + 32 * J);
+              tc_ld(col_a + 32 * z, a);
+              tc_wait_ld(a);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const ulonglong2 ff = f[j];
-              r[2 * j] = pack2(mul2(raw_pair(a[4 * j], a[4 * j + 1]), ff.x));
-              r[2 * j + 1] = pack2(mul2(raw_pair(a[4 * j + 2], a[4 * j + 3]), ff.y));
-            }
-            if (J >= w4) {
-              const int to = J == w4 ? lane : -1;         // the last column to keep
+              for (int j = 0; j < 8; ++j) {
+                const ulonglong2 ff = f[j];
+                r[2 * j] = pack2(mul2(raw_pair(a[4 * j], a[4 * j + 1]), ff.x));
+                r[2 * j + 1] = pack2(mul2(raw_pair(a[4 * j + 2], a[4 * j + 3]), ff.y));
+              }
+              if (J == w4) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                r[j] &= 2 * j + 1 <= to ? 0xFFFFFFFFu : 2 * j <= to ? 0xFFFFu : 0u;
+                for (int j = 0; j < 16; ++j)
+                  r[j] &= 2 * j + 1 <= lane ? 0xFFFFFFFFu : 2 * j <= lane ? 0xFFFFu : 0u;
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) r[j] = 0;
             }
             tc_st16(col_a + 16 * z, r);
           }
@@ -802,14 +885,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&c.p_full);
-          mbar_arrive(&c.tab_empty[buf]);
+          mbar_arrive(&c.tab_empty[m & 1]);
         }
         // the chunk's outputs: through Q's tile, or by rows where it is not full
         KDA_WAIT_WARP(c.o_full, one);
         tc_fence_after();
         const bool full = rows == kChunk;
         const uint32_t tile = smem_addr(sq + buf * kTile + side * kHalf) + i * 128;
-        __nv_bfloat16 *to = p.output + (info.row + i) * p.o_stride + info.head * kDim + 64 * side;
+        __nv_bfloat16 *to = p.output + static_cast<int64_t>(row + i) * p.o_stride + head * kDim + 64 * side;
         const f32x2 of2 = pair(of, of);
 #pragma unroll 1
         for (int j = 0; j < 2; ++j) {
@@ -845,37 +928,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 20) {
     regs_dec<56>();
     // ------------------------------------------------------------------- K''
-    Info info;
-    uint32_t m = 0, n = 0, quarter = 0;
-    const int half = (warp - 12) >> 2;                     // which 16 of the 32 keys
+    // Two warpgroups, 16 of the 32 keys each (without outputs: four, of which
+    // two take the odd quarters).
+    constexpr int kStep = kOut ? 1 : 2;
+    const int half = (warp >> 2) & 1, first = kOut || warp < 12 ? 0 : 1;
+    uint32_t m = 0, n = 0, done = 0;                       // done: quarters of the chunks before
     // this lane's row of the matrices that it addresses (token, 16-byte group)
     const uint32_t at_k =
         smem_addr(sk) + tile_at(8 * (lane >> 4) + (lane & 7), 4 * w4 + 2 * half + ((lane >> 3) & 1));
-    const uint32_t at_t = tmem + (static_cast<uint32_t>(32 * w4 + 16 * half) << 16) + kColK;
-    while (next_chunk(c, m, info, lane)) {
-      if (info.rows == 0) continue;
-      const int buf = n & 1, rows = info.rows, quarters = (rows + 31) >> 5;
-      const uint32_t two = (n >> 1) & 1;
-      const Table &tab = c.tab[buf];
-      if (half == 0) {
-        KDA_WAIT_WARP(c.full_v[buf], two);
-        if (rows < 32 * quarters) {
-          // rows behind the sequence's end become zeros: they are other rows of
-          // the tensor (or stale), and 0 * NaN is not 0
-          const int at = threadIdx.x & 127;
-#pragma unroll 1
-          for (int x = at; x < (32 * quarters - rows) * 16; x += 128)
-            *reinterpret_cast<uint4 *>(sv + buf * kTile + tile_at(rows + (x >> 4), x & 15)) =
-                make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-        }
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * w4 + 16 * half) << 16);
+    for (; next_table(c, m); ++m) {
+      const Table &tab = c.tab[m & 1];
+      const int rows = tab.info.rows, quarters = (rows + 31) >> 5;
+      if (rows == 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.tab_empty[m & 1]);
+        continue;
       }
-      KDA_WAIT_WARP(c.tab_full[buf], two);
+      const int buf = n & 1;
+      const uint32_t two = (n >> 1) & 1;
       KDA_WAIT_WARP(c.full_k[buf], two);
-      int i = 0;
+      int i = first;
 #pragma unroll 1
-      for (; i < quarters; ++i, ++quarter) {
-        const int kb = quarter & 1;
+      for (; i < quarters; i += kStep) {
+        const uint32_t quarter = done + i, kb = quarter % C::kKq;
         // factors of the 8 tokens a lane sees: 8 j + 2 (lane % 4) + {0, 1}
         float sum = 0.0f;
         for (int m = i + 1; m < 4; ++m) sum += tab.total[m];
@@ -911,11 +987,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           mid[y] = upper_halves(v1);
           lo[y] = upper_halves(v2);
         }
-        KDA_WAIT_WARP(c.kq_empty[kb], ((quarter >> 1) & 1) ^ 1);
+        KDA_WAIT_WARP(c.kq_empty[kb], (quarter / C::kKq & 1) ^ 1);
         tc_fence_after();
-        tc_st_16x128(at_t + kb * kColsK, hi);
-        tc_st_16x128(at_t + kb * kColsK + 16, mid);
-        tc_st_16x128(at_t + kb * kColsK + 32, lo);
+        const uint32_t to = lanes + C::kq(kb);
+        tc_st_16x128(to, hi);
+        tc_st_16x128(to + 16, mid);
+        tc_st_16x128(to + 32, lo);
+        if (i == 0 && half == 0) {
+          // the first K'' also says that V is there
+          KDA_WAIT_WARP(c.full_v[buf], two);
+          if (rows < 32 * quarters) {
+            // rows behind the sequence's end become zeros: they are other rows of
+            // the tensor (or stale), and 0 * NaN is not 0
+            const int at = threadIdx.x & 127;
+#pragma unroll 1
+            for (int x = at; x < (32 * quarters - rows) * 16; x += 128)
+              *reinterpret_cast<uint4 *>(sv + buf * kTile + tile_at(rows + (x >> 4), x & 15)) =
+                  make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c.v_ok[buf]);
+        }
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -925,21 +1018,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&c.empty_k[buf]);
-        mbar_arrive(&c.tab_empty[buf]);
+        mbar_arrive(&c.tab_empty[m & 1]);
       }
+      done += quarters;
       ++n;
     }
     __syncwarp();
   } else {
     regs_inc<184>();
     // -------------------------------------------------------------- the page
-    Info info;
     uint32_t m = 0, n = 0;
     const int d = 32 * w4 + lane;                          // key
-    const uint32_t col_u = tmem + (static_cast<uint32_t>(32 * w4) << 16) + kColU;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * w4) << 16);
     f32x2 s[kDim / 2];                                     // value rows 2 i, 2 i + 1
     float all = 0.0f;                                      // the unit's decay (logarithm)
-    while (next_chunk(c, m, info, lane)) {
+    for (; next_table(c, m); ++m) {
+      const Table &tab = c.tab[m & 1];
+      const Info info = tab.info;
+      const float total = tab.sum, ref = tab.ref;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.tab_empty[m & 1]);
       if (info.first) {
         all = 0.0f;
         if (info.from) {
@@ -952,13 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (info.rows > 0) {
-        const int buf = n & 1;
         const uint32_t one = n & 1;
-        const Table &tab = c.tab[buf];
-        KDA_WAIT_WARP(c.tab_full[buf], (n >> 1) & 1);
-        const float total = tab.sum, ref = tab.ref;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.tab_empty[buf]);
         if (kOut) {
           // the page's copy for Q S^T; the product before has read the last one
           if (n > 0) KDA_WAIT_WARP(c.qs_full, one ^ 1);
@@ -976,7 +1068,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float keep = exp2_approx(total);
         const f32x2 keep2 = pair(keep, keep);
         all += total;
-        KDA_WAIT_WARP(c.u_full, one);
+        const uint32_t ub = n % C::kU, col_u = lanes + C::u(n);
+        KDA_WAIT_WARP(c.u_full[ub], n / C::kU & 1);
         tc_fence_after();
         uint32_t u[32];
 #pragma unroll
@@ -989,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c.u_empty);
+        if (lane == 0) mbar_arrive(&c.u_empty[ub]);
         ++n;
       }
       if (info.last && info.to) {
@@ -1024,31 +1117,47 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The pages that the segments of split sequences start from, in place of their
 // contributions: S_0 = the sequence's first page, S_(g+1) = 2^decay_g S_g + U_g.
-// Each thread walks 4 elements of a page over the segments.
+// Each thread walks 4 elements of a page over the segments, eight segments'
+// loads in flight (one at a time, 19 segments of 32 heads took 227 us).
 __global__ void __launch_bounds__(256) segment_kernel(const __grid_constant__ PromptParams p) {
-  constexpr int kBlocks = kPage / (4 * 256);
+  constexpr int kBlocks = kPage / (4 * 256), kBatch = 8;
   const int part = blockIdx.x % kBlocks, item = blockIdx.x / kBlocks;
   const int b = item / p.heads, h = item % p.heads;
   Seq seq;
   if (resolve_seq(p, b, &seq) || seq.len <= p.seg_len) return;
-  const int segs = (seq.len + p.seg_len - 1) / p.seg_len;
+  const int last = (seq.len + p.seg_len - 1) / p.seg_len - 1;
   const int at = part * 256 + threadIdx.x;
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (seq.src) s = reinterpret_cast<const float4 *>(page_of(p.state, seq.src, p.heads, h))[at];
-  for (int g = 0; g < segs; ++g) {
-    const int64_t page = ws_index(p, seq.start + g * p.seg_len, g == segs - 1, h);
-    float4 *ws = reinterpret_cast<float4 *>(p.ws_state + page * kPage) + at;
-    float4 u = s;
-    if (g < segs - 1) u = *ws;
-    *ws = s;
-    if (g < segs - 1) {
-      const float keep = exp2_approx(p.ws_decay[page]);
-      s.x = __fmaf_rn(s.x, keep, u.x);
-      s.y = __fmaf_rn(s.y, keep, u.y);
-      s.z = __fmaf_rn(s.z, keep, u.z);
-      s.w = __fmaf_rn(s.w, keep, u.w);
-    }
+  // (full segments' pages are heads apart)
+  const int64_t first = ws_index(p, seq.start, false, h);
+  float4 *ws = reinterpret_cast<float4 *>(p.ws_state + first * kPage) + at;
+  const float *decay = p.ws_decay + first;
+  const int64_t step = static_cast<int64_t>(p.heads) * (kPage / 4);
+  for (int g = 0; g < last; g += kBatch) {
+    float4 u[kBatch];
+    float keep[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (g + i < last) {
+        u[i] = ws[i * step];
+        keep[i] = decay[i * p.heads];
+      }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (g + i < last) {
+        ws[i * step] = s;
+        const float f = exp2_approx(keep[i]);
+        s.x = __fmaf_rn(s.x, f, u[i].x);
+        s.y = __fmaf_rn(s.y, f, u[i].y);
+        s.z = __fmaf_rn(s.z, f, u[i].z);
+        s.w = __fmaf_rn(s.w, f, u[i].w);
+      }
+    ws += kBatch * step;
+    decay += kBatch * p.heads;
   }
+  const int64_t end = ws_index(p, seq.start + last * p.seg_len, true, h);
+  reinterpret_cast<float4 *>(p.ws_state + end * kPage)[at] = s;
 }
 
 // ---------------------------------------------------------------------- host
