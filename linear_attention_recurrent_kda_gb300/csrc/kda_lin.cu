@@ -26,6 +26,7 @@ namespace lin {
 
 constexpr int kWarps = 2;                               // of a CTA (recurrent forms)
 constexpr int kParts = kDim / (kWarps * kRows);         // CTAs of a page
+constexpr int kMostHeads = 1 << 16;
 
 struct StepParams {
   int batch, heads, group, num_slots, decay_rows;
@@ -146,6 +147,7 @@ static int check_common(const Args *a, int64_t count) {
   if (count < 0 || a->heads < 0 || a->qk_heads < 1 || a->heads % a->qk_heads != 0)
     return KDA_ERR_SHAPE;
   if (a->decay_rows != 0 && a->decay_rows != 1) return KDA_ERR_SHAPE;
+  if (a->heads > kMostHeads) return KDA_ERR_SHAPE;
   if (count * a->heads * kParts > 0x7fffffffll) return KDA_ERR_SHAPE;
   const int64_t kw = int64_t(a->qk_heads) * kDim, vw = int64_t(a->heads) * kDim;
   if (!stride_ok(a->q_stride, kw) || !stride_ok(a->k_stride, kw) || !stride_ok(a->v_stride, vw) ||
@@ -201,9 +203,14 @@ struct Plan {
   int64_t workspace;      // bytes
 };
 
-constexpr int kRecurrentMost = 16;
+// Up to 8 tokens the recurrent form, which reads each page once and starts at
+// once: 8 tokens take 5.4 us against 7.4 (8 items of 128 x 128), 7.7 against 8.0
+// (128 items) and 83 against 77 (2048 items); 16 tokens 8.7, 11.9 and 138 us
+// against 7.5, 8.4 and 78.
+constexpr int kRecurrentMost = 8;
 constexpr int kShares = 152;            // SMs that the work is shared among
-constexpr int kShortestSegment = 256;
+constexpr int kShortestSegment = 256;   // tokens
+constexpr int kSplitCost = 896;         // of splitting, in tokens of one head
 
 // The sizes' part of the checks, and the plan.
 static int plan_prompt(const kda_lin_prompt_args *a, Plan *plan) {
@@ -217,11 +224,15 @@ static int plan_prompt(const kda_lin_prompt_args *a, Plan *plan) {
   plan->workspace = 0;
   if (plan->chunked) {
     // A sequence much longer than an SM's share of all tokens x heads would keep
-    // its SM busy alone: it is split, into segments of a quarter share.
+    // its SM busy alone.  Split, the share costs a second pass over keys and values
+    // (0.6 of the first) and two more launches: it pays from 2 shares and 896 tokens
+    // on (one sequence of 2048 tokens: 32 heads 52 us whole, 41 split; 64 heads 52
+    // and 70; 64 heads of 4096 tokens: 98 and 107).  Segments of a quarter share
+    // even out what the last ones leave.
     const int64_t share = static_cast<int64_t>(a->tokens) * a->heads / kShares;
     int64_t len = (share / 4 + 127) / 128 * 128;
     if (len < kShortestSegment) len = kShortestSegment;
-    if (longest > share * 8 / 5 && longest > 2 * len) {
+    if (longest > 2 * share + kSplitCost) {
       plan->seg_len = static_cast<int>(len);
       plan->segs = static_cast<int>((longest + len - 1) / len);
       if (static_cast<int64_t>(a->seqs) * plan->segs * a->heads > 0x7fffffffll)

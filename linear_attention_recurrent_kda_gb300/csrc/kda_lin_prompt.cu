@@ -8,34 +8,46 @@
 // Four products of 128^3 a chunk, one unit (sequence or segment of it, head)
 // after the other per CTA, one CTA per SM.
 //
-// Factors.  K'' takes its exponents from sums inside 32-token blocks (f =
-// 2^(sum of the tokens behind, in the block)) and the totals of the blocks
-// behind: sums of numbers of one sign, nothing cancels.  P: in a chunk whose
-// decay is above 2^-128 ("mild"), O = 2^(b_i - r) (Q (2^r S)^T + P' V) with
-// P'_ij = A_ij 2^(r - b_j), r half the chunk's logarithm rounded to a whole
-// number: every factor is within 2^+-64, one product per element of A and one per
-// element of O.  Stronger decays take a row factor times f_j off the diagonal
-// blocks, both <= 1, 2^(bl_i - bl_j) on them (bl: prefix sums in the block), and
-// O = Q S^T is scaled by rows before P V joins it.  Logarithms below -160 (base
-// 2) count as -160: the factor is 0 in FP32 either way, and a reset of -inf
-// stays a number.
+// Factors.  Exponents are sums inside 32-token blocks (bl: prefix sums; sums of the
+// tokens behind) and of whole blocks: numbers of one sign, nothing cancels.  P: in
+// a chunk whose decay is above 2^-128 ("mild"), O = 2^(b_i - r) (Q (2^r S)^T + P' V)
+// with P'_ij = A_ij 2^(r - b_j), r half the chunk's logarithm rounded to a whole
+// number: every factor is within 2^+-64, one product per element of A and one
+// per element of O.  Stronger decays take a row factor times a column factor off
+// the diagonal blocks, both <= 1, and 2^(bl_i - bl_j) on them, and O = Q S^T is
+// scaled by rows before P V joins it.  Logarithms below -160 (base 2) count as
+// -160: the factor is 0 in FP32 either way, and a reset of -inf stays a number.
 //
 // Precision.  The page stays in FP32 registers.  K'' = factor * key is the one
-// FP32 operand of the page's update; it is split into three BF16 parts (what
-// they leave is 2^-24 of it), so the update is exact to FP32's own rounding;
-// one part would put 2^-9 into the page, two 2^-16.  P and the page's copy for
-// Q S^T are rounded to BF16 once: they only feed an output that is itself
-// rounded to BF16, and the FP32 sum keeps their errors at that size.
+// operand of the page's update that BF16 does not hold; it goes in three BF16
+// parts, each the rounding of what the ones before leave, which hold its 24 bits:
+// the update is exact to FP32's own rounding (one part would put 2^-9 into the
+// page, two 2^-17).  P and the page's copy for Q S^T are rounded to BF16 once: they
+// only feed an output that is itself rounded to BF16, and the FP32 sum keeps
+// their errors at that size.
 //
-// Roles (768 threads, 24 warps): TMA loads and stores (warp 0), MMA issue for the page
-// (U; warp 1) and for the outputs (A, Q S^T, P V; warp 3), the work and its decay
-// tables (warp 2); five warpgroups: P and O (4-11, 64 columns a
-// warp), K'' (12-19, 16 keys a warp), the page (20-23).  K'' is built transposed (lanes = keys) by transposing shared-memory
-// matrix loads straight into TMEM, as the A operand: no shared memory is
-// written for it.  P is written over A in TMEM.
-//   TMEM columns: A / P 0 (P's halves at 0 and 64), O 128, U (the update) 256, K'' 384 (2 x 48).
+// Roles (768 threads, 24 warps): TMA loads and stores (warp 0), MMA issue for the
+// page (U; warp 1) and for the outputs (A, Q S^T, P V; warp 3), the work and its
+// decay tables (warp 2); five warpgroups: P and O (4-11, 64 columns a warp), K''
+// (12-19, 16 keys a warp), the page (20-23).  K'' is built transposed (lanes =
+// keys) by transposing shared-memory matrix loads straight into TMEM, as the A
+// operand: no shared memory is written for it.  P is written over A in TMEM.
+//   TMEM columns: A / P 0 (P's halves at 0 and 64), O 128, U (the update) 256, K''
+//   384 (2 x 48).
 //   Shared memory: Q, K, V double-buffered (32 KiB tiles, 128-byte swizzle) and
 //   the page's BF16 copy; O leaves through Q's tile.
+//
+// What bounds it (GB300, one sequence of 32749 tokens, 32 heads): 184 us for the
+// pass with outputs = 3.4 us a chunk and SM, 5.9 TB/s (0.86 of the copy peak); with
+// keys and queries shared by 8 heads (16 sequences x 64 heads, 185 us) the bytes
+// halve and the time does not: a chunk moves about 480 KB through shared memory
+// (MMA operands 256 KB), 3.8k of its 5.3k cycles, the tensor pipe is busy for 45%
+// and the schedulers issue in 55% of the cycles.  Roles were made short where
+// they could be: unrolled roles missed the instruction cache (7.9 warps waiting for
+// instructions per issue; 375 us at the start).  Not kept, measured there: K'' in
+// four parts from packed BF16 products (fewer instructions, a third more products
+// for U: 205 us), next tiles prefetched to L2 (205 us), one MMA warp for all
+// products (211 us), the issue loops rolled (232 us).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -70,7 +82,7 @@ struct Info {
 
 // The chunk with its factors, for the roles that compute.
 struct Table {
-  float f[kChunk];     // 2^(sum of the tokens behind, in the 32-token block)
+  float w[kChunk];     // K'': 2^(sum of the tokens behind, in the chunk)
   float x[kChunk];     // mild: 2^(ref - b); else bl, prefix sums in the block
   float total[4];      // the blocks' logarithms
   float sum;           // the chunk's
@@ -92,8 +104,8 @@ struct Ctrl {
   Table tab[2];
   Move move[kInfos];
   uint64_t move_full[kInfos], move_empty[kInfos];
-  uint64_t full_q[2], full_k[2], full_v[2];      // TMA landed
-  uint64_t empty_k[2], empty_v[2];
+  uint64_t full_q[2], full_k[3], full_v[3];      // TMA landed
+  uint64_t empty_k[3], empty_v[3];
   uint64_t st_full[2];                           // O staged in Q's tile (or written)
   uint64_t tab_full[2], tab_empty[2];
   uint64_t v_ok[2];                              // V there, zeros behind the end
@@ -108,10 +120,10 @@ constexpr int kSmem = 7 * kTile + sizeof(Ctrl);
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
 // Without outputs A's and O's columns are free: the update has two accumulators
-// and K'' four buffers.
+// and K'' four buffers; Q's tiles make a third buffer for K and V.
 template <bool kOut>
 struct Cols {
-  static constexpr uint32_t kU = kOut ? 1 : 2, kKq = kOut ? 2 : 4;
+  static constexpr uint32_t kU = kOut ? 1 : 2, kKq = kOut ? 2 : 4, kBufs = kOut ? 2 : 3;
   __device__ static uint32_t u(uint32_t n) { return kOut || (n & 1) == 0 ? kColU : kColA; }
   __device__ static uint32_t kq(uint32_t b) {
     return b < 2 ? kColK + b * kColsK : kColO + (b - 2) * kColsK;
@@ -330,8 +342,10 @@ __device__ __forceinline__ float strong_rows(const Table &tab, uint32_t col_a, i
       const float row = exp2_approx(sum);
 #pragma unroll
       for (int j = 0; j < 16; ++j)
-        r[j] = pack2(__uint_as_float(a[2 * j]) * (row * tab.f[32 * J + 2 * j]),
-                     __uint_as_float(a[2 * j + 1]) * (row * tab.f[32 * J + 2 * j + 1]));
+        r[j] = pack2(__uint_as_float(a[2 * j]) *
+                         (row * exp2_approx(tab.total[J] - tab.x[32 * J + 2 * j])),
+                     __uint_as_float(a[2 * j + 1]) *
+                         (row * exp2_approx(tab.total[J] - tab.x[32 * J + 2 * j + 1])));
     } else {
       const int to = J == w4 ? lane : -1;               // the last column to keep
 #pragma unroll
@@ -474,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                  const __grid_constant__ CUtensorMap map_v,
                  const __grid_constant__ CUtensorMap map_o) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t *sq = smem, *sk = smem + 2 * kTile, *sv = smem + 4 * kTile, *ss = smem + 6 * kTile;
+  uint8_t *sq = smem, *sk = smem + (kOut ? 2 : 0) * kTile, *sv = smem + (kOut ? 4 : 3) * kTile,
+          *ss = smem + 6 * kTile;
   Ctrl &c = *reinterpret_cast<Ctrl *>(smem + 7 * kTile);
   using C = Cols<kOut>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -495,12 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.full_q[i], 1);
-      mbar_init(&c.full_k[i], 1);
-      mbar_init(&c.full_v[i], 1);
       mbar_init(&c.st_full[i], 8);
       mbar_init(&c.v_ok[i], 4);
-      mbar_init(&c.empty_k[i], kOut ? 9 : 16);
-      mbar_init(&c.empty_v[i], kOut ? 2 : 1);
       mbar_init(&c.tab_full[i], 1);
       mbar_init(&c.tab_empty[i], 20);
       mbar_init(&c.u_full[i], 1);
@@ -511,6 +522,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&c.qs_full, 1);
     mbar_init(&c.o_full, 1);
     mbar_init(&c.o_empty, 8);
+    for (uint32_t i = 0; i < C::kBufs; ++i) {
+      mbar_init(&c.full_k[i], 1);
+      mbar_init(&c.full_v[i], 1);
+      mbar_init(&c.empty_k[i], kOut ? 9 : 16);
+      mbar_init(&c.empty_v[i], kOut ? 2 : 1);
+    }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&c.kq_full[i], 8);
       mbar_init(&c.kq_empty[i], 1);
@@ -564,8 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (next_move(c, m, info, lane)) {
         if (info.rows == 0) continue;
         ok = false;
-        const int buf = n & 1, boxes = (info.rows + 31) >> 5;
-        const uint32_t parity = ((n >> 1) & 1) ^ 1;
+        const int buf = n % C::kBufs, boxes = (info.rows + 31) >> 5;
+        const uint32_t parity = (n / C::kBufs & 1) ^ 1;
         const int xk = info.head / p.group * kDim, xv = info.head * kDim;
         // boxes of 32 rows x 64 columns, one a lane
         auto load = [&](uint8_t *tile, const CUtensorMap *map, int x, uint64_t *bar) {
@@ -605,8 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t m = 0, n = 0;
       while (next_move(c, m, info, lane)) {
         if (info.rows == 0) continue;
-        const int buf = n & 1, quarters = (info.rows + 31) >> 5;
-        const uint32_t one = n & 1, two = (n >> 1) & 1;
+        const int buf = n % C::kBufs, quarters = (info.rows + 31) >> 5;
         // U = K''^T V, quarter by quarter of 32 tokens
         // (the first K'' also says that V is there)
         const uint32_t ub = n % C::kU, ur = n / C::kU & 1;
@@ -723,27 +739,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float all = (t0 + t1) + (t2 + t3);
         const bool mild = all >= kMild && all <= 0.0f;
         const float ref = mild ? floorf(0.5f * all) : 0.0f;
-        float4 x, f;
+        float4 x, w;
         x.x = before + g[0];
         x.y = x.x + g[1];
         x.z = x.y + g[2];
         x.w = x.z + g[3];
+        const int block = lane >> 3;
         if (mild) {
-          const float base = ref - (lane < 8 ? 0.0f : lane < 16 ? t0 : lane < 24 ? t0 + t1 : t0 + t1 + t2);
+          const float base =
+              ref - (block == 0 ? 0.0f : block == 1 ? t0 : block == 2 ? t0 + t1 : t0 + t1 + t2);
           x.x = exp2_approx(base - x.x);
           x.y = exp2_approx(base - x.y);
           x.z = exp2_approx(base - x.z);
           x.w = exp2_approx(base - x.w);
         }
+        behind += block == 3 ? 0.0f : block == 2 ? t3 : block == 1 ? t2 + t3 : t1 + (t2 + t3);
         const float s3 = behind, s2 = s3 + g[3], s1 = s2 + g[2], s0 = s1 + g[1];
-        f.x = exp2_approx(s0);
-        f.y = exp2_approx(s1);
-        f.z = exp2_approx(s2);
-        f.w = exp2_approx(s3);
+        w.x = exp2_approx(s0);
+        w.y = exp2_approx(s1);
+        w.z = exp2_approx(s2);
+        w.w = exp2_approx(s3);
         KDA_WAIT_WARP(c.tab_empty[buf], round ^ 1);
         Table &tab = c.tab[buf];
         reinterpret_cast<float4 *>(tab.x)[lane] = x;
-        reinterpret_cast<float4 *>(tab.f)[lane] = f;
+        reinterpret_cast<float4 *>(tab.w)[lane] = w;
         if ((lane & 7) == 0) tab.total[lane >> 3] = total;
         if (lane == 1) {
           tab.sum = all;
@@ -945,22 +964,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&c.tab_empty[m & 1]);
         continue;
       }
-      const int buf = n & 1;
-      const uint32_t two = (n >> 1) & 1;
+      const int buf = n % C::kBufs;
+      const uint32_t two = n / C::kBufs & 1;
       KDA_WAIT_WARP(c.full_k[buf], two);
       int i = first;
 #pragma unroll 1
       for (; i < quarters; i += kStep) {
         const uint32_t quarter = done + i, kb = quarter % C::kKq;
         // factors of the 8 tokens a lane sees: 8 j + 2 (lane % 4) + {0, 1}
-        float sum = 0.0f;
-        for (int m = i + 1; m < 4; ++m) sum += tab.total[m];
-        const float block = exp2_approx(sum);
-        f32x2 f[4];
+        f32x2 w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          f[j] = mul2(reinterpret_cast<const f32x2 *>(tab.f + 32 * i + 8 * j)[lane & 3],
-                      pair(block, block));
+          w[j] = reinterpret_cast<const f32x2 *>(tab.w + 32 * i + 8 * j)[lane & 3];
         uint32_t raw[8], hi[8], mid[8], lo[8];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -977,15 +992,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             raw[y] &= 8 * j + 1 < valid ? 0xFFFFFFFFu : 8 * j < valid ? 0xFFFFu : 0u;
           }
         }
-        // three parts by truncation: 8 + 8 + 8 bits hold all 24
+        // three parts of 8 bits hold all 24
 #pragma unroll
         for (int y = 0; y < 8; ++y) {
-          const f32x2 v = mul2(raw_pair(raw[y] << 16, raw[y] & 0xFFFF0000u), f[y >> 1]);
-          const f32x2 v1 = sub2(v, v & 0xFFFF0000FFFF0000ull);
-          const f32x2 v2 = sub2(v1, v1 & 0xFFFF0000FFFF0000ull);
-          hi[y] = upper_halves(v);
-          mid[y] = upper_halves(v1);
-          lo[y] = upper_halves(v2);
+          const f32x2 v = mul2(raw_pair(raw[y] << 16, raw[y] & 0xFFFF0000u), w[y >> 1]);
+          hi[y] = pack2(v);
+          const f32x2 v1 = sub2(v, raw_pair(hi[y] << 16, hi[y] & 0xFFFF0000u));
+          mid[y] = pack2(v1);
+          lo[y] = pack2(sub2(v1, raw_pair(mid[y] << 16, mid[y] & 0xFFFF0000u)));
         }
         KDA_WAIT_WARP(c.kq_empty[kb], (quarter / C::kKq & 1) ^ 1);
         tc_fence_after();
@@ -1007,7 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&c.v_ok[buf]);
+          if (kOut && lane == 0) mbar_arrive(&c.v_ok[buf]);
         }
         tc_wait_st();
         tc_fence_before();

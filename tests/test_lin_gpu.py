@@ -108,6 +108,24 @@ def test_long_sequences_in_segments(lens, H, Hk, per_token):
     verify(inp, launch(inp, src=src, dst=dst, max_seq=max(lens)), 2, src, dst)
 
 
+def test_segments_of_many_chunks():
+    """Segments of 7 chunks (every buffer comes round), checked on two heads."""
+    H, n, heads = 64, 8192 + 77, (5, 63)
+    inp = make([n], H, H, slots=3, seed=16, scale_g=0.02)
+    args = kl.KdaLinPromptArgs(seqs=1, heads=H, qk_heads=H, tokens=n, max_seq=n, q_stride=H * D,
+                               k_stride=H * D, v_stride=H * D, o_stride=H * D)
+    assert kl.prompt_workspace(args) > 0
+    out, state = launch(inp, src=[2], dst=[2])
+    for h in heads:
+        sl = slice(h * D, h * D + D)
+        ref, mag, S, M = linref.prompt(inp["q"][:, sl], inp["k"][:, sl], inp["v"][:, sl],
+                                       inp["decay"][:, h:h + 1], [0, n], 0.5,
+                                       inp["state"][:, h:h + 1], [2])
+        off = (out[:, sl].double() - ref).abs()
+        assert torch.all(off <= linref.out_bound(ref, mag, n, True))
+        assert torch.all((state[2, h:h + 1].double() - S[0]).abs() <= linref.state_bound(M[0], n))
+
+
 @pytest.mark.parametrize("path", PATHS)
 def test_without_a_state(path):
     inp = make([3, 140], 2, 2, seed=5)
