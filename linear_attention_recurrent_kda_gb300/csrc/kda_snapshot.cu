@@ -24,7 +24,7 @@ namespace snap {
 
 constexpr int kDim = 128;
 constexpr int kPage = kDim * kDim;
-constexpr int kRows = 16;                        // rows of a warp
+constexpr int kRows = 8;                         // rows of a warp
 constexpr int kWarps = 2;                        // of a CTA
 constexpr int kParts = kDim / (kRows * kWarps);  // CTAs of a page
 
@@ -49,19 +49,25 @@ __device__ __forceinline__ bool resolve(const Params &p, int e, int *slot, int *
   return true;
 }
 
-__device__ __forceinline__ int quantise(float x, float scale, float half, float inv) {
-  float c = rintf(x * inv);
-  const float r = __fmaf_rn(-c, scale, x);
-  const float away = fabsf(r);
-  const bool odd = static_cast<int>(c) & 1;
-  if (away > half || (away == half && odd)) c += copysignf(1.0f, r);
-  return static_cast<int>(c);
+// The code of x in the low bits: x / scale to the nearest whole number.  Adding
+// 1.5 * 2^23 rounds x * inv to one; `half` is scale / 2.
+__device__ __forceinline__ uint32_t quantise(float x, float scale, float half, float inv) {
+  constexpr float kMagic = 12582912.0f;
+  const float t = __fmaf_rn(x, inv, kMagic);
+  uint32_t code = __float_as_uint(t);
+  const float r = __fmaf_rn(__fsub_rn(kMagic, t), scale, x);
+  if (fabsf(r) >= half) {
+    // not the nearest, or a tie: then the even one
+    if (fabsf(r) > half || (code & 1u)) code += r > 0.0f ? 1u : 0xFFFFFFFFu;
+  }
+  return code;
 }
 
 template <int kBits>
 __global__ void __launch_bounds__(kWarps * 32) save_kernel(const __grid_constant__ Params p) {
   constexpr int kLanes = kBits == 8 ? 32 : 8;   // lanes that share a scale
   constexpr int kGroups = 32 / kLanes;          // scales of a row
+  constexpr int kOwn = (kRows + kLanes - 1) / kLanes;         // scales a lane works out
   constexpr float kTop = kBits == 8 ? 127.0f : 7.0f;
   const int part = blockIdx.x % kParts, item = blockIdx.x / kParts;
   const int e = item / p.heads, h = item % p.heads;
@@ -71,13 +77,17 @@ __global__ void __launch_bounds__(kWarps * 32) save_kernel(const __grid_constant
   const float4 *page = p.state + (static_cast<int64_t>(slot) * p.heads + h) * (kPage / 4) +
                        row0 * (kDim / 4) + lane;
   const int64_t kept = static_cast<int64_t>(snap) * p.heads + h;
-  float *scales = p.scales + (kept * kDim + row0) * kGroups;
   float4 x[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) x[i] = __ldcs(page + i * (kDim / 4));
+  // Every group's largest magnitude, as an integer (an infinity or NaN tops every
+  // finite one), and its scale in one lane of the group: the divisions, two of 20
+  // instructions, are done once per scale instead of once per lane and row.
+  float scale[kOwn], inv[kOwn];
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) scale[k] = 0.0f;
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    // largest magnitude as an integer: an infinity or NaN tops every finite one
     uint32_t m = max(max(__float_as_uint(x[i].x) & 0x7fffffffu, __float_as_uint(x[i].y) & 0x7fffffffu),
                      max(__float_as_uint(x[i].z) & 0x7fffffffu, __float_as_uint(x[i].w) & 0x7fffffffu));
     if (kLanes == 32) {
@@ -86,29 +96,39 @@ __global__ void __launch_bounds__(kWarps * 32) save_kernel(const __grid_constant
 #pragma unroll
       for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     }
-    const float top = __uint_as_float(m);
-    float scale = __fdiv_rn(top, kTop);
-    int c[4] = {0, 0, 0, 0};
-    if (m >= 0x7f800000u) {
-      scale = __uint_as_float(0x7fffffffu);
-    } else if (top < 0x1p-118f) {
-      scale = 0.0f;
-    } else {
-      const float inv = __fdiv_rn(1.0f, scale), half = 0.5f * scale;
-      c[0] = quantise(x[i].x, scale, half, inv);
-      c[1] = quantise(x[i].y, scale, half, inv);
-      c[2] = quantise(x[i].z, scale, half, inv);
-      c[3] = quantise(x[i].w, scale, half, inv);
+    if ((lane & (kLanes - 1)) == (i & (kLanes - 1))) scale[i / kLanes] = __uint_as_float(m);
+  }
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) {
+    const float top = scale[k];
+    const bool bad = !(top <= 3.402823466e38f), small = top < 0x1p-118f;
+    scale[k] = bad ? __uint_as_float(0x7fffffffu) : small ? 0.0f : __fdiv_rn(top, kTop);
+    inv[k] = bad || small ? 0.0f : __fdiv_rn(1.0f, scale[k]);
+    const int i = k * kLanes + (lane & (kLanes - 1));
+    if (i < kRows) p.scales[(kept * kDim + row0 + i) * kGroups + lane / kLanes] = scale[k];
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int from = (lane & ~(kLanes - 1)) | (i & (kLanes - 1));
+    const float s = __shfl_sync(0xffffffffu, scale[i / kLanes], from);
+    const float v = __shfl_sync(0xffffffffu, inv[i / kLanes], from);
+    const float half = 0.5f * s;
+    uint32_t c[4] = {0, 0, 0, 0};
+    if (v > 0.0f) {
+      c[0] = quantise(x[i].x, s, half, v);
+      c[1] = quantise(x[i].y, s, half, v);
+      c[2] = quantise(x[i].z, s, half, v);
+      c[3] = quantise(x[i].w, s, half, v);
     }
     if (kBits == 8) {
-      const uint32_t w = (c[0] & 255) | (c[1] & 255) << 8 | (c[2] & 255) << 16 | (c[3] & 255) << 24;
+      const uint32_t w =
+          __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
       static_cast<uint32_t *>(p.codes)[(kept * kDim + row0 + i) * 32 + lane] = w;
     } else {
       const uint32_t w = (c[0] & 15) | (c[1] & 15) << 4 | (c[2] & 15) << 8 | (c[3] & 15) << 12;
       static_cast<uint16_t *>(p.codes)[(kept * kDim + row0 + i) * 32 + lane] =
           static_cast<uint16_t>(w);
     }
-    if (lane % kLanes == 0) scales[i * kGroups + lane / kLanes] = scale;
   }
 }
 
