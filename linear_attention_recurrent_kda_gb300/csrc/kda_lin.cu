@@ -1,17 +1,18 @@
 // Linear attention with one decay per head: the single-token step, the
 // token-by-token prompt form, and the checks and dispatch of both calls.
 //
-// Both forms keep a page slice in registers: a warp holds 16 value rows, lane
-// l the keys 4l .. 4l+3 of each (a row is one 512-byte access of the warp), so
-// that S q needs one 16-shuffle reduce-scatter for 16 rows.  A product v k is
-// rounded before it joins the decayed state: both are exact BF16 values, so it
-// is exact in FP32.
+// Both forms keep a page slice in registers: a warp holds 8 value rows, lane l
+// the keys 4l .. 4l+3 of each (a row is one 512-byte access of the warp), so that
+// S q needs one reduce-scatter for 8 rows.  A product v k is of two BF16 values
+// and exact in FP32.
 //
 // The step is HBM-bound (a page read and written per item, 128 KiB against
-// 160 kflop).  CTAs of two warps, a quarter page each: all 16 loads of a thread
-// are in flight at once and the many small CTAs of an SM keep its memory
-// queue full without a pipeline; a batch of few requests still spreads over
-// the SMs.
+// 160 kflop).  CTAs of two warps, an eighth of a page each: all loads of a
+// thread are in flight at once and the many small CTAs of an SM keep its
+// memory queue full without a pipeline; a batch of few requests still spreads
+// over the SMs.  GB300: 256 requests x 32 heads 159 us = 6.8 TB/s, the copy's
+// rate (16 rows a warp: 160 us); 64 x 32 with 8 padded 38.8 us (0.90); 4 x 8 2.5 us,
+// a launch.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(kWarps * 32) step_kernel(const __grid_constant
   const float o = token_step(s, d, k, q, v, lane);
 #pragma unroll
   for (int i = 0; i < kRows; ++i) __stcs(page + i * 32, s[i]);
-  if ((lane & 1) == 0) out[lane >> 1] = __float2bfloat16_rn(p.scale * o);
+  if (lane % kSpan == 0) out[lane / kSpan] = __float2bfloat16_rn(p.scale * o);
 }
 
 // Token by token over a sequence: the operands of token t + 1 are loaded while
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       p.v + seq.start * p.v_stride + h * kDim + row0 + (lane & (kRows - 1));
   const float *gp = p.decay + (p.decay_rows ? static_cast<int64_t>(seq.start) * p.heads : 0) + h;
   const int64_t g_step = p.decay_rows ? p.heads : 0;
-  __nv_bfloat16 *out = p.output + seq.start * p.o_stride + h * kDim + row0 + (lane >> 1);
+  __nv_bfloat16 *out = p.output + seq.start * p.o_stride + h * kDim + row0 + lane / kSpan;
   uint2 kn = make_uint2(0, 0), qn = kn;
   __nv_bfloat16 vn = __float2bfloat16_rn(0.0f);
   float gn = 0.0f;
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     unpack4(kc, k);
     unpack4(qc, q);
     const float o = token_step(s, d, k, q, v, lane);
-    if ((lane & 1) == 0) *out = __float2bfloat16_rn(p.scale * o);
+    if (lane % kSpan == 0) *out = __float2bfloat16_rn(p.scale * o);
     out += p.o_stride;
   }
   if (seq.dst) {
@@ -203,11 +204,11 @@ struct Plan {
   int64_t workspace;      // bytes
 };
 
-// Up to 8 tokens the recurrent form, which reads each page once and starts at
-// once: 8 tokens take 5.4 us against 7.4 (8 items of 128 x 128), 7.7 against 8.0
-// (128 items) and 83 against 77 (2048 items); 16 tokens 8.7, 11.9 and 138 us
-// against 7.5, 8.4 and 78.
-constexpr int kRecurrentMost = 8;
+// Short sequences take the recurrent form, which reads each page once and starts
+// at once.  8 tokens: 5.2 us against 7.5 chunked (32 items of 128 x 128), 7.4
+// against 8.0 (128 items), 83 against 78 (2048 items); 12 tokens: 6.7 against 7.5,
+// 9.6 against 8.0 and 109 against 79.
+constexpr int kRecurrentMost = 8, kRecurrentMostFew = 12, kFewItems = 64;
 constexpr int kShares = 152;            // SMs that the work is shared among
 constexpr int kShortestSegment = 256;   // tokens
 constexpr int kSplitCost = 896;         // of splitting, in tokens of one head
@@ -218,7 +219,9 @@ static int plan_prompt(const kda_lin_prompt_args *a, Plan *plan) {
   if (a->tokens < 0 || a->max_seq < 0 || (a->state && a->num_slots < 1)) return KDA_ERR_SHAPE;
   if (a->path < 0 || a->path > 2) return KDA_ERR_PATH;
   const int64_t longest = a->max_seq < a->tokens ? a->max_seq : a->tokens;
-  plan->chunked = longest > 0 && (a->path == 2 || (a->path == 0 && longest > kRecurrentMost));
+  const int64_t items = static_cast<int64_t>(a->seqs) * a->heads;
+  const int recurrent_most = items <= kFewItems ? kRecurrentMostFew : kRecurrentMost;
+  plan->chunked = longest > 0 && (a->path == 2 || (a->path == 0 && longest > recurrent_most));
   plan->segs = 1;
   plan->seg_len = longest > 0 ? static_cast<int>(longest) : 1;
   plan->workspace = 0;
@@ -235,7 +238,7 @@ static int plan_prompt(const kda_lin_prompt_args *a, Plan *plan) {
     if (longest > 2 * share + kSplitCost) {
       plan->seg_len = static_cast<int>(len);
       plan->segs = static_cast<int>((longest + len - 1) / len);
-      if (static_cast<int64_t>(a->seqs) * plan->segs * a->heads > 0x7fffffffll)
+      if (items * plan->segs > 0x7fffffffll || items > 0x7fffffffll / kSegmentBlocks)
         return KDA_ERR_SHAPE;
       plan->workspace = ws_pages(a->tokens, len, a->heads) * (kPage + 1) * 4;
     }
@@ -248,8 +251,9 @@ static int run_prompt(const kda_lin_prompt_args *a, cudaStream_t stream) {
   Plan plan;
   if (const int rc = plan_prompt(a, &plan)) return rc;
   if (a->seqs == 0 || a->heads == 0) return KDA_SUCCESS;
-  if (!a->seq_starts || !a->decay) return KDA_ERR_NULL_POINTER;
-  if (a->tokens > 0 && (!a->q || !a->k || !a->v || !a->output)) return KDA_ERR_NULL_POINTER;
+  if (!a->seq_starts) return KDA_ERR_NULL_POINTER;
+  if (a->tokens > 0 && (!a->q || !a->k || !a->v || !a->decay || !a->output))
+    return KDA_ERR_NULL_POINTER;
   if ((a->src_slots || a->dst_slots) && !a->state) return KDA_ERR_NULL_POINTER;
   if (!rows_aligned(a) || !aligned(a->seq_starts, 4) || !aligned(a->src_slots, 4) ||
       !aligned(a->dst_slots, 4))

@@ -17,7 +17,8 @@ namespace lin {
 
 constexpr int kDim = 128;                 // keys and value rows of a page
 constexpr int kPage = kDim * kDim;        // floats of a page
-constexpr int kRows = 16;                 // value rows a warp holds (recurrent forms)
+constexpr int kRows = 8;                  // value rows a warp holds (recurrent forms)
+constexpr int kSpan = 32 / kRows;         // lanes that share a row's sum
 
 struct PromptParams {
   int seqs, heads, group, tokens, max_seq, num_slots, decay_rows;  // group = heads / qk_heads
@@ -68,7 +69,7 @@ __device__ __forceinline__ void unpack4(const uint2 &u, float (&f)[4]) {
 }
 
 // One token on a warp's kRows value rows: lane l holds keys 4l .. 4l+3 of each
-// row.  vrow: lane r < kRows holds v of row r.  Returns S q of row lane / 2
+// row.  vrow: lane r < kRows holds v of row r.  Returns S q of row lane / kSpan
 // (FP32, unscaled).
 __device__ __forceinline__ float token_step(float4 (&s)[kRows], float d, const float (&k)[4],
                                             const float (&q)[4], float vrow, int lane) {
@@ -90,6 +91,8 @@ __device__ __forceinline__ float token_step(float4 (&s)[kRows], float d, const f
 inline int64_t ws_pages(int64_t tokens, int64_t seg_len, int64_t heads) {
   return 2 * (tokens / seg_len + 1) * heads;
 }
+
+constexpr int kSegmentBlocks = kPage / (4 * 256);   // CTAs of a page in the segments' scan
 
 // The chunked form (kda_lin_prompt.cu): enqueues its kernels for checked
 // parameters.  Returns a KDA_* code.

@@ -1134,8 +1134,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Each thread walks 4 elements of a page over the segments, eight segments'
 // loads in flight (one at a time, 19 segments of 32 heads took 227 us).
 __global__ void __launch_bounds__(256) segment_kernel(const __grid_constant__ PromptParams p) {
-  constexpr int kBlocks = kPage / (4 * 256), kBatch = 8;
-  const int part = blockIdx.x % kBlocks, item = blockIdx.x / kBlocks;
+  constexpr int kBatch = 8;
+  const int part = blockIdx.x % kSegmentBlocks, item = blockIdx.x / kSegmentBlocks;
   const int b = item / p.heads, h = item % p.heads;
   Seq seq;
   if (resolve_seq(p, b, &seq) || seq.len <= p.seg_len) return;
@@ -1227,7 +1227,7 @@ int launch_chunked(const PromptParams &p, int qk_heads, int dev, int sms, cudaSt
   if (p.segs > 1) {
     chunk_kernel<false><<<grid, kThreads, kSmem, stream>>>(p, q, k, v, o);
     if (cudaGetLastError() != cudaSuccess) return KDA_ERR_LAUNCH;
-    segment_kernel<<<p.seqs * p.heads * (kPage / 1024), 256, 0, stream>>>(p);
+    segment_kernel<<<p.seqs * p.heads * kSegmentBlocks, 256, 0, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return KDA_ERR_LAUNCH;
   }
   chunk_kernel<true><<<grid, kThreads, kSmem, stream>>>(p, q, k, v, o);

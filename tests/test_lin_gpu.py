@@ -251,6 +251,118 @@ def test_other_stream_and_graph(path):
     assert torch.equal(want[1], dev["state"].cpu())
 
 
+def on_device(inp, src=None, dst=None, **kw):
+    """The arguments of one call, as device copies of its own."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    n, width = inp["v"].shape
+    a = {x: inp[x].cuda() for x in ("q", "k", "v", "decay", "state")}
+    return dict(a, seq_starts=torch.tensor(inp["starts"], **i32), scale=0.5,
+                output=torch.zeros(n, width, dtype=bf16, device="cuda"),
+                src_slots=None if src is None else torch.tensor(src, **i32),
+                dst_slots=None if dst is None else torch.tensor(dst, **i32), **kw)
+
+
+def test_split_calls_on_two_streams_and_in_two_graphs():
+    """Calls that need a workspace, at the same time on two streams and replayed
+    from two graphs in turn, do not share it."""
+    inps = [make([1500, 200], 2, 2, slots=4, seed=20), make([1400], 2, 1, slots=4, seed=21)]
+    wants = [launch(x, src=[1] * (len(x["starts"]) - 1), dst=[2, 3][:len(x["starts"]) - 1])
+             for x in inps]
+
+    def check(kws):
+        torch.cuda.synchronize()
+        for kw, want in zip(kws, wants):
+            assert torch.equal(kw["output"].cpu(), want[0])
+            assert torch.equal(kw["state"].cpu(), want[1])
+
+    def fresh():
+        return [on_device(x, [1] * (len(x["starts"]) - 1), [2, 3][:len(x["starts"]) - 1])
+                for x in inps]
+
+    kws, streams = fresh(), [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for kw, s in zip(kws, streams):
+            kda_lin_prompt(**kw, stream=s)
+    check(kws)
+    kws, graphs = fresh(), [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for kw, graph in zip(kws, graphs):
+        with torch.cuda.graph(graph):
+            kda_lin_prompt(**kw)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+    check(kws)
+
+
+@pytest.mark.parametrize("lens,H,Hk", [([700, 33, 128, 1, 500, 256], 32, 8), ([2600, 90], 8, 8)])
+def test_relaunches_give_the_same_bits(lens, H, Hk):
+    """300 launches in a row, whole sequences and split ones, decays mild and
+    strong: every one has the first one's bits."""
+    B = len(lens)
+    inp = make(lens, H, Hk, slots=2 * B + 1, seed=23, scale_g=0.1)
+    inp["decay"][:, ::3] *= 40.0                       # strong chunks in every third head
+    kw = on_device(inp, [1 + r for r in range(B)], [B + 1 + r for r in range(B)], max_seq=max(lens))
+    kda_lin_prompt(**kw)
+    out, state = kw["output"].clone(), kw["state"].clone()
+    bad = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        kw["output"].fill_(float("nan"))
+        kw["state"][B + 1:].fill_(float("nan"))
+        kda_lin_prompt(**kw)
+        bad += (kw["output"] != out).sum() + (kw["state"] != state).sum()
+    assert int(bad) == 0
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_rows_past_32_bit_offsets(path):
+    """The last rows of tensors of more than 2^31 elements."""
+    H, n = 64, 2 ** 31 // (64 * D) + 301
+    inp = make([200, 61], H, H, seed=22)
+    want = launch(inp, path=path)[0]
+    big = {x: torch.zeros(n, H * D, dtype=bf16, device="cuda") for x in ("q", "k", "v", "output")}
+    decay = torch.zeros(n, H, device="cuda")
+    for x in ("q", "k", "v"):
+        big[x][-261:] = inp[x].cuda()
+    decay[-261:] = inp["decay"].cuda()
+    kda_lin_prompt(**big, decay=decay, scale=0.5, path=path, max_seq=200,
+                   seq_starts=torch.tensor([n - 261, n - 61, n], dtype=torch.int32, device="cuda"))
+    assert torch.equal(big["output"][-261:].cpu(), want)
+    assert not big["output"][:-261].any()
+
+
+@pytest.mark.parametrize("B,H", [(200, 4), (700, 3), (900, 2), (1, 300)])
+def test_many_units(B, H):
+    """More units than SMs: dealt by length (up to 8 a CTA and 768 sequences) and
+    in turn.  Sequences of the same rows and lengths give the same bits wherever
+    they run."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(1, 140, (B,), generator=g).tolist()
+    lens[::7] = [0] * len(lens[::7])
+    lens[0] = 33
+    base = make([140], H, 1, slots=2, seed=B)
+    starts, rows = [0], []
+    for x in lens:
+        starts.append(starts[-1] + x)
+        rows += list(range(x))
+    at = torch.tensor(rows)
+    inp = dict(base, **{x: base[x][at] for x in ("q", "k", "v", "decay")}, starts=starts)
+    inp["state"] = torch.zeros(B + 2, H, D, D)
+    inp["state"][1] = base["state"][1]
+    out, state = launch(inp, src=[1] * B, dst=list(range(2, B + 2)), path=2, max_seq=140)
+    first = {}
+    for r, x in enumerate(lens):
+        a, b = starts[r], starts[r + 1]
+        if x not in first:
+            one = {k: v[a:b] if k in ("q", "k", "v", "decay") else v for k, v in inp.items()}
+            one.update(starts=[0, x], state=torch.cat([inp["state"][:2], inp["state"][:1]]))
+            first[x] = launch(one, src=[1], dst=[2], path=2)
+        assert torch.equal(out[a:b], first[x][0]), r
+        assert torch.equal(state[r + 2], first[x][1][2]), r
+
+
 # ------------------------------------------------------------------------- step
 
 def step_ref(inp, state, slots, scale):
