@@ -200,7 +200,7 @@ static int run_step(const kda_lin_step_args *a, cudaStream_t stream) {
 // How a prompt call runs.
 struct Plan {
   bool chunked;
-  int segs, seg_len;      // segments of a sequence, their tokens
+  int slots, seg_len;     // of segments; 0 slots: sequences stay whole
   int64_t workspace;      // bytes
 };
 
@@ -222,7 +222,7 @@ static int plan_prompt(const kda_lin_prompt_args *a, Plan *plan) {
   const int64_t items = static_cast<int64_t>(a->seqs) * a->heads;
   const int recurrent_most = items <= kFewItems ? kRecurrentMostFew : kRecurrentMost;
   plan->chunked = longest > 0 && (a->path == 2 || (a->path == 0 && longest > recurrent_most));
-  plan->segs = 1;
+  plan->slots = 0;
   plan->seg_len = longest > 0 ? static_cast<int>(longest) : 1;
   plan->workspace = 0;
   if (plan->chunked) {
@@ -235,10 +235,12 @@ static int plan_prompt(const kda_lin_prompt_args *a, Plan *plan) {
     const int64_t share = static_cast<int64_t>(a->tokens) * a->heads / kShares;
     int64_t len = (share / 4 + 127) / 128 * 128;
     if (len < kShortestSegment) len = kShortestSegment;
-    if (longest > 2 * share + kSplitCost) {
+    // (the slots of the segments are at most 4 an SM and one for each head; with
+    // more heads than that leaves room for, there are enough units without)
+    if (longest > 2 * share + kSplitCost && slots_of(a->tokens, len) * a->heads <= kList * kShares) {
       plan->seg_len = static_cast<int>(len);
-      plan->segs = static_cast<int>((longest + len - 1) / len);
-      if (items * plan->segs > 0x7fffffffll || items > 0x7fffffffll / kSegmentBlocks)
+      plan->slots = static_cast<int>(slots_of(a->tokens, len));
+      if ((static_cast<int64_t>(plan->slots) + a->seqs) * a->heads > 0x7fffffffll)
         return KDA_ERR_SHAPE;
       plan->workspace = ws_pages(a->tokens, len, a->heads) * (kPage + 1) * 4;
     }
@@ -272,7 +274,7 @@ static int run_prompt(const kda_lin_prompt_args *a, cudaStream_t stream) {
   p.max_seq = a->max_seq < a->tokens ? a->max_seq : a->tokens;
   p.num_slots = a->num_slots;
   p.decay_rows = a->decay_rows;
-  p.segs = plan.segs;
+  p.slots = plan.slots;
   p.seg_len = plan.seg_len;
   p.q_stride = a->q_stride;
   p.k_stride = a->k_stride;

@@ -22,7 +22,7 @@ constexpr int kSpan = 32 / kRows;         // lanes that share a row's sum
 
 struct PromptParams {
   int seqs, heads, group, tokens, max_seq, num_slots, decay_rows;  // group = heads / qk_heads
-  int segs, seg_len;      // segments a sequence may be split into (1: not split), their tokens
+  int slots, seg_len;     // sequences longer than seg_len are split; slots for their segments
   int64_t q_stride, k_stride, v_stride, o_stride;
   const __nv_bfloat16 *q, *k, *v;
   const float *decay;
@@ -31,7 +31,7 @@ struct PromptParams {
   __nv_bfloat16 *output;
   float scale;
   int32_t *err;
-  float *ws_state;        // pages of the segments when segs > 1 (kda_lin_prompt.cu)
+  float *ws_state;        // pages of the segments when slots > 0 (kda_lin_prompt.cu)
   float *ws_decay;        // their total decays
 };
 
@@ -87,12 +87,16 @@ __device__ __forceinline__ float token_step(float4 (&s)[kRows], float d, const f
   return warp_reduce_scatter<kRows>(dot, lane);
 }
 
-// Pages of workspace of the chunked form with these segments.
+constexpr int kList = 8;       // units of a CTA that its kernel keeps in order and searches for
+
+// Slots of the chunked form's segments, and its pages of workspace.
+inline int64_t slots_of(int64_t tokens, int64_t seg_len) { return tokens / seg_len + 1; }
 inline int64_t ws_pages(int64_t tokens, int64_t seg_len, int64_t heads) {
-  return 2 * (tokens / seg_len + 1) * heads;
+  return 2 * slots_of(tokens, seg_len) * heads;
 }
 
-constexpr int kSegmentBlocks = kPage / (4 * 256);   // CTAs of a page in the segments' scan
+// threads of a CTA and CTAs of a page in the segments' scan
+constexpr int kSegmentThreads = 256, kSegmentBlocks = kPage / (4 * kSegmentThreads);
 
 // The chunked form (kda_lin_prompt.cu): enqueues its kernels for checked
 // parameters.  Returns a KDA_* code.

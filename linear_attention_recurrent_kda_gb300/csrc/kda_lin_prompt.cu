@@ -98,7 +98,6 @@ struct Move {
 };
 
 constexpr int kInfos = 4;
-constexpr int kList = 16;      // units of a CTA that can be put in order
 
 struct Ctrl {
   Table tab[2];
@@ -112,7 +111,8 @@ struct Ctrl {
   uint64_t kq_full[4], kq_empty[4];              // K'' quarters in TMEM
   uint64_t u_full[2], u_empty[2];
   uint64_t a_full, p_full, qs_full, o_full, o_empty, s_full;
-  uint32_t list[kList];                          // the CTA's units, where sorted
+  uint32_t list[kList];                          // the CTA's first units, where sorted
+  int found[kList];                              // the sequence of each that is a slot's, or -1
   uint32_t tmem, abort;
 };
 
@@ -364,43 +364,70 @@ __device__ __forceinline__ float strong_rows(const Table &tab, uint32_t col_a, i
 
 // -------------------------------------------------------------- units, chunks
 
+// A unit's rows, head and pages.
 struct Unit {
-  int b, h, seg, segs;     // sequence, head, segment of its segments
-  int row, n;              // first row, tokens
-  int src, dst;
+  int row, n, head;
+  const float *from;
+  float *to, *decay;
 };
 
-// A unit's segment: whether it has work in this kernel, and which rows.
+// A segment's page in the workspace.  All segments but a sequence's last have
+// seg_len rows, so first_row / seg_len tells them apart; the last ones (shorter:
+// another sequence's first may start in the same seg_len rows) have pages of
+// their own behind.
+__device__ __forceinline__ int64_t ws_index(const PromptParams &p, int first_row, bool last, int h) {
+  const int64_t at = first_row / p.seg_len + (last ? p.slots : 0);
+  return at * p.heads + h;
+}
+
+// The items of work, each times the heads: first the slots, slot r for the
+// segment of seg_len rows, not its sequence's last, that starts in rows r * seg_len
+// .. (r + 1) * seg_len - 1 (at most one: it covers the last of them); then, with
+// outputs, every sequence's last segment.  There are no more than the rows need,
+// however long the longest sequence is.
 template <bool kOut>
-__device__ __forceinline__ bool segment_of(const PromptParams &p, const Seq &s, int seg, int *segs,
-                                           int *n) {
-  *segs = s.len > p.seg_len ? (s.len + p.seg_len - 1) / p.seg_len : 1;
-  const int left = s.len - seg * p.seg_len;
-  *n = left < p.seg_len ? left : p.seg_len;
-  return seg < (kOut ? *segs : *segs - 1);
+__device__ __forceinline__ int items_of(const PromptParams &p) {
+  return p.slots + (kOut ? p.seqs : 0);
+}
+
+// Whether sequence s has slot r's segment, and which one that is.
+__device__ __forceinline__ bool in_slot(const PromptParams &p, const Seq &s, int r, int *seg) {
+  const int64_t end = static_cast<int64_t>(r + 1) * p.seg_len - 1;
+  if (s.start > end) return false;
+  const int64_t n = (end - s.start) / p.seg_len;
+  *seg = static_cast<int>(n);
+  return (n + 1) * p.seg_len < s.len;
+}
+
+__device__ __forceinline__ int segments_of(const PromptParams &p, const Seq &s) {
+  return s.len > p.seg_len ? (s.len + p.seg_len - 1) / p.seg_len : 1;
 }
 
 // Puts this CTA's units in order: all units by length, the longest first, dealt
-// to the CTAs forth and back, so that each gets long and short ones (256 ragged
-// sequences: 12% less time than every grid-th unit).  Units of a sequence's
-// segment follow one another (heads).  One thread a segment ranks it by counting
-// the longer ones; `keys` is scratch.  All threads call it.
+// to the CTAs forth and back, so that each gets long and short ones (8 ragged
+// sequences x 32 heads: 86 -> 78 us; 16 x 64 heads 212 -> 197 us).  One thread an
+// item ranks it by counting the longer ones; `keys` is scratch.  All threads call
+// it.
 template <bool kOut>
 __device__ __forceinline__ void order_units(const PromptParams &p, int *keys, uint32_t *list) {
-  const int pairs = p.seqs * p.segs, i = threadIdx.x;
+  const int items = items_of<kOut>(p), i = threadIdx.x;
   int key = -1;
-  if (i < pairs) {
+  if (i < items) {
     Seq s;
-    int segs, n;
-    if (!resolve_seq(p, i / p.segs, &s) && segment_of<kOut>(p, s, i % p.segs, &segs, &n)) key = n;
+    if (i < p.slots) {
+      for (int b = 0, seg; b < p.seqs && key < 0; ++b)
+        if (!resolve_seq(p, b, &s) && in_slot(p, s, i, &seg)) key = p.seg_len;
+    } else if (!resolve_seq(p, i - p.slots, &s)) {
+      key = s.len - (segments_of(p, s) - 1) * p.seg_len;
+    }
     keys[i] = key;
   }
   __syncthreads();
-  if (i < pairs) {
+  if (i < items) {
     uint32_t rank = 0;
 #pragma unroll 8
-    for (int j = 0; j < pairs; ++j) rank += keys[j] > key || (keys[j] == key && j < i);
-    const uint32_t lo = rank * p.heads, units = static_cast<uint32_t>(pairs) * p.heads;
+    for (int j = 0; j < items; ++j) rank += keys[j] > key || (keys[j] == key && j < i);
+    const uint32_t lo = rank * p.heads, units = static_cast<uint32_t>(items) * p.heads;
     for (uint32_t k = 0, base = 0; k < kList && base < units; ++k, base += gridDim.x) {
       const uint32_t r = base + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
       if (r - lo < static_cast<uint32_t>(p.heads)) list[k] = i * p.heads + (r - lo);
@@ -409,55 +436,85 @@ __device__ __forceinline__ void order_units(const PromptParams &p, int *keys, ui
   fence_proxy_async_smem();
 }
 
-// Walks this CTA's units.
+// This CTA's k-th unit; -1: none this round (forth and back: the last round may
+// pass over this CTA), -2: no more.
+__device__ __forceinline__ int64_t unit_at(uint32_t k, int64_t units, const uint32_t *list) {
+  const int64_t base = static_cast<int64_t>(k) * gridDim.x;
+  if (base >= units) return -2;
+  const int64_t place = base + (list && (k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  if (place >= units) return -1;
+  return list ? list[k % kList] : place;
+}
+
+// The sequences of this CTA's slot units (the host keeps them among the first
+// kList).  All threads call it; `found` holds -1.
+template <bool kOut>
+__device__ __forceinline__ void find_slots(const PromptParams &p, const uint32_t *list, int *found) {
+  const int64_t units = static_cast<int64_t>(items_of<kOut>(p)) * p.heads;
+  for (uint32_t k = 0; k < kList; ++k) {
+    const int64_t at = unit_at(k, units, list);
+    if (at < 0 || at >= static_cast<int64_t>(p.slots) * p.heads) continue;
+    for (int b = threadIdx.x; b < p.seqs; b += kThreads) {
+      Seq s;
+      int seg;
+      if (!resolve_seq(p, b, &s) && in_slot(p, s, static_cast<int>(at / p.heads), &seg)) found[k] = b;
+    }
+  }
+}
+
+// Walks this CTA's units (a whole warp).
 template <bool kOut>
 struct Walk {
   const PromptParams &p;
   const uint32_t *list;    // NULL: every grid-th unit
+  const int *found;
   uint32_t k;
   Unit unit;
 
-  __device__ Walk(const PromptParams &p_, const uint32_t *list_) : p(p_), list(list_), k(0) {}
+  __device__ Walk(const PromptParams &p_, const uint32_t *list_, const int *found_)
+      : p(p_), list(list_), found(found_), k(0) {}
   // The next unit that has work for this kernel.
-  __device__ bool next(bool report) {
-    const int64_t units = static_cast<int64_t>(p.seqs) * p.segs * p.heads;   // < 2^31
+  __device__ bool next(int lane) {
+    const int64_t units = static_cast<int64_t>(items_of<kOut>(p)) * p.heads;   // < 2^31
     while (true) {
-      const int64_t place = static_cast<int64_t>(k) * gridDim.x +
-                            (list && (k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      // (forth and back: the last round may pass over this CTA)
-      if (static_cast<int64_t>(k) * gridDim.x >= units) return false;
-      const uint32_t at = list ? list[k % kList] : static_cast<uint32_t>(place);
+      const int64_t place = unit_at(k, units, list);
+      if (place == -2) return false;
       ++k;
-      if (place >= units) continue;
-      const uint32_t rest = at / p.heads;
-      unit.h = at - rest * p.heads;
-      unit.b = rest / p.segs;
-      unit.seg = rest - unit.b * p.segs;
+      if (place < 0) continue;
+      const uint32_t at = static_cast<uint32_t>(place);
+      const int item = at / p.heads;
+      unit.head = at - static_cast<uint32_t>(item) * p.heads;
+      const bool slot = item < p.slots;
+      const int b = slot ? found[(k - 1) % kList] : item - p.slots;
+      if (b < 0) continue;
       Seq s;
-      if (const int bad = resolve_seq(p, unit.b, &s)) {
-        if (report && p.err) atomicOr(p.err, bad);
+      if (const int bad = resolve_seq(p, b, &s)) {
+        if (lane == 0 && p.err) atomicOr(p.err, bad);
         continue;
       }
-      if (!segment_of<kOut>(p, s, unit.seg, &unit.segs, &unit.n)) continue;
-      unit.row = s.start + unit.seg * p.seg_len;
-      unit.src = s.src;
-      unit.dst = s.dst;
+      int seg;
+      if (!slot || !in_slot(p, s, item, &seg)) seg = segments_of(p, s) - 1;
+      unit.row = s.start + seg * p.seg_len;
+      const int left = s.len - seg * p.seg_len;
+      unit.n = left < p.seg_len ? left : p.seg_len;
+      unit.from = nullptr;
+      unit.to = unit.decay = nullptr;
+      if (s.len > p.seg_len) {
+        const int64_t page = ws_index(p, unit.row, !slot, unit.head);
+        if (kOut) {
+          unit.from = p.ws_state + page * kPage;
+        } else {
+          unit.to = p.ws_state + page * kPage;
+          unit.decay = p.ws_decay + page;
+        }
+      } else if (s.src) {
+        unit.from = page_of(p.state, s.src, p.heads, unit.head);
+      }
+      if (kOut && !slot && s.dst) unit.to = page_of(p.state, s.dst, p.heads, unit.head);
       return true;
     }
   }
 };
-
-// A segment's page in the workspace.  All segments but a sequence's last have
-// seg_len rows, so first_row / seg_len tells them apart; the last ones (shorter:
-// another sequence's first may start in the same seg_len rows) have pages of
-// their own behind.
-__device__ __forceinline__ int64_t ws_index(const PromptParams &p, int first_row, bool last, int h) {
-  const int64_t at = first_row / p.seg_len + (last ? p.tokens / p.seg_len + 1 : 0);
-  return at * p.heads + h;
-}
-__device__ __forceinline__ int64_t ws_index(const PromptParams &p, const Unit &u) {
-  return ws_index(p, u.row, u.seg == u.segs - 1, u.h);
-}
 
 // The next chunk of a role (a whole warp; m counts them).  False: no more.
 __device__ __forceinline__ bool next_move(Ctrl &c, uint32_t &m, Move &move, int lane) {
@@ -537,10 +594,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (smem_addr(smem) & 1023u) c.abort = 1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  const int64_t all_units = static_cast<int64_t>(p.seqs) * p.segs * p.heads;
-  const bool sorted = all_units > gridDim.x && p.seqs * static_cast<int64_t>(p.segs) <= kThreads &&
-                      all_units <= static_cast<int64_t>(gridDim.x) * kList;
-  if (sorted) order_units<kOut>(p, reinterpret_cast<int *>(sq), c.list);
+  const int64_t items = items_of<kOut>(p), all_units = items * p.heads;
+  const bool sorted = all_units > gridDim.x && items <= kThreads &&
+                      all_units <= static_cast<int64_t>(gridDim.x) * kList &&
+                      (p.slots == 0 || p.seqs <= 64);      // (a slot looks at every sequence)
+  if (threadIdx.x < kList) c.found[threadIdx.x] = -1;
+  if (sorted) order_units<kOut>(p, reinterpret_cast<int *>(smem), c.list);
+  if (p.slots > 0) {
+    __syncthreads();
+    find_slots<kOut>(p, sorted ? c.list : nullptr, c.found);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -654,34 +717,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 2) {
       // -------------------------------------- the work, and its decay tables
-      Walk<kOut> it(p, sorted ? c.list : nullptr);
+      Walk<kOut> it(p, sorted ? c.list : nullptr, c.found);
       Info next;
       int t = 0;                                           // tokens of the unit handed out
       bool unit = false;
       // the next chunk into `next`, and its decays (4 a lane)
       auto look = [&](float (&g)[4]) {
         if (!unit) {
-          if (!it.next(lane == 0)) {
+          if (!it.next(lane)) {
             next = Info{-1};
             g[0] = g[1] = g[2] = g[3] = 0.0f;
             return;
           }
-          const Unit &u = it.unit;
-          next.head = u.h;
-          next.from = nullptr;
-          next.to = next.decay = nullptr;
-          if (!kOut || u.segs > 1) {
-            float *page = p.ws_state + ws_index(p, u) * kPage;
-            if (kOut) {
-              next.from = page;
-            } else {
-              next.to = page;
-              next.decay = p.ws_decay + ws_index(p, u);
-            }
-          } else if (u.src) {
-            next.from = page_of(p.state, u.src, p.heads, u.h);
-          }
-          if (kOut && u.seg == u.segs - 1 && u.dst) next.to = page_of(p.state, u.dst, p.heads, u.h);
+          next.head = it.unit.head;
+          next.from = it.unit.from;
+          next.to = it.unit.to;
+          next.decay = it.unit.decay;
           t = 0;
         }
         const int left = it.unit.n - t;
@@ -1131,16 +1182,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The pages that the segments of split sequences start from, in place of their
 // contributions: S_0 = the sequence's first page, S_(g+1) = 2^decay_g S_g + U_g.
-// Each thread walks 4 elements of a page over the segments, eight segments'
-// loads in flight (one at a time, 19 segments of 32 heads took 227 us).
-__global__ void __launch_bounds__(256) segment_kernel(const __grid_constant__ PromptParams p) {
+// A block takes a sequence or, where there are fewer, a slot, and has work if the
+// slot's segment is a sequence's first (200 short sequences beside a split one cost
+// 100 us in blocks that find nothing).  Each thread walks 4 elements of a page over
+// the segments, eight segments' loads in flight (one at a time, 19 segments of 32
+// heads took 227 us instead of 15).
+__global__ void __launch_bounds__(kSegmentThreads)
+    segment_kernel(const __grid_constant__ PromptParams p) {
   constexpr int kBatch = 8;
   const int part = blockIdx.x % kSegmentBlocks, item = blockIdx.x / kSegmentBlocks;
-  const int b = item / p.heads, h = item % p.heads;
+  const int h = item % p.heads;
   Seq seq;
-  if (resolve_seq(p, b, &seq) || seq.len <= p.seg_len) return;
+  if (p.seqs <= p.slots) {
+    if (resolve_seq(p, item / p.heads, &seq) || seq.len <= p.seg_len) return;
+  } else {
+    __shared__ int found;
+    if (threadIdx.x == 0) found = -1;
+    __syncthreads();
+    for (int b = threadIdx.x, seg; b < p.seqs; b += kSegmentThreads)
+      if (!resolve_seq(p, b, &seq) && in_slot(p, seq, item / p.heads, &seg) && seg == 0) found = b;
+    __syncthreads();
+    if (found < 0) return;
+    resolve_seq(p, found, &seq);
+  }
   const int last = (seq.len + p.seg_len - 1) / p.seg_len - 1;
-  const int at = part * 256 + threadIdx.x;
+  const int at = part * kSegmentThreads + threadIdx.x;
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (seq.src) s = reinterpret_cast<const float4 *>(page_of(p.state, seq.src, p.heads, h))[at];
   // (full segments' pages are heads apart)
@@ -1222,15 +1288,18 @@ int launch_chunked(const PromptParams &p, int qk_heads, int dev, int sms, cudaSt
       !set_smem_limit_once(seg_done, dev, reinterpret_cast<const void *>(chunk_kernel<false>),
                            kSmem))
     return KDA_ERR_LAUNCH;
-  const int64_t units = static_cast<int64_t>(p.seqs) * p.segs * p.heads;
-  const int grid = units < sms ? static_cast<int>(units) : sms;
-  if (p.segs > 1) {
-    chunk_kernel<false><<<grid, kThreads, kSmem, stream>>>(p, q, k, v, o);
+  if (static_cast<int64_t>(p.slots) * p.heads > static_cast<int64_t>(kList) * sms)
+    return KDA_ERR_SHAPE;  // (find_slots; not on a whole GPU)
+  auto grid_of = [&](int64_t items) {
+    return static_cast<int>(items * p.heads < sms ? items * p.heads : sms);
+  };
+  if (p.slots > 0) {
+    chunk_kernel<false><<<grid_of(p.slots), kThreads, kSmem, stream>>>(p, q, k, v, o);
     if (cudaGetLastError() != cudaSuccess) return KDA_ERR_LAUNCH;
-    segment_kernel<<<p.seqs * p.heads * kSegmentBlocks, 256, 0, stream>>>(p);
+    segment_kernel<<<(p.seqs < p.slots ? p.seqs : p.slots) * p.heads * kSegmentBlocks, kSegmentThreads, 0, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return KDA_ERR_LAUNCH;
   }
-  chunk_kernel<true><<<grid, kThreads, kSmem, stream>>>(p, q, k, v, o);
+  chunk_kernel<true><<<grid_of(static_cast<int64_t>(p.slots) + p.seqs), kThreads, kSmem, stream>>>(p, q, k, v, o);
   return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
 }
 

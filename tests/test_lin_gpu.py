@@ -108,6 +108,18 @@ def test_long_sequences_in_segments(lens, H, Hk, per_token):
     verify(inp, launch(inp, src=src, dst=dst, max_seq=max(lens)), 2, src, dst)
 
 
+@pytest.mark.parametrize("lens,max_seq", [([1500] + [7, 40, 0] * 27 + [1400, 300], 1500),
+                                          ([60, 129] * 20, None)], ids=["mixed", "loose bound"])
+def test_split_sequences_among_many(lens, max_seq):
+    """Two split sequences among 81 short ones, and a bound on the lengths that
+    would allow splits where there are none."""
+    B = len(lens)
+    inp = make(lens, 2, 2, slots=2 * B + 1, seed=24, scale_g=0.1)
+    src = [r + 1 if r % 3 else 0 for r in range(B)]
+    dst = [B + 1 + r for r in range(B)]
+    verify(inp, launch(inp, src=src, dst=dst, max_seq=max_seq), 2, src, dst)
+
+
 def test_segments_of_many_chunks():
     """Segments of 7 chunks (every buffer comes round), checked on two heads."""
     H, n, heads = 64, 8192 + 77, (5, 63)
