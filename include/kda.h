@@ -288,7 +288,7 @@ int kda_oproj(const kda_oproj_args *args, void *stream);
 /* Arguments of one prompt call (kda_lin_prompt). */
 typedef struct kda_lin_prompt_args {
   int32_t seqs;             /* sequences (0 is a no-op)                        */
-  int32_t heads;            /* value heads H (0 is a no-op)                    */
+  int32_t heads;            /* value heads H, <= 65536 (0 is a no-op)          */
   int32_t qk_heads;         /* query / key heads, a divisor of heads           */
   int32_t tokens;           /* rows of q, k, v and output                      */
   int32_t max_seq;          /* no sequence is longer than this                 */
@@ -325,10 +325,15 @@ int64_t kda_lin_prompt_workspace(const kda_lin_prompt_args *args);
 /* Prompt form over ragged sequences, chunked: a sequence's outputs and last
  * state from its first state.  Rows that no sequence covers are left as they
  * are; a sequence without tokens copies its first state.  A sequence with a
- * flagged slot (KDA_DEVERR_SLOT) or range (KDA_DEVERR_SEQ) writes nothing.
- * Sequences must not overlap.  A non-finite value in a live row may reach
+ * flagged slot (KDA_DEVERR_SLOT) or range (KDA_DEVERR_SEQ) writes nothing.  A
+ * non-finite value in a live row may reach
  * every output of its 128-token chunk and what follows it; rows outside the
- * sequence reach nothing.  Up to three kernels on `stream`, in order. */
+ * sequence reach nothing.  The output must not overlap the inputs.  The page is
+ * held and updated in FP32; products that only feed the BF16 output are rounded to
+ * BF16 once.  Errors: KDA_ERR_NULL_ARGS, KDA_ERR_NULL_POINTER, KDA_ERR_SHAPE (sizes
+ * and strides outside the rules above), KDA_ERR_PATH, KDA_ERR_ALIGNMENT,
+ * KDA_ERR_WORKSPACE, KDA_ERR_DEVICE, KDA_ERR_LAUNCH; nothing is launched on error.
+ * Up to three kernels on `stream`, in order. */
 int kda_lin_prompt(const kda_lin_prompt_args *args, void *stream);
 
 /* Arguments of one single-token step (kda_lin_step). */

@@ -37,17 +37,25 @@
 //   Shared memory: Q, K, V double-buffered (32 KiB tiles, 128-byte swizzle) and
 //   the page's BF16 copy; O leaves through Q's tile.
 //
-// What bounds it (GB300, one sequence of 32749 tokens, 32 heads): 184 us for the
-// pass with outputs = 3.4 us a chunk and SM, 5.9 TB/s (0.86 of the copy peak); with
-// keys and queries shared by 8 heads (16 sequences x 64 heads, 185 us) the bytes
-// halve and the time does not: a chunk moves about 480 KB through shared memory
-// (MMA operands 256 KB), 3.8k of its 5.3k cycles, the tensor pipe is busy for 45%
-// and the schedulers issue in 55% of the cycles.  Roles were made short where
-// they could be: unrolled roles missed the instruction cache (7.9 warps waiting for
-// instructions per issue; 375 us at the start).  Not kept, measured there: K'' in
-// four parts from packed BF16 products (fewer instructions, a third more products
-// for U: 205 us), next tiles prefetched to L2 (205 us), one MMA warp for all
-// products (211 us), the issue loops rolled (232 us).
+// Split sequences.  A sequence much longer than an SM's share is cut into segments:
+// chunk_kernel<false> sums each segment's own contribution to the page (from zeros),
+// segment_kernel turns those into the pages the segments start from, and
+// chunk_kernel<true> runs the segments side by side.
+//
+// What bounds it (GB300).  One sequence of 32749 tokens, 32 heads: 185 us for the
+// pass with outputs = 3.4 us a chunk and SM, 5.9 TB/s (0.86 of the copy's rate),
+// 113 us for the pass without (4.7 TB/s), 16 us between.  With keys and queries
+// shared by 8 heads (16 sequences x 64 heads, 188 us) the bytes halve and the time
+// does not: a chunk moves about 480 KB through shared memory (MMA operands 256 KB),
+// 3.8k of its 5.3k cycles at 128 bytes a cycle, the tensor pipe is busy for 43-48%
+// of the time and K'' takes one warpgroup pair 4.8k cycles.  What made it fast:
+// roles short enough for the instruction cache (unrolled and each walking the work
+// for itself 377 us, 7.9 warps waiting for instructions per issue; then 231), K''
+// and the outputs over two warpgroups each (212), units dealt by length (190).
+// Not kept, measured there: K'' in four parts from packed BF16 products (fewer
+// instructions, a third more products for U: 205 us), the next tiles prefetched to
+// L2 (205 us), one MMA warp for all products (211 us), the issue loops rolled (232
+// us), the next keys loaded ahead (spills: 197-213 us).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
