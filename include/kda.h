@@ -316,17 +316,18 @@ typedef struct kda_lin_prompt_args {
   int64_t workspace_bytes;  /* at least kda_lin_prompt_workspace(args)         */
 } kda_lin_prompt_args;
 
-/* Bytes of workspace that kda_lin_prompt needs for these sizes (`seqs`,
- * `heads`, `tokens`, `max_seq`, `path` are read), 0 for none or for sizes that
- * it refuses; -1 when args is NULL.  The workspace holds nothing between
+/* Bytes of workspace that kda_lin_prompt needs for args' sizes and strides (no
+ * pointer is followed), 0 for none or for sizes that it refuses; -1 when args is
+ * NULL.  The workspace holds nothing between
  * calls; calls that may run at the same time need their own. */
 int64_t kda_lin_prompt_workspace(const kda_lin_prompt_args *args);
 
 /* Prompt form over ragged sequences, chunked: a sequence's outputs and last
  * state from its first state.  Rows that no sequence covers are left as they
  * are; a sequence without tokens copies its first state.  A sequence with a
- * flagged slot (KDA_DEVERR_SLOT) or range (KDA_DEVERR_SEQ) writes nothing.  A
- * non-finite value in a live row may reach
+ * flagged slot (KDA_DEVERR_SLOT) or range (KDA_DEVERR_SEQ) writes nothing; starts
+ * out of order can make other sequences share rows, whose outputs are then any of
+ * theirs.  A non-finite value in a live row may reach
  * every output of its 128-token chunk and what follows it; rows outside the
  * sequence reach nothing.  The output must not overlap the inputs.  The page is
  * held and updated in FP32; products that only feed the BF16 output are rounded to

@@ -327,19 +327,19 @@ def _rows(name, t, rows, width, index):
     """(address, row stride) of a BF16 CUDA tensor [rows, width] whose rows may be
     slices of wider rows: elements of a row adjacent, any row stride that the
     library takes."""
-    if _cuda_index(name, t) != index:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.shape != (rows, width):
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16
+            and t.get_device() == index and t.shape == (rows, width)):
+        if _cuda_index(name, t) != index:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+        if t.dtype is not torch.bfloat16:
+            raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
         raise ValueError(f"{name} must have shape {(rows, width)}, got {tuple(t.shape)}")
     step, one = t.stride()
     if rows <= 1:
         step = width
-    if one != 1 or step % 8 or step < width:
-        if width:
-            raise ValueError(f"{name}: the elements of a row must be adjacent and rows a "
-                             f"multiple of 8 elements apart, got strides {tuple(t.stride())}")
+    if (one != 1 or step % 8 or step < width) and width:
+        raise ValueError(f"{name}: the elements of a row must be adjacent and rows a "
+                         f"multiple of 8 elements apart, got strides {tuple(t.stride())}")
     return t.data_ptr(), step
 
 
@@ -427,13 +427,11 @@ def kda_lin_prompt(*, q, k, v, decay, seq_starts, output, scale: float, state=No
     if workspace is not None:
         a.workspace = _want("workspace", workspace, torch.uint8, None, index)
         a.workspace_bytes = workspace.numel()
-    else:
-        need = _lib.prompt_workspace(a)
-        if need > 0:
-            # from the pool of the stream that uses it: freed behind its kernels
-            with torch.cuda.device(index), torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
-            a.workspace, a.workspace_bytes = workspace.data_ptr(), need
+    elif (need := _lib.prompt_workspace(a)) > 0:
+        # from the pool of the stream that uses it: freed behind its kernels
+        with torch.cuda.device(index), torch.cuda.stream(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), need
     _run("kda_lin_prompt", a, index, stream)
 
 

@@ -240,3 +240,19 @@ def test_quantiser_reference():
         c, s = linref.quantise(x, bits)
         off = np.abs(linref.dequantise(c, s) - x).reshape(4, s.shape[-1], -1)
         assert np.all(off <= s[..., None] * (0.5 + 1e-6)) and np.abs(c).max() == top
+
+
+def test_workspace_sizes():
+    """None for whole sequences, some for split ones (pages of the segments and
+    their decays), none for refused sizes; a missing or short one is refused."""
+    assert kl.load().kda_lin_prompt_workspace(None) == -1
+    assert kl.prompt_workspace(prompt_args()) == 0
+    assert kl.prompt_workspace(prompt_args(heads=-1)) == 0
+    split = dict(seqs=1, tokens=20000, max_seq=20000)
+    need = kl.prompt_workspace(prompt_args(**split))
+    assert need > 0 and need % ((128 * 128 + 1) * 4 * 4) == 0
+    assert kl.prompt_workspace(prompt_args(path=1, **split)) == 0
+    assert kl.prompt_workspace(prompt_args(**dict(split, max_seq=200))) == 0
+    for kw in (dict(), dict(workspace=FAKE, workspace_bytes=need - 1),
+               dict(workspace=FAKE + 128, workspace_bytes=need)):
+        assert kl.call("kda_lin_prompt", prompt_args(**split, **kw), 0) == kl.KDA_ERR_WORKSPACE
