@@ -4,14 +4,14 @@
 // Both forms keep a page slice in registers: a warp holds 8 value rows, lane l
 // the keys 4l .. 4l+3 of each (a row is one 512-byte access of the warp), so that
 // S q needs one reduce-scatter for 8 rows.  A product v k is of two BF16 values
-// and exact in FP32.
+// and exact in FP32; the decay is applied as decay_of says.
 //
 // The step is HBM-bound (a page read and written per item, 128 KiB against
 // 160 kflop).  CTAs of two warps, an eighth of a page each: all loads of a
 // thread are in flight at once and the many small CTAs of an SM keep its
 // memory queue full without a pipeline; a batch of few requests still spreads
 // over the SMs.  GB300: 256 requests x 32 heads 159 us = 6.8 TB/s, the copy's
-// rate (16 rows a warp: 160 us); 64 x 32 with 8 padded 38.8 us (0.90); 4 x 8 2.5 us,
+// rate (16 rows a warp: 160 us); 64 x 32 with 8 padded 38.6 us (0.90); 4 x 8 2.3 us,
 // a launch.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -61,8 +61,8 @@ __global__ void __launch_bounds__(kWarps * 32) step_kernel(const __grid_constant
   unpack4(__ldg(reinterpret_cast<const uint2 *>(p.k + r * p.k_stride + h / p.group * kDim) + lane), k);
   unpack4(__ldg(reinterpret_cast<const uint2 *>(p.q + r * p.q_stride + h / p.group * kDim) + lane), q);
   const float v = __bfloat162float(p.v[r * p.v_stride + h * kDim + row0 + (lane & (kRows - 1))]);
-  const float d =
-      expf(__ldg(p.decay + (p.decay_rows ? static_cast<int64_t>(r) * p.heads : 0) + h));
+  const Decay d =
+      decay_of(__ldg(p.decay + (p.decay_rows ? static_cast<int64_t>(r) * p.heads : 0) + h));
   const float o = token_step(s, d, k, q, v, lane);
 #pragma unroll
   for (int i = 0; i < kRows; ++i) __stcs(page + i * 32, s[i]);
@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(kWarps * 32)
   float gn = 0.0f;
   for (int t = 0; t <= seq.len; ++t) {
     const uint2 kc = kn, qc = qn;
-    const float v = __bfloat162float(vn), d = expf(gn);
+    const float v = __bfloat162float(vn);
+    const Decay d = decay_of(gn);
     if (t < seq.len) {
       kn = __ldg(kp);
       qn = __ldg(qp);
@@ -205,10 +206,11 @@ struct Plan {
 };
 
 // Short sequences take the recurrent form, which reads each page once and starts
-// at once.  8 tokens: 5.2 us against 7.5 chunked (32 items of 128 x 128), 7.4
-// against 8.0 (128 items), 83 against 78 (2048 items); 12 tokens: 6.7 against 7.5,
-// 9.6 against 8.0 and 109 against 79.
-constexpr int kRecurrentMost = 8, kRecurrentMostFew = 12, kFewItems = 64;
+// at once.  12 tokens: 7.5 us against 7.7 chunked (32 items of 128 x 128), 11.1
+// against 8.2 (128 items), 123 against 76 (2048 items); 8 tokens: 5.7 against 7.7,
+// 8.4 against 8.2 and 91 against 76; 4 tokens: 4.0 against 7.7, 5.6 against 8.2 and 62
+// against 75.
+constexpr int kRecurrentMost = 6, kRecurrentMostFew = 12, kFewItems = 64;
 constexpr int kShares = 152;            // SMs that the work is shared among
 constexpr int kShortestSegment = 256;   // tokens
 constexpr int kSplitCost = 896;         // of splitting, in tokens of one head

@@ -68,19 +68,31 @@ __device__ __forceinline__ void unpack4(const uint2 &u, float (&f)[4]) {
   f[3] = __uint_as_float(u.y & 0xFFFF0000u);
 }
 
+// A token's decay exp(g) as keep + change, keep 0 or 1.  Rounded to FP32, a factor
+// near 1 is off by up to 2^-25 the same way at every token: over the 12000 tokens
+// of a slow head 1e-4 of the page.  exp(g) - 1 is off by 2^-25 of itself.
+struct Decay {
+  float keep, change;
+};
+__device__ __forceinline__ Decay decay_of(float g) {
+  const float less = expm1f(g);
+  const bool slow = less > -0.5f;
+  return Decay{slow ? 1.0f : 0.0f, slow ? less : expf(g)};
+}
+
 // One token on a warp's kRows value rows: lane l holds keys 4l .. 4l+3 of each
 // row.  vrow: lane r < kRows holds v of row r.  Returns S q of row lane / kSpan
 // (FP32, unscaled).
-__device__ __forceinline__ float token_step(float4 (&s)[kRows], float d, const float (&k)[4],
+__device__ __forceinline__ float token_step(float4 (&s)[kRows], const Decay &d, const float (&k)[4],
                                             const float (&q)[4], float vrow, int lane) {
   float dot[kRows];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     const float v = __shfl_sync(0xffffffffu, vrow, r);
-    s[r].x = __fmaf_rn(s[r].x, d, v * k[0]);
-    s[r].y = __fmaf_rn(s[r].y, d, v * k[1]);
-    s[r].z = __fmaf_rn(s[r].z, d, v * k[2]);
-    s[r].w = __fmaf_rn(s[r].w, d, v * k[3]);
+    s[r].x = __fmaf_rn(s[r].x, d.keep, __fmaf_rn(s[r].x, d.change, v * k[0]));
+    s[r].y = __fmaf_rn(s[r].y, d.keep, __fmaf_rn(s[r].y, d.change, v * k[1]));
+    s[r].z = __fmaf_rn(s[r].z, d.keep, __fmaf_rn(s[r].z, d.change, v * k[2]));
+    s[r].w = __fmaf_rn(s[r].w, d.keep, __fmaf_rn(s[r].w, d.change, v * k[3]));
     dot[r] = __fmaf_rn(s[r].w, q[3],
                        __fmaf_rn(s[r].z, q[2], __fmaf_rn(s[r].y, q[1], s[r].x * q[0])));
   }

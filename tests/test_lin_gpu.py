@@ -470,6 +470,23 @@ def test_prepared_step_repeats_and_replays():
     assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
 
 
+@pytest.mark.parametrize("path", PATHS)
+def test_slow_decays_over_many_tokens(path):
+    """A decay near 1, the same at every token, does not drift: the last page
+    after 6000 tokens is within 2e-6 of the 64-bit recurrence (2-norm).  A token
+    rounds the page twice, at random (6000 ** 0.5 * 2 ** -24 = 5e-6 if all of them
+    stayed; with a decay of exp(-1e-3) the last 1000 do: 2e-6, times the share of
+    a uniform rounding error, 3 ** -0.5); a factor rounded to FP32 would be off by
+    up to 2 ** -25 every time, 3e-5."""
+    n = 6000
+    inp = make([n], 1, 1, slots=3, seed=25)
+    inp["decay"] = torch.full((1,), -1e-3)
+    _, state = launch(inp, src=[1], dst=[2], path=path)
+    _, _, S, _ = linref.prompt(inp["q"], inp["k"], inp["v"], inp["decay"], [0, n], 0.5,
+                               inp["state"], [1])
+    assert float((state[2].double() - S[0]).norm() / S[0].norm()) < 2e-6
+
+
 def test_prompt_recurrent_form_equals_steps_bitwise():
     """The recurrent prompt form is the step token by token: the same bits."""
     inp = make([11], 3, 3, slots=3, seed=13)
