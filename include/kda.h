@@ -327,10 +327,10 @@ int64_t kda_lin_prompt_workspace(const kda_lin_prompt_args *args);
  * are; a sequence without tokens copies its first state.  A sequence with a
  * flagged slot (KDA_DEVERR_SLOT) or range (KDA_DEVERR_SEQ) writes nothing; starts
  * out of order can make other sequences share rows, whose outputs are then any of
- * theirs.  A non-finite value in a live row may reach
- * every output of its 128-token chunk and what follows it; rows outside the
- * sequence reach nothing.  The output must not overlap the inputs.  The page is
- * held and updated in FP32; products that only feed the BF16 output are rounded to
+ * theirs.  An infinity or NaN in a live row reaches what the formulas send it
+ * to, its own and later tokens of its sequence and head, as an infinity or NaN;
+ * rows outside the sequence reach nothing.  The output must not overlap the
+ * inputs.  The page is held and updated in FP32; products that only feed the BF16 output are rounded to
  * BF16 once.  Errors: KDA_ERR_NULL_ARGS, KDA_ERR_NULL_POINTER, KDA_ERR_SHAPE (sizes
  * and strides outside the rules above), KDA_ERR_PATH, KDA_ERR_ALIGNMENT,
  * KDA_ERR_WORKSPACE, KDA_ERR_DEVICE, KDA_ERR_LAUNCH; nothing is launched on error.

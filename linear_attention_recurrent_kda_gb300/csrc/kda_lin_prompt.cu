@@ -26,6 +26,14 @@
 // only feed an output that is itself rounded to BF16, and the FP32 sum keeps
 // their errors at that size.
 //
+// Infinities and NaN.  P V multiplies the values of later tokens by zeros, and
+// 0 * NaN is not 0.  So P V runs after the page's warps have read the chunk's
+// update, where an odd value shows in every key of its column: they put zeros in
+// V's place for it, and the outputs of the column are NaN from that token on.
+// That costs 1-3% (1-3 us of 72 and 189, 12 of 407 where pages are carried);
+// looking at V itself, by whichever warps, cost 4-25%: shared memory and
+// instructions are what the kernel is short of.
+//
 // Roles (768 threads, 24 warps): TMA loads and stores (warp 0), MMA issue for the
 // page (U; warp 1) and for the outputs (A, Q S^T, P V; warp 3), the work and its
 // decay tables (warp 2); five warpgroups: P and O (4-11, 64 columns a warp), K''
@@ -115,13 +123,15 @@ struct Ctrl {
   uint64_t empty_k[3], empty_v[3];
   uint64_t st_full[2];                           // O staged in Q's tile (or written)
   uint64_t tab_full[2], tab_empty[2];
-  uint64_t v_ok[2];                              // V there, zeros behind the end
+  uint64_t v_ok[2];                              // V there: zeros behind the end, finite
   uint64_t kq_full[4], kq_empty[4];              // K'' quarters in TMEM
   uint64_t u_full[2], u_empty[2];
   uint64_t a_full, p_full, qs_full, o_full, o_empty, s_full;
   uint32_t list[kList];                          // the CTA's first units, where sorted
   int found[kList];                              // the sequence of each that is a slot's, or -1
   uint32_t tmem, abort;
+  uint8_t odd_row[2][kDim];                      // an odd column's first non-finite row
+  uint8_t odd[2][4];                             // whether 32 columns of V have one
 };
 
 constexpr int kSmem = 7 * kTile + sizeof(Ctrl);
@@ -309,8 +319,6 @@ __device__ __forceinline__ uint32_t pack2(f32x2 v) {
   unpair(v, lo, hi);
   return pack2(lo, hi);
 }
-__device__ __forceinline__ float low_half(uint32_t r) { return __uint_as_float(r << 16); }
-__device__ __forceinline__ float high_half(uint32_t r) { return __uint_as_float(r & 0xFFFF0000u); }
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -324,13 +332,39 @@ __device__ __forceinline__ uint32_t tile_at(int row, int group) {
   return static_cast<uint32_t>((group >> 3) * kHalf + row * 128 + (((group & 7) ^ (row & 7)) << 4));
 }
 
-__device__ __forceinline__ uint32_t upper_halves(f32x2 v) {
-  return __byte_perm(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32), 0x7632);
-}
 __device__ __forceinline__ f32x2 raw_pair(uint32_t lo, uint32_t hi) {
   f32x2 r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
   return r;
+}
+
+// Notes the first row with an infinity or NaN (255: none) of each of a warp's 32
+// columns of V, and puts zeros in their places.  A lane looks at 8 columns, every
+// 8th row.
+__device__ __forceinline__ void clear_odd(uint8_t *tile, int w4, int lane, int rows,
+                                          uint8_t (&odd_row)[kDim]) {
+  const int row = (lane & 4) + (lane >> 3);
+  uint8_t *at = tile + tile_at(row, 4 * w4 + (lane & 3));
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i, at += 4) {                // 2 columns at a time
+    uint32_t first = 0xFFFFu;                           // a byte a column
+#pragma unroll 1
+    for (int k = 15; k >= 0; --k) {
+      const uint32_t r = row + 8 * k;
+      if (r >= static_cast<uint32_t>(rows)) continue;
+      uint32_t *to = reinterpret_cast<uint32_t *>(at + 1024 * k);
+      const uint32_t x = *to, lo = (x & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u,
+                     hi = (x & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
+      if (lo) first = (first & 0xFF00u) | r;
+      if (hi) first = (first & 0xFFu) | r << 8;
+      if (lo | hi) *to = x & ~(lo | hi);
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1)
+      first = __vminu4(first, __shfl_xor_sync(0xffffffffu, first, o));
+    if (lane < 4)
+      *reinterpret_cast<uint16_t *>(odd_row + 32 * w4 + 8 * lane + 2 * i) = first;
+  }
 }
 
 // P of a chunk with strong decays, 64 columns (`side`) of a warp's 32 rows: a row
@@ -576,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.full_q[i], 1);
       mbar_init(&c.st_full[i], 8);
-      mbar_init(&c.v_ok[i], 4);
+      mbar_init(&c.v_ok[i], 8);
       mbar_init(&c.tab_full[i], 1);
       mbar_init(&c.tab_empty[i], 20);
       mbar_init(&c.u_full[i], 1);
@@ -618,8 +652,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = c.tmem;
 
 // A wait that ran out leaves the role's loop; whole warps leave together.
-#define KDA_WAIT(bar, parity)                        \
-  if (!wait_phase(&(bar), (parity), &c.abort)) break
 #define KDA_WAIT_WARP(bar, parity)                                                \
   if (!__all_sync(0xffffffffu, wait_phase(&(bar), (parity), &c.abort))) break
 
@@ -992,6 +1024,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        if (*reinterpret_cast<const uint32_t *>(c.odd[buf])) {
+          // columns with infinities or NaN in V: zeros stood in for them
+#pragma unroll 1
+          for (int x = 0; x < 64; ++x) {
+            const int col = 64 * side + x;
+            if (!c.odd[buf][col >> 5] || c.odd_row[buf][col] > i) continue;
+            if (full)
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(
+                               tile + (((x >> 3) ^ (lane & 7)) << 4) + (x & 7) * 2),
+                           "h"(static_cast<uint16_t>(0x7FFF))
+                           : "memory");
+            else if (i < rows)
+              to[x] = __ushort_as_bfloat16(0x7FFF);
+          }
+        }
         tc_fence_before();
         fence_proxy_async_smem();
         __syncwarp();
@@ -1145,17 +1192,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         KDA_WAIT_WARP(c.u_full[ub], n / C::kU & 1);
         tc_fence_after();
         uint32_t u[32];
+        f32x2 odd2 = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           tc_ld(col_u + 32 * j, u);
           tc_wait_ld(u);
 #pragma unroll
-          for (int m = 0; m < 16; ++m)
-            s[16 * j + m] = fma2(s[16 * j + m], keep2, raw_pair(u[2 * m], u[2 * m + 1]));
+          for (int m = 0; m < 16; ++m) {
+            const f32x2 x = raw_pair(u[2 * m], u[2 * m + 1]);
+            s[16 * j + m] = fma2(s[16 * j + m], keep2, x);
+            if (kOut) odd2 = fma2(x, 0, odd2);
+          }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&c.u_empty[ub]);
+        if (kOut) {
+          // the update has read V, and shows whether there is an infinity or NaN in
+          // it (a key's, or an overflow, finds none)
+          const int buf = n & 1;
+          float x, y;
+          unpair(odd2, x, y);
+          const bool odd = __any_sync(0xffffffffu, !(x + y == 0.0f));
+          if (odd) {
+            clear_odd(sv + buf * kTile, w4, lane, info.rows, c.odd_row[buf]);
+            fence_proxy_async_smem();
+          }
+          if (lane == 0) c.odd[buf][w4] = odd;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c.v_ok[buf]);
+        }
         ++n;
       }
       if (info.last && info.to) {
@@ -1172,7 +1238,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   }
 #undef KDA_WAIT_WARP
-#undef KDA_WAIT
 
   __syncthreads();
   if (*abort_flag) {

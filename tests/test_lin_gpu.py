@@ -192,6 +192,76 @@ def test_rows_outside_a_sequence_reach_nothing(path, bad):
 
 
 @pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("strong", [False, True])
+def test_non_finite_values_reach_no_earlier_token(path, bad, strong):
+    """Infinities and NaN among a sequence's own values: the tokens before, the
+    other columns, heads and sequences stay as they are without them, the column
+    itself is non-finite from there on."""
+    lens = [300, 128, 70, 5]
+    inp = make(lens, 2, 1, slots=9, seed=31, scale_g=6.0 if strong else 0.3)
+    src, dst = [1, 2, 0, 4], [5, 6, 7, 8]
+    clean = launch(inp, src=src, dst=dst, path=path)
+    # (token, column): ends of chunks, of 8, 32 and 64 columns, twice in one column
+    places = [(127, 0), (128, 7), (255, 8), (130, 31), (250, 31), (299, 63), (0, 64), (260, 127),
+              (150, 128 + 5), (300, 33), (427, 200), (428 + 33, 255), (428 + 69, 1), (498, 90)]
+    dirty = dict(inp, v=inp["v"].clone())
+    for t, col in places:
+        dirty["v"][t, col] = bad
+    got = launch(dirty, src=src, dst=dst, path=path)
+    out, state = clean[0].clone(), clean[1].clone()
+    gone = torch.zeros(out.shape, dtype=torch.bool)
+    rows_gone = torch.zeros(state.shape[:3], dtype=torch.bool)
+    for t, col in places:
+        r = max(i for i in range(4) if inp["starts"][i] <= t)
+        gone[t:inp["starts"][r + 1], col] = True
+        rows_gone[dst[r], col // D, col % D] = True
+    assert not torch.any(torch.isfinite(got[0][gone]))
+    assert torch.equal(got[0][~gone], out[~gone])
+    assert not torch.any(torch.isfinite(got[1][rows_gone]))
+    assert torch.equal(got[1][~rows_gone], state[~rows_gone])
+
+
+def test_non_finite_values_in_segments():
+    """The same in a sequence that is split."""
+    inp = make([1300], 1, 1, slots=2, seed=32, scale_g=0.05)
+    clean = launch(inp, dst=[1], path=2)
+    v = inp["v"].clone()
+    v[700, 3], v[1290, 100] = float("nan"), float("inf")
+    got = launch(dict(inp, v=v), dst=[1], path=2)
+    gone = torch.zeros(v.shape, dtype=torch.bool)
+    gone[700:, 3] = gone[1290:, 100] = True
+    assert not torch.any(torch.isfinite(got[0][gone]))
+    assert torch.equal(got[0][~gone], clean[0][~gone])
+    assert not torch.any(torch.isfinite(got[1][1, 0, [3, 100]]))
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("name", ["q", "k", "decay"])
+def test_non_finite_inputs_reach_no_earlier_token(path, name):
+    """A NaN query spoils its own token's outputs, a NaN key or decay its own
+    and the later ones of its sequence and head."""
+    inp = make([300, 20], 2, 2, slots=3, seed=33)
+    clean = launch(inp, dst=[1, 2], path=path)
+    x = inp[name].clone()
+    x[170, 1 if name == "decay" else 200] = float("nan")
+    got = launch(dict(inp, **{name: x}), dst=[1, 2], path=path)
+    gone = torch.zeros(got[0].shape, dtype=torch.bool)
+    gone[170:171 if name == "q" else 300, 128:] = True
+    assert torch.all(torch.isnan(got[0][gone]))
+    same = ~gone
+    if path == 2 and name == "decay":
+        # (the chunk's factors take another form beside a NaN: within the bound instead)
+        same[128:170, 128:] = False
+        ref, mag, _, _ = linref.prompt(inp["q"], inp["k"], inp["v"], inp["decay"], inp["starts"],
+                                       0.5)
+        at = (slice(128, 170), slice(128, 256))
+        off = (got[0][at].double() - ref[at]).abs()
+        assert torch.all(off <= linref.out_bound(ref[at], mag[at], 300, True))
+    assert torch.equal(got[0][same], clean[0][same])
+
+
+@pytest.mark.parametrize("path", PATHS)
 def test_slices_of_wider_rows(path):
     """q, k and v as column slices of one projection, the output as a slice too."""
     inp = make([200, 37], 2, 2, slots=3, seed=9)
