@@ -50,10 +50,10 @@
 // segment_kernel turns those into the pages the segments start from, and
 // chunk_kernel<true> runs the segments side by side.
 //
-// What bounds it (GB300).  One sequence of 32749 tokens, 32 heads: 185 us for the
-// pass with outputs = 3.4 us a chunk and SM, 5.9 TB/s (0.86 of the copy's rate),
+// What bounds it (GB300).  One sequence of 32749 tokens, 32 heads: 192 us for the
+// pass with outputs = 3.5 us a chunk and SM, 5.7 TB/s (0.84 of the copy's rate),
 // 113 us for the pass without (4.7 TB/s), 16 us between.  With keys and queries
-// shared by 8 heads (16 sequences x 64 heads, 188 us) the bytes halve and the time
+// shared by 8 heads (16 sequences x 64 heads, 192 us) the bytes halve and the time
 // does not: a chunk moves about 480 KB through shared memory (MMA operands 256 KB),
 // 3.8k of its 5.3k cycles at 128 bytes a cycle, the tensor pipe is busy for 43-48%
 // of the time and K'' takes one warpgroup pair 4.8k cycles.  What made it fast:
@@ -63,7 +63,8 @@
 // Not kept, measured there: K'' in four parts from packed BF16 products (fewer
 // instructions, a third more products for U: 205 us), the next tiles prefetched to
 // L2 (205 us), one MMA warp for all products (211 us), the issue loops rolled (232
-// us), the next keys loaded ahead (spills: 197-213 us).
+// us), the next keys loaded ahead (spills: 197-213 us), a third warpgroup for K''
+// with 48 registers a thread (208-215 us).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
