@@ -397,14 +397,20 @@ int kda_snapshot_save(const kda_snapshot_args *args, void *stream);
  * written are distinct, a snapshot may be read into several.  Rules as above. */
 int kda_snapshot_load(const kda_snapshot_args *args, void *stream);
 
-/* Self-test of the bounded on-chip waits that every kernel above uses: one
- * CTA waits on an mbarrier that nothing completes; the wait gives up after
- * its wall-clock limit (2 s), KDA_DEVERR_TIMEOUT is OR-ed into *err (a
- * device word, 4-byte aligned) and the kernel returns -- no trap, no fault,
- * the context stays usable.  For failure-detection tests.  Returns
+/* Self-test of the bounded on-chip wait of the KDA step, the replay and the
+ * output projection: one CTA waits on an mbarrier that nothing completes; the
+ * wait gives up after its wall-clock limit (2 s), KDA_DEVERR_TIMEOUT is OR-ed
+ * into *err (a device word, 4-byte aligned) and the kernel returns -- no trap, no
+ * fault, the context stays usable.  For failure-detection tests.  Returns
  * KDA_ERR_NULL_POINTER / KDA_ERR_ALIGNMENT / KDA_ERR_LAUNCH or KDA_SUCCESS;
  * one kernel on `stream`. */
 int kda_selftest_wait_timeout(int32_t *err, void *stream);
+
+/* The same for the wait of kda_lin_prompt's chunked form (the other kernels of
+ * the linear attention and the snapshots wait for nothing on the chip): a CTA of
+ * that form's size takes TMEM, passes a completed phase, waits for one that
+ * nothing completes until the same limit, and leaves as that form leaves. */
+int kda_selftest_lin_wait_timeout(int32_t *err, void *stream);
 
 /* Static description of a return code (never NULL). */
 const char *kda_strerror(int code);

@@ -165,24 +165,30 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
 }
 // Waits for the phase of `parity`, in a dozen instructions (the roles' loops
 // share the instruction cache, and their code is what fills it).  Each try may
-// sleep for a microsecond; after 2^21 tries, or when another thread raised
-// `abort`, the wait gives up, raises it and returns false.
+// sleep for a microsecond.  After kWaitLimitNs of wall clock, or when another
+// thread raised `abort`, the wait gives up, raises it and returns false.  The
+// clock's low word is enough: tries are microseconds apart and the limit is under
+// half of what it holds.  Lanes may get different answers, so the branches are not
+// uniform ones.
+static_assert(kWaitLimitNs < (1ull << 31), "the clock's low word");
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, uint32_t *abort) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .u32 n, a;\n mov.u32 n, 2097152;\n"
+      "{\n .reg .pred p, q;\n .reg .u32 t0, t, a;\n mov.u32 t0, %%globaltimer_lo;\n"
       "again:\n"
       " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, 1000;\n"
-      " @p bra.uni done;\n"
+      " @p bra done;\n"
       " ld.volatile.shared.u32 a, [%3];\n"
-      " sub.u32 n, n, 1;\n"
-      " setp.ne.u32 q, n, 0;\n"
+      " mov.u32 t, %%globaltimer_lo;\n"
+      " sub.u32 t, t, t0;\n"
+      " setp.lt.u32 q, t, %4;\n"
       " setp.eq.and.u32 q, a, 0, q;\n"
       " @q bra again;\n"
       " st.volatile.shared.u32 [%3], 1;\n"
       "done:\n selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity), "r"(smem_addr(abort))
+      : "r"(smem_addr(bar)), "r"(parity), "r"(smem_addr(abort)),
+        "n"(static_cast<uint32_t>(kWaitLimitNs))
       : "memory");
   return ok != 0;
 }
@@ -578,6 +584,35 @@ __device__ __forceinline__ bool next_table(Ctrl &c, uint32_t m) {
 
 // -------------------------------------------------------------------- kernel
 
+// A wait that ran out leaves the role's loop; whole warps leave together.
+#define KDA_WAIT_WARP(bar, parity)                                                \
+  if (!__all_sync(0xffffffffu, wait_phase(&(bar), (parity), &c.abort))) break
+
+// TMEM, all 512 columns (one CTA per SM); one warp calls it.
+__device__ __forceinline__ void take_tmem(uint32_t *to) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                   smem_addr(to))
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+
+// The CTA's end, for all threads: reports a wait that ran out, and frees TMEM.
+__device__ __forceinline__ void leave(volatile uint32_t *abort_flag, uint32_t tmem, int warp,
+                                      int32_t *err) {
+  __syncthreads();
+  if (*abort_flag) {
+    // copies and products in flight end within microseconds: give them time
+    // before the shared memory and TMEM go
+    const uint64_t t0 = global_ns();
+    for (int i = 0; i < 4096 && global_ns() - t0 < 200000ull; ++i) __nanosleep(1000);
+    if (threadIdx.x == 0 && err) atomicOr(err, KDA_DEVERR_TIMEOUT);
+    __syncthreads();
+  }
+  tc_fence_after();
+  if (warp == 3)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
 // kOut: outputs and last states.  Otherwise: each segment's own contribution
 // to the page (from zeros) and its total decay, for every segment but a
 // sequence's last.
@@ -596,12 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int w4 = warp & 3;                           // TMEM lanes 32 w4 .. of this warp
   volatile uint32_t *abort_flag = &c.abort;
 
-  if (warp == 3) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                     smem_addr(&c.tmem))
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  if (warp == 3) take_tmem(&c.tmem);
   if (threadIdx.x == 0) {
     c.abort = 0;
     for (int i = 0; i < kInfos; ++i) {
@@ -651,10 +681,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c.tmem;
-
-// A wait that ran out leaves the role's loop; whole warps leave together.
-#define KDA_WAIT_WARP(bar, parity)                                                \
-  if (!__all_sync(0xffffffffu, wait_phase(&(bar), (parity), &c.abort))) break
 
   if (*abort_flag) {
     // nothing runs
@@ -1238,21 +1264,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   }
-#undef KDA_WAIT_WARP
-
-  __syncthreads();
-  if (*abort_flag) {
-    // copies and products in flight end within microseconds: give them time
-    // before the shared memory and TMEM go
-    const uint64_t t0 = global_ns();
-    for (int i = 0; i < 4096 && global_ns() - t0 < 200000ull; ++i) __nanosleep(1000);
-    if (threadIdx.x == 0 && p.err) atomicOr(p.err, KDA_DEVERR_TIMEOUT);
-    __syncthreads();
-  }
-  tc_fence_after();
-  if (warp == 3)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  leave(&c.abort, tmem, warp, p.err);
 }
+
+// Self-test: the wait above running out, and the way out behind it.  A CTA of the
+// chunked form's size takes TMEM and waits in its roles' manner, first for a phase
+// that is complete, then for one that nothing completes.
+__global__ void __launch_bounds__(kThreads, 1) wait_test_kernel(int32_t *err) {
+  __shared__ struct { uint64_t complete, never; uint32_t tmem, abort; } c;
+  const int warp = threadIdx.x >> 5;
+  if (warp == 3) take_tmem(&c.tmem);
+  if (threadIdx.x == 0) {
+    c.abort = 0;
+    mbar_init(&c.complete, 1);
+    mbar_init(&c.never, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c.tmem;
+  if (threadIdx.x == 0) mbar_arrive(&c.complete);
+  int passed = 0;
+  while (true) {
+    KDA_WAIT_WARP(c.complete, 0);
+    ++passed;
+    KDA_WAIT_WARP(c.never, 0);
+    ++passed;
+    break;
+  }
+  __syncwarp();
+  leave(&c.abort, tmem, warp, __syncthreads_and(passed == 1) ? err : nullptr);
+}
+#undef KDA_WAIT_WARP
 
 // The pages that the segments of split sequences start from, in place of their
 // contributions: S_0 = the sequence's first page, S_(g+1) = 2^decay_g S_g + U_g.
@@ -1379,3 +1423,10 @@ int launch_chunked(const PromptParams &p, int qk_heads, int dev, int sms, cudaSt
 
 }  // namespace lin
 }  // namespace kda
+
+extern "C" int kda_selftest_lin_wait_timeout(int32_t *err, void *stream) {
+  if (!err) return KDA_ERR_NULL_POINTER;
+  if (reinterpret_cast<uintptr_t>(err) & 3u) return KDA_ERR_ALIGNMENT;
+  kda::lin::wait_test_kernel<<<1, kda::lin::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(err);
+  return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
+}

@@ -36,7 +36,7 @@ KDA_DEVERR_SEQ = 8
 EXPORTED = ("kda_decode", "kda_verify", "kda_step_noalloc", "kda_recover", "kda_oproj",
             "kda_lin_prompt_workspace", "kda_lin_prompt", "kda_lin_step",
             "kda_snapshot_save", "kda_snapshot_load",
-            "kda_selftest_wait_timeout", "kda_strerror", "kda_abi_version")
+            "kda_selftest_wait_timeout", "kda_selftest_lin_wait_timeout", "kda_strerror", "kda_abi_version")
 
 
 class KdaArgs(ctypes.Structure):
@@ -161,8 +161,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
                              ctypes.c_int)):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, res
-    lib.kda_selftest_wait_timeout.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
-    lib.kda_selftest_wait_timeout.restype = ctypes.c_int
+    for fn in (lib.kda_selftest_wait_timeout, lib.kda_selftest_lin_wait_timeout):
+        fn.argtypes, fn.restype = [ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int
     lib.kda_strerror.argtypes = [ctypes.c_int]
     lib.kda_strerror.restype = ctypes.c_char_p
     lib.kda_abi_version.argtypes = []
