@@ -327,7 +327,7 @@ int64_t kda_lin_prompt_workspace(const kda_lin_prompt_args *args);
  * are; a sequence without tokens copies its first state.  A sequence with a
  * flagged slot (KDA_DEVERR_SLOT) or range (KDA_DEVERR_SEQ) writes nothing; starts
  * out of order can make other sequences share rows, whose outputs are then any of
- * theirs.  An infinity or NaN in a live row reaches what the formulas send it
+ * theirs, and flag (KDA_DEVERR_SEQ) every sequence that the call would have split.  An infinity or NaN in a live row reaches what the formulas send it
  * to, its own and later tokens of its sequence and head, as an infinity or NaN;
  * rows outside the sequence reach nothing.  The output must not overlap the
  * inputs.  The page is held and updated in FP32; products that only feed the BF16 output are rounded to

@@ -495,6 +495,17 @@ __device__ __forceinline__ int64_t unit_at(uint32_t k, int64_t units, const uint
   return list ? list[k % kList] : place;
 }
 
+// Whether no sequence starts before the one before it ends, as far as this thread
+// looks.  Otherwise two sequences may share rows, and split ones would then share
+// pages of the workspace (their index goes by the row): such a call runs none of
+// the sequences that it would split.  256 sequences: one load a thread.
+__device__ __forceinline__ bool in_order(const PromptParams &p, int threads) {
+  bool ok = true;
+  for (int b = threadIdx.x; b < p.seqs; b += threads)
+    ok = ok && __ldg(p.seq_starts + b) <= __ldg(p.seq_starts + b + 1);
+  return ok;
+}
+
 // The sequences of this CTA's slot units (the host keeps them among the first
 // kList).  All threads call it; `found` holds -1.
 template <bool kOut>
@@ -517,11 +528,12 @@ struct Walk {
   const PromptParams &p;
   const uint32_t *list;    // NULL: every grid-th unit
   const int *found;
+  bool ordered;            // else: split sequences are flagged
   uint32_t k;
   Unit unit;
 
-  __device__ Walk(const PromptParams &p_, const uint32_t *list_, const int *found_)
-      : p(p_), list(list_), found(found_), k(0) {}
+  __device__ Walk(const PromptParams &p_, const uint32_t *list_, const int *found_, bool ordered_)
+      : p(p_), list(list_), found(found_), ordered(ordered_), k(0) {}
   // The next unit that has work for this kernel.
   __device__ bool next(int lane) {
     const int64_t units = static_cast<int64_t>(items_of<kOut>(p)) * p.heads;   // < 2^31
@@ -537,7 +549,9 @@ struct Walk {
       const int b = slot ? found[(k - 1) % kList] : item - p.slots;
       if (b < 0) continue;
       Seq s;
-      if (const int bad = resolve_seq(p, b, &s)) {
+      int bad = resolve_seq(p, b, &s);
+      if (!ordered && s.len > p.seg_len) bad |= KDA_DEVERR_SEQ;
+      if (bad) {
         if (lane == 0 && p.err) atomicOr(p.err, bad);
         continue;
       }
@@ -673,8 +687,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                       (p.slots == 0 || p.seqs <= 64);      // (a slot looks at every sequence)
   if (threadIdx.x < kList) c.found[threadIdx.x] = -1;
   if (sorted) order_units<kOut>(p, reinterpret_cast<int *>(smem), c.list);
-  if (p.slots > 0) {
-    __syncthreads();
+  // (without slots nothing is split)
+  const bool ordered = p.slots == 0 || __syncthreads_and(in_order(p, kThreads));
+  if (p.slots > 0 && ordered) {
     find_slots<kOut>(p, sorted ? c.list : nullptr, c.found);
   }
   tc_fence_before();
@@ -784,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 2) {
       // -------------------------------------- the work, and its decay tables
-      Walk<kOut> it(p, sorted ? c.list : nullptr, c.found);
+      Walk<kOut> it(p, sorted ? c.list : nullptr, c.found, ordered);
       Info next;
       int t = 0;                                           // tokens of the unit handed out
       bool unit = false;
@@ -1311,6 +1326,7 @@ __global__ void __launch_bounds__(kSegmentThreads)
   const int part = blockIdx.x % kSegmentBlocks, item = blockIdx.x / kSegmentBlocks;
   const int h = item % p.heads;
   Seq seq;
+  if (!__syncthreads_and(in_order(p, kSegmentThreads))) return;
   if (p.seqs <= p.slots) {
     if (resolve_seq(p, item / p.heads, &seq) || seq.len <= p.seg_len) return;
   } else {

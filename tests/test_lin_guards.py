@@ -35,3 +35,31 @@ def test_wait_of_the_chunked_form_runs_out_and_the_context_stays_usable():
     assert 1.9 < waited < 3.0, waited
     inp = make([130] * 40, 4, 4, seed=40)
     verify(inp, launch(inp, path=2), 2)
+
+
+@pytest.mark.gpu
+def test_starts_out_of_order_beside_sequences_that_would_be_split():
+    """Sequences that share rows would share pages of the workspace: none that
+    would be split runs, and the others are as they are without them."""
+    from tests.test_lin_gpu import launch, make, verify
+    inp = make([3000, 1000, 100, 40], 2, 2, slots=9, seed=41)
+    assert kl.prompt_workspace(kl.KdaLinPromptArgs(
+        seqs=5, heads=2, qk_heads=2, tokens=4140, max_seq=3000, q_stride=256, k_stride=256,
+        v_stride=256, o_stride=256)) > 0
+    bad = dict(inp, starts=[0, 3000, 1000, 4000, 4100, 4140])
+    src, dst = [1, 2, 3, 4, 0], [1, 5, 6, 7, 8]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, state = launch(bad, src=src, dst=dst, max_seq=3000, err=err)
+    assert int(err) == kl.KDA_DEVERR_SEQ
+    assert torch.all(torch.isnan(out[:4000]))
+    for slot in (0, 1, 2, 3, 4, 5, 6):
+        assert torch.equal(state[slot], inp["state"][slot])
+    rest = {n: inp[n][4000:] for n in ("q", "k", "v", "decay")}
+    rest.update(starts=[0, 100, 140], state=inp["state"])
+    state[[1, 5, 6]] = inp["state"][[1, 5, 6]]
+    verify(rest, (out[4000:], state), 2, [4, 0], [7, 8])
+    # in order again, everything runs and nothing is flagged
+    err.zero_()
+    good = dict(inp, starts=[0, 3000, 3000, 4000, 4100, 4140])
+    verify(good, launch(good, src=src, dst=dst, max_seq=3000, err=err), 2, src, dst)
+    assert int(err) == 0
