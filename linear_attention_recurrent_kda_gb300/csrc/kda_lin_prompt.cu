@@ -22,9 +22,10 @@
 // operand of the page's update that BF16 does not hold; it goes in three BF16
 // parts, each the rounding of what the ones before leave, which hold its 24 bits:
 // the update is exact to FP32's own rounding (one part would put 2^-9 into the
-// page, two 2^-17).  P and the page's copy for Q S^T are rounded to BF16 once: they
-// only feed an output that is itself rounded to BF16, and the FP32 sum keeps
-// their errors at that size.
+// page, two 2^-17).  What the page's own factor loses to rounding goes into the next
+// chunk's (carried_factor), so a slow head's page does not drift.  P and the page's
+// copy for Q S^T are rounded to BF16 once: they only feed an output that is itself
+// rounded to BF16, and the FP32 sum keeps their errors at that size.
 //
 // Infinities and NaN.  P V multiplies the values of later tokens by zeros, and
 // 0 * NaN is not 0.  So P V runs after the page's warps have read the chunk's
@@ -1193,7 +1194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int d = 32 * w4 + lane;                          // key
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * w4) << 16);
     f32x2 s[kDim / 2];                                     // value rows 2 i, 2 i + 1
-    float all = 0.0f;                                      // the unit's decay (logarithm)
+    float all = 0.0f, carry = 0.0f;                        // the unit's decay (logarithm)
     for (; next_table(c, m); ++m) {
       const Table &tab = c.tab[m & 1];
       const Info info = tab.info;
@@ -1201,7 +1202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&c.tab_empty[m & 1]);
       if (info.first) {
-        all = 0.0f;
+        all = carry = 0.0f;
         if (info.from) {
 #pragma unroll
           for (int i = 0; i < kDim / 2; ++i)
@@ -1227,7 +1228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&c.s_full);
         }
-        const float keep = exp2_approx(total);
+        const float keep = carried_factor(total, carry);
         const f32x2 keep2 = pair(keep, keep);
         all += total;
         const uint32_t ub = n % C::kU, col_u = lanes + C::u(n);
@@ -1348,24 +1349,25 @@ __global__ void __launch_bounds__(kSegmentThreads)
   float4 *ws = reinterpret_cast<float4 *>(p.ws_state + first * kPage) + at;
   const float *decay = p.ws_decay + first;
   const int64_t step = static_cast<int64_t>(p.heads) * (kPage / 4);
+  float carry = 0.0f;
   for (int g = 0; g < last; g += kBatch) {
     float4 u[kBatch];
-    float keep[kBatch];
+    float log2[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
       if (g + i < last) {
         u[i] = ws[i * step];
-        keep[i] = decay[i * p.heads];
+        log2[i] = decay[i * p.heads];
       }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
       if (g + i < last) {
         ws[i * step] = s;
-        const float f = exp2_approx(keep[i]);
-        s.x = __fmaf_rn(s.x, f, u[i].x);
-        s.y = __fmaf_rn(s.y, f, u[i].y);
-        s.z = __fmaf_rn(s.z, f, u[i].z);
-        s.w = __fmaf_rn(s.w, f, u[i].w);
+        const float keep = carried_factor(log2[i], carry);
+        s.x = __fmaf_rn(s.x, keep, u[i].x);
+        s.y = __fmaf_rn(s.y, keep, u[i].y);
+        s.z = __fmaf_rn(s.z, keep, u[i].z);
+        s.w = __fmaf_rn(s.w, keep, u[i].w);
       }
     ws += kBatch * step;
     decay += kBatch * p.heads;

@@ -1,0 +1,87 @@
+"""How exact the chunked form's pages stay (kda_lin_prompt): relative errors in the
+2-norm against the recurrence in 64 bits, chunk by chunk, with limits that come
+from FP32's own rounding."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from linear_attention_recurrent_kda_gb300 import lib as kl
+from linear_attention_recurrent_kda_gb300.api import kda_lin_prompt
+from tests import linref
+
+D = 128
+U32 = linref.U32
+
+
+def last_pages(k, v, decay, first):
+    """Pages [H, 128, 128] after k [n, Hk * 128], v [n, H * 128] and decay [n, H] or
+    [H] from `first`, in 64 bits: S' = e^b_C S + sum_j e^(b_C - b_j) v_j k_j^T."""
+    n, H = v.shape[0], v.shape[1] // D
+    S = first.double()
+    for a in range(0, n, 128):
+        b = min(a + 128, n)
+        g = (decay[a:b] if decay.dim() == 2 else decay.expand(b - a, H)).double().T   # [H, C]
+        behind = g.flip(1).cumsum(1).flip(1) - g
+        kk = k[a:b].double().view(b - a, -1, D).transpose(0, 1)
+        kk = kk.repeat_interleave(H // kk.shape[0], 0) * behind.exp()[..., None]
+        vv = v[a:b].double().view(b - a, H, D).permute(1, 2, 0)
+        S = g.sum(1).exp()[:, None, None] * S + vv @ kk
+    return S
+
+
+def test_the_reference_is_the_recurrence():
+    g = torch.Generator().manual_seed(3)
+    n, H = 300, 2
+    k, v = torch.randn(n, D, generator=g), torch.randn(n, H * D, generator=g)
+    S0 = torch.randn(2, H, D, D, generator=g)
+    for decay in (-torch.rand(n, H, generator=g), -torch.rand(H, generator=g)):
+        S = linref.prompt(k, k, v, decay, [0, n], 1.0, S0, [1])[2][0]
+        assert torch.allclose(last_pages(k, v, decay, S0[1]), S, rtol=1e-12, atol=1e-12)
+
+
+def prompt(n, H, Hk, decay, *, seed, first=0.0, split):
+    """One sequence of n tokens through the chunked form; (got, inputs)."""
+    g = torch.Generator("cuda").manual_seed(seed)
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=g, device="cuda")
+
+    k = randn(n, Hk, D)
+    k = (k / k.norm(dim=-1, keepdim=True)).view(n, Hk * D).to(torch.bfloat16)
+    v = randn(n, H * D).to(torch.bfloat16)
+    state = randn(2, H, D, D) * first
+    i32 = dict(dtype=torch.int32, device="cuda")
+    need = kl.prompt_workspace(kl.KdaLinPromptArgs(
+        seqs=1, heads=H, qk_heads=Hk, tokens=n, max_seq=n, q_stride=Hk * D, k_stride=Hk * D,
+        v_stride=H * D, o_stride=H * D))
+    assert (need > 0) == split
+    S0 = state[1].clone()
+    kda_lin_prompt(q=k, k=k, v=v, decay=decay.cuda(), seq_starts=torch.tensor([0, n], **i32),
+                   output=torch.empty_like(v), scale=1.0, state=state,
+                   src_slots=torch.tensor([1], **i32), dst_slots=torch.tensor([1], **i32), path=2)
+    return state[1], (k, v, decay.cuda(), S0)
+
+
+def errors(got, want):
+    """Relative error of each head's page."""
+    return (got.double() - want).flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,split", [(80, False), (8, True)])
+def test_pages_of_very_slow_heads_do_not_drift(H, split):
+    """256 chunks at decays of exp(-1e-6) to exp(-1e-5) a token, from a page that
+    outweighs what is added.  A chunk's factor rounded to FP32 would be off by up to
+    U32 / 2 the same way at every chunk, 256 of them 7.6e-6 (split: 64 segments,
+    1.9e-6), and no two heads' factors round alike.  Without that the page rounds
+    once a chunk (split: 4 chunks and 64 segments), at random, an rms of at most
+    U32 / 3^0.5: twice the square root of their number of these, and the exponent's
+    own error, 8 U32 of at most 0.33."""
+    n = 256 * 128
+    decay = -torch.logspace(-6, -5, H)
+    got, inp = prompt(n, H, 8, decay, seed=50, first=64.0, split=split)
+    roundings = 256 if not split else 4 + 64
+    limit = (2 * (roundings / 3) ** 0.5 + 8 * 0.33) * U32
+    off = errors(got, last_pages(*inp))
+    assert float(off.max()) < limit, (float(off.max()), limit)
