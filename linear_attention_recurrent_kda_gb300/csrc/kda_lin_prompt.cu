@@ -9,14 +9,18 @@
 // after the other per CTA, one CTA per SM.
 //
 // Factors.  Exponents are sums inside 32-token blocks (bl: prefix sums; sums of the
-// tokens behind) and of whole blocks: numbers of one sign, nothing cancels.  P: in
+// tokens behind) and of whole blocks, numbers of one sign.  P: in
 // a chunk whose decay is above 2^-128 ("mild"), O = 2^(b_i - r) (Q (2^r S)^T + P' V)
 // with P'_ij = A_ij 2^(r - b_j), r half the chunk's logarithm rounded to a whole
 // number: every factor is within 2^+-64, one product per element of A and one
 // per element of O.  Stronger decays take a row factor times a column factor off
 // the diagonal blocks, both <= 1, and 2^(bl_i - bl_j) on them, and O = Q S^T is
-// scaled by rows before P V joins it.  Logarithms below -160 (base 2) count as
-// -160: the factor is 0 in FP32 either way, and a reset of -inf stays a number.
+// scaled by rows before P V joins it.  Those differences would lose their digits
+// behind many resets (7e-4 of the factor after 28, summed in FP32): from a block's
+// logarithm of -512 on (where FP32's sums are 2^-14 off) bl is summed in whole numbers
+// and kept from the middle of the block's range: within +-2048, 2^-14 off, a
+// difference 2^-13, the factor 8.5e-5, where P is rounded to 2^-9.  Logarithms below -128 (base 2) count as -128: subnormal factors are 0
+// either way, and a reset of -inf stays a number.
 //
 // Precision.  The page stays in FP32 registers.  K'' = factor * key is the one
 // operand of the page's update that BF16 does not hold; it goes in three BF16
@@ -84,8 +88,10 @@ constexpr int kThreads = 768;
 constexpr int kHalf = 128 * 128;                 // bytes of a [128][64] BF16 tile
 constexpr int kTile = 2 * kHalf;                 // bytes of a [128][128] BF16 tile
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLowest = -160.0f;               // of a decay's base-2 logarithm
+constexpr float kLowest = -128.0f;               // of a decay's base-2 logarithm
 constexpr float kMild = -128.0f;                 // a chunk's, for the one-factor form of P
+constexpr float kManyDigits = -512.0f;           // a block's, from which bl is summed exactly
+constexpr float kFixed = 262144.0f;              // 32 tokens of +-128, times 2^18, fit 31 bits
 
 constexpr uint32_t kColA = 0, kColO = 128, kColU = 256, kColK = 384, kColsK = 48;
 
@@ -101,8 +107,9 @@ struct Info {
 // The chunk with its factors, for the roles that compute.
 struct Table {
   float w[kChunk];     // K'': 2^(sum of the tokens behind, in the chunk)
-  float x[kChunk];     // mild: 2^(ref - b); else bl, prefix sums in the block
+  float x[kChunk];     // mild: 2^(ref - b); else bl (prefix sums in the block) - middle
   float total[4];      // the blocks' logarithms
+  float middle[4];     // strong: half of that, or 0
   float sum;           // the chunk's
   float ref;           // mild: r, else 0
   uint32_t mild, pad;
@@ -377,10 +384,11 @@ __device__ __forceinline__ void clear_odd(uint8_t *tile, int w4, int lane, int r
 
 // P of a chunk with strong decays, 64 columns (`side`) of a warp's 32 rows: a row
 // factor times f off the diagonal block, 2^(bl_i - bl_j) on it, zeros behind.
-// bl: this row's prefix sum in its block.  Returns the row's factor of Q S^T.
+// x: this row's of the table.  Returns the row's factor of Q S^T.
 __device__ __forceinline__ float strong_rows(const Table &tab, uint32_t col_a, int side, int w4,
-                                             int lane, float bl) {
+                                             int lane, float x) {
   uint32_t a[32], r[16];
+  const float bl = x + tab.middle[w4];                  // this row's prefix sum in its block
 #pragma unroll 1
   for (int z = 0; z < 2; ++z) {
     const int J = 2 * side + z;
@@ -389,20 +397,20 @@ __device__ __forceinline__ float strong_rows(const Table &tab, uint32_t col_a, i
     if (J < w4) {
       float sum = bl;                                   // and the blocks between
       for (int m = J + 1; m < w4; ++m) sum += tab.total[m];
-      const float row = exp2_approx(sum);
+      const float row = exp2_approx(sum), end = tab.x[32 * J + 31];
 #pragma unroll
       for (int j = 0; j < 16; ++j)
         r[j] = pack2(__uint_as_float(a[2 * j]) *
-                         (row * exp2_approx(tab.total[J] - tab.x[32 * J + 2 * j])),
+                         (row * exp2_approx(end - tab.x[32 * J + 2 * j])),
                      __uint_as_float(a[2 * j + 1]) *
-                         (row * exp2_approx(tab.total[J] - tab.x[32 * J + 2 * j + 1])));
+                         (row * exp2_approx(end - tab.x[32 * J + 2 * j + 1])));
     } else {
       const int to = J == w4 ? lane : -1;               // the last column to keep
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const float x = __uint_as_float(a[2 * j]) * exp2_approx(bl - tab.x[32 * J + 2 * j]);
-        const float y = __uint_as_float(a[2 * j + 1]) * exp2_approx(bl - tab.x[32 * J + 2 * j + 1]);
-        r[j] = pack2(2 * j <= to ? x : 0.0f, 2 * j + 1 <= to ? y : 0.0f);
+        const float p = __uint_as_float(a[2 * j]) * exp2_approx(x - tab.x[32 * J + 2 * j]);
+        const float q = __uint_as_float(a[2 * j + 1]) * exp2_approx(x - tab.x[32 * J + 2 * j + 1]);
+        r[j] = pack2(2 * j <= to ? p : 0.0f, 2 * j + 1 <= to ? q : 0.0f);
       }
     }
     tc_st16(col_a + 16 * z, r);
@@ -701,7 +709,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (*abort_flag) {
     // nothing runs
   } else if (warp < 4) {
-    regs_dec<56>();
+    // registers: 64, 64, 56 and 176 a thread (4 + 8 + 8 + 4 warps) are the 768 x 80
+    // of the launch.  With 56 here the table warp spilled the decays it loads ahead,
+    // and so waited for them (ragged prompts 79 -> 88 us); the page spills below 176.
+    regs_dec<64>();
     if (warp == 0) {
       // ------------------------------------------------- TMA loads and stores
       Move info;
@@ -851,6 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 4; ++j) {
           g[j] = ahead[j] * kLog2e;
           if (g[j] < kLowest) g[j] = kLowest;
+          if (g[j] > -kLowest) g[j] = -kLowest;
         }
         if (rows >= 0) look(ahead);
         const float sum = (g[0] + g[1]) + (g[2] + g[3]);
@@ -874,6 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool mild = all >= kMild && all <= 0.0f;
         const float ref = mild ? floorf(0.5f * all) : 0.0f;
         float4 x, w;
+        float middle = 0.0f;
         x.x = before + g[0];
         x.y = x.x + g[1];
         x.z = x.y + g[2];
@@ -886,6 +899,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           x.y = exp2_approx(base - x.y);
           x.z = exp2_approx(base - x.z);
           x.w = exp2_approx(base - x.w);
+        } else if (fminf(fminf(t0, t1), fminf(t2, t3)) < kManyDigits) {
+          int e[4], own = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) own += e[j] = __float2int_rn(g[j] * kFixed);
+          int upto = own;
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) {
+            const int a = __shfl_up_sync(0xffffffffu, upto, o, 8);
+            if ((lane & 7) >= o) upto += a;
+          }
+          const int half = __shfl_sync(0xffffffffu, upto, 7, 8) >> 1;
+          middle = __int2float_rn(half) * (1.0f / kFixed);
+          int at = upto - own - half;
+          // (a NaN among them stays one)
+          auto next = [&](float sum, int e) {
+            at += e;
+            return sum == sum ? __int2float_rn(at) * (1.0f / kFixed) : sum;
+          };
+          x.x = next(x.x, e[0]);
+          x.y = next(x.y, e[1]);
+          x.z = next(x.z, e[2]);
+          x.w = next(x.w, e[3]);
         }
         behind += block == 3 ? 0.0f : block == 2 ? t3 : block == 1 ? t2 + t3 : t1 + (t2 + t3);
         const float s3 = behind, s2 = s3 + g[3], s1 = s2 + g[2], s0 = s1 + g[1];
@@ -897,7 +932,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         Table &tab = c.tab[buf];
         reinterpret_cast<float4 *>(tab.x)[lane] = x;
         reinterpret_cast<float4 *>(tab.w)[lane] = w;
-        if ((lane & 7) == 0) tab.total[lane >> 3] = total;
+        if ((lane & 7) == 0) {
+          tab.total[lane >> 3] = total;
+          tab.middle[lane >> 3] = middle;
+        }
         if (lane == 1) {
           tab.sum = all;
           tab.ref = ref;
@@ -1188,7 +1226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    regs_inc<184>();
+    regs_inc<176>();
     // -------------------------------------------------------------- the page
     uint32_t m = 0, n = 0;
     const int d = 32 * w4 + lane;                          // key

@@ -85,3 +85,41 @@ def test_pages_of_very_slow_heads_do_not_drift(H, split):
     limit = (2 * (roundings / 3) ** 0.5 + 8 * 0.33) * U32
     off = errors(got, last_pages(*inp))
     assert float(off.max()) < limit, (float(off.max()), limit)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("low", [-float("inf"), -70.0])
+def test_decays_behind_many_strong_ones_keep_their_digits(low):
+    """One chunk whose 32-token blocks start with up to 28 resets (or decays of
+    2^-100) and go on mildly.  v is the identity, q k of one sign and the first page
+    zero: output (i, j) is the masked product P_ij alone, rounded to BF16 once, so it
+    is within half a last place of the exact one.  The factor's own error is allowed
+    8.5e-5 (a difference of sums within +-2048 in FP32, 2^-13, times ln 2) and 1e-5
+    for the sums' terms and exp2, in half last places (2^-8 to 2^-9 of the value) at
+    most 0.05; sums of up to 28 * 160 from one end would leave 7e-4."""
+    n, H = 128, 12
+    g = torch.Generator().manual_seed(51)
+    q, k = (torch.rand(n, H * D, generator=g).add(0.1).to(torch.bfloat16) for _ in "qk")
+    decay = -0.05 * torch.rand(n, H, generator=g)
+    for h in range(H):
+        for block in range(4):
+            strong = int(torch.randint(8, 29, (1,), generator=g))
+            decay[32 * block:32 * block + strong, h] = low
+    v = torch.eye(n).repeat(1, H).to(torch.bfloat16)
+    out = torch.empty(n, H * D, dtype=torch.bfloat16, device="cuda")
+    kda_lin_prompt(q=q.cuda(), k=k.cuda(), v=v.cuda(), decay=decay.cuda(), output=out, scale=1.0,
+                   seq_starts=torch.tensor([0, n], dtype=torch.int32, device="cuda"), path=2)
+    got = out.cpu().double().view(n, H, D)
+    worst = 0.0
+    for h in range(H):
+        sl = slice(h * D, h * D + D)
+        w = torch.zeros(n, n, dtype=torch.float64)
+        for i in range(n):
+            for j in range(i + 1):
+                w[i, j] = decay[j + 1:i + 1, h].double().sum().exp()
+        want = (q[:, sl].double() @ k[:, sl].double().T) * w
+        near = want >= 2.0 ** -90
+        half = torch.exp2(torch.floor(torch.log2(want[near]))) * linref.U16
+        worst = max(worst, float(((got[:, h] - want)[near].abs() / half).max()))
+        assert torch.all(got[:, h][~near].abs() < 2.0 ** -89)
+    assert worst < 1.05, worst
