@@ -883,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float t0 = __shfl_sync(0xffffffffu, total, 0), t1 = __shfl_sync(0xffffffffu, total, 8),
                     t2 = __shfl_sync(0xffffffffu, total, 16), t3 = __shfl_sync(0xffffffffu, total, 24);
         const float all = (t0 + t1) + (t2 + t3);
-        const bool mild = all >= kMild && all <= 0.0f;
+        const bool mild = all > kMild && all <= 0.0f;    // (a reset is strong)
         const float ref = mild ? floorf(0.5f * all) : 0.0f;
         float4 x, w;
         float middle = 0.0f;

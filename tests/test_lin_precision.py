@@ -123,3 +123,28 @@ def test_decays_behind_many_strong_ones_keep_their_digits(low):
         worst = max(worst, float(((got[:, h] - want)[near].abs() / half).max()))
         assert torch.all(got[:, h][~near].abs() < 2.0 ** -89)
     assert worst < 1.05, worst
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("path", [1, 2])
+def test_one_reset_among_no_decays_leaves_nothing(path):
+    """A single reset in a chunk without other decays, from a page of 2^100: the
+    tokens from it on have the bits that they have from an empty page."""
+    n, at = 200, 70
+    g = torch.Generator().manual_seed(52)
+    q, k, v = (torch.randn(n, D, generator=g).to(torch.bfloat16).cuda() for _ in "qkv")
+    decay = torch.zeros(n, 1)
+    decay[at] = -float("inf")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    outs = []
+    for first in (2.0 ** 100, 0.0):
+        state = torch.full((2, 1, D, D), first, device="cuda")
+        vv = v.clone()
+        if first == 0.0:
+            vv[:at] = 0
+        out = torch.empty_like(v)
+        kda_lin_prompt(q=q, k=k, v=vv, decay=decay.cuda(), output=out, scale=1.0, state=state,
+                       seq_starts=torch.tensor([0, n], **i32), path=path,
+                       src_slots=torch.tensor([1], **i32), dst_slots=torch.tensor([1], **i32))
+        outs.append((out[at:], state[1]))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
