@@ -310,6 +310,14 @@ def _want(name, t, dtype, shape, index):
     return t.data_ptr()
 
 
+def _count(name, n):
+    """A number of rows, slots or entries that the library's 32-bit field holds (ctypes
+    would keep its low bits)."""
+    if n >= 1 << 31:
+        raise ValueError(f"{name}: {n} are more than the library counts (2^31 - 1)")
+    return n
+
+
 def _maybe(name, t, dtype, shape, index):
     return None if t is None else _want(name, t, dtype, shape, index)
 
@@ -349,7 +357,7 @@ def _lin_shape(q, v):
     _cuda_index("q", q)
     if v.dim() != 2 or q.dim() != 2 or v.shape[1] % DK or q.shape[1] % DK or not q.shape[1]:
         raise ValueError("q, k and v must be rows of whole heads of 128")
-    rows, width = v.shape
+    rows, width = _count("v", v.shape[0]), v.shape[1]
     H, Hk = width // DK, q.shape[1] // DK
     if H % Hk:
         raise ValueError(f"{H} value heads are not a multiple of {Hk} query heads")
@@ -365,7 +373,7 @@ def _state(state, H, index):
     ptr = _want("state", state, torch.float32, None, index)
     if state.dim() != 4 or state.shape[1:] != (H, DK, DK):
         raise ValueError(f"state must be [num_slots, {H}, 128, 128], got {tuple(state.shape)}")
-    return ptr, state.shape[0]
+    return ptr, _count("state", state.shape[0])
 
 
 def _run(entry, args, index, stream):
@@ -411,7 +419,7 @@ def kda_lin_prompt(*, q, k, v, decay, seq_starts, output, scale: float, state=No
     sp = _want("seq_starts", seq_starts, i32, None, index)
     if seq_starts.dim() != 1 or seq_starts.shape[0] < 1:
         raise ValueError("seq_starts must be [seqs + 1]")
-    B = seq_starts.shape[0] - 1
+    B = _count("seq_starts", seq_starts.shape[0] - 1)
     src = _maybe("src_slots", src_slots, i32, (B,), index)
     dst = _maybe("dst_slots", dst_slots, i32, (B,), index)
     if state is None:
@@ -475,7 +483,7 @@ def _snapshot(entry, state, slots, codes, scales, snaps, err, stream):
     index = _cuda_index("state", state)
     if state.dim() != 4:
         raise ValueError("state must be [num_slots, heads, 128, 128]")
-    num_slots, H = state.shape[:2]
+    num_slots, H = _count("state", state.shape[0]), state.shape[1]
     _want("state", state, torch.float32, (num_slots, H, DK, DK), index)
     if _cuda_index("codes", codes) == index and codes.dtype is torch.int8:
         bits, width, groups = 8, DK, (DK,)
@@ -483,10 +491,10 @@ def _snapshot(entry, state, slots, codes, scales, snaps, err, stream):
         bits, width, groups = 4, DK // 2, (DK, 4)
     else:
         raise TypeError("codes must be an int8 (8 bits) or uint8 (4 bits) tensor")
-    n = codes.shape[0] if codes.dim() else 0
+    n = _count("codes", codes.shape[0]) if codes.dim() else 0
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be an int32 tensor [count]")
-    i32, count = torch.int32, slots.shape[0]
+    i32, count = torch.int32, _count("slots", slots.shape[0])
     a = _lib.KdaSnapshotArgs(
         count, H, num_slots, n, bits, _want("slots", slots, i32, None, index),
         _want("snaps", snaps, i32, (count,), index), state.data_ptr(),

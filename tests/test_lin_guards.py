@@ -9,6 +9,8 @@ import pytest
 import torch
 
 from linear_attention_recurrent_kda_gb300 import lib as kl
+from linear_attention_recurrent_kda_gb300.api import (kda_lin_prompt, kda_snapshot_load,
+                                                      kda_snapshot_save)
 
 
 def test_wait_selftest_refusals():
@@ -63,3 +65,21 @@ def test_starts_out_of_order_beside_sequences_that_would_be_split():
     good = dict(inp, starts=[0, 3000, 3000, 4000, 4100, 4140])
     verify(good, launch(good, src=src, dst=dst, max_seq=3000, err=err), 2, src, dst)
     assert int(err) == 0
+
+
+@pytest.mark.gpu
+def test_counts_past_32_bits_are_refused():
+    """2^32 + 1 entries are not 1 entry (the list is never read)."""
+    many = torch.empty(2 ** 32 + 1, dtype=torch.int32, device="cuda")
+    state = torch.full((2, 1, 128, 128), 3.0, device="cuda")
+    codes = torch.full((2, 1, 128, 128), 85, dtype=torch.int8, device="cuda")
+    scales = torch.full((2, 1, 128), -3.0, device="cuda")
+    for f in (kda_snapshot_save, kda_snapshot_load):
+        with pytest.raises(ValueError, match="2\\^31"):
+            f(state=state, slots=many, codes=codes, scales=scales, snaps=many)
+    x = torch.zeros(3, 128, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="2\\^31"):
+        kda_lin_prompt(q=x, k=x, v=x, decay=torch.zeros(1, device="cuda"), seq_starts=many,
+                       output=torch.empty_like(x), scale=1.0)
+    torch.cuda.synchronize()
+    assert torch.all(state == 3.0) and torch.all(codes == 85) and torch.all(scales == -3.0)
