@@ -343,9 +343,11 @@ def _rows(name, t, rows, width, index):
             raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
         raise ValueError(f"{name} must have shape {(rows, width)}, got {tuple(t.shape)}")
     step, one = t.stride()
+    if not width:
+        return t.data_ptr(), 0
     if rows <= 1:
         step = width
-    if (one != 1 or step % 8 or step < width) and width:
+    if one != 1 or step % 8 or step < width:
         raise ValueError(f"{name}: the elements of a row must be adjacent and rows a "
                          f"multiple of 8 elements apart, got strides {tuple(t.stride())}")
     return t.data_ptr(), step

@@ -9,8 +9,8 @@ import pytest
 import torch
 
 from linear_attention_recurrent_kda_gb300 import lib as kl
-from linear_attention_recurrent_kda_gb300.api import (kda_lin_prompt, kda_snapshot_load,
-                                                      kda_snapshot_save)
+from linear_attention_recurrent_kda_gb300.api import (kda_lin_prompt, kda_lin_step,
+                                                      kda_snapshot_load, kda_snapshot_save)
 
 
 def test_wait_selftest_refusals():
@@ -83,3 +83,19 @@ def test_counts_past_32_bits_are_refused():
                        output=torch.empty_like(x), scale=1.0)
     torch.cuda.synchronize()
     assert torch.all(state == 3.0) and torch.all(codes == 85) and torch.all(scales == -3.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("per_token", [False, True])
+def test_no_heads_are_a_no_op(per_token):
+    """As in the C ABI, for several rows too."""
+    q = torch.zeros(5, 128, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros(5, 0, dtype=torch.bfloat16, device="cuda")
+    decay = torch.zeros((5, 0) if per_token else (0,), device="cuda")
+    kw = dict(q=q, k=q, v=v, decay=decay, output=torch.empty_like(v), scale=1.0,
+              state=torch.zeros(6, 0, 128, 128, device="cuda"))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    kda_lin_prompt(**kw, seq_starts=torch.tensor([0, 2, 5], **i32),
+                   dst_slots=torch.tensor([1, 2], **i32))
+    kda_lin_step(**kw, slots=torch.arange(1, 6, **i32))
+    torch.cuda.synchronize()
