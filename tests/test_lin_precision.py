@@ -148,3 +148,42 @@ def test_one_reset_among_no_decays_leaves_nothing(path):
                        src_slots=torch.tensor([1], **i32), dst_slots=torch.tensor([1], **i32))
         outs.append((out[at:], state[1]))
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+PARTS_LIMIT = 6e-7
+
+
+def test_two_parts_of_a_key_would_break_the_limit():
+    """The limit of the next test lies between what a factor times a key leaves in two
+    BF16 parts (each element off by up to 2^-18, evenly: an rms of about 2^-18 /
+    3^0.5 * 0.75) and in three."""
+    g = torch.Generator().manual_seed(53)
+    k = torch.randn(128, D, generator=g).to(torch.bfloat16).float()
+    v = torch.randn(128, D, generator=g).to(torch.bfloat16).double()
+    w = torch.exp(-0.15 * torch.arange(127, -1, -1.0))
+    full = w[:, None] * k
+    for parts, fails in ((2, True), (3, False)):
+        left, held = full.clone(), torch.zeros_like(full, dtype=torch.float64)
+        for _ in range(parts):
+            part = left.to(torch.bfloat16).float()
+            held, left = held + part.double(), left - part
+        want = v.T @ full.double()
+        off = float((v.T @ held - want).norm() / want.norm())
+        assert (off > 2 * PARTS_LIMIT) if fails else (off < PARTS_LIMIT / 8), (parts, off)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("first", [0.0, 1.0], ids=["empty", "carried"])
+@pytest.mark.parametrize("rate", [0.01, 0.3, 3.0], ids=["slow", "mild", "strong"])
+@pytest.mark.parametrize("n,H", [(128, 4), (77, 4), (40 * 128 - 5, 80)])
+def test_pages_keep_the_digits_of_fp32(n, H, rate, first):
+    """Whole sequences of one chunk and of 40.  Expected of a page, in the 2-norm:
+    sums of 128 tokens in three parts on the tensor cores, 24 steps off by up to a
+    last place each, 24^0.5 * 2 U32 / 3^0.5 = 3.4e-7; factors and exponents 1.3e-7; the
+    page's own update in the 10 chunks that a slow page remembers 1.1e-7: 4e-7
+    together.  Two parts of a factor times a key would leave 1.6e-6."""
+    g = torch.Generator().manual_seed(n + H)
+    decay = -rate * torch.rand(n, H, generator=g)
+    got, inp = prompt(n, H, 4, decay, seed=54, first=first, split=False)
+    off = errors(got, last_pages(*inp))
+    assert float(off.max()) < PARTS_LIMIT, (float(off.max()), off)
