@@ -363,7 +363,9 @@ int kda_lin_step(const kda_lin_step_args *args, void *stream);
 /* ---- Snapshots: state pages kept in 8 or 4 bits ------------------------------
  *
  * A snapshot keeps one slot's pages (of the KDA step or of the linear
- * attention above) for later: a prefix cache, a request to fork.  Codes are
+ * attention above) for later: a prefix cache, a request to fork.  It holds the
+ * state pages only: the KDA step's convolution window of the slot (conv_state[slot])
+ * is the caller's to copy beside it.  Codes are
  * whole numbers -L .. L, L = 127 (bits 8) or 7 (bits 4), with one FP32 scale
  * for a group of keys of one value row (bits 8: the row's 128 keys; bits 4: 32
  * keys).  With m the group's largest magnitude: scale = m / L rounded to FP32

@@ -509,7 +509,8 @@ def _snapshot(entry, state, slots, codes, scales, snaps, err, stream):
 def kda_snapshot_save(*, state, slots, codes, scales, snaps, err=None,
                       stream: Optional[torch.cuda.Stream] = None) -> None:
     """Keep the pages ``state[slots[i]]`` as snapshots ``snaps[i]`` in 8 or 4
-    bits (include/kda.h ``kda_snapshot_save``).
+    bits (include/kda.h ``kda_snapshot_save``).  The KDA step's convolution windows
+    (``conv_state``) are not part of them: copy a slot's beside its snapshot.
 
     ``state`` f32 [num_slots, heads, 128, 128]; ``codes`` int8 [num_snaps, heads,
     128, 128] (8 bits) or uint8 [num_snaps, heads, 128, 64] (4 bits); ``scales``
