@@ -331,7 +331,10 @@ int64_t kda_lin_prompt_workspace(const kda_lin_prompt_args *args);
  * to, its own and later tokens of its sequence and head, as an infinity or NaN;
  * rows outside the sequence reach nothing.  The output must not overlap the
  * inputs.  The page is held and updated in FP32; products that only feed the BF16 output are rounded to
- * BF16 once.  Errors: KDA_ERR_NULL_ARGS, KDA_ERR_NULL_POINTER, KDA_ERR_SHAPE (sizes
+ * BF16 once.  The chunked form takes factors of up to 2^64 both ways on the way to an
+ * output: q k and the page's elements keep their digits from 2^-62 on (what is smaller
+ * is off by up to 2^-62 times v or q), and the sums of |q k v| and |S q| have to be
+ * below 2^62; path 1 has no such limits.  Errors: KDA_ERR_NULL_ARGS, KDA_ERR_NULL_POINTER, KDA_ERR_SHAPE (sizes
  * and strides outside the rules above), KDA_ERR_PATH, KDA_ERR_ALIGNMENT,
  * KDA_ERR_WORKSPACE, KDA_ERR_DEVICE, KDA_ERR_LAUNCH; nothing is launched on error.
  * Up to three kernels on `stream`, in order. */
@@ -355,7 +358,8 @@ typedef struct kda_lin_step_args {
   int32_t *err;             /* optional device word for KDA_DEVERR_* flags     */
 } kda_lin_step_args;
 
-/* Recurrent form, one token per request.  Live requests have distinct slots.
+/* Recurrent form, one token per request.  Live requests have distinct slots; the
+ * output must not overlap the inputs.
  * A slot >= num_slots raises KDA_DEVERR_SLOT and is handled as padding.  One
  * kernel on `stream`. */
 int kda_lin_step(const kda_lin_step_args *args, void *stream);

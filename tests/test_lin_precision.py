@@ -187,3 +187,18 @@ def test_pages_keep_the_digits_of_fp32(n, H, rate, first):
     got, inp = prompt(n, H, 4, decay, seed=54, first=first, split=False)
     off = errors(got, last_pages(*inp))
     assert float(off.max()) < PARTS_LIMIT, (float(off.max()), off)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("power", [-54, 50])
+def test_magnitudes_that_the_one_factor_form_holds(power):
+    """Keys and pages of 2^-54 and 2^50 in chunks whose decay, 2^-120, is near the limit of
+    the form that takes factors of up to 2^60 both ways: products q k stay above the
+    normal range's end (2^-54 / 16 * 2^-60 > 2^-126), sums below the largest number."""
+    from tests.test_lin_gpu import launch, make, verify
+    inp = make([300, 128], 2, 2, slots=4, seed=55)
+    inp["k"] = (inp["k"].float() * 2.0 ** power).to(torch.bfloat16)
+    inp["state"] = inp["state"] * 2.0 ** power
+    inp["decay"] = -0.65 + 0.0 * inp["decay"]
+    src, dst = [1, 0], [2, 3]
+    verify(inp, launch(inp, src=src, dst=dst, path=2), 2, src, dst)
