@@ -30,7 +30,7 @@ constexpr int kParts = kDim / (kWarps * kRows);         // CTAs of a page
 constexpr int kMostHeads = 1 << 16;
 
 struct StepParams {
-  int batch, heads, group, num_slots, decay_rows;
+  int heads, group, num_slots, decay_rows;
   int64_t q_stride, k_stride, v_stride, o_stride;
   const __nv_bfloat16 *q, *k, *v;
   const float *decay;
@@ -176,7 +176,6 @@ static int run_step(const kda_lin_step_args *a, cudaStream_t stream) {
   DeviceFacts df;
   if (!current_device(&dev, &df)) return KDA_ERR_DEVICE;
   StepParams p;
-  p.batch = a->batch;
   p.heads = a->heads;
   p.group = a->heads / a->qk_heads;
   p.num_slots = a->num_slots;

@@ -112,7 +112,7 @@ struct Table {
   float middle[4];     // strong: half of that, or 0
   float sum;           // the chunk's
   float ref;           // mild: r, else 0
-  uint32_t mild, pad;
+  uint32_t mild;
   Info info;
 };
 static_assert(sizeof(Table) % 16 == 0, "vector loads");

@@ -31,7 +31,7 @@ constexpr int kWarps = 2;                        // of a CTA
 constexpr int kParts = kDim / (kRows * kWarps);  // CTAs of a page
 
 struct Params {
-  int count, heads, num_slots, num_snaps;
+  int heads, num_slots, num_snaps;
   const int32_t *slots, *snaps;
   float4 *state;
   void *codes;
@@ -187,7 +187,6 @@ static int run(const kda_snapshot_args *a, bool save, cudaStream_t stream) {
   DeviceFacts df;
   if (!current_device(&dev, &df)) return KDA_ERR_DEVICE;
   Params p;
-  p.count = a->count;
   p.heads = a->heads;
   p.num_slots = a->num_slots;
   p.num_snaps = a->num_snaps;
