@@ -29,7 +29,11 @@
 // page, two 2^-17).  What the page's own factor loses to rounding goes into the next
 // chunk's (carried_factor), so a slow head's page does not drift.  P and the page's
 // copy for Q S^T are rounded to BF16 once: they only feed an output that is itself
-// rounded to BF16, and the FP32 sum keeps their errors at that size.
+// rounded to BF16, and the FP32 sum keeps their errors at that size (outputs against
+// 64 bits, 2-norm: 2.3e-3, of which the output's own rounding is 1.7e-3).  Second
+// parts of both would add a third to the products, and a tile for the page's that
+// shared memory does not have; token by token (path 1) nothing is rounded but the
+// output.
 //
 // Infinities and NaN.  P V multiplies the values of later tokens by zeros, and
 // 0 * NaN is not 0.  So P V runs after the page's warps have read the chunk's
@@ -1436,25 +1440,31 @@ static EncodeTiled encode_tiled() {
 
 // BF16 rows [rows][width], `stride` elements apart, in boxes of 64 columns.
 static bool rows_map(CUtensorMap *map, const void *base, int64_t width, int64_t rows,
-                     int64_t stride, int box_rows) {
+                     int64_t stride, int box_rows, int dev) {
   const EncodeTiled encode = encode_tiled();
   if (!encode) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
   const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)}, ones[2] = {1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides,
-                box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-         CUDA_SUCCESS;
+  auto run = [&] {
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides,
+                  box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult rc = run();
+  // a driver call does not make the device's context the thread's, as a launch does:
+  // this may be a host thread's first
+  if (rc == CUDA_ERROR_INVALID_CONTEXT && cudaSetDevice(dev) == cudaSuccess) rc = run();
+  return rc == CUDA_SUCCESS;
 }
 
 int launch_chunked(const PromptParams &p, int qk_heads, int dev, int sms, cudaStream_t stream) {
   CUtensorMap q, k, v, o;
   const int64_t kw = int64_t(qk_heads) * kDim, vw = int64_t(p.heads) * kDim;
-  if (!rows_map(&q, p.q, kw, p.tokens, p.q_stride, 32) ||
-      !rows_map(&k, p.k, kw, p.tokens, p.k_stride, 32) ||
-      !rows_map(&v, p.v, vw, p.tokens, p.v_stride, 32) ||
-      !rows_map(&o, p.output, vw, p.tokens, p.o_stride, kChunk))
+  if (!rows_map(&q, p.q, kw, p.tokens, p.q_stride, 32, dev) ||
+      !rows_map(&k, p.k, kw, p.tokens, p.k_stride, 32, dev) ||
+      !rows_map(&v, p.v, vw, p.tokens, p.v_stride, 32, dev) ||
+      !rows_map(&o, p.output, vw, p.tokens, p.o_stride, kChunk, dev))
     return KDA_ERR_LAUNCH;
   static std::atomic<bool> out_done[kMaxDevices], seg_done[kMaxDevices];
   if (!set_smem_limit_once(out_done, dev, reinterpret_cast<const void *>(chunk_kernel<true>),

@@ -3,6 +3,9 @@ runs out, sequences out of order, and sizes that the C structs cannot hold."""
 from __future__ import annotations
 
 import ctypes
+import os
+import subprocess
+import sys
 import time
 
 import pytest
@@ -99,3 +102,75 @@ def test_no_heads_are_a_no_op(per_token):
                    dst_slots=torch.tensor([1, 2], **i32))
     kda_lin_step(**kw, slots=torch.arange(1, 6, **i32))
     torch.cuda.synchronize()
+
+
+CHILD = r"""
+import threading, torch
+from linear_attention_recurrent_kda_gb300 import api
+from tests.test_lin_gpu import make, on_device
+
+def prompt(lens, path, seed):
+    inp = make(lens, 4, 2, slots=2 * len(lens) + 1, seed=seed, scale_g=0.1)
+    B = len(lens)
+    kw = on_device(inp, list(range(1, B + 1)), list(range(B + 1, 2 * B + 1)), path=path)
+    return (lambda s: api.kda_lin_prompt(**kw, stream=s)), [kw["output"], kw["state"]]
+
+def step(seed):
+    inp = make([1] * 6, 4, 4, slots=7, seed=seed)
+    d = {n: inp[n].cuda() for n in ("q", "k", "v", "decay", "state")}
+    out = torch.zeros(6, 512, dtype=torch.bfloat16, device="cuda")
+    slots = torch.arange(1, 7, dtype=torch.int32, device="cuda")
+    return (lambda s: api.kda_lin_step(s, **d, slots=slots, output=out, scale=0.5)), [out, d["state"]]
+
+def fork(bits, seed):
+    g = torch.Generator("cuda").manual_seed(seed)
+    state = torch.randn(9, 3, 128, 128, generator=g, device="cuda")
+    codes = torch.zeros(5, 3, 128, 16 * bits, device="cuda",
+                        dtype=torch.int8 if bits == 8 else torch.uint8)
+    scales = torch.zeros((5, 3, 128) if bits == 8 else (5, 3, 128, 4), device="cuda")
+    ids = torch.arange(1, 5, dtype=torch.int32, device="cuda")
+    kw = dict(state=state, codes=codes, scales=scales, snaps=ids)
+    def run(s):
+        api.kda_snapshot_save(**kw, slots=ids, stream=s)
+        api.kda_snapshot_load(**kw, slots=ids + 4, stream=s)
+    return run, [state, codes, scales]
+
+def jobs():
+    return [prompt([1500, 40], 0, 1), prompt([1400], 2, 2), prompt([200, 30], 2, 3),
+            prompt([9, 3], 1, 4), step(5), step(6), fork(8, 7), fork(4, 8)]
+
+mine, failures = jobs(), []
+torch.cuda.synchronize()
+gate = threading.Barrier(len(mine))
+
+def work(run):
+    try:
+        s = torch.cuda.Stream()
+        gate.wait()
+        with torch.cuda.stream(s):
+            run(s)
+    except Exception as e:
+        failures.append(repr(e))
+
+threads = [threading.Thread(target=work, args=(run,)) for run, _ in mine]
+[t.start() for t in threads]
+[t.join() for t in threads]
+torch.cuda.synchronize()
+assert not failures, failures
+for (_, got), (run, want) in zip(mine, jobs()):
+    run(None)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+print("same bits")
+"""
+
+
+@pytest.mark.gpu
+def test_first_calls_from_several_host_threads():
+    """A fresh process whose first calls come from eight threads at once, each on its
+    own stream: the bits of the same calls one after another."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", CHILD], cwd=root, capture_output=True, text=True,
+                         timeout=300)
+    assert res.returncode == 0, res.stderr[-3000:]
+    assert "same bits" in res.stdout
