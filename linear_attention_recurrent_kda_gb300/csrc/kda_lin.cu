@@ -230,9 +230,11 @@ static int plan_prompt(const kda_lin_prompt_args *a, Plan *plan) {
     // A sequence much longer than an SM's share of all tokens x heads would keep
     // its SM busy alone.  Split, the share costs a second pass over keys and values
     // (0.6 of the first) and two more launches: it pays from 2 shares and 896 tokens
-    // on (one sequence of 2048 tokens: 32 heads 52 us whole, 41 split; 64 heads 52
-    // and 70; 64 heads of 4096 tokens: 98 and 107).  Segments of a quarter share
-    // even out what the last ones leave.
+    // on (one sequence, whole and split: 1 head of 1024 tokens 26 and 26 us, of 768 21
+    // and 26, of 2048 45 and 27; 8 heads of 1024 26 and 28, of 1280 31 and 28, of 8192
+    // 165 and 46; 16 heads of 1024 26 and 28, of 1536 36 and 29; 32 heads of 1280 31
+    // and 39, of 2048 46 and 45; 64 heads of 2048 52 and 70, of 4096 98 and 107).
+    // Segments of a quarter share even out what the last ones leave.
     const int64_t share = static_cast<int64_t>(a->tokens) * a->heads / kShares;
     int64_t len = (share / 4 + 127) / 128 * 128;
     if (len < kShortestSegment) len = kShortestSegment;
