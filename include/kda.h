@@ -334,7 +334,8 @@ int64_t kda_lin_prompt_workspace(const kda_lin_prompt_args *args);
  * BF16 once.  The chunked form takes factors of up to 2^64 both ways on the way to an
  * output: q k and the page's elements keep their digits from 2^-62 on (what is smaller
  * is off by up to 2^-62 times v or q), and the sums of |q k v| and |S q| have to be
- * below 2^62, and factors under 2^-126 are 0; path 1 has no such limits.  Errors: KDA_ERR_NULL_ARGS, KDA_ERR_NULL_POINTER, KDA_ERR_SHAPE (sizes
+ * below 2^62, the scale is
+ * within 2^-62 and 2^62, and factors under 2^-126 are 0; path 1 has no such limits.  Errors: KDA_ERR_NULL_ARGS, KDA_ERR_NULL_POINTER, KDA_ERR_SHAPE (sizes
  * and strides outside the rules above), KDA_ERR_PATH, KDA_ERR_ALIGNMENT,
  * KDA_ERR_WORKSPACE, KDA_ERR_DEVICE, KDA_ERR_LAUNCH; nothing is launched on error.
  * Up to three kernels on `stream`, in order. */
