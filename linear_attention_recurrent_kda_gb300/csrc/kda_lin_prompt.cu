@@ -30,10 +30,11 @@
 // chunk's (carried_factor), so a slow head's page does not drift.  P and the page's
 // copy for Q S^T are rounded to BF16 once: they only feed an output that is itself
 // rounded to BF16, and the FP32 sum keeps their errors at that size (outputs against
-// 64 bits, 2-norm: 2.3e-3, of which the output's own rounding is 1.7e-3).  Second
-// parts of both would add a third to the products, and a tile for the page's that
-// shared memory does not have; token by token (path 1) nothing is rounded but the
-// output.
+// 64 bits, 2-norm: 2.34e-3, of which the output's own rounding is 1.66e-3).  Second
+// parts of both leave 1.66e-3 and take a third more products, the page's one after
+// the other through one tile: 202 -> 270 us (16 prompts x 64 heads), 77 -> 95 (8
+// ragged ones x 32), 430 -> 512 (256 suffixes) and 336 -> 401 (32749 tokens), not
+// kept.  Token by token (path 1) nothing is rounded but the output.
 //
 // Infinities and NaN.  P V multiplies the values of later tokens by zeros, and
 // 0 * NaN is not 0.  So P V runs after the page's warps have read the chunk's
