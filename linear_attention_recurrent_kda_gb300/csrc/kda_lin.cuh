@@ -80,25 +80,22 @@ __device__ __forceinline__ Decay decay_of(float g) {
   return Decay{slow ? 1.0f : 0.0f, slow ? less : expf(g)};
 }
 // A chunk's or segment's decay 2^x as one factor, whose rounding would repeat in the
-// same way: near 1 the part that FP32 cannot hold goes into the next one's factor
+// same way: from 1/2 to 1 the part that FP32 cannot hold goes into the next one's factor
 // (`carry`, 0 at first), so that the product over any number of them is off by 2^-24
 // at most, at the cost of no second product for each element of the page (S + S (2^x - 1):
 // 205 us instead of 195, 16 prompts x 64 heads).
 __device__ __forceinline__ float carried_factor(float x, float &carry) {
-  if (!(x > -1.0f)) {
-    carry = 0.0f;
-    return exp2_approx(x);
-  }
-  // e^y - 1 = y (1 + y/2 (1 + y/3 (...))), y in (-ln 2, 0]: what the 11th term leaves
+  // e^y - 1 = y (1 + y/2 (1 + y/3 (...))), y in [-ln 2, 0]: what the 11th term leaves
   // is under 2^-28 of it
   const float y = x * 0.6931471805599453f;
   float t = 1.0f;
 #pragma unroll
   for (int n = 10; n > 1; --n) t = __fmaf_rn(y * t, 1.0f / n, 1.0f);
   const float less = __fmaf_rn(y, t, carry);
-  const float factor = 1.0f + less;
-  carry = less - (factor - 1.0f);      // exact
-  return factor;
+  const float factor = 1.0f + less, left = less - (factor - 1.0f);      // exact
+  const bool slow = fabsf(x + 0.5f) <= 0.5f;
+  carry = slow ? left : 0.0f;
+  return slow ? factor : exp2_approx(x);
 }
 
 // One token on a warp's kRows value rows: lane l holds keys 4l .. 4l+3 of each

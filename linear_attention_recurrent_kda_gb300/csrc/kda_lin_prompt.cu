@@ -904,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           x.y = exp2_approx(base - x.y);
           x.z = exp2_approx(base - x.z);
           x.w = exp2_approx(base - x.w);
-        } else if (fminf(fminf(t0, t1), fminf(t2, t3)) < kManyDigits) {
+        } else if (__builtin_expect(fminf(fminf(t0, t1), fminf(t2, t3)) < kManyDigits, 0)) {
           int e[4], own = 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j) own += e[j] = __float2int_rn(g[j] * kFixed);
@@ -1257,6 +1257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (info.rows > 0) {
         const uint32_t one = n & 1;
+        const float keep = carried_factor(total, carry);
         if (kOut) {
           // the page's copy for Q S^T; the product before has read the last one
           if (n > 0) KDA_WAIT_WARP(c.qs_full, one ^ 1);
@@ -1271,7 +1272,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&c.s_full);
         }
-        const float keep = carried_factor(total, carry);
         const f32x2 keep2 = pair(keep, keep);
         all += total;
         const uint32_t ub = n % C::kU, col_u = lanes + C::u(n);
