@@ -16,7 +16,7 @@
 // per element of O.  Stronger decays take a row factor times a column factor off
 // the diagonal blocks, both <= 1, and 2^(bl_i - bl_j) on them, and O = Q S^T is
 // scaled by rows before P V joins it.  Those differences would lose their digits
-// behind many resets (7e-4 of the factor after 28, summed in FP32): from a block's
+// behind many resets (7e-4 of the factor after 28, summed in FP32): from a chunk's
 // logarithm of -512 on (where FP32's sums are 2^-14 off) bl is summed in whole numbers
 // and kept from the middle of the block's range: within +-2048, 2^-14 off, a
 // difference 2^-13, the factor 8.5e-5, where P is rounded to 2^-9.  Logarithms below -128 (base 2) count as -128: subnormal factors are 0
@@ -95,7 +95,7 @@ constexpr int kTile = 2 * kHalf;                 // bytes of a [128][128] BF16 t
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -128.0f;               // of a decay's base-2 logarithm
 constexpr float kMild = -128.0f;                 // a chunk's, for the one-factor form of P
-constexpr float kManyDigits = -512.0f;           // a block's, from which bl is summed exactly
+constexpr float kManyDigits = -512.0f;           // a chunk's, from which bl is summed exactly
 constexpr float kFixed = 262144.0f;              // 32 tokens of +-128, times 2^18, fit 31 bits
 
 constexpr uint32_t kColA = 0, kColO = 128, kColU = 256, kColK = 384, kColsK = 48;
@@ -178,24 +178,24 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
 }
 // Waits for the phase of `parity`, in a dozen instructions (the roles' loops
 // share the instruction cache, and their code is what fills it).  Each try may
-// sleep for a microsecond.  After kWaitLimitNs of wall clock, or when another
-// thread raised `abort`, the wait gives up, raises it and returns false.  The
-// clock's low word is enough: tries are microseconds apart and the limit is under
-// half of what it holds.  Lanes may get different answers, so the branches are not
-// uniform ones.
+// sleep for a microsecond.  After kWaitLimitNs of wall clock the wait gives up,
+// raises `abort` and returns false.  It does not look at `abort` itself, which cost
+// 2-5% of the time in the 30 waits of a chunk (210 us instead of 198 with 16 prompts
+// x 64 heads): a role that waits for one that left runs out by itself, so the kernel
+// ends after 2 s a role, 14 s, at the latest.  The clock's low word is enough: tries
+// are microseconds apart and the limit is under half of what it holds.  Lanes may get
+// different answers, so the branches are not uniform ones.
 static_assert(kWaitLimitNs < (1ull << 31), "the clock's low word");
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, uint32_t *abort) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .u32 t0, t, a;\n mov.u32 t0, %%globaltimer_lo;\n"
+      "{\n .reg .pred p, q;\n .reg .u32 t0, t;\n mov.u32 t0, %%globaltimer_lo;\n"
       "again:\n"
       " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, 1000;\n"
       " @p bra done;\n"
-      " ld.volatile.shared.u32 a, [%3];\n"
       " mov.u32 t, %%globaltimer_lo;\n"
       " sub.u32 t, t, t0;\n"
       " setp.lt.u32 q, t, %4;\n"
-      " setp.eq.and.u32 q, a, 0, q;\n"
       " @q bra again;\n"
       " st.volatile.shared.u32 [%3], 1;\n"
       "done:\n selp.u32 %0, 1, 0, p;\n}"
@@ -515,6 +515,7 @@ __device__ __forceinline__ int64_t unit_at(uint32_t k, int64_t units, const uint
 // the sequences that it would split.  256 sequences: one load a thread.
 __device__ __forceinline__ bool in_order(const PromptParams &p, int threads) {
   bool ok = true;
+#pragma unroll 1
   for (int b = threadIdx.x; b < p.seqs; b += threads)
     ok = ok && __ldg(p.seq_starts + b) <= __ldg(p.seq_starts + b + 1);
   return ok;
@@ -867,7 +868,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 4; ++j) {
           g[j] = ahead[j] * kLog2e;
           if (g[j] < kLowest) g[j] = kLowest;
-          if (g[j] > -kLowest) g[j] = -kLowest;
         }
         if (rows >= 0) look(ahead);
         const float sum = (g[0] + g[1]) + (g[2] + g[3]);
@@ -891,7 +891,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool mild = all > kMild && all <= 0.0f;    // (a reset is strong)
         const float ref = mild ? floorf(0.5f * all) : 0.0f;
         float4 x, w;
-        float middle = 0.0f;
         x.x = before + g[0];
         x.y = x.x + g[1];
         x.z = x.y + g[2];
@@ -904,28 +903,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           x.y = exp2_approx(base - x.y);
           x.z = exp2_approx(base - x.z);
           x.w = exp2_approx(base - x.w);
-        } else if (__builtin_expect(fminf(fminf(t0, t1), fminf(t2, t3)) < kManyDigits, 0)) {
-          int e[4], own = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) own += e[j] = __float2int_rn(g[j] * kFixed);
-          int upto = own;
-#pragma unroll
-          for (int o = 1; o < 8; o <<= 1) {
-            const int a = __shfl_up_sync(0xffffffffu, upto, o, 8);
-            if ((lane & 7) >= o) upto += a;
-          }
-          const int half = __shfl_sync(0xffffffffu, upto, 7, 8) >> 1;
-          middle = __int2float_rn(half) * (1.0f / kFixed);
-          int at = upto - own - half;
-          // (a NaN among them stays one)
-          auto next = [&](float sum, int e) {
-            at += e;
-            return sum == sum ? __int2float_rn(at) * (1.0f / kFixed) : sum;
-          };
-          x.x = next(x.x, e[0]);
-          x.y = next(x.y, e[1]);
-          x.z = next(x.z, e[2]);
-          x.w = next(x.w, e[3]);
         }
         behind += block == 3 ? 0.0f : block == 2 ? t3 : block == 1 ? t2 + t3 : t1 + (t2 + t3);
         const float s3 = behind, s2 = s3 + g[3], s1 = s2 + g[2], s0 = s1 + g[1];
@@ -939,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         reinterpret_cast<float4 *>(tab.w)[lane] = w;
         if ((lane & 7) == 0) {
           tab.total[lane >> 3] = total;
-          tab.middle[lane >> 3] = middle;
+          tab.middle[lane >> 3] = 0.0f;
         }
         if (lane == 1) {
           tab.sum = all;
@@ -948,6 +925,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           tab.info = info;
         }
         __syncwarp();
+        if (kOut && __builtin_expect(all < kManyDigits, 0)) {
+          // (a lane a token, from the decays again, in short loops: code that never runs
+          // costs too, where it stands among the other)
+#pragma unroll 1
+          for (int i = 0; i < kChunk; i += 32) {
+            const int64_t at = p.decay_rows ? static_cast<int64_t>(info.row + i + lane) * p.heads : 0;
+            const float g = i + lane < rows ? __ldg(p.decay + at + info.head) * kLog2e : 0.0f;
+            int upto = __float2int_rn(fminf(fmaxf(g, kLowest), -kLowest) * kFixed);
+#pragma unroll 1
+            for (int o = 1; o < 32; o <<= 1) {
+              const int before = __shfl_up_sync(0xffffffffu, upto, o);
+              if (lane >= o) upto += before;
+            }
+            const int half = __shfl_sync(0xffffffffu, upto, 31) >> 1;
+            float *to = tab.x + i + lane;
+            if (*to == *to) *to = __int2float_rn(upto - half) * (1.0f / kFixed);  // (NaN stays)
+            if (lane == 0) tab.middle[i >> 5] = __int2float_rn(half) * (1.0f / kFixed);
+          }
+          __syncwarp();
+        }
         if (lane == 0) mbar_arrive(&c.tab_full[buf]);
         if (rows < 0) break;
       }
