@@ -62,10 +62,10 @@
 //
 // What bounds it (GB300).  One sequence of 32749 tokens, 32 heads: 192 us for the
 // pass with outputs = 3.5 us a chunk and SM, 5.7 TB/s (0.84 of the copy's rate),
-// 113 us for the pass without (4.7 TB/s), 16 us between.  With keys and queries
-// shared by 8 heads (16 sequences x 64 heads, 192 us) the bytes halve and the time
+// 109 us for the pass without (5.2 TB/s), 17 us between.  With keys and queries
+// shared by 8 heads (16 sequences x 64 heads, 189-197 us) the bytes halve and the time
 // does not: a chunk moves about 480 KB through shared memory (MMA operands 256 KB),
-// 3.8k of its 5.3k cycles at 128 bytes a cycle, the tensor pipe is busy for 43-48%
+// 3.8k of its 5.3k cycles at 128 bytes a cycle, the tensor pipe is busy for 42-46%
 // of the time and K'' takes one warpgroup pair 4.8k cycles.  What made it fast:
 // roles short enough for the instruction cache (unrolled and each walking the work
 // for itself 377 us, 7.9 warps waiting for instructions per issue; then 231), K''
