@@ -326,17 +326,21 @@ int64_t kda_lin_prompt_workspace(const kda_lin_prompt_args *args);
  * state from its first state.  Rows that no sequence covers are left as they
  * are; a sequence without tokens copies its first state.  A sequence with a
  * flagged slot (KDA_DEVERR_SLOT) or range (KDA_DEVERR_SEQ) writes nothing; starts
- * out of order can make other sequences share rows, whose outputs are then any of
- * theirs, and flag (KDA_DEVERR_SEQ) every sequence that the call would have split.  An infinity or NaN in a live row reaches what the formulas send it
- * to, its own and later tokens of its sequence and head, as an infinity or NaN;
- * rows outside the sequence reach nothing.  The output must not overlap the
- * inputs.  The page is held and updated in FP32; products that only feed the BF16 output are rounded to
- * BF16 once.  The chunked form takes factors of up to 2^64 both ways on the way to an
- * output: q k and the page's elements keep their digits from 2^-62 on (what is smaller
- * is off by up to 2^-62 times v or q), and the sums of |q k v| and |S q| have to be
- * below 2^62, the scale is
- * within 2^-62 and 2^62, and factors under 2^-126 are 0; path 1 has no such limits.  Errors: KDA_ERR_NULL_ARGS, KDA_ERR_NULL_POINTER, KDA_ERR_SHAPE (sizes
- * and strides outside the rules above), KDA_ERR_PATH, KDA_ERR_ALIGNMENT,
+ * out of order can make other sequences share rows, whose outputs are then any
+ * of theirs, and flag (KDA_DEVERR_SEQ) every sequence that the call would have
+ * split.  An infinity or NaN in a live row reaches what the formulas send it to,
+ * its own and later tokens of its sequence and head, as an infinity or NaN; rows
+ * outside the sequence reach nothing.  The output must not overlap the inputs.
+ *
+ * The page is held and updated in FP32; products that only feed the BF16 output
+ * are rounded to BF16 once.  The chunked form takes factors of up to 2^64 both
+ * ways on the way to an output: q k and the page's elements keep their digits
+ * from 2^-62 on (what is smaller is off by up to 2^-62 times v or q), the sums of
+ * |q k v| and |S q| have to be below 2^62 and the scale within 2^-62 and 2^62, and
+ * factors under 2^-126 are 0; path 1 has no such limits.
+ *
+ * Errors: KDA_ERR_NULL_ARGS, KDA_ERR_NULL_POINTER, KDA_ERR_SHAPE (sizes and
+ * strides outside the rules above), KDA_ERR_PATH, KDA_ERR_ALIGNMENT,
  * KDA_ERR_WORKSPACE, KDA_ERR_DEVICE, KDA_ERR_LAUNCH; nothing is launched on error.
  * Up to three kernels on `stream`, in order. */
 int kda_lin_prompt(const kda_lin_prompt_args *args, void *stream);

@@ -19,8 +19,9 @@
 // behind many resets (7e-4 of the factor after 28, summed in FP32): from a chunk's
 // logarithm of -512 on (where FP32's sums are 2^-14 off) bl is summed in whole numbers
 // and kept from the middle of the block's range: within +-2048, 2^-14 off, a
-// difference 2^-13, the factor 8.5e-5, where P is rounded to 2^-9.  Logarithms below -128 (base 2) count as -128: subnormal factors are 0
-// either way, and a reset of -inf stays a number.
+// difference 2^-13, the factor 8.5e-5, where P is rounded to 2^-9.  Logarithms below
+// -128 (base 2) count as -128: subnormal factors are 0 either way, and a reset of -inf
+// stays a number.
 //
 // Precision.  The page stays in FP32 registers.  K'' = factor * key is the one
 // operand of the page's update that BF16 does not hold; it goes in three BF16
@@ -930,7 +931,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // costs too, where it stands among the other)
 #pragma unroll 1
           for (int i = 0; i < kChunk; i += 32) {
-            const int64_t at = p.decay_rows ? static_cast<int64_t>(info.row + i + lane) * p.heads : 0;
+            const int64_t at =
+                p.decay_rows ? static_cast<int64_t>(info.row + i + lane) * p.heads : 0;
             const float g = i + lane < rows ? __ldg(p.decay + at + info.head) * kLog2e : 0.0f;
             int upto = __float2int_rn(fminf(fmaxf(g, kLowest), -kLowest) * kFixed);
 #pragma unroll 1

@@ -2,7 +2,8 @@
 //
 // The kernels of the step, the replay and the output projection wait on mbarriers
 // through kda::mbar_wait (the chunked linear attention has a wait and a self-test of
-// its own, in kda_lin_prompt.cu), which gives up after kWaitLimitNs of wall clock, raises the CTA's abort flag and
+// its own, in kda_lin_prompt.cu), which gives up after kWaitLimitNs of wall clock,
+// raises the CTA's abort flag and
 // lets the kernel report KDA_DEVERR_TIMEOUT and return.  This kernel exercises
 // exactly that path: one CTA initialises an mbarrier that nothing will
 // complete, every thread waits on it, the wait runs out, and thread 0 ORs

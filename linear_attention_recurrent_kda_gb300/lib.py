@@ -36,7 +36,8 @@ KDA_DEVERR_SEQ = 8
 EXPORTED = ("kda_decode", "kda_verify", "kda_step_noalloc", "kda_recover", "kda_oproj",
             "kda_lin_prompt_workspace", "kda_lin_prompt", "kda_lin_step",
             "kda_snapshot_save", "kda_snapshot_load",
-            "kda_selftest_wait_timeout", "kda_selftest_lin_wait_timeout", "kda_strerror", "kda_abi_version")
+            "kda_selftest_wait_timeout", "kda_selftest_lin_wait_timeout",
+            "kda_strerror", "kda_abi_version")
 
 
 class KdaArgs(ctypes.Structure):
