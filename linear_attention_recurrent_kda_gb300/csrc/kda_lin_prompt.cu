@@ -33,9 +33,10 @@
 // rounded to BF16, and the FP32 sum keeps their errors at that size (outputs against
 // 64 bits, 2-norm: 2.34e-3, of which the output's own rounding is 1.66e-3).  Second
 // parts of both leave 1.66e-3 and take a third more products, the page's one after
-// the other through one tile: 202 -> 270 us (16 prompts x 64 heads), 77 -> 95 (8
-// ragged ones x 32), 430 -> 512 (256 suffixes) and 336 -> 401 (32749 tokens), not
-// kept.  Token by token (path 1) nothing is rounded but the output.
+// the other through one tile: 197 -> 261 us (16 prompts x 64 heads), 71 -> 92 (8
+// ragged ones x 32), 415 -> 503 (256 suffixes) and 317 -> 379 (32749 tokens); of P
+// alone 1.71e-3 to 2.05e-3 at 237, 80, 431 and 334 us.  Neither is kept.  Token by
+// token (path 1) nothing is rounded but the output.
 //
 // Infinities and NaN.  P V multiplies the values of later tokens by zeros, and
 // 0 * NaN is not 0.  So P V runs after the page's warps have read the chunk's
