@@ -2,8 +2,11 @@
  * kda.h -- C ABI of the GB300 (sm_103a) KDA decode / speculative-verify step,
  * its record replay (kda_recover), the output-projection consumer epilogue
  * that follows the attention layer (kda_oproj), linear attention with one
- * decay per head (kda_lin_prompt, kda_lin_step) and snapshots of state pages
- * in 8 or 4 bits (kda_snapshot_save, kda_snapshot_load).
+ * decay per head (kda_lin_prompt, kda_lin_step), snapshots of state pages
+ * in 8 or 4 bits (kda_snapshot_save, kda_snapshot_load), and the operators of a
+ * selective-state-space layer: its short convolution (kda_conv_prompt,
+ * kda_conv_step), its scan (kda_ssm_prompt, kda_ssm_step) and its projections
+ * (kda_linear).
  *
  * The operation is the one defined by the vLLM API page
  *   "vllm.models.kimi_k3.nvidia.specialized_decode.cutedsl.kda.wide"
@@ -37,7 +40,7 @@
  * Ownership and threading: the caller owns every buffer; every pointer is a
  * DEVICE pointer of the current device.  The library allocates nothing,
  * never synchronises, and enqueues exactly one kernel on `stream` per call
- * (kda_lin_prompt: up to three).
+ * (kda_lin_prompt, kda_ssm_prompt: up to three).
  * Calls are reentrant and may come from several host threads at once (the
  * first call on a device reads its attributes and configures the kernel
  * under a lock); two calls that write the same pool regions must be ordered
@@ -70,13 +73,16 @@ enum {
   KDA_ERR_RECORD = 4,         /* record with tokens == 1 (KdaWide.__init__)    */
   KDA_ERR_NULL_POINTER = 5,   /* a required pointer is NULL                    */
   KDA_ERR_CONV_WIDTH = 6,     /* conv_width < tokens + 2, or too wide to stage */
+                              /* (kda_conv_*: width < taps - 1)                */
   KDA_ERR_ALIGNMENT = 7,      /* a pointer breaks its alignment rule (below)   */
   KDA_ERR_SHAPE = 8,          /* negative sizes, num_slots < 1, slot_cols <    */
                               /* tokens, or an item count beyond 2^31-1        */
   KDA_ERR_DEVICE = 9,         /* no usable device, or not an sm_103 device     */
   KDA_ERR_LAUNCH = 10,        /* the kernel launch failed (CUDA error)         */
   KDA_ERR_PATH = 11,          /* path outside 0..2                             */
-  KDA_ERR_WORKSPACE = 12      /* kda_lin_prompt: workspace missing or too small */
+  KDA_ERR_WORKSPACE = 12,     /* kda_lin_prompt, kda_ssm_prompt: workspace     */
+                              /* missing or too small                          */
+  KDA_ERR_ACTIVATION = 13     /* kda_linear: activation not a KDA_ACT_*        */
 };
 
 /* Device-side error flags, OR-ed into *err when err != NULL.  An item that
@@ -87,7 +93,7 @@ enum {
   KDA_DEVERR_ACCEPTED = 2,    /* accepted[r] outside 1..tokens                 */
   KDA_DEVERR_TIMEOUT = 4,     /* an on-chip copy wait ran out (the kernel      */
                               /* stopped early; outputs are incomplete)        */
-  KDA_DEVERR_SEQ = 8          /* kda_lin_prompt: seq_starts out of order or     */
+  KDA_DEVERR_SEQ = 8          /* prompt calls: seq_starts out of order or       */
                               /* outside 0..tokens, or a sequence longer than  */
                               /* max_seq                                       */
 };
@@ -407,6 +413,198 @@ int kda_snapshot_save(const kda_snapshot_args *args, void *stream);
 /* Reads snapshot snaps[i] back into state[slots[i]], all heads; the slots
  * written are distinct, a snapshot may be read into several.  Rules as above. */
 int kda_snapshot_load(const kda_snapshot_args *args, void *stream);
+
+/* ---- Short causal convolution ------------------------------------------------
+ *
+ * The depthwise convolution in front of a recurrent layer, for prompts and for
+ * single tokens.  Per channel c, over a sequence's inputs x and the taps - 1
+ * inputs before it:
+ *     y_t = bias_c + sum_j weight[j, c] x[t - taps + 1 + j, c],
+ *     output = BF16(silu(y)) or BF16(y),
+ * summed in FP32 from the bias on, oldest input first, with the KDA step's
+ * arithmetic: on a KDA layer's q, k and v (parts 3, taps 4, conv_state as the
+ * window) a prompt leaves the bits that decoding it token by token would.
+ * A window pool [num_slots, channels, width] keeps a slot's last inputs, oldest
+ * first, in columns 0 .. taps - 2; other columns are left alone.  Rows of x and
+ * output are BF16 [channels] and may be slices of wider rows: strides are
+ * multiples of 8 elements and at least the row's width.  x, output, weight, bias and
+ * window are 16-byte aligned, the index arrays 4.  The output must not overlap
+ * the inputs. */
+
+/* Arguments of one prompt call (kda_conv_prompt). */
+typedef struct kda_conv_prompt_args {
+  int32_t seqs;             /* sequences (0 is a no-op)                        */
+  int32_t channels;         /* a multiple of 8 * parts (0 is a no-op)          */
+  int32_t parts;            /* blocks of channels that `weight` is stored in   */
+  int32_t taps;             /* 2..4                                            */
+  int32_t tokens;           /* rows of x and output                            */
+  int32_t num_slots;        /* slots of `window` (ignored without slots)       */
+  int32_t width;            /* columns of `window`, >= taps - 1                */
+  int32_t window_f32;       /* window holds FP32 instead of BF16               */
+  int32_t silu;             /* nonzero: SiLU on the output                     */
+  int64_t x_stride, o_stride;               /* elements between rows           */
+  const void *x;            /* bf16 [tokens, channels]                         */
+  const void *weight;       /* bf16 [parts, taps, channels / parts]            */
+  const void *bias;         /* bf16 [channels] or NULL                         */
+  const int32_t *seq_starts;/* i32 [seqs + 1]: sequence r is rows              */
+                            /* seq_starts[r] .. seq_starts[r + 1] - 1          */
+  const int32_t *src_slots; /* i32 [seqs] or NULL: window a sequence continues */
+                            /* from; <= 0 (or NULL): zeros.  May be shared     */
+  const int32_t *dst_slots; /* i32 [seqs] or NULL: window its last inputs go   */
+                            /* to; <= 0 (or NULL): dropped.  Distinct, and no  */
+                            /* other sequence's src; may be its own src        */
+  void *window;             /* [num_slots, channels, width] (with slots)       */
+  void *output;             /* bf16 [tokens, channels]                         */
+  int32_t *err;             /* optional device word for KDA_DEVERR_* flags     */
+} kda_conv_prompt_args;
+
+/* Rows that no sequence covers are left as they are; a sequence shorter than
+ * taps - 1 keeps the newest of its first window.  A sequence with a flagged slot
+ * (KDA_DEVERR_SLOT) or range (KDA_DEVERR_SEQ) writes nothing; where starts are out
+ * of order, the call's other sequences may be incomplete.  Errors: KDA_ERR_NULL_ARGS,
+ * KDA_ERR_SHAPE, KDA_ERR_CONV_WIDTH, KDA_ERR_NULL_POINTER, KDA_ERR_ALIGNMENT,
+ * KDA_ERR_DEVICE, KDA_ERR_LAUNCH; nothing is launched on error.  One kernel on
+ * `stream`. */
+int kda_conv_prompt(const kda_conv_prompt_args *args, void *stream);
+
+/* Arguments of one single-token call (kda_conv_step). */
+typedef struct kda_conv_step_args {
+  int32_t batch;            /* requests, one row each (0 is a no-op)           */
+  int32_t channels, parts, taps;
+  int32_t num_slots, width, window_f32, silu;
+  int64_t x_stride, o_stride;               /* elements between rows           */
+  const void *x;            /* bf16 [batch, channels]                          */
+  const void *weight;       /* bf16 [parts, taps, channels / parts]            */
+  const void *bias;         /* bf16 [channels] or NULL                         */
+  const int32_t *slots;     /* i32 [batch]: the window, shifted in place;      */
+                            /* <= 0 = padding (a row of zeros, nothing else    */
+                            /* written)                                        */
+  void *window;             /* [num_slots, channels, width]           in/out   */
+  void *output;             /* bf16 [batch, channels]                          */
+  int32_t *err;             /* optional device word for KDA_DEVERR_* flags     */
+} kda_conv_step_args;
+
+/* One token per request.  Live requests have distinct slots.  A slot >= num_slots
+ * raises KDA_DEVERR_SLOT and is handled as padding.  One kernel on `stream`. */
+int kda_conv_step(const kda_conv_step_args *args, void *stream);
+
+/* ---- Selective state-space scan ----------------------------------------------
+ *
+ * Per channel c with `states` states h_n, B and C shared by the channels of a
+ * group (channel c reads group c / (channels / groups)):
+ *     s_t = dt[t, c] + dt_bias[c], then softplus(s) = log(1 + exp(s)) if asked,
+ *     h_n <- exp(s_t a[c, n]) h_n + s_t x[t, c] b[t, n],
+ *     y_t = sum_n c[t, n] h_n + d[c] x[t, c],     output = BF16(y silu(z)),
+ * in FP32, with the state in FP32 [num_slots, channels, states].  a is the decays'
+ * rate, < 0 in use (-exp of a stored logarithm).  dt_bias, d and z may be NULL (0, 0,
+ * no gate).  Rows of x, dt, b, c, z and output are BF16 and may be slices of wider
+ * rows: strides are multiples of 8 elements and at least the row's own width.  They,
+ * a and state are 16-byte aligned, the other arrays 4.  The output must not overlap
+ * the inputs. */
+
+/* Arguments of one prompt call (kda_ssm_prompt). */
+typedef struct kda_ssm_prompt_args {
+  int32_t seqs;             /* sequences (0 is a no-op)                        */
+  int32_t channels;         /* a multiple of 8 * groups (0 is a no-op)         */
+  int32_t states;           /* 16, 32 or 64                                    */
+  int32_t groups;           /* of channels that share b and c                  */
+  int32_t tokens;           /* rows                                            */
+  int32_t max_seq;          /* no sequence is longer than this                 */
+  int32_t num_slots;        /* slots of `state` (ignored without slots)        */
+  int32_t softplus;         /* nonzero: softplus on dt + dt_bias               */
+  int32_t path;             /* 0 = automatic; 1 = sequences whole; 2 = long    */
+                            /* ones in segments                                */
+  int64_t x_stride, dt_stride, b_stride, c_stride, z_stride, o_stride;
+  const void *x, *dt;       /* bf16 [tokens, channels]                         */
+  const float *a;           /* f32 [channels, states]                          */
+  const void *b, *c;        /* bf16 [tokens, groups * states]                  */
+  const float *d;           /* f32 [channels] or NULL                          */
+  const void *z;            /* bf16 [tokens, channels] or NULL                 */
+  const float *dt_bias;     /* f32 [channels] or NULL                          */
+  const int32_t *seq_starts;/* i32 [seqs + 1]: sequence r is rows              */
+                            /* seq_starts[r] .. seq_starts[r + 1] - 1          */
+  const int32_t *src_slots; /* i32 [seqs] or NULL: state a sequence starts     */
+                            /* from; <= 0 (or NULL): zeros.  May be shared     */
+  const int32_t *dst_slots; /* i32 [seqs] or NULL: where its last state goes;  */
+                            /* <= 0 (or NULL): dropped.  Distinct, and no      */
+                            /* other sequence's src; may be its own src        */
+  float *state;             /* f32 [num_slots, channels, states] (with slots)  */
+  void *output;             /* bf16 [tokens, channels]                         */
+  int32_t *err;             /* optional device word for KDA_DEVERR_* flags     */
+  void *workspace;          /* 256-byte aligned; NULL when none is needed      */
+  int64_t workspace_bytes;  /* at least kda_ssm_prompt_workspace(args)         */
+} kda_ssm_prompt_args;
+
+/* Bytes of workspace that kda_ssm_prompt needs for args' sizes and strides (no
+ * pointer is followed), 0 for none or for sizes that it refuses; -1 when args is
+ * NULL.  The workspace holds nothing between calls; calls that may run at the same
+ * time need their own. */
+int64_t kda_ssm_prompt_workspace(const kda_ssm_prompt_args *args);
+
+/* Rows that no sequence covers are left as they are; a sequence without tokens
+ * copies its first state.  A sequence with a flagged slot (KDA_DEVERR_SLOT) or range
+ * (KDA_DEVERR_SEQ) writes nothing; where starts are out of order, the call's other
+ * sequences may be incomplete.  Errors: KDA_ERR_NULL_ARGS, KDA_ERR_SHAPE,
+ * KDA_ERR_PATH, KDA_ERR_NULL_POINTER, KDA_ERR_ALIGNMENT, KDA_ERR_WORKSPACE,
+ * KDA_ERR_DEVICE, KDA_ERR_LAUNCH; nothing is launched on error.  Up to three
+ * kernels on `stream`, in order. */
+int kda_ssm_prompt(const kda_ssm_prompt_args *args, void *stream);
+
+/* Arguments of one single-token step (kda_ssm_step). */
+typedef struct kda_ssm_step_args {
+  int32_t batch;            /* requests, one row each (0 is a no-op)           */
+  int32_t channels, states, groups;
+  int32_t num_slots, softplus;
+  int64_t x_stride, dt_stride, b_stride, c_stride, z_stride, o_stride;
+  const void *x, *dt;       /* bf16 [batch, channels]                          */
+  const float *a;           /* f32 [channels, states]                          */
+  const void *b, *c;        /* bf16 [batch, groups * states]                   */
+  const float *d;           /* f32 [channels] or NULL                          */
+  const void *z;            /* bf16 [batch, channels] or NULL                  */
+  const float *dt_bias;     /* f32 [channels] or NULL                          */
+  const int32_t *slots;     /* i32 [batch]: the state, updated in place; <= 0  */
+                            /* = padding (a row of zeros, nothing else written) */
+  float *state;             /* f32 [num_slots, channels, states]      in/out   */
+  void *output;             /* bf16 [batch, channels]                          */
+  int32_t *err;             /* optional device word for KDA_DEVERR_* flags     */
+} kda_ssm_step_args;
+
+/* One token per request.  Live requests have distinct slots.  A slot >= num_slots
+ * raises KDA_DEVERR_SLOT and is handled as padding.  One kernel on `stream`. */
+int kda_ssm_step(const kda_ssm_step_args *args, void *stream);
+
+/* ---- Projections ---------------------------------------------------------------
+ *
+ *     output = BF16(act(x W^T + bias) + residual),
+ * x [rows, inner] and W [outer, inner] (a linear layer's weight) BF16, products
+ * summed in FP32 on the tensor cores, the epilogue in FP32, one rounding. */
+enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1, KDA_ACT_GELU = 2 /* with erf */,
+       KDA_ACT_SOFTPLUS = 3 };
+
+/* Arguments of one product (kda_linear).  All rows may be slices of wider rows:
+ * strides are multiples of 8 elements and at least the row's own width, which may
+ * be odd.  All pointers but err (4) are 16-byte aligned. */
+typedef struct kda_linear_args {
+  int32_t rows;             /* of x and output (0 is a no-op)                  */
+  int32_t inner;            /* length of the sums, >= 1                        */
+  int32_t outer;            /* columns of output (0 is a no-op)                */
+  int32_t activation;       /* a KDA_ACT_*                                     */
+  int64_t x_stride, w_stride, r_stride, o_stride;   /* elements between rows   */
+  const void *x;            /* bf16 [rows, inner]                              */
+  const void *weight;       /* bf16 [outer, inner]                             */
+  const void *bias;         /* bf16 [outer] or NULL                            */
+  const void *residual;     /* bf16 [rows, outer] or NULL; may be the output   */
+                            /* itself (same address and stride)                */
+  void *output;             /* bf16 [rows, outer]; overlaps no other input     */
+  int32_t *err;             /* optional device word for KDA_DEVERR_* flags     */
+} kda_linear_args;
+
+/* Columns behind `outer` in a wider row are left as they are.  An infinity or NaN
+ * reaches the sums that it is part of only.  Errors: KDA_ERR_NULL_ARGS,
+ * KDA_ERR_SHAPE, KDA_ERR_ACTIVATION, KDA_ERR_NULL_POINTER, KDA_ERR_ALIGNMENT,
+ * KDA_ERR_DEVICE, KDA_ERR_LAUNCH; nothing is launched on error.  One kernel on
+ * `stream`. */
+int kda_linear(const kda_linear_args *args, void *stream);
 
 /* Self-test of the bounded on-chip wait of the KDA step, the replay and the
  * output projection: one CTA waits on an mbarrier that nothing completes; the

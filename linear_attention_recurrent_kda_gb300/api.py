@@ -346,8 +346,8 @@ def _rows(name, t, rows, width, index):
     if not width:
         return t.data_ptr(), 0
     if rows <= 1:
-        step = width
-    if one != 1 or step % 8 or step < width:
+        step = -(-width // 8) * 8
+    if (one != 1 and width > 1) or step % 8 or step < width:
         raise ValueError(f"{name}: the elements of a row must be adjacent and rows a "
                          f"multiple of 8 elements apart, got strides {tuple(t.stride())}")
     return t.data_ptr(), step
@@ -524,3 +524,237 @@ def kda_snapshot_load(*, codes, scales, snaps, state, slots, err=None,
     """Read the snapshots ``snaps[i]`` back into ``state[slots[i]]``; see
     ``kda_snapshot_save``."""
     _snapshot("kda_snapshot_load", state, slots, codes, scales, snaps, err, stream)
+
+
+# ------------------------------------------------------ short causal convolution
+
+def _sequences(seq_starts, src_slots, dst_slots, index):
+    """(count, addresses) of a prompt call's sequences."""
+    i32 = torch.int32
+    sp = _want("seq_starts", seq_starts, i32, None, index)
+    if seq_starts.dim() != 1 or seq_starts.shape[0] < 1:
+        raise ValueError("seq_starts must be [seqs + 1]")
+    B = _count("seq_starts", seq_starts.shape[0] - 1)
+    return (B, sp, _maybe("src_slots", src_slots, i32, (B,), index),
+            _maybe("dst_slots", dst_slots, i32, (B,), index))
+
+
+def _conv_shape(x, weight):
+    """(device index, rows, channels, parts, taps)"""
+    index = _cuda_index("x", x)
+    _cuda_index("weight", weight)
+    if x.dim() != 2 or weight.dim() not in (2, 3):
+        raise ValueError("x must be [tokens, channels], weight [taps, channels] or "
+                         "[parts, taps, channels / parts]")
+    parts, taps = (1, weight.shape[0]) if weight.dim() == 2 else weight.shape[:2]
+    if parts * weight.shape[-1] != x.shape[1]:
+        raise ValueError(f"weight {tuple(weight.shape)} is not of {x.shape[1]} channels")
+    return index, _count("x", x.shape[0]), _count("channels", x.shape[1]), parts, taps
+
+
+def _window(window, channels, index):
+    """(address, slots, width, whether FP32) of a window pool."""
+    if not isinstance(window, torch.Tensor) or window.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("window must be a bfloat16 or float32 tensor")
+    ptr = _want("window", window, window.dtype, None, index)
+    if window.dim() != 3 or window.shape[1] != channels:
+        raise ValueError(f"window must be [num_slots, {channels}, width], got {tuple(window.shape)}")
+    return (ptr, _count("window", window.shape[0]), _count("window", window.shape[2]),
+            int(window.dtype is torch.float32))
+
+
+def kda_conv_prompt(*, x, weight, seq_starts, output, bias=None, window=None, src_slots=None,
+                    dst_slots=None, silu: bool = True, err=None,
+                    stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Short causal depthwise convolution over ragged prompts (include/kda.h
+    ``kda_conv_prompt``).
+
+    ``x``, ``output`` bf16 [tokens, channels] (each may be a slice of wider rows);
+    ``weight`` bf16 [taps, channels], or [parts, taps, channels / parts] as the KDA
+    step keeps it (``conv_weight``); ``bias`` bf16 [channels]; ``seq_starts`` i32
+    [seqs + 1]; ``window`` bf16 or f32 [num_slots, channels, width] (the KDA step's
+    ``conv_state``) with ``src_slots`` (the windows the sequences continue from) and
+    ``dst_slots`` (where their last inputs go), i32 [seqs] each or None."""
+    bf = torch.bfloat16
+    index, rows, C, parts, taps = _conv_shape(x, weight)
+    xp, xs = _rows("x", x, rows, C, index)
+    op, os_ = _rows("output", output, rows, C, index)
+    B, sp, src, dst = _sequences(seq_starts, src_slots, dst_slots, index)
+    if window is None:
+        if src_slots is not None or dst_slots is not None:
+            raise ValueError("window is required with src_slots or dst_slots")
+        wp, num_slots, width, f32 = None, 0, 0, 0
+    else:
+        wp, num_slots, width, f32 = _window(window, C, index)
+    _run("kda_conv_prompt", _lib.KdaConvPromptArgs(
+        B, C, parts, taps, rows, num_slots, width, f32, int(bool(silu)), xs, os_, xp,
+        _want("weight", weight, bf, None, index), _maybe("bias", bias, bf, (C,), index), sp, src,
+        dst, wp, op, _maybe("err", err, torch.int32, None, index)), index, stream)
+
+
+class KdaConvStep:
+    """A prepared single-token convolution (include/kda.h ``kda_conv_step``) over
+    fixed device tensors.
+
+    ``x``, ``output`` bf16 [batch, channels]; ``weight``, ``bias``, ``window`` as in
+    ``kda_conv_prompt``, the window shifted in place; ``slots`` i32 [batch] (<= 0:
+    padding).  Validates once and launches with ``__call__(stream)``; the tensors'
+    contents may change between calls, their storage may not."""
+
+    def __init__(self, *, x, weight, slots, window, output, bias=None, silu: bool = True, err=None):
+        bf = torch.bfloat16
+        self.index, rows, C, parts, taps = index, rows, C, parts, taps = _conv_shape(x, weight)
+        xp, xs = _rows("x", x, rows, C, index)
+        op, os_ = _rows("output", output, rows, C, index)
+        wp, num_slots, width, f32 = _window(window, C, index)
+        self.args = _lib.KdaConvStepArgs(
+            rows, C, parts, taps, num_slots, width, f32, int(bool(silu)), xs, os_, xp,
+            _want("weight", weight, bf, None, index), _maybe("bias", bias, bf, (C,), index),
+            _want("slots", slots, torch.int32, (rows,), index), wp, op,
+            _maybe("err", err, torch.int32, None, index))
+        # keep the tensors alive as long as the prepared step
+        self._keep = (x, weight, slots, window, output, bias, err)
+
+    def __call__(self, stream: Optional[torch.cuda.Stream] = None) -> None:
+        _run("kda_conv_step", self.args, self.index, stream)
+
+
+def kda_conv_step(stream: Optional[torch.cuda.Stream] = None, **kw) -> None:
+    """One single-token convolution on ``stream``; see ``KdaConvStep``."""
+    KdaConvStep(**kw)(stream)
+
+
+# ------------------------------------------------------- selective state-space scan
+
+def _ssm_rows(x, dt, a, b, c, d, z, dt_bias, output):
+    """What the scan's calls share: (device index, rows, channels, states, groups,
+    strides and addresses in the structs' order)."""
+    f32 = torch.float32
+    index = _cuda_index("x", x)
+    _cuda_index("a", a)
+    _cuda_index("b", b)
+    if x.dim() != 2 or a.dim() != 2 or b.dim() != 2:
+        raise ValueError("x must be [tokens, channels], a [channels, states], b and c "
+                         "[tokens, groups * states]")
+    rows, C, N = _count("x", x.shape[0]), _count("channels", x.shape[1]), _count("a", a.shape[1])
+    ap = _want("a", a, f32, (C, N), index)
+    groups = _count("b", b.shape[1]) // N if N else 0
+    if not N or not groups or groups * N != b.shape[1]:
+        raise ValueError(f"b must be [tokens, groups * {N}], got {tuple(b.shape)}")
+    (xp, xs), (tp, ts) = _rows("x", x, rows, C, index), _rows("dt", dt, rows, C, index)
+    (bp, bs), (cp, cs) = (_rows(n, t, rows, groups * N, index) for n, t in (("b", b), ("c", c)))
+    zp, zs = (None, 0) if z is None else _rows("z", z, rows, C, index)
+    op, os_ = _rows("output", output, rows, C, index)
+    return (index, rows, C, N, groups, (xs, ts, bs, cs, zs, os_),
+            (xp, tp, ap, bp, cp, _maybe("d", d, f32, (C,), index), zp,
+             _maybe("dt_bias", dt_bias, f32, (C,), index)), op)
+
+
+def _ssm_state(state, C, N, index):
+    ptr = _want("state", state, torch.float32, None, index)
+    if state.dim() != 3 or state.shape[1:] != (C, N):
+        raise ValueError(f"state must be [num_slots, {C}, {N}], got {tuple(state.shape)}")
+    return ptr, _count("state", state.shape[0])
+
+
+def kda_ssm_prompt(*, x, dt, a, b, c, seq_starts, output, d=None, z=None, dt_bias=None,
+                   softplus: bool = True, state=None, src_slots=None, dst_slots=None,
+                   max_seq: Optional[int] = None, err=None, path: int = 0, workspace=None,
+                   stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Selective state-space scan over ragged prompts (include/kda.h
+    ``kda_ssm_prompt``).
+
+    ``x``, ``dt``, ``z``, ``output`` bf16 [tokens, channels], ``b``, ``c`` bf16
+    [tokens, groups * states] (each may be a slice of wider rows); ``a`` f32
+    [channels, states], the decays' rate (below 0); ``d``, ``dt_bias`` f32
+    [channels]; ``seq_starts`` i32 [seqs + 1]; ``state`` f32 [num_slots, channels,
+    states] with ``src_slots`` (the states the sequences start from) and
+    ``dst_slots`` (where their last states go), i32 [seqs] each or None.
+    ``max_seq``: no sequence is longer (default: ``tokens``; the tighter, the better
+    the work is laid out).  ``workspace``: a CUDA uint8 tensor of at least
+    ``lib.ssm_workspace`` bytes; by default allocated for the call, on the stream it
+    runs on."""
+    index, rows, C, N, G, strides, ptrs, op = _ssm_rows(x, dt, a, b, c, d, z, dt_bias, output)
+    B, sp, src, dst = _sequences(seq_starts, src_slots, dst_slots, index)
+    if state is None:
+        if src_slots is not None or dst_slots is not None:
+            raise ValueError("state is required with src_slots or dst_slots")
+        state_p, num_slots = None, 0
+    else:
+        state_p, num_slots = _ssm_state(state, C, N, index)
+    args = _lib.KdaSsmPromptArgs(
+        B, C, N, G, rows, rows if max_seq is None else min(int(max_seq), rows), num_slots,
+        int(bool(softplus)), int(path), *strides, *ptrs, sp, src, dst, state_p, op,
+        _maybe("err", err, torch.int32, None, index))
+    if workspace is not None:
+        args.workspace = _want("workspace", workspace, torch.uint8, None, index)
+        args.workspace_bytes = workspace.numel()
+    elif (need := _lib.ssm_workspace(args)) > 0:
+        # from the pool of the stream that uses it: freed behind its kernels
+        with torch.cuda.device(index), torch.cuda.stream(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        args.workspace, args.workspace_bytes = workspace.data_ptr(), need
+    _run("kda_ssm_prompt", args, index, stream)
+
+
+class KdaSsmStep:
+    """A prepared single-token step of the selective scan (include/kda.h
+    ``kda_ssm_step``) over fixed device tensors.
+
+    Rows ``x``, ``dt``, ``z``, ``output`` bf16 [batch, channels], ``b``, ``c`` bf16
+    [batch, groups * states]; ``a``, ``d``, ``dt_bias`` as in ``kda_ssm_prompt``;
+    ``slots`` i32 [batch] (<= 0: padding); ``state`` f32 [num_slots, channels,
+    states], updated in place.  Validates once and launches with
+    ``__call__(stream)``; the tensors' contents may change between calls, their
+    storage may not."""
+
+    def __init__(self, *, x, dt, a, b, c, slots, state, output, d=None, z=None, dt_bias=None,
+                 softplus: bool = True, err=None):
+        self.index, rows, C, N, G, strides, ptrs, op = _ssm_rows(x, dt, a, b, c, d, z, dt_bias,
+                                                                 output)
+        state_p, num_slots = _ssm_state(state, C, N, self.index)
+        self.args = _lib.KdaSsmStepArgs(
+            rows, C, N, G, num_slots, int(bool(softplus)), *strides, *ptrs,
+            _want("slots", slots, torch.int32, (rows,), self.index), state_p, op,
+            _maybe("err", err, torch.int32, None, self.index))
+        # keep the tensors alive as long as the prepared step
+        self._keep = (x, dt, a, b, c, slots, state, output, d, z, dt_bias, err)
+
+    def __call__(self, stream: Optional[torch.cuda.Stream] = None) -> None:
+        _run("kda_ssm_step", self.args, self.index, stream)
+
+
+def kda_ssm_step(stream: Optional[torch.cuda.Stream] = None, **kw) -> None:
+    """One single-token step of the scan on ``stream``; see ``KdaSsmStep``."""
+    KdaSsmStep(**kw)(stream)
+
+
+# --------------------------------------------------------------------- projections
+
+ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "gelu": 2, "softplus": 3}
+
+
+def kda_linear(*, x, weight, output, bias=None, residual=None, activation: Optional[str] = None,
+               err=None, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """output = act(x weight^T + bias) + residual (include/kda.h ``kda_linear``).
+
+    ``x`` bf16 [rows, inner], ``weight`` bf16 [outer, inner], ``residual`` and
+    ``output`` bf16 [rows, outer] (each may be a slice of wider rows; the residual may
+    be the output itself); ``bias`` bf16 [outer]; ``activation`` None, "none",
+    "silu", "gelu" (with erf) or "softplus"."""
+    index = _cuda_index("x", x)
+    _cuda_index("weight", weight)
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError("x must be [rows, inner], weight [outer, inner]")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(map(str, ACTIVATIONS))}, "
+                         f"got {activation!r}")
+    rows, K = _count("x", x.shape[0]), _count("inner", x.shape[1])
+    N = _count("weight", weight.shape[0])
+    (xp, xs), (wp, ws) = _rows("x", x, rows, K, index), _rows("weight", weight, N, K, index)
+    op, os_ = _rows("output", output, rows, N, index)
+    rp, rs = (None, 0) if residual is None else _rows("residual", residual, rows, N, index)
+    _run("kda_linear", _lib.KdaLinearArgs(
+        rows, K, N, ACTIVATIONS[activation], xs, ws, rs, os_, xp, wp,
+        _maybe("bias", bias, torch.bfloat16, (N,), index), rp, op,
+        _maybe("err", err, torch.int32, None, index)), index, stream)

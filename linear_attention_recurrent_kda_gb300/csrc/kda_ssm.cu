@@ -1,0 +1,199 @@
+// Selective scan: the single-token step, and the checks and dispatch of both
+// calls.
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "../../include/kda.h"
+#include "kda_device.cuh"
+#include "kda_host.h"
+#include "kda_ssm.cuh"
+
+namespace kda {
+namespace ssm {
+
+constexpr int kThreads = 128;
+constexpr int kRequests = 4;     // of a thread: they share its part of a
+
+// A thread: 4 states of a channel, of kRequests requests, all loads in flight at
+// once.  Groups of channels are multiples of 8, so a warp's channels are of one
+// group, and all there or none.
+template <int kStates>
+__global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ Params p,
+                                                        int blocks) {
+  constexpr int kLanes = kStates / 4;
+  const int block = blockIdx.x % blocks, first = blockIdx.x / blocks * kRequests;
+  const int channel = (block * kThreads + threadIdx.x) / kLanes, quad = threadIdx.x % kLanes;
+  if (channel >= p.channels) return;
+  int slot[kRequests];
+  float4 h[kRequests];
+#pragma unroll
+  for (int i = 0; i < kRequests; ++i) {
+    slot[i] = first + i < p.batch ? __ldg(p.slots + first + i) : 0;
+    if (slot[i] >= p.seqs.num_slots) {
+      if (p.err && block == 0 && threadIdx.x == 0) atomicOr(p.err, KDA_DEVERR_SLOT);
+      slot[i] = 0;
+    }
+    if (slot[i] > 0)
+      h[i] = __ldcs(reinterpret_cast<const float4 *>(state_of(p, slot[i], channel, kStates)) + quad);
+  }
+  float4 a = __ldg(reinterpret_cast<const float4 *>(p.a + static_cast<int64_t>(channel) * kStates) + quad);
+  a.x *= kLog2e, a.y *= kLog2e, a.z *= kLog2e, a.w *= kLog2e;
+  const float d = p.d ? __ldg(p.d + channel) : 0.0f;
+  const float bias = p.dt_bias ? __ldg(p.dt_bias + channel) : 0.0f;
+  const int states = channel / p.span * kStates + 4 * quad;
+#pragma unroll
+  for (int i = 0; i < kRequests; ++i) {
+    const int64_t row = first + i;
+    if (row >= p.batch) continue;
+    __nv_bfloat16 *out = p.output + row * p.o_stride + channel;
+    if (slot[i] <= 0) {
+      if (quad == 0) *out = __float2bfloat16_rn(0.0f);
+      continue;
+    }
+    const float x = __bfloat162float(p.x[row * p.x_stride + channel]);
+    float s = __bfloat162float(p.dt[row * p.dt_stride + channel]) + bias;
+    if (p.softplus) s = softplus(s);
+    float bn[4], cn[4];
+    unpack4(__ldg(reinterpret_cast<const uint2 *>(p.b + row * p.b_stride + states)), bn);
+    unpack4(__ldg(reinterpret_cast<const uint2 *>(p.c + row * p.c_stride + states)), cn);
+    const float sx = s * x;
+    h[i].x = decayed(h[i].x, decay_of(s * a.x), sx * bn[0]);
+    h[i].y = decayed(h[i].y, decay_of(s * a.y), sx * bn[1]);
+    h[i].z = decayed(h[i].z, decay_of(s * a.z), sx * bn[2]);
+    h[i].w = decayed(h[i].w, decay_of(s * a.w), sx * bn[3]);
+    __stcs(reinterpret_cast<float4 *>(state_of(p, slot[i], channel, kStates)) + quad, h[i]);
+    float y = cn[0] * h[i].x + cn[1] * h[i].y + cn[2] * h[i].z + cn[3] * h[i].w;
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+    if (quad == 0) {
+      y = __fmaf_rn(d, x, y);
+      if (p.z) y *= silu_approx(__bfloat162float(p.z[row * p.z_stride + channel]));
+      *out = __float2bfloat16_rn(y);
+    }
+  }
+}
+
+template <int kStates>
+static int launch_step(const Params &p, cudaStream_t stream) {
+  const int per = kThreads / (kStates / 4), blocks = (p.channels + per - 1) / per;
+  const int64_t grid = (static_cast<int64_t>(p.batch) + kRequests - 1) / kRequests * blocks;
+  if (grid > 0x7fffffffll) return KDA_ERR_SHAPE;
+  step_kernel<kStates><<<static_cast<int>(grid), kThreads, 0, stream>>>(p, blocks);
+  return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
+}
+
+template <class Args>
+static int check(const Args *a, int64_t rows) {
+  if (a->channels < 0 || a->groups < 1 || a->channels % (8 * int64_t(a->groups)) != 0)
+    return KDA_ERR_SHAPE;
+  if (rows < 0 || (a->states != 16 && a->states != 32 && a->states != 64)) return KDA_ERR_SHAPE;
+  const int64_t shared = int64_t(a->groups) * a->states;
+  if (!stride_ok(a->x_stride, a->channels) || !stride_ok(a->dt_stride, a->channels) ||
+      !stride_ok(a->b_stride, shared) || !stride_ok(a->c_stride, shared) ||
+      !stride_ok(a->o_stride, a->channels) || (a->z && !stride_ok(a->z_stride, a->channels)))
+    return KDA_ERR_SHAPE;
+  return KDA_SUCCESS;
+}
+template <class Args>
+static bool rows_aligned(const Args *a) {
+  return aligned(a->x, 16) && aligned(a->dt, 16) && aligned(a->b, 16) && aligned(a->c, 16) &&
+         aligned(a->z, 16) && aligned(a->output, 16) && aligned(a->a, 16) && aligned(a->state, 16) &&
+         aligned(a->d, 4) && aligned(a->dt_bias, 4) && aligned(a->err, 4);
+}
+template <class Args>
+static Params params_of(const Args *a) {
+  Params p = {};
+  p.seqs.num_slots = a->num_slots;
+  p.channels = a->channels;
+  p.span = a->channels / a->groups;
+  p.softplus = a->softplus != 0;
+  p.x_stride = a->x_stride;
+  p.dt_stride = a->dt_stride;
+  p.b_stride = a->b_stride;
+  p.c_stride = a->c_stride;
+  p.z_stride = a->z_stride;
+  p.o_stride = a->o_stride;
+  p.x = static_cast<const __nv_bfloat16 *>(a->x);
+  p.dt = static_cast<const __nv_bfloat16 *>(a->dt);
+  p.b = static_cast<const __nv_bfloat16 *>(a->b);
+  p.c = static_cast<const __nv_bfloat16 *>(a->c);
+  p.z = static_cast<const __nv_bfloat16 *>(a->z);
+  p.a = a->a;
+  p.d = a->d;
+  p.dt_bias = a->dt_bias;
+  p.state = a->state;
+  p.output = static_cast<__nv_bfloat16 *>(a->output);
+  p.err = a->err;
+  return p;
+}
+
+static int run_step(const kda_ssm_step_args *a, cudaStream_t stream) {
+  if (!a) return KDA_ERR_NULL_ARGS;
+  if (const int rc = check(a, a->batch)) return rc;
+  if (a->num_slots < 1) return KDA_ERR_SHAPE;
+  if (a->batch == 0 || a->channels == 0) return KDA_SUCCESS;
+  if (!a->x || !a->dt || !a->a || !a->b || !a->c || !a->slots || !a->state || !a->output)
+    return KDA_ERR_NULL_POINTER;
+  if (!rows_aligned(a) || !aligned(a->slots, 4)) return KDA_ERR_ALIGNMENT;
+  int dev = 0;
+  DeviceFacts df;
+  if (!current_device(&dev, &df)) return KDA_ERR_DEVICE;
+  Params p = params_of(a);
+  p.slots = a->slots;
+  p.batch = a->batch;
+  return a->states == 16 ? launch_step<16>(p, stream)
+                         : a->states == 32 ? launch_step<32>(p, stream) : launch_step<64>(p, stream);
+}
+
+static int plan_prompt(const kda_ssm_prompt_args *a, int64_t *workspace) {
+  if (const int rc = check(a, a->tokens)) return rc;
+  const bool pool = a->src_slots || a->dst_slots;
+  if (a->seqs < 0 || a->max_seq < 0 || (pool && a->num_slots < 1)) return KDA_ERR_SHAPE;
+  if (a->path < 0 || a->path > 2) return KDA_ERR_PATH;
+  *workspace = 0;
+  return KDA_SUCCESS;
+}
+
+static int run_prompt(const kda_ssm_prompt_args *a, cudaStream_t stream) {
+  if (!a) return KDA_ERR_NULL_ARGS;
+  int64_t workspace;
+  if (const int rc = plan_prompt(a, &workspace)) return rc;
+  if (a->seqs == 0 || a->channels == 0) return KDA_SUCCESS;
+  if (!a->seq_starts || !a->a || ((a->src_slots || a->dst_slots) && !a->state)) return KDA_ERR_NULL_POINTER;
+  if (a->tokens > 0 && (!a->x || !a->dt || !a->b || !a->c || !a->output))
+    return KDA_ERR_NULL_POINTER;
+  if (!rows_aligned(a) || !aligned(a->seq_starts, 4) || !aligned(a->src_slots, 4) ||
+      !aligned(a->dst_slots, 4))
+    return KDA_ERR_ALIGNMENT;
+  if (workspace > 0 && (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < workspace))
+    return KDA_ERR_WORKSPACE;
+  int dev = 0;
+  DeviceFacts df;
+  if (!current_device(&dev, &df)) return KDA_ERR_DEVICE;
+  Params p = params_of(a);
+  p.seqs.count = a->seqs;
+  p.seqs.tokens = a->tokens;
+  p.seqs.longest = a->max_seq < a->tokens ? a->max_seq : a->tokens;
+  p.seqs.starts = a->seq_starts;
+  p.seqs.src_slots = a->src_slots;
+  p.seqs.dst_slots = a->dst_slots;
+  return launch_prompt(p, a->states, stream);
+}
+
+}  // namespace ssm
+}  // namespace kda
+
+extern "C" int kda_ssm_step(const kda_ssm_step_args *args, void *stream) {
+  return kda::ssm::run_step(args, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int kda_ssm_prompt(const kda_ssm_prompt_args *args, void *stream) {
+  return kda::ssm::run_prompt(args, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int64_t kda_ssm_prompt_workspace(const kda_ssm_prompt_args *args) {
+  int64_t workspace;
+  if (!args) return -1;
+  return kda::ssm::plan_prompt(args, &workspace) ? 0 : workspace;
+}

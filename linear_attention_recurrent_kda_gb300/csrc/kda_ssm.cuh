@@ -1,0 +1,71 @@
+// Shared by the selective scan's kernels: parameters, and the arithmetic of one
+// token.  Per channel, with N states:
+//   s = softplus(dt + dt_bias),  h_n <- exp(s a_n) h_n + s x b_n,
+//   y = sum_n c_n h_n + d x,     out = y silu(z).
+#pragma once
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "../../include/kda.h"
+#include "kda_device.cuh"
+#include "kda_rows.cuh"
+
+namespace kda {
+namespace ssm {
+
+using namespace rows;
+
+struct Params {
+  Seqs seqs;                     // prompt
+  const int32_t *slots;          // step
+  int batch;
+  int channels, span, softplus;  // span: channels of a group
+  int64_t x_stride, dt_stride, b_stride, c_stride, z_stride, o_stride;
+  const __nv_bfloat16 *x, *dt, *b, *c, *z;
+  const float *a, *d, *dt_bias;
+  float *state;
+  __nv_bfloat16 *output;
+  int32_t *err;
+};
+
+// A token's decay 2^x as keep + change, keep 0 or 1: near 1 a factor rounded to
+// FP32 is off the same way at every token of a constant step, and a slow state
+// drifts (2^-25 a token); 2^x - 1 is off by 2^-23 of itself, which no number of
+// tokens adds up.
+struct Decay {
+  float keep, change;
+};
+__device__ __forceinline__ Decay decay_of(float x) {
+  // (2^x - 1) / x on [-1, 0]: interpolated at the Chebyshev points, degree 5, off by
+  // 2^-26 of it
+  float t = 1.14919952e-4f;
+  t = __fmaf_rn(t, x, 1.29163684e-3f);
+  t = __fmaf_rn(t, x, 9.59703512e-3f);
+  t = __fmaf_rn(t, x, 5.54992296e-2f);
+  t = __fmaf_rn(t, x, 2.40226090e-1f);
+  t = __fmaf_rn(t, x, 6.93147182e-1f);
+  const bool slow = fabsf(x + 0.5f) <= 0.5f;
+  return Decay{slow ? 1.0f : 0.0f, slow ? t * x : exp2_approx(x)};
+}
+__device__ __forceinline__ float decayed(float h, const Decay &d, float add) {
+  return __fmaf_rn(h, d.keep, __fmaf_rn(h, d.change, add));
+}
+
+// 4 BF16 values of an 8-byte vector.
+__device__ __forceinline__ void unpack4(const uint2 &u, float (&f)[4]) {
+  f[0] = __uint_as_float(u.x << 16);
+  f[1] = __uint_as_float(u.x & 0xFFFF0000u);
+  f[2] = __uint_as_float(u.y << 16);
+  f[3] = __uint_as_float(u.y & 0xFFFF0000u);
+}
+
+__device__ __forceinline__ float *state_of(const Params &p, int slot, int channel, int states) {
+  return p.state + (static_cast<int64_t>(slot) * p.channels + channel) * states;
+}
+
+// Enqueues the prompt form for checked parameters.  Returns a KDA_* code.
+int launch_prompt(const Params &p, int states, cudaStream_t stream);
+
+}  // namespace ssm
+}  // namespace kda

@@ -1391,6 +1391,7 @@ const char *kda_strerror(int code) {
     case KDA_ERR_LAUNCH: return "kernel launch failed";
     case KDA_ERR_PATH: return "path must be 0, 1 or 2";
     case KDA_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
+    case KDA_ERR_ACTIVATION: return "activation must be 0, 1, 2 or 3";
     default: return "unknown error code";
   }
 }

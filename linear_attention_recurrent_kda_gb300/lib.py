@@ -27,6 +27,7 @@ KDA_ERR_DEVICE = 9
 KDA_ERR_LAUNCH = 10
 KDA_ERR_PATH = 11
 KDA_ERR_WORKSPACE = 12
+KDA_ERR_ACTIVATION = 13
 KDA_PATH_AUTO, KDA_PATH_PERSISTENT, KDA_PATH_SPLIT = 0, 1, 2
 KDA_DEVERR_SLOT = 1
 KDA_DEVERR_ACCEPTED = 2
@@ -36,6 +37,8 @@ KDA_DEVERR_SEQ = 8
 EXPORTED = ("kda_decode", "kda_verify", "kda_step_noalloc", "kda_recover", "kda_oproj",
             "kda_lin_prompt_workspace", "kda_lin_prompt", "kda_lin_step",
             "kda_snapshot_save", "kda_snapshot_load",
+            "kda_conv_prompt", "kda_conv_step", "kda_ssm_prompt_workspace", "kda_ssm_prompt",
+            "kda_ssm_step", "kda_linear",
             "kda_selftest_wait_timeout", "kda_selftest_lin_wait_timeout",
             "kda_strerror", "kda_abi_version")
 
@@ -123,6 +126,70 @@ class KdaSnapshotArgs(ctypes.Structure):
     ]
 
 
+class KdaConvPromptArgs(ctypes.Structure):
+    """Mirror of ``struct kda_conv_prompt_args``."""
+    _fields_ = [
+        ("seqs", ctypes.c_int32), ("channels", ctypes.c_int32), ("parts", ctypes.c_int32),
+        ("taps", ctypes.c_int32), ("tokens", ctypes.c_int32), ("num_slots", ctypes.c_int32),
+        ("width", ctypes.c_int32), ("window_f32", ctypes.c_int32), ("silu", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64), ("o_stride", ctypes.c_int64),
+        ("x", _P), ("weight", _P), ("bias", _P), ("seq_starts", _P), ("src_slots", _P),
+        ("dst_slots", _P), ("window", _P), ("output", _P), ("err", _P),
+    ]
+
+
+class KdaConvStepArgs(ctypes.Structure):
+    """Mirror of ``struct kda_conv_step_args``."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("channels", ctypes.c_int32), ("parts", ctypes.c_int32),
+        ("taps", ctypes.c_int32), ("num_slots", ctypes.c_int32), ("width", ctypes.c_int32),
+        ("window_f32", ctypes.c_int32), ("silu", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64), ("o_stride", ctypes.c_int64),
+        ("x", _P), ("weight", _P), ("bias", _P), ("slots", _P), ("window", _P), ("output", _P),
+        ("err", _P),
+    ]
+
+
+class KdaSsmPromptArgs(ctypes.Structure):
+    """Mirror of ``struct kda_ssm_prompt_args``."""
+    _fields_ = [
+        ("seqs", ctypes.c_int32), ("channels", ctypes.c_int32), ("states", ctypes.c_int32),
+        ("groups", ctypes.c_int32), ("tokens", ctypes.c_int32), ("max_seq", ctypes.c_int32),
+        ("num_slots", ctypes.c_int32), ("softplus", ctypes.c_int32), ("path", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64), ("dt_stride", ctypes.c_int64),
+        ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64),
+        ("z_stride", ctypes.c_int64), ("o_stride", ctypes.c_int64),
+        ("x", _P), ("dt", _P), ("a", _P), ("b", _P), ("c", _P), ("d", _P), ("z", _P),
+        ("dt_bias", _P), ("seq_starts", _P), ("src_slots", _P), ("dst_slots", _P),
+        ("state", _P), ("output", _P), ("err", _P), ("workspace", _P),
+        ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
+class KdaSsmStepArgs(ctypes.Structure):
+    """Mirror of ``struct kda_ssm_step_args``."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("channels", ctypes.c_int32), ("states", ctypes.c_int32),
+        ("groups", ctypes.c_int32), ("num_slots", ctypes.c_int32), ("softplus", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64), ("dt_stride", ctypes.c_int64),
+        ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64),
+        ("z_stride", ctypes.c_int64), ("o_stride", ctypes.c_int64),
+        ("x", _P), ("dt", _P), ("a", _P), ("b", _P), ("c", _P), ("d", _P), ("z", _P),
+        ("dt_bias", _P), ("slots", _P), ("state", _P), ("output", _P), ("err", _P),
+    ]
+
+
+class KdaLinearArgs(ctypes.Structure):
+    """Mirror of ``struct kda_linear_args``."""
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("inner", ctypes.c_int32), ("outer", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64), ("w_stride", ctypes.c_int64),
+        ("r_stride", ctypes.c_int64), ("o_stride", ctypes.c_int64),
+        ("x", _P), ("weight", _P), ("bias", _P), ("residual", _P), ("output", _P), ("err", _P),
+    ]
+
+
 class KdaError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"KDA error {code}: {msg}")
@@ -159,7 +226,17 @@ def load(path: str | None = None) -> ctypes.CDLL:
                             ("kda_snapshot_save", [ctypes.POINTER(KdaSnapshotArgs), _P],
                              ctypes.c_int),
                             ("kda_snapshot_load", [ctypes.POINTER(KdaSnapshotArgs), _P],
-                             ctypes.c_int)):
+                             ctypes.c_int),
+                            ("kda_conv_prompt", [ctypes.POINTER(KdaConvPromptArgs), _P],
+                             ctypes.c_int),
+                            ("kda_conv_step", [ctypes.POINTER(KdaConvStepArgs), _P],
+                             ctypes.c_int),
+                            ("kda_ssm_prompt_workspace", [ctypes.POINTER(KdaSsmPromptArgs)],
+                             ctypes.c_int64),
+                            ("kda_ssm_prompt", [ctypes.POINTER(KdaSsmPromptArgs), _P],
+                             ctypes.c_int),
+                            ("kda_ssm_step", [ctypes.POINTER(KdaSsmStepArgs), _P], ctypes.c_int),
+                            ("kda_linear", [ctypes.POINTER(KdaLinearArgs), _P], ctypes.c_int)):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, res
     for fn in (lib.kda_selftest_wait_timeout, lib.kda_selftest_lin_wait_timeout):
@@ -185,3 +262,8 @@ def call(entry: str, args, stream_handle: int) -> int:
 def prompt_workspace(args) -> int:
     """Bytes of workspace that ``kda_lin_prompt`` needs for these sizes."""
     return (_lib or load()).kda_lin_prompt_workspace(args)
+
+
+def ssm_workspace(args) -> int:
+    """Bytes of workspace that ``kda_ssm_prompt`` needs for these sizes."""
+    return (_lib or load()).kda_ssm_prompt_workspace(args)
