@@ -146,19 +146,42 @@ static int run_step(const kda_ssm_step_args *a, cudaStream_t stream) {
                          : a->states == 32 ? launch_step<32>(p, stream) : launch_step<64>(p, stream);
 }
 
-static int plan_prompt(const kda_ssm_prompt_args *a, int64_t *workspace) {
+// Rows of a piece of a split sequence (0: sequences stay whole), and the workspace.
+struct Plan {
+  int piece;
+  int64_t workspace;
+};
+constexpr int kShortestPiece = 256;      // rows
+
+static int plan_prompt(const kda_ssm_prompt_args *a, Plan *plan) {
   if (const int rc = check(a, a->tokens)) return rc;
   const bool pool = a->src_slots || a->dst_slots;
   if (a->seqs < 0 || a->max_seq < 0 || (pool && a->num_slots < 1)) return KDA_ERR_SHAPE;
   if (a->path < 0 || a->path > 2) return KDA_ERR_PATH;
-  *workspace = 0;
+  plan->piece = 0;
+  plan->workspace = 0;
+  const int64_t longest = a->max_seq < a->tokens ? a->max_seq : a->tokens;
+  if (a->path == 1 || longest <= kShortestPiece) return KDA_SUCCESS;
+  // CTAs of 128 threads with 16 states each; four of an SM run at a time
+  const int64_t threads = static_cast<int64_t>(a->channels) * (a->states / 16);
+  const int64_t blocks = (threads + 127) / 128, slots = 152 * 4;
+  const int64_t share = a->tokens * blocks / slots;      // rows of one of them
+  if (a->path == 0 && longest < 4 * share + 512) return KDA_SUCCESS;
+  int64_t piece = (share + 15) / 16 * 16;
+  if (piece < kShortestPiece) piece = kShortestPiece;
+  if (piece >= longest) {
+    if (a->path == 0) return KDA_SUCCESS;
+    piece = kShortestPiece;
+  }
+  plan->piece = static_cast<int>(piece);
+  plan->workspace = pieces_of(a->tokens, a->seqs, plan->piece) * a->channels * (a->states + 1) * 4;
   return KDA_SUCCESS;
 }
 
 static int run_prompt(const kda_ssm_prompt_args *a, cudaStream_t stream) {
   if (!a) return KDA_ERR_NULL_ARGS;
-  int64_t workspace;
-  if (const int rc = plan_prompt(a, &workspace)) return rc;
+  Plan plan;
+  if (const int rc = plan_prompt(a, &plan)) return rc;
   if (a->seqs == 0 || a->channels == 0) return KDA_SUCCESS;
   if (!a->seq_starts || !a->a || ((a->src_slots || a->dst_slots) && !a->state)) return KDA_ERR_NULL_POINTER;
   if (a->tokens > 0 && (!a->x || !a->dt || !a->b || !a->c || !a->output))
@@ -166,7 +189,8 @@ static int run_prompt(const kda_ssm_prompt_args *a, cudaStream_t stream) {
   if (!rows_aligned(a) || !aligned(a->seq_starts, 4) || !aligned(a->src_slots, 4) ||
       !aligned(a->dst_slots, 4))
     return KDA_ERR_ALIGNMENT;
-  if (workspace > 0 && (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < workspace))
+  if (plan.workspace > 0 && (!a->workspace || !aligned(a->workspace, 256) ||
+                             a->workspace_bytes < plan.workspace))
     return KDA_ERR_WORKSPACE;
   int dev = 0;
   DeviceFacts df;
@@ -178,7 +202,12 @@ static int run_prompt(const kda_ssm_prompt_args *a, cudaStream_t stream) {
   p.seqs.starts = a->seq_starts;
   p.seqs.src_slots = a->src_slots;
   p.seqs.dst_slots = a->dst_slots;
-  return launch_prompt(p, a->states, stream);
+  p.piece = plan.piece;
+  if (plan.piece > 0) {
+    p.ws_state = static_cast<float *>(a->workspace);
+    p.ws_step = p.ws_state + pieces_of(a->tokens, a->seqs, plan.piece) * a->channels * a->states;
+  }
+  return launch_prompt(p, a->states, dev, stream);
 }
 
 }  // namespace ssm
@@ -193,7 +222,7 @@ extern "C" int kda_ssm_prompt(const kda_ssm_prompt_args *args, void *stream) {
 }
 
 extern "C" int64_t kda_ssm_prompt_workspace(const kda_ssm_prompt_args *args) {
-  int64_t workspace;
   if (!args) return -1;
-  return kda::ssm::plan_prompt(args, &workspace) ? 0 : workspace;
+  kda::ssm::Plan plan;
+  return kda::ssm::plan_prompt(args, &plan) ? 0 : plan.workspace;
 }

@@ -27,6 +27,10 @@ struct Params {
   float *state;
   __nv_bfloat16 *output;
   int32_t *err;
+  // prompt: CTAs across the channels, and of a group; with pieces (> 0 rows each), what
+  // they leave: states [piece][channel][N] and sums of steps [piece][channel]
+  int blocks, group_blocks, piece;
+  float *ws_state, *ws_step;
 };
 
 // A token's decay 2^x as keep + change, keep 0 or 1: near 1 a factor rounded to
@@ -65,7 +69,7 @@ __device__ __forceinline__ float *state_of(const Params &p, int slot, int channe
 }
 
 // Enqueues the prompt form for checked parameters.  Returns a KDA_* code.
-int launch_prompt(const Params &p, int states, cudaStream_t stream);
+int launch_prompt(Params &p, int states, int dev, cudaStream_t stream);
 
 }  // namespace ssm
 }  // namespace kda
