@@ -45,9 +45,7 @@ __device__ __forceinline__ float exp_of(float x) {
 // interpolated in q^2 at the Chebyshev points (degree 4, 4e-9).  NaN stays NaN.
 __device__ __forceinline__ float softplus(float x) {
   const float e = exp_of(fabsf(x) > 100.0f ? -100.0f : -fabsf(x));     // (0 from -88 on)
-  const float b = 2.0f + e, r = rcp_approx(b);
-  float q = e * r;
-  q = __fmaf_rn(__fmaf_rn(-q, b, e), r, q);
+  const float q = e * rcp_approx(2.0f + e);
   const float u = q * q;
   float t = 0.14078890f;
   t = __fmaf_rn(t, u, 0.13982579f);

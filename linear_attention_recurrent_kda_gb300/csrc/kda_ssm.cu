@@ -146,11 +146,12 @@ static int run_step(const kda_ssm_step_args *a, cudaStream_t stream) {
                          : a->states == 32 ? launch_step<32>(p, stream) : launch_step<64>(p, stream);
 }
 
-// Rows of a piece of a split sequence (0: sequences stay whole), and the workspace.
+// How a prompt call runs.
 struct Plan {
-  int piece;
-  int64_t workspace;
+  int held, piece;         // states of a thread; rows of a piece (0: sequences stay whole)
+  int64_t workspace;       // bytes
 };
+constexpr int kSms = 152, kCtas = 4;     // that the work is shared among, with 16 states a thread
 constexpr int kShortestPiece = 256;      // rows
 
 static int plan_prompt(const kda_ssm_prompt_args *a, Plan *plan) {
@@ -158,21 +159,25 @@ static int plan_prompt(const kda_ssm_prompt_args *a, Plan *plan) {
   const bool pool = a->src_slots || a->dst_slots;
   if (a->seqs < 0 || a->max_seq < 0 || (pool && a->num_slots < 1)) return KDA_ERR_SHAPE;
   if (a->path < 0 || a->path > 2) return KDA_ERR_PATH;
+  const int64_t longest = a->max_seq < a->tokens ? a->max_seq : a->tokens;
+  const int64_t threads = static_cast<int64_t>(a->channels) * (a->states / 16);
+  const int64_t blocks = (threads + 127) / 128;          // CTAs of a sequence or piece
+  // 8 states a thread make twice the warps, with a third more instructions in all: better
+  // where warps are few (one sequence of 4096 tokens x 4096 channels 461 us instead of
+  // 656, 8 of 1145 on average 319 instead of 345), worse where an SM has its four CTAs
+  // (32749 tokens in pieces 1250 instead of 1098).
+  plan->held = blocks * a->seqs <= 2 * kSms ? 8 : 16;
   plan->piece = 0;
   plan->workspace = 0;
-  const int64_t longest = a->max_seq < a->tokens ? a->max_seq : a->tokens;
   if (a->path == 1 || longest <= kShortestPiece) return KDA_SUCCESS;
-  // CTAs of 128 threads with 16 states each; four of an SM run at a time
-  const int64_t threads = static_cast<int64_t>(a->channels) * (a->states / 16);
-  const int64_t blocks = (threads + 127) / 128, slots = 152 * 4;
-  const int64_t share = a->tokens * blocks / slots;      // rows of one of them
-  if (a->path == 0 && longest < 4 * share + 512) return KDA_SUCCESS;
-  int64_t piece = (share + 15) / 16 * 16;
-  if (piece < kShortestPiece) piece = kShortestPiece;
-  if (piece >= longest) {
-    if (a->path == 0) return KDA_SUCCESS;
-    piece = kShortestPiece;
-  }
+  // Whole, the longest sequence takes 0.14 us a token; in pieces, all tokens go through
+  // two passes at 1.1 ns a CTA and token.  (1 x 2048 tokens x 4096 channels: 230 us whole,
+  // 104 in pieces; the 8 ragged ones 319 and 329.)
+  const int64_t work = a->tokens * blocks;
+  if (a->path == 0 && 140 * longest < 11 * work / 10 + 15000) return KDA_SUCCESS;
+  int64_t piece = (work / (kSms * kCtas) + 15) / 16 * 16;
+  if (piece < kShortestPiece || piece >= longest) piece = kShortestPiece;
+  plan->held = 16;
   plan->piece = static_cast<int>(piece);
   plan->workspace = pieces_of(a->tokens, a->seqs, plan->piece) * a->channels * (a->states + 1) * 4;
   return KDA_SUCCESS;
@@ -207,7 +212,7 @@ static int run_prompt(const kda_ssm_prompt_args *a, cudaStream_t stream) {
     p.ws_state = static_cast<float *>(a->workspace);
     p.ws_step = p.ws_state + pieces_of(a->tokens, a->seqs, plan.piece) * a->channels * a->states;
   }
-  return launch_prompt(p, a->states, dev, stream);
+  return launch_prompt(p, a->states, plan.held, dev, stream);
 }
 
 }  // namespace ssm

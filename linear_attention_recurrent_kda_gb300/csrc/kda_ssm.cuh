@@ -68,8 +68,9 @@ __device__ __forceinline__ float *state_of(const Params &p, int slot, int channe
   return p.state + (static_cast<int64_t>(slot) * p.channels + channel) * states;
 }
 
-// Enqueues the prompt form for checked parameters.  Returns a KDA_* code.
-int launch_prompt(Params &p, int states, int dev, cudaStream_t stream);
+// Enqueues the prompt form for checked parameters, with `held` (8, or 16, as pieces
+// need) states a thread.  Returns a KDA_* code.
+int launch_prompt(Params &p, int states, int held, int dev, cudaStream_t stream);
 
 }  // namespace ssm
 }  // namespace kda

@@ -1,26 +1,31 @@
 // Selective scan over ragged prompts.
 //
-// A thread holds 16 states of a channel in registers (N / 16 lanes a channel) and
-// walks the tokens; a CTA of 128 threads takes 2048 / N channels of one group.
-// Tiles of 16 tokens of x, dt and z come by asynchronous copies, two tiles in
-// flight; b and c go through registers into FP32 in shared memory, from where
-// every lane of a warp reads the same words.
+// A thread holds kHeld states of a channel in registers (N / kHeld lanes a channel)
+// and walks the tokens; a CTA of 128 threads takes channels of one group.  Tiles of 16
+// tokens of x, dt and z come by asynchronous copies, two tiles in flight; b and c go
+// through registers into FP32 in shared memory, from where every lane of a warp reads
+// the same words.  What is the same for all states of a channel is computed once per
+// token, two channels to an instruction, by the warp that owns the channel: the steps
+// s and s x before the tile's walk, skip and gate behind it, through shared memory.
 //
 // Decays.  exp(s a) = ex2(s (a log2 e)) per token and state on the approximate exp2,
 // and FP32 holds a factor near 1 to 2^-25: a state that remembers 1000 tokens would
 // drift by 2e-5 of itself or more, to one side.  So over a tile the product of the
-// factors that were used is kept too, less 1 (m <- m e + (e - 1), where e - 1 is exact),
-// and at its end the state is corrected by (exp(a sum s) - 1 - m) h_0, with exp - 1 from
-// a polynomial (decay_of): two operations per token and state and 20 per tile and
-// state, where a polynomial at every token would take 8.
+// factors that were used is kept too, less 1 (m <- m + q + m q, with q = e e' - 1 of two
+// tokens in one operation), and at the end of two tiles the state is corrected by
+// (exp(a sum s) - 1 - m) h_0, with exp - 1 from a polynomial (decay_of): 1.5 operations
+// per token and state and 20 per two tiles and state, where a polynomial at every
+// token would take 8.
 //
 // Split sequences.  A sequence much longer than an SM's share is cut into pieces:
-// scan_kernel<N, false> sums each piece's own contribution to the state (from zeros)
-// and its steps; scan_kernel<N, true> runs the pieces side by side, each from the
-// state that it sums up itself from the pieces before.
+// scan_kernel<.., false> sums each piece's own contribution to the state, from its
+// end backwards (every exponent is a sum of steps, so nothing drifts there), and its
+// steps; scan_kernel<.., true> runs the pieces side by side, each from the state that
+// it sums up itself from the pieces before.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "../../include/kda.h"
 #include "kda_device.cuh"
@@ -32,16 +37,21 @@ namespace ssm {
 
 constexpr int kThreads = 128;
 constexpr int kTile = 16;                        // tokens
-constexpr int kHeld = 16;                        // states of a thread
 
-template <int kStates>
+template <int kStates, int kHeld>
 struct Stage {
   static constexpr int kLanes = kStates / kHeld;             // of a channel
   static constexpr int kChannels = kThreads / kLanes;        // of a CTA
+  static constexpr int kOwn = 32 / kLanes;                   // of a warp
   static constexpr int kVectors = kChannels / 8;             // 16 bytes each, of a row
   static constexpr int kShared = kTile * 2 * kStates / 8;    // vectors of b and c
   __nv_bfloat16 x[2][kTile][kChannels], dt[2][kTile][kChannels], z[2][kTile][kChannels];
   float b[2][kTile][kStates], c[2][kTile][kStates];
+  float2 steps[kTile][kChannels];                            // s and s x, then y
+  ulonglong2 before[kHeld / 4][kThreads];                    // the states before two tiles
+  // Channel c of token t of x, dt and z: odd tokens' halves of 128 bytes change places, so
+  // that lanes which read two tokens' 64 bytes meet no bank twice.
+  __device__ static int at(int t, int c) { return kChannels >= 64 ? c ^ ((t & 1) << 5) : c; }
 };
 
 __device__ __forceinline__ void copy16(void *to, const void *from) {
@@ -53,7 +63,7 @@ __device__ __forceinline__ void copies_done() {
 
 // The piece's start: the sequence's first state, and over the pieces before it,
 // h <- exp(a s) h + u with their steps' sums s and contributions u.
-template <int kStates>
+template <int kStates, int kHeld>
 __device__ __forceinline__ void start_of(const Params &p, const Seq &seq, int64_t first, int before,
                                          int channel, int held, const f32x2 (&a)[kHeld / 2],
                                          f32x2 (&h)[kHeld / 2]) {
@@ -86,8 +96,8 @@ __device__ __forceinline__ void start_of(const Params &p, const Seq &seq, int64_
   }
 }
 
-// h + h_0 (exp(a s) - 1 - used) for decays down to 1/2 a tile; what a stronger one is
-// off by, the next tiles forget.
+// h + h_0 (exp(a s) - 1 - used), for decays down to 1/2: `used` is off by 2^-24 of 1,
+// which a stronger decay's own state would show, and its states remember 50 tokens.
 __device__ __forceinline__ f32x2 corrected(f32x2 h, f32x2 h0, f32x2 a, float s, f32x2 product) {
   float v[2], v0[2], x[2], used[2];
   unpair(h, v[0], v[1]);
@@ -97,14 +107,57 @@ __device__ __forceinline__ f32x2 corrected(f32x2 h, f32x2 h0, f32x2 a, float s, 
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const Decay d = decay_of(s * x[i]);
-    if (d.keep != 0.0f) v[i] = __fmaf_rn(v0[i], d.change - used[i], v[i]);
+    v[i] = d.keep != 0.0f ? __fmaf_rn(v0[i], d.change - used[i], v[i]) : v[i];
   }
   return pair(v[0], v[1]);
 }
 
-template <int kStates, bool kOut>
-__global__ void __launch_bounds__(kThreads, 4) scan_kernel(const __grid_constant__ Params p) {
-  using S = Stage<kStates>;
+__device__ __forceinline__ f32x2 two(float v) { return pair(v, v); }
+__device__ __forceinline__ f32x2 unpack2(uint32_t u) {
+  return pair(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// softplus() of two values.
+__device__ __forceinline__ f32x2 softplus2(f32x2 v) {
+  float lo, hi, pl, ph;
+  unpair(v, lo, hi);
+  const f32x2 a = pair(min_nan(fabsf(lo), 100.0f), min_nan(fabsf(hi), 100.0f));
+  const f32x2 p = mul2(a, two(kLog2e));
+  const f32x2 left = fma2(a, two(-1.925963033e-8f), fma2(a, two(-kLog2e), p));
+  unpair(p, pl, ph);
+  f32x2 e = pair(exp2_approx(-pl), exp2_approx(-ph));
+  e = fma2(mul2(e, left), two(0.6931471806f), e);
+  float bl, bh;
+  unpair(add2(e, two(2.0f)), bl, bh);
+  const f32x2 q = mul2(e, pair(rcp_approx(bl), rcp_approx(bh)));
+  const f32x2 u = mul2(q, q);
+  f32x2 t = fma2(two(2 * 0.14078890f), u, two(2 * 0.13982579f));
+  t = fma2(t, u, two(2 * 0.20012298f));
+  t = fma2(t, u, two(2 * 0.33333161f));
+  t = fma2(t, u, two(2.0f));
+  return fma2(q, t, pair(max_nan(lo, 0.0f), max_nan(hi, 0.0f)));
+}
+// silu() of two values.
+__device__ __forceinline__ f32x2 silu2(f32x2 z) {
+  float lo, hi;
+  unpair(mul2(z, two(-kLog2e)), lo, hi);
+  unpair(add2(pair(exp2_approx(lo), exp2_approx(hi)), two(1.0f)), lo, hi);
+  return mul2(z, pair(rcp_approx(lo), rcp_approx(hi)));
+}
+
+template <int kStates, int kHeld, bool kOut>
+__global__ void __launch_bounds__(kThreads, kHeld == 16 ? 4 : 6) scan_kernel(const __grid_constant__ Params p) {
+  using S = Stage<kStates, kHeld>;
   extern __shared__ __align__(16) uint8_t raw[];
   S &st = *reinterpret_cast<S *>(raw);
   const int block = blockIdx.x % p.blocks;
@@ -141,15 +194,26 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const __grid_constant
   const bool live = mine < wide;
   const int channel = channel0 + (live ? mine : 0);
 
-  auto load = [&](int tile) {                      // x, dt, z of a tile
+  // x, dt and z of a tile: this thread's vectors are kStep tokens apart
+  constexpr int kStep = kThreads / S::kVectors < kTile ? kThreads / S::kVectors : kTile;
+  constexpr int kCopies = kTile / kStep;
+  static_assert(kThreads % S::kVectors == 0 && kTile % kStep == 0, "whole rows");
+  const int copy_t = tid / S::kVectors, copy_c = tid % S::kVectors * 8;
+  const int copy_to = copy_c < wide && copy_t < kStep ? rows - copy_t : 0;        // the first token that is not there
+  const __nv_bfloat16 *from_x = p.x + (row0 + copy_t) * p.x_stride + channel0 + copy_c;
+  const __nv_bfloat16 *from_dt = p.dt + (row0 + copy_t) * p.dt_stride + channel0 + copy_c;
+  const __nv_bfloat16 *from_z =
+      kOut && p.z ? p.z + (row0 + copy_t) * p.z_stride + channel0 + copy_c : nullptr;
+  auto load = [&](int tile) {
     const int buf = tile & 1;
-    for (int i = tid; i < kTile * S::kVectors; i += kThreads) {
-      const int t = i / S::kVectors, v = i % S::kVectors;
-      if (tile * kTile + t < rows && 8 * v < wide) {
-        const int64_t row = row0 + tile * kTile + t;
-        copy16(&st.x[buf][t][8 * v], p.x + row * p.x_stride + channel0 + 8 * v);
-        copy16(&st.dt[buf][t][8 * v], p.dt + row * p.dt_stride + channel0 + 8 * v);
-        if (kOut && p.z) copy16(&st.z[buf][t][8 * v], p.z + row * p.z_stride + channel0 + 8 * v);
+    const int64_t rows_before = static_cast<int64_t>(tile) * kTile;
+#pragma unroll
+    for (int k = 0; k < kCopies; ++k) {
+      const int t = copy_t + k * kStep, c = S::at(t, copy_c);
+      if (tile * kTile + k * kStep < copy_to) {
+        copy16(&st.x[buf][t][c], from_x + (rows_before + k * kStep) * p.x_stride);
+        copy16(&st.dt[buf][t][c], from_dt + (rows_before + k * kStep) * p.dt_stride);
+        if (kOut && from_z) copy16(&st.z[buf][t][c], from_z + (rows_before + k * kStep) * p.z_stride);
       }
     }
   };
@@ -183,8 +247,11 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const __grid_constant
     }
   };
 
-  load(0);
-  fetch(0);
+  const int tiles = (rows + kTile - 1) / kTile;
+  if (rows > 0) {                                  // contributions are summed from the end
+    load(kOut ? 0 : tiles - 1);
+    fetch(kOut ? 0 : tiles - 1);
+  }
   f32x2 a[kHeld / 2], h[kHeld / 2];
   {
     const float4 *from =
@@ -196,83 +263,197 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const __grid_constant
       a[2 * i + 1] = pair(v.z * kLog2e, v.w * kLog2e);
     }
   }
-  const float skip = p.d ? __ldg(p.d + channel) : 0.0f;
-  const float bias = p.dt_bias ? __ldg(p.dt_bias + channel) : 0.0f;
+  // for what is once a token: two channels, every kStride-th token, of this lane
+  constexpr int kPairs = S::kOwn / 2, kStride = 32 / kPairs;
+  const int lane = tid & 31, own = (tid >> 5) * S::kOwn, at2 = own + lane % kPairs * 2;
+  const int t2 = lane / kPairs;
+  const bool live2 = at2 < wide;
+  f32x2 skip = 0, bias = 0;
+  if (live2) {
+    const int c = channel0 + at2;
+    if (p.d) skip = pair(__ldg(p.d + c), __ldg(p.d + c + 1));
+    if (p.dt_bias) bias = pair(__ldg(p.dt_bias + c), __ldg(p.dt_bias + c + 1));
+  }
   if (kOut) {
-    start_of<kStates>(p, seq, first, piece, channel, held, a, h);
+    start_of<kStates, kHeld>(p, seq, first, piece, channel, held, a, h);
   } else {
 #pragma unroll
     for (int i = 0; i < kHeld / 2; ++i) h[i] = 0;
   }
-  float steps = 0.0f;                              // of the piece
-  __nv_bfloat16 *out = kOut ? p.output + row0 * p.o_stride + channel : nullptr;
+  float sum = 0.0f;                                // steps of two tiles, or of the piece
+  f32x2 used[kHeld / 2];
+  __nv_bfloat16 *out = kOut ? p.output + (row0 + t2) * p.o_stride + channel0 + at2 : nullptr;
 
-  for (int tile = 0; tile * kTile < rows; ++tile) {
+  for (int i = 0; i < tiles; ++i) {
+    const int tile = kOut ? i : tiles - 1 - i;
     const int buf = tile & 1, count = min(kTile, rows - tile * kTile);
     copies_done();
     spread(tile);
     __syncthreads();
-    if ((tile + 1) * kTile < rows) {
-      load(tile + 1);
-      fetch(tile + 1);
+    if (i + 1 < tiles) {
+      load(kOut ? tile + 1 : tile - 1);
+      fetch(kOut ? tile + 1 : tile - 1);
     }
-    f32x2 h0[kHeld / 2], used[kHeld / 2];
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kHeld / 2; ++i) {
-      h0[i] = h[i];
-      used[i] = 0;
-    }
-#pragma unroll 2
-    for (int t = 0; t < count; ++t) {
-      const float x = __bfloat162float(st.x[buf][t][mine]);
-      float s = __bfloat162float(st.dt[buf][t][mine]) + bias;
-      if (p.softplus) s = softplus(s);
-      sum += s;
-      const f32x2 ss = pair(s, s), sx = pair(s * x, s * x);
-      const ulonglong2 *bn = reinterpret_cast<const ulonglong2 *>(st.b[buf][t] + held);
-      const ulonglong2 *cn = reinterpret_cast<const ulonglong2 *>(st.c[buf][t] + held);
-      f32x2 y = 0;
+    if (kOut && (tile & 1) == 0) {
+      sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < kHeld / 2; i += 2) {
-        const ulonglong2 bb = bn[i / 2];
-        f32x2 e[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float lo, hi;
-          unpair(mul2(ss, a[i + k]), lo, hi);
-          e[k] = pair(exp2_approx(lo), exp2_approx(hi));
-          used[i + k] = fma2(used[i + k], e[k], add2(e[k], pair(-1.0f, -1.0f)));
-        }
-        h[i] = fma2(h[i], e[0], mul2(sx, bb.x));
-        h[i + 1] = fma2(h[i + 1], e[1], mul2(sx, bb.y));
-        if (kOut) {
-          const ulonglong2 cc = cn[i / 2];
-          y = fma2(h[i], cc.x, y);
-          y = fma2(h[i + 1], cc.y, y);
-        }
-      }
-      if (kOut) {
-        float lo, hi;
-        unpair(y, lo, hi);
-        float v = lo + hi;
-#pragma unroll
-        for (int o = 1; o < S::kLanes; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        v = __fmaf_rn(skip, x, v);
-        if (p.z) v *= silu_approx(__bfloat162float(st.z[buf][t][mine]));
-        if (live && held == 0) *out = __float2bfloat16_rn(v);
-        out += p.o_stride;
+        st.before[i / 2][tid] = make_ulonglong2(h[i], h[i + 1]);
+        used[i] = used[i + 1] = 0;
       }
     }
-    steps += sum;
+    // (rows behind the piece's end and channels behind the group's: what is there is
+    // computed with, and goes nowhere)
+    auto steps_of = [&](auto soft) {
 #pragma unroll
-    for (int i = 0; i < kHeld / 2; ++i) h[i] = corrected(h[i], h0[i], a[i], sum, used[i]);
+      for (int k = 0; k < kTile / kStride; ++k) {
+        const int t = t2 + k * kStride;
+        const f32x2 x = unpack2(*reinterpret_cast<const uint32_t *>(&st.x[buf][t][S::at(t, at2)]));
+        f32x2 v = add2(unpack2(*reinterpret_cast<const uint32_t *>(&st.dt[buf][t][S::at(t, at2)])), bias);
+        if (decltype(soft)::value) v = softplus2(v);
+        float4 w;
+        unpair(v, w.x, w.z);
+        unpair(mul2(v, x), w.y, w.w);
+        *reinterpret_cast<float4 *>(&st.steps[t][at2]) = w;
+      }
+    };
+    if (p.softplus)
+      steps_of(std::true_type());
+    else
+      steps_of(std::false_type());
+    __syncwarp();
+    // kMany tokens at a time: what they add up to leaves the registers behind them,
+    // so that the next one's loads and exponents need not wait for a store
+    auto walk = [&](int t0, auto many) {
+      constexpr int kMany = decltype(many)::value;
+      float2 w[kMany];
+      float ys[kMany];
+#pragma unroll
+      for (int u = 0; u < kMany; ++u) w[u] = st.steps[t0 + u][mine];
+      auto decay = [&](float s, int i) {
+        float lo, hi;
+        unpair(mul2(two(s), a[i]), lo, hi);
+        return pair(exp2_approx(lo), exp2_approx(hi));
+      };
+      f32x2 e[kHeld / 2], last[kHeld / 2];
+#pragma unroll
+      for (int i = 0; i < kHeld / 2; ++i) e[i] = decay(w[0].x, i);
+#pragma unroll
+      for (int u = 0; u < kMany; ++u) {
+        const int t = t0 + u;
+        sum += w[u].x;
+        const f32x2 sx = two(w[u].y);
+        const ulonglong2 *bn = reinterpret_cast<const ulonglong2 *>(st.b[buf][t] + held);
+        const ulonglong2 *cn = reinterpret_cast<const ulonglong2 *>(st.c[buf][t] + held);
+        f32x2 y[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < kHeld / 2; i += 2) {
+          const ulonglong2 bb = bn[i / 2], cc = cn[i / 2];
+#pragma unroll
+          for (int k = i; k < i + 2; ++k) {
+            const f32x2 now = e[k];
+            if (u + 1 < kMany) e[k] = decay(w[u + 1].x, k);      // the next token's, ahead
+            if (u & 1) {                             // two tokens: m (q + 1) + q, q = e e - 1
+              const f32x2 q = fma2(last[k], now, two(-1.0f));
+              used[k] = add2(fma2(used[k], q, q), used[k]);
+            } else if (u + 1 == kMany) {
+              used[k] = fma2(used[k], now, add2(now, two(-1.0f)));
+            } else {
+              last[k] = now;
+            }
+            h[k] = fma2(h[k], now, mul2(sx, k == i ? bb.x : bb.y));
+            y[k - i] = fma2(h[k], k == i ? cc.x : cc.y, y[k - i]);
+          }
+        }
+        float lo, hi;
+        unpair(add2(y[0], y[1]), lo, hi);
+        ys[u] = lo + hi;
+      }
+#pragma unroll
+      for (int o = 1; o < S::kLanes; o <<= 1)
+#pragma unroll
+        for (int u = 0; u < kMany; ++u) ys[u] += __shfl_xor_sync(0xffffffffu, ys[u], o);
+      if (S::kLanes > 1) __syncwarp();                 // all lanes of the channel have read w
+#pragma unroll
+      for (int u = 0; u < kMany; ++u)
+        if (held == 0) st.steps[t0 + u][mine].x = ys[u];
+    };
+    // A piece's contribution: sum_t exp(a sum of the steps behind t) s_t x_t b_t.
+    auto gather = [&](int t0, auto many) {
+      constexpr int kMany = decltype(many)::value;
+      float2 w[kMany];
+#pragma unroll
+      for (int u = 0; u < kMany; ++u) w[u] = st.steps[t0 - u][mine];
+#pragma unroll
+      for (int u = 0; u < kMany; ++u) {
+        const ulonglong2 *bn = reinterpret_cast<const ulonglong2 *>(st.b[buf][t0 - u] + held);
+#pragma unroll
+        for (int i = 0; i < kHeld / 2; i += 2) {
+          const ulonglong2 bb = bn[i / 2];
+#pragma unroll
+          for (int k = i; k < i + 2; ++k) {
+            float lo, hi;
+            unpair(mul2(two(sum), a[k]), lo, hi);
+            h[k] = fma2(pair(exp2_approx(lo), exp2_approx(hi)), mul2(two(w[u].y), k == i ? bb.x : bb.y),
+                        h[k]);
+          }
+        }
+        sum += w[u].x;
+      }
+    };
+    if (kOut) {
+      int t = 0;
+#pragma unroll 1
+      for (; t + 4 <= count; t += 4) walk(t, std::integral_constant<int, 4>());
+#pragma unroll 1
+      for (; t < count; ++t) walk(t, std::integral_constant<int, 1>());
+    } else {
+      int t = count - 1;
+#pragma unroll 1
+      for (; t >= 3; t -= 4) gather(t, std::integral_constant<int, 4>());
+#pragma unroll 1
+      for (; t >= 0; --t) gather(t, std::integral_constant<int, 1>());
+      __syncwarp();
+    }
+    if (kOut) {
+      __syncwarp();
+      const int ends = live2 ? count : 0;
+      const int64_t step = kStride * p.o_stride;
+      auto outputs = [&](auto gated) {
+#pragma unroll
+        for (int k = 0; k < kTile / kStride; ++k) {
+          const int t = t2 + k * kStride;
+          const float4 w = *reinterpret_cast<const float4 *>(&st.steps[t][at2]);
+          const f32x2 x = unpack2(*reinterpret_cast<const uint32_t *>(&st.x[buf][t][S::at(t, at2)]));
+          f32x2 y = fma2(skip, x, pair(w.x, w.z));
+          if (decltype(gated)::value)
+            y = mul2(y, silu2(unpack2(*reinterpret_cast<const uint32_t *>(&st.z[buf][t][S::at(t, at2)]))));
+          float lo, hi;
+          unpair(y, lo, hi);
+          if (t < ends) *reinterpret_cast<uint32_t *>(out + k * step) = pack2(lo, hi);
+        }
+      };
+      if (p.z)
+        outputs(std::true_type());
+      else
+        outputs(std::false_type());
+      out += kTile * p.o_stride;
+      __syncwarp();
+    }
+    if (kOut && ((tile & 1) || i + 1 == tiles)) {
+#pragma unroll
+      for (int i = 0; i < kHeld / 2; i += 2) {
+        const ulonglong2 h0 = st.before[i / 2][tid];
+        h[i] = corrected(h[i], h0.x, a[i], sum, used[i]);
+        h[i + 1] = corrected(h[i + 1], h0.y, a[i + 1], sum, used[i + 1]);
+      }
+    }
   }
   if (!live) return;
   float *to = nullptr;
   if (!kOut) {
     to = p.ws_state + (n * p.channels + channel) * kStates + held;
-    if (held == 0) p.ws_step[n * p.channels + channel] = steps;
+    if (held == 0) p.ws_step[n * p.channels + channel] = sum;
   } else if (seq.dst && row0 + rows == seq.start + seq.len) {
     to = state_of(p, seq.dst, channel, kStates) + held;
   }
@@ -287,31 +468,41 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const __grid_constant
   }
 }
 
-template <int kStates>
+template <int kStates, int kHeld>
 static int launch(Params &p, cudaStream_t stream, int dev) {
-  using S = Stage<kStates>;
+  using S = Stage<kStates, kHeld>;
   p.group_blocks = (p.span + S::kChannels - 1) / S::kChannels;
   p.blocks = p.channels / p.span * p.group_blocks;
   const int64_t units = p.piece > 0 ? pieces_of(p.seqs.tokens, p.seqs.count, p.piece) : p.seqs.count;
   if (units * p.blocks > 0x7fffffffll) return KDA_ERR_SHAPE;
-  static std::atomic<bool> out_done[kMaxDevices], sum_done[kMaxDevices];
-  if (!set_smem_limit_once(out_done, dev, reinterpret_cast<const void *>(scan_kernel<kStates, true>),
-                           sizeof(S)) ||
-      !set_smem_limit_once(sum_done, dev, reinterpret_cast<const void *>(scan_kernel<kStates, false>),
+  static std::atomic<bool> out_done[kMaxDevices];
+  if (!set_smem_limit_once(out_done, dev, reinterpret_cast<const void *>(scan_kernel<kStates, kHeld, true>),
                            sizeof(S)))
     return KDA_ERR_LAUNCH;
   const int grid = static_cast<int>(units * p.blocks);
-  if (p.piece > 0) {
-    scan_kernel<kStates, false><<<grid, kThreads, sizeof(S), stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return KDA_ERR_LAUNCH;
+  if constexpr (kHeld == 16) {
+    if (p.piece > 0) {
+      static std::atomic<bool> sum_done[kMaxDevices];
+      if (!set_smem_limit_once(sum_done, dev,
+                               reinterpret_cast<const void *>(scan_kernel<kStates, kHeld, false>), sizeof(S)))
+        return KDA_ERR_LAUNCH;
+      scan_kernel<kStates, kHeld, false><<<grid, kThreads, sizeof(S), stream>>>(p);
+      if (cudaGetLastError() != cudaSuccess) return KDA_ERR_LAUNCH;
+    }
   }
-  scan_kernel<kStates, true><<<grid, kThreads, sizeof(S), stream>>>(p);
+  scan_kernel<kStates, kHeld, true><<<grid, kThreads, sizeof(S), stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
 }
 
-int launch_prompt(Params &p, int states, int dev, cudaStream_t stream) {
-  return states == 16 ? launch<16>(p, stream, dev)
-                      : states == 32 ? launch<32>(p, stream, dev) : launch<64>(p, stream, dev);
+template <int kHeld>
+static int launch_of(Params &p, int states, int dev, cudaStream_t stream) {
+  return states == 16 ? launch<16, kHeld>(p, stream, dev)
+                      : states == 32 ? launch<32, kHeld>(p, stream, dev)
+                                     : launch<64, kHeld>(p, stream, dev);
+}
+
+int launch_prompt(Params &p, int states, int held, int dev, cudaStream_t stream) {
+  return held == 8 ? launch_of<8>(p, states, dev, stream) : launch_of<16>(p, states, dev, stream);
 }
 
 }  // namespace ssm

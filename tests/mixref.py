@@ -68,8 +68,9 @@ def ssm(x, dt, a, b, c, starts, d=None, z=None, dt_bias=None, soft=True, state=N
     by half a place; softplus by exp2, its argument, a reciprocal refined once, a
     polynomial and their products: below 2^-20 with the slope s' <= s); the exponent
     s a log2 e by ds and three roundings; the decay f by that times its exponent, and
-    by its own evaluation: 2^-22 of f, or of 1 - f where h + h (f - 1) is taken; the
-    addition s x b by ds and two roundings; three roundings of the sum itself."""
+    by its own evaluation, 2^-22 of f (the approximate exp2; forms of f - 1 are nearer, and
+    tests of slow states hold the drift to less); the addition s x b by ds and two
+    roundings; three roundings of the sum itself."""
     x, dt, a, b, c = (f64(t) for t in (x, dt, a, b, c))
     rows, C = x.shape
     N = a.shape[1]
@@ -92,8 +93,7 @@ def ssm(x, dt, a, b, c, starts, d=None, z=None, dt_bias=None, soft=True, state=N
         for t in range(starts[r], starts[r + 1]):
             g = s[t][:, None] * a
             f = torch.exp(g)
-            df = f * g.abs() * (ds[t][:, None] + 3 * U32) + torch.where(
-                g.abs() < 0.7, (1 - f).abs(), f) * APPROX + TINY
+            df = f * g.abs() * (ds[t][:, None] + 3 * U32) + f * APPROX + TINY
             add = (s[t] * x[t])[:, None] * b[t]
             e[r] = f * e[r] + df * (h[r].abs() + e[r]) + add.abs() * (ds[t][:, None] + 2 * U32)
             h[r] = f * h[r] + add
