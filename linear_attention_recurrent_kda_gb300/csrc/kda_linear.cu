@@ -1,15 +1,17 @@
 // output = BF16(act(x W^T + bias) + residual), on the 5th-generation tensor cores.
 //
-// A CTA takes 128 features (rows of W) and up to 256 tokens: the product's M is
-// the features and its N the tokens, so that few tokens cost few columns, and W is
-// read once where 256 tokens suffice.  One warp loads 64-wide tiles of both with
-// TMA through a ring, one issues the products into TMEM, four take the sums out.
-// Where tiles are fewer than SMs, a cluster of CTAs shares a tile: each sums a
-// range of the inner dimension, and the sums are joined through distributed shared
-// memory in the order of the ranks.
+// Two forms.  Few tiles: a CTA takes 128 features (rows of W) and up to 256 tokens; the
+// product's M is the features and its N the tokens, so that few tokens cost few columns
+// and W is read once.  One warp loads 64-wide tiles of both with TMA through a ring, one
+// issues the products into TMEM.  A cluster of CTAs may share a tile: each sums a range
+// of the inner dimension, and the sums are joined through distributed shared memory,
+// 8 features a thread, in the order of the ranges.  Many tiles: below.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
+#include <type_traits>
+#include <stdio.h>
+#include <stdlib.h>
 
 #include "../../include/kda.h"
 #include "kda_device.cuh"
@@ -22,16 +24,18 @@ namespace linear {
 
 using namespace rows;
 
-constexpr int kThreads = 192;                    // 4 epilogue warps, TMA, products
+constexpr int kThreads = 256;                    // TMA in warp 4, products in warp 5
 constexpr int kM = 128, kK = 64;                 // features of a tile, inner of a block
 constexpr int kMostN = 256;
-constexpr int kMostStages = 8;
-constexpr int kRing = 200 * 1024;                // bytes of the ring, at most
+constexpr int kMostStages = 10;
 constexpr int kATile = kM * kK * 2;
+// Bytes of the ring: all that an SM has, or half, where CTAs are more than SMs and 4
+// stages fit, so that one's loads run while another starts or ends.
+constexpr int kHalfRing = 96 * 1024, kRing = 192 * 1024;
 
 struct Params {
   int rows, inner, outer, act;
-  int tile_n, stages, blocks, split;             // blocks: of kK along inner
+  int tile_n, stages, ring, blocks, split;       // blocks: of kK along inner
   int64_t r_stride, o_stride;
   const __nv_bfloat16 *bias, *residual;
   __nv_bfloat16 *output;
@@ -43,8 +47,8 @@ struct Ctrl {
   uint32_t tmem, abort;
 };
 
-constexpr int kSmem = kRing + 1024 + sizeof(Ctrl);
-static_assert(kSmem <= 232448, "shared memory of one CTA");
+constexpr int smem_of(int ring) { return ring + 1024 + static_cast<int>(sizeof(Ctrl)); }
+static_assert(smem_of(kRing) <= 232448, "shared memory of one CTA");
 
 __device__ __forceinline__ float activated(float y, int act) {
   if (act == KDA_ACT_SILU) return silu_approx(y);
@@ -53,18 +57,49 @@ __device__ __forceinline__ float activated(float y, int act) {
   return y;
 }
 
-__device__ __forceinline__ void finish(const Params &p, int row, int feature, float bias, float y) {
-  y = activated(y + bias, p.act);
-  if (p.residual) y += __bfloat162float(p.residual[row * p.r_stride + feature]);
-  p.output[row * p.o_stride + feature] = __float2bfloat16_rn(y);
+__device__ __forceinline__ void ld_cluster(uint32_t from, float &a, float &b, float &c, float &d) {
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(a), "=f"(b), "=f"(c), "=f"(d)
+               : "r"(from)
+               : "memory");
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+// The epilogue of 8 features of a token (fewer at the end of the row).
+template <int kAct>
+__device__ __forceinline__ void finish(const Params &p, int64_t row, int feature, const float (&bias)[8],
+                                       const uint4 &residual, float (&y)[8]) {
+  const int left = p.outer - feature;
+  float add[8];
+  unpack8(residual, add);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = activated(y[e] + bias[e], kAct) + add[e];
+  __nv_bfloat16 *out = p.output + row * p.o_stride + feature;
+  if (left >= 8) {
+    *reinterpret_cast<uint4 *>(out) = pack8(y);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (e < left) out[e] = __float2bfloat16_rn(y[e]);
+  }
+}
+// 8 BF16 of a row, zeros behind its end.
+__device__ __forceinline__ uint4 vector_of(const __nv_bfloat16 *from, int left) {
+  if (left >= 8) return *reinterpret_cast<const uint4 *>(from);
+  const uint16_t *at = reinterpret_cast<const uint16_t *>(from);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 7; ++e)
+    if (e < left) w[e / 2] |= static_cast<uint32_t>(at[e]) << (16 * (e & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int kAct>
+__global__ void __launch_bounds__(kThreads, 2)
     product_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap wmap,
                    const __grid_constant__ CUtensorMap xmap) {
   extern __shared__ uint8_t raw[];
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  Ctrl &c = *reinterpret_cast<Ctrl *>(ring + kRing);
+  Ctrl &c = *reinterpret_cast<Ctrl *>(ring + p.ring);
   const int warp = threadIdx.x >> 5;
   const int rank = blockIdx.x % p.split, feature0 = blockIdx.x / p.split * kM;
   const int row0 = blockIdx.y * p.tile_n;
@@ -128,54 +163,85 @@ __global__ void __launch_bounds__(kThreads, 1)
   // every warp: what the ring holds is used up behind this
   const bool ok = wait_phase(&c.done, 0, &c.abort);
   tc_fence_after();
-  const int feature = feature0 + threadIdx.x;
   const int rows = min(p.tile_n, p.rows - row0);
-  if (p.split == 1) {
-    if (warp < 4) {
-      const float bias =
-          p.bias && feature < p.outer ? __bfloat162float(p.bias[feature]) : 0.0f;
-      for (int n = 0; n < rows; n += 32) {
-        uint32_t r[32];
-        tc_ld(tmem + (static_cast<uint32_t>(warp * 32) << 16) + n, r);
-        tc_wait_ld(r);
-        if (feature < p.outer && ok) {
+  float *part = reinterpret_cast<float *>(ring);           // [token][feature]
+  __syncthreads();
+  if (warp < 4) {
+    for (int n = 0; n < rows; n += 32) {
+      uint32_t r[32];
+      tc_ld(tmem + (static_cast<uint32_t>(warp * 32) << 16) + n, r);
+      tc_wait_ld(r);
+      float *to = part + n * kM + threadIdx.x;
+      if (n + 32 <= rows) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (n + i < rows) finish(p, row0 + n + i, feature, bias, __uint_as_float(r[i]));
-        }
-      }
-    }
-  } else {
-    float *part = reinterpret_cast<float *>(ring);           // [token][feature]
-    __syncthreads();
-    if (warp < 4) {
-      for (int n = 0; n < rows; n += 32) {
-        uint32_t r[32];
-        tc_ld(tmem + (static_cast<uint32_t>(warp * 32) << 16) + n, r);
-        tc_wait_ld(r);
+        for (int i = 0; i < 32; ++i) to[i * kM] = __uint_as_float(r[i]);
+      } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          if (n + i < rows) part[(n + i) * kM + threadIdx.x] = __uint_as_float(r[i]);
+          if (n + i < rows) to[i * kM] = __uint_as_float(r[i]);
       }
     }
-    cluster_sync_all();
-    if (warp < 4 && feature < p.outer && ok) {
-      const float bias = p.bias ? __bfloat162float(p.bias[feature]) : 0.0f;
-      for (int n = rank; n < rows; n += p.split) {
-        float y = 0.0f;
-        for (int q = 0; q < p.split; ++q) {
-          float v;
-          asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                       : "=f"(v)
-                       : "r"(cluster_map(part + n * kM + threadIdx.x, q))
-                       : "memory");
-          y += v;
-        }
-        finish(p, row0 + n, feature, bias, y);
-      }
-    }
-    cluster_sync_all();
   }
+  if (p.split == 1)
+    __syncthreads();
+  else
+    cluster_sync_all();
+  if (ok) {
+    // 16 threads a token; this CTA's share of them
+    const int first = static_cast<int>(static_cast<int64_t>(rows) * rank / p.split);
+    const int last = static_cast<int>(static_cast<int64_t>(rows) * (rank + 1) / p.split);
+    const int at = threadIdx.x % 16 * 8, feature = feature0 + at, left = p.outer - feature;
+    if (left > 0) {
+      float bias[8];
+      unpack8(p.bias ? vector_of(p.bias + feature, left) : make_uint4(0, 0, 0, 0), bias);
+      // kMany tokens in flight
+      auto join = [&](int n0, auto many) {
+        constexpr int kMany = decltype(many)::value, kStep = kThreads / 16;
+        float y[kMany][8];
+        uint4 residual[kMany];
+#pragma unroll
+        for (int u = 0; u < kMany; ++u) {
+          const float *mine = part + (n0 + u * kStep) * kM + at;
+          if (p.split == 1) {
+            const float4 lo = reinterpret_cast<const float4 *>(mine)[0];
+            const float4 hi = reinterpret_cast<const float4 *>(mine)[1];
+            y[u][0] = lo.x, y[u][1] = lo.y, y[u][2] = lo.z, y[u][3] = lo.w;
+            y[u][4] = hi.x, y[u][5] = hi.y, y[u][6] = hi.z, y[u][7] = hi.w;
+          } else {
+            float v[8][8];                                   // all in flight, then added in order
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (q < p.split) {
+                const uint32_t from = cluster_map(mine, q);
+                ld_cluster(from, v[q][0], v[q][1], v[q][2], v[q][3]);
+                ld_cluster(from + 16, v[q][4], v[q][5], v[q][6], v[q][7]);
+              }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[u][e] = v[0][e];
+#pragma unroll
+            for (int q = 1; q < 8; ++q)
+              if (q < p.split)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[u][e] += v[q][e];
+          }
+          residual[u] = p.residual
+                            ? vector_of(p.residual + static_cast<int64_t>(row0 + n0 + u * kStep) * p.r_stride +
+                                            feature, left)
+                            : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < kMany; ++u)
+          finish<kAct>(p, row0 + n0 + u * kStep, feature, bias, residual[u], y[u]);
+      };
+      int n = first + threadIdx.x / 16;
+      if (p.split == 1)
+        for (; n + 3 * (kThreads / 16) < last; n += 4 * (kThreads / 16))
+          join(n, std::integral_constant<int, 4>());
+      for (; n < last; n += kThreads / 16) join(n, std::integral_constant<int, 1>());
+    }
+  }
+  __syncwarp();
+  if (p.split > 1) cluster_sync_all();                     // what others read stays until they did
   tc_fence_before();
   __syncthreads();
   if (*static_cast<volatile uint32_t *>(&c.abort)) {
@@ -195,17 +261,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ many tokens
 //
-// Tiles of 128 tokens x 256 features, one CTA an SM that walks its tiles: one warp
-// loads, one issues products, two warpgroups take the sums of the tile before (the two
-// halves of TMEM hold a tile each) through swizzled shared memory, 64 features at a
-// time, the residual in by TMA and the output out by TMA, which clips it (to whole
-// vectors of 8: a copy that ends inside one wrote an element behind; threads store the
-// last few features).
-constexpr int kTileRows = 128, kTileCols = 256, kTileStages = 4;
+// Tiles of 256 tokens x 256 features, a pair of CTAs on two SMs that walks its tiles.
+// A CTA holds 128 tokens' sums and loads their rows and 128 features' of W; a product
+// takes the tokens of both and the features of both, so that a CTA loads 32 KiB where
+// one alone would load 48 for as many products (128 x 256 tiles of single CTAs: 323 us
+// where pairs take PAIRUS, 9159 x 4096 x 7168; their loads came in at 70 bytes a cycle and
+// SM).  One warp loads, one of the first CTA issues the products, two warpgroups take
+// the sums of the tile before (the two halves of TMEM hold a tile each) through swizzled
+// shared memory, 64 features at a time, the residual in by TMA and the output out by
+// TMA, which clips it (to whole vectors of 8: a copy that ends inside one wrote an
+// element behind; threads store the last few features).
+constexpr int kTileRows = 256, kTileCols = 256, kTileStages = 6;     // of a pair
 constexpr int kTileThreads = 384;                // TMA, products, 2 idle; 8 epilogue warps
-constexpr int kTileStage = (kTileRows + kTileCols) * kK * 2;
-constexpr int kChunk = kTileRows * 64 * 2;       // bytes of 64 features
-constexpr int kGroupRows = 16;                   // tiles along the tokens that run side by side
+constexpr int kTileStage = (kTileRows + kTileCols) / 2 * kK * 2;     // of a CTA
+constexpr int kChunk = 128 * 64 * 2;             // bytes of 64 features
+constexpr int kGroupRows = 8;                    // tiles along the tokens that run side by side
 
 struct TileCtrl {
   uint64_t full[kTileStages], empty[kTileStages], sums_full[2], sums_empty[2], residual[2];
@@ -213,6 +283,35 @@ struct TileCtrl {
 };
 constexpr int kTileSmem = kTileStages * kTileStage + 2 * kChunk + 1024 + sizeof(TileCtrl);
 static_assert(kTileSmem <= 232448, "shared memory of one CTA");
+
+// The pair's forms of a load (whose bytes count on the first CTA's barrier), a product,
+// a commit (which arrives in both CTAs) and an arrival on the first CTA's barrier.
+__device__ __forceinline__ void pair_load(void *dst, const CUtensorMap *map, int x, int y,
+                                          uint32_t bar_in_first) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(bar_in_first)
+      : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void pair_commit(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_addr(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void arrive_in(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 
 struct Tile {
   int row, col;
@@ -239,7 +338,7 @@ __device__ __forceinline__ bool group_sync_or(int group, bool pred) {
 }
 
 template <int kAct>
-__global__ void __launch_bounds__(kTileThreads, 1)
+__global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
     tile_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap xmap,
                 const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap rmap,
                 const __grid_constant__ CUtensorMap omap) {
@@ -248,6 +347,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint8_t *chunks = ring + kTileStages * kTileStage;
   TileCtrl &c = *reinterpret_cast<TileCtrl *>(chunks + 2 * kChunk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int pair0 = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int tiles_m = (p.rows + kTileRows - 1) / kTileRows;
   const int tiles_n = (p.outer + kTileCols - 1) / kTileCols, tiles = tiles_m * tiles_n;
   if (threadIdx.x == 0) {
@@ -258,19 +359,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.sums_full[i], 1);
-      mbar_init(&c.sums_empty[i], 8);
+      mbar_init(&c.sums_empty[i], 16);           // both CTAs' warps
       mbar_init(&c.residual[i], 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_addr(&c.tmem))
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();                              // both CTAs' barriers are there
   tc_fence_after();
   const uint32_t tmem = c.tmem;
 
@@ -278,25 +380,31 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (elect_one()) {
       int s = 0, phase = 1;
       bool ok = true;
-      for (int n = blockIdx.x; n < tiles && ok; n += gridDim.x) {
+      for (int n = pair0; n < tiles && ok; n += pairs) {
         const Tile tile = tile_of(n, tiles_m, tiles_n);
         for (int k = 0; k < p.blocks; ++k) {
           if (!(ok = wait_phase(&c.empty[s], phase, &c.abort))) break;
           uint8_t *a = ring + s * kTileStage;
-          mbar_arrive_expect_tx(&c.full[s], kTileStage);
-          tma_load(a, &xmap, k * kK, tile.row, &c.full[s]);
-          tma_load(a + kTileRows * kK * 2, &wmap, k * kK, tile.col, &c.full[s]);
+          const uint32_t bar = cluster_map(&c.full[s], 0);
+          if (rank == 0) mbar_arrive_expect_tx(&c.full[s], 2 * kTileStage);
+          pair_load(a, &xmap, k * kK, tile.row + 128 * rank, bar);
+          pair_load(a + kTileStage / 2, &wmap, k * kK, tile.col + 128 * rank, bar);
           if (++s == kTileStages) s = 0, phase ^= 1;
         }
       }
+      // the products that still read the ring arrive on barriers of both CTAs
+      for (int i = 0; i < kTileStages && ok; ++i) {
+        ok = wait_phase(&c.empty[s], phase, &c.abort);
+        if (++s == kTileStages) s = 0, phase ^= 1;
+      }
     }
   } else if (warp == 1) {
-    if (elect_one()) {
+    if (rank == 0 && elect_one()) {
       constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((kTileCols >> 3) << 17) |
                                  ((kTileRows >> 4) << 24);
       int s = 0, phase = 0, i = 0;
       bool ok = true;
-      for (int n = blockIdx.x; n < tiles && ok; n += gridDim.x, ++i) {
+      for (int n = pair0; n < tiles && ok; n += pairs, ++i) {
         const int half = i & 1;
         if (!wait_phase(&c.sums_empty[half], ((i >> 1) & 1) ^ 1, &c.abort)) break;
         tc_fence_after();
@@ -305,13 +413,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (!(ok = wait_phase(&c.full[s], phase, &c.abort))) break;
           tc_fence_after();
           const uint32_t a = smem_addr(ring + s * kTileStage);
-          const uint64_t da = desc_k_major(a), db = desc_k_major(a + kTileRows * kK * 2);
+          const uint64_t da = desc_k_major(a), db = desc_k_major(a + kTileStage / 2);
 #pragma unroll
-          for (int j = 0; j < kK / 16; ++j) tc_mma_ss(d, da + 2 * j, db + 2 * j, idesc, k > 0 || j > 0);
-          tc_commit(&c.empty[s]);
+          for (int j = 0; j < kK / 16; ++j) pair_mma(d, da + 2 * j, db + 2 * j, idesc, k > 0 || j > 0);
+          pair_commit(&c.empty[s]);
           if (++s == kTileStages) s = 0, phase ^= 1;
         }
-        tc_commit(&c.sums_full[half]);
+        pair_commit(&c.sums_full[half]);
       }
     }
   } else if (warp >= 4) {
@@ -319,16 +427,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const bool leader = (threadIdx.x & 127) == 0;
     uint8_t *chunk = chunks + group * kChunk, *mine = chunk + row * 128;
     int i = 0, loads = 0;
-    for (int n = blockIdx.x; n < tiles; n += gridDim.x, ++i) {
-      const Tile tile = tile_of(n, tiles_m, tiles_n);
+    for (int n = pair0; n < tiles; n += pairs, ++i) {
+      Tile tile = tile_of(n, tiles_m, tiles_n);
+      tile.row += 128 * rank;
       const int half = i & 1;
       bool stop = false;
       for (int part = 0; part < 2; ++part) {
         const int col = tile.col + group * 128 + part * 64;
+        const bool there = col < p.outer && tile.row < p.rows;
         bool ok = true;
         if (leader) {
           bulk_wait_read(0);                       // the chunk's last output has left
-          if (p.residual && col < p.outer) {
+          if (p.residual && there) {
             mbar_arrive_expect_tx(&c.residual[group], kChunk);
             tma_load(chunk, &rmap, col, tile.row, &c.residual[group]);
           }
@@ -351,9 +461,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (part == 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&c.sums_empty[half]);
+          if (lane == 0) arrive_in(cluster_map(&c.sums_empty[half], 0));
         }
-        if (col >= p.outer) continue;
+        if (!there) continue;
         if (p.residual) ok = wait_phase(&c.residual[group], loads++ & 1, &c.abort);
 #pragma unroll
         for (int g = 0; g < 8; ++g) {              // 8 features, 16 bytes
@@ -405,6 +515,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();                              // nothing comes from the other CTA any more
   if (*static_cast<volatile uint32_t *>(&c.abort)) {
     // copies and products in flight end within microseconds: give them time
     // before the shared memory and TMEM go
@@ -415,22 +526,43 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
 
 typedef void (*TileKernel)(const Params, const CUtensorMap, const CUtensorMap, const CUtensorMap,
                            const CUtensorMap);
 
+// Pairs of CTAs that run at a time (half the SMs, less where one has no partner).
+static int pairs_of(int dev, const void *kernel) {
+  static std::atomic<int> known[kMaxDevices];
+  int pairs = known[dev].load(std::memory_order_acquire);
+  if (pairs == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kTileThreads);
+    cfg.dynamicSmemBytes = kTileSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess) return 0;
+    known[dev].store(pairs, std::memory_order_release);
+  }
+  return pairs;
+}
+
 static int launch_tiles(const kda_linear_args *a, const Params &p, int dev, int sms, cudaStream_t stream) {
   const int64_t tiles = static_cast<int64_t>((a->rows + kTileRows - 1) / kTileRows) *
                         ((a->outer + kTileCols - 1) / kTileCols);
   if (tiles > 0x7fffffffll - sms) return KDA_ERR_SHAPE;
   CUtensorMap x, w, r = {}, o;
-  if (!rows_map(&x, a->x, a->inner, a->rows, a->x_stride, kTileRows, dev) ||
-      !rows_map(&w, a->weight, a->inner, a->outer, a->w_stride, kTileCols, dev) ||
-      !rows_map(&o, a->output, a->outer / 8 * 8, a->rows, a->o_stride, kTileRows, dev) ||
-      (a->residual && !rows_map(&r, a->residual, a->outer, a->rows, a->r_stride, kTileRows, dev)))
+  if (!rows_map(&x, a->x, a->inner, a->rows, a->x_stride, 128, dev) ||
+      !rows_map(&w, a->weight, a->inner, a->outer, a->w_stride, 128, dev) ||
+      !rows_map(&o, a->output, a->outer / 8 * 8, a->rows, a->o_stride, 128, dev) ||
+      (a->residual && !rows_map(&r, a->residual, a->outer, a->rows, a->r_stride, 128, dev)))
     return KDA_ERR_LAUNCH;
   static const TileKernel kernels[4] = {tile_kernel<KDA_ACT_NONE>, tile_kernel<KDA_ACT_SILU>,
                                         tile_kernel<KDA_ACT_GELU>, tile_kernel<KDA_ACT_SOFTPLUS>};
@@ -438,8 +570,43 @@ static int launch_tiles(const kda_linear_args *a, const Params &p, int dev, int 
   const TileKernel kernel = kernels[p.act];
   if (!set_smem_limit_once(done[p.act], dev, reinterpret_cast<const void *>(kernel), kTileSmem))
     return KDA_ERR_LAUNCH;
-  kernel<<<static_cast<int>(tiles < sms ? tiles : sms), kTileThreads, kTileSmem, stream>>>(p, x, w, r, o);
+  const int pairs = pairs_of(dev, reinterpret_cast<const void *>(kernel));
+  if (pairs < 1) return KDA_ERR_LAUNCH;
+  kernel<<<2 * static_cast<int>(tiles < pairs ? tiles : pairs), kTileThreads, kTileSmem, stream>>>(p, x, w, r, o);
   return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
+}
+
+typedef void (*ProductKernel)(const Params, const CUtensorMap, const CUtensorMap);
+
+// Which form and layout: the cheapest by a model of an SM's cycles for its CTAs, a
+// block of the inner dimension costing its products (2 a token) or its bytes at 48 a
+// cycle, whichever is more.  tile_n 0: many tiles.
+struct Plan {
+  int tile_n, split;
+};
+static Plan plan_of(int rows, int blocks, int outer, int sms) {
+  const int64_t tiles_m = (outer + kM - 1) / kM;
+  Plan best = {0, 1};
+  double least = 1e300;
+  if (rows > kMostN && outer >= 8) {
+    const int64_t tiles = (rows + kTileRows - 1) / kTileRows * ((outer + kTileCols - 1) / int64_t(kTileCols));
+    least = static_cast<double>((tiles + sms - 1) / sms) * blocks * 600 + 5000;
+  }
+  for (int tile_n = 16; tile_n <= kMostN; tile_n += tile_n < 64 ? 16 : 32) {
+    if (tile_n - 32 >= rows) break;
+    const int64_t tiles = tiles_m * ((rows + tile_n - 1) / tile_n);
+    const double bytes = (kATile + tile_n * kK * 2) / 48.0, block = bytes > 2 * tile_n ? bytes : 2 * tile_n;
+    for (int split = 1; split <= 8 && split <= blocks; ++split) {
+      const int64_t ctas = (tiles * split + sms - 1) / sms;
+      const double cost = static_cast<double>(ctas) * ((blocks + split - 1) / split * block + 12 * tile_n + 600) +
+                          3000 + (split > 1 ? 1200 : 0);
+      if (cost < least) {
+        least = cost;
+        best = {tile_n, split};
+      }
+    }
+  }
+  return best;
 }
 
 static int run(const kda_linear_args *a, cudaStream_t stream) {
@@ -468,28 +635,36 @@ static int run(const kda_linear_args *a, cudaStream_t stream) {
   p.residual = static_cast<const __nv_bfloat16 *>(a->residual);
   p.output = static_cast<__nv_bfloat16 *>(a->output);
   p.err = a->err;
-  p.tile_n = a->rows >= kMostN ? kMostN : (a->rows + 15) / 16 * 16;
   p.blocks = (a->inner + kK - 1) / kK;
-  if (a->rows > kMostN && a->outer >= 8) return launch_tiles(a, p, dev, df.sms, stream);
-  p.stages = kRing / (kATile + p.tile_n * kK * 2);
-  if (p.stages > kMostStages) p.stages = kMostStages;
+  Plan plan = plan_of(a->rows, p.blocks, a->outer, df.sms);
+  if (getenv("LT")) plan.tile_n = atoi(getenv("LT"));
+  if (getenv("LS")) plan.split = atoi(getenv("LS"));
+  if (getenv("LP")) printf("plan %d %d\n", plan.tile_n, plan.split);
+
+  if (plan.tile_n == 0) return launch_tiles(a, p, dev, df.sms, stream);
+  p.tile_n = plan.tile_n;
+  p.split = plan.split;
+  const int stage = kATile + p.tile_n * kK * 2;
   const int tiles_m = (a->outer + kM - 1) / kM, tiles_n = (a->rows + p.tile_n - 1) / p.tile_n;
-  if (tiles_n > 65535) return KDA_ERR_SHAPE;
-  p.split = 1;
-  while (p.split < 8 && 2 * p.split * static_cast<int64_t>(tiles_m) * tiles_n <= df.sms &&
-         2 * p.split <= p.blocks)
-    p.split *= 2;
+  const bool few = static_cast<int64_t>(tiles_m) * tiles_n * p.split <= df.sms;
+  p.ring = !few && kHalfRing / stage >= 4 ? kHalfRing : kRing;
+  p.stages = p.ring / stage;
+  if (p.stages > kMostStages) p.stages = kMostStages;
+  if (tiles_n > 65535 || static_cast<int64_t>(tiles_m) * p.split > 0x7fffffffll) return KDA_ERR_SHAPE;
   CUtensorMap w, x;
   if (!rows_map(&w, a->weight, a->inner, a->outer, a->w_stride, kM, dev) ||
       !rows_map(&x, a->x, a->inner, a->rows, a->x_stride, p.tile_n, dev))
     return KDA_ERR_LAUNCH;
-  static std::atomic<bool> done[kMaxDevices];
-  if (!set_smem_limit_once(done, dev, reinterpret_cast<const void *>(product_kernel), kSmem))
+  static const ProductKernel kernels[4] = {product_kernel<KDA_ACT_NONE>, product_kernel<KDA_ACT_SILU>,
+                                           product_kernel<KDA_ACT_GELU>, product_kernel<KDA_ACT_SOFTPLUS>};
+  static std::atomic<bool> done[4][kMaxDevices];
+  const ProductKernel kernel = kernels[p.act];
+  if (!set_smem_limit_once(done[p.act], dev, reinterpret_cast<const void *>(kernel), smem_of(kRing)))
     return KDA_ERR_LAUNCH;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles_m * p.split, tiles_n);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = smem_of(p.ring);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -497,7 +672,7 @@ static int run(const kda_linear_args *a, cudaStream_t stream) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, product_kernel, p, w, x) != cudaSuccess) return KDA_ERR_LAUNCH;
+  if (cudaLaunchKernelEx(&cfg, kernel, p, w, x) != cudaSuccess) return KDA_ERR_LAUNCH;
   return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
 }
 
