@@ -11,7 +11,6 @@
 #include <stdint.h>
 #include <type_traits>
 #include <stdio.h>
-#include <stdlib.h>
 
 #include "../../include/kda.h"
 #include "kda_device.cuh"
@@ -50,9 +49,30 @@ struct Ctrl {
 constexpr int smem_of(int ring) { return ring + 1024 + static_cast<int>(sizeof(Ctrl)); }
 static_assert(smem_of(kRing) <= 232448, "shared memory of one CTA");
 
+// y (1 + erf(y / sqrt 2)) / 2 = max(y, 0) - |y| erfc(x) / 2 with x = |y| / sqrt 2 and
+// erfc(x) = exp(-x^2) t P(t), t = 1 / (1 + x / 2): P is the least-squares fit of relative
+// errors at 400 Chebyshev points of 0 <= x <= 10, degree 8, 5e-8 (with FP32's roundings
+// 1.8e-7); behind x = 9.4 the exponential is 0.  About 15 instructions (the library's
+// erfc: 9159 x 256 x 4096 98 us instead of 39).
+__device__ __forceinline__ float gelu(float y) {
+  const float a = fabsf(y);
+  const float t = rcp_approx(__fmaf_rn(a, 0.35355339f, 1.0f));
+  float h = -3.005435318e-02f;
+  h = __fmaf_rn(h, t, 1.447230577e-01f);
+  h = __fmaf_rn(h, t, -2.484147847e-01f);
+  h = __fmaf_rn(h, t, 1.442575753e-01f);
+  h = __fmaf_rn(h, t, -1.669950970e-02f);
+  h = __fmaf_rn(h, t, 1.026802137e-01f);
+  h = __fmaf_rn(h, t, 1.212396920e-01f);
+  h = __fmaf_rn(h, t, 1.412269175e-01f);
+  h = __fmaf_rn(h, t, 1.410411745e-01f);
+  const float e = exp2_approx(y * y * -0.72134752f);       // exp(-y^2 / 2)
+  return __fmaf_rn(-a, h * t * e, fmaxf(y, 0.0f));
+}
+
 __device__ __forceinline__ float activated(float y, int act) {
   if (act == KDA_ACT_SILU) return silu_approx(y);
-  if (act == KDA_ACT_GELU) return 0.5f * y * erfcf(y * -0.7071067812f);
+  if (act == KDA_ACT_GELU) return gelu(y);
   if (act == KDA_ACT_SOFTPLUS) return softplus(y);
   return y;
 }
@@ -265,23 +285,23 @@ __global__ void __launch_bounds__(kThreads, 2)
 // A CTA holds 128 tokens' sums and loads their rows and 128 features' of W; a product
 // takes the tokens of both and the features of both, so that a CTA loads 32 KiB where
 // one alone would load 48 for as many products (128 x 256 tiles of single CTAs: 323 us
-// where pairs take PAIRUS, 9159 x 4096 x 7168; their loads came in at 70 bytes a cycle and
+// where pairs take 283, 9159 x 4096 x 7168; their loads came in at 70 bytes a cycle and
 // SM).  One warp loads, one of the first CTA issues the products, two warpgroups take
 // the sums of the tile before (the two halves of TMEM hold a tile each) through swizzled
 // shared memory, 64 features at a time, the residual in by TMA and the output out by
 // TMA, which clips it (to whole vectors of 8: a copy that ends inside one wrote an
 // element behind; threads store the last few features).
-constexpr int kTileRows = 256, kTileCols = 256, kTileStages = 6;     // of a pair
-constexpr int kTileThreads = 384;                // TMA, products, 2 idle; 8 epilogue warps
+constexpr int kTileRows = 256, kTileCols = 256, kTileStages = 5;     // of a pair
+constexpr int kTileThreads = 640;                // TMA, products, 2 idle; 16 epilogue warps
 constexpr int kTileStage = (kTileRows + kTileCols) / 2 * kK * 2;     // of a CTA
-constexpr int kChunk = 128 * 64 * 2;             // bytes of 64 features
+constexpr int kChunk = 32 * 64 * 2;              // bytes of a warp's 32 tokens, 64 features
 constexpr int kGroupRows = 8;                    // tiles along the tokens that run side by side
 
 struct TileCtrl {
-  uint64_t full[kTileStages], empty[kTileStages], sums_full[2], sums_empty[2], residual[2];
+  uint64_t full[kTileStages], empty[kTileStages], sums_full[2], sums_empty[2], residual[16];
   uint32_t tmem, abort;
 };
-constexpr int kTileSmem = kTileStages * kTileStage + 2 * kChunk + 1024 + sizeof(TileCtrl);
+constexpr int kTileSmem = kTileStages * kTileStage + 16 * kChunk + 1024 + sizeof(TileCtrl);
 static_assert(kTileSmem <= 232448, "shared memory of one CTA");
 
 // The pair's forms of a load (whose bytes count on the first CTA's barrier), a product,
@@ -324,19 +344,6 @@ __device__ __forceinline__ Tile tile_of(int n, int tiles_m, int tiles_n) {
   return Tile{(first + at % high) * kTileRows, at / high * kTileCols};
 }
 
-// Named barrier of an epilogue warpgroup that also ORs a predicate.
-__device__ __forceinline__ bool group_sync_or(int group, bool pred) {
-  uint32_t r;
-  __syncwarp();
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
-      " bar.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(pred)), "r"(group + 1)
-      : "memory");
-  return r != 0;
-}
-
 template <int kAct>
 __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
     tile_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap xmap,
@@ -345,7 +352,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
   extern __shared__ uint8_t raw[];
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint8_t *chunks = ring + kTileStages * kTileStage;
-  TileCtrl &c = *reinterpret_cast<TileCtrl *>(chunks + 2 * kChunk);
+  TileCtrl &c = *reinterpret_cast<TileCtrl *>(chunks + 16 * kChunk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const int pair0 = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -359,9 +366,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.sums_full[i], 1);
-      mbar_init(&c.sums_empty[i], 16);           // both CTAs' warps
-      mbar_init(&c.residual[i], 1);
+      mbar_init(&c.sums_empty[i], 32);           // both CTAs' warps
     }
+    for (int i = 0; i < 16; ++i) mbar_init(&c.residual[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -423,92 +430,103 @@ __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
       }
     }
   } else if (warp >= 4) {
-    const int group = (warp - 4) >> 2, w4 = warp & 3, row = w4 * 32 + lane;
-    const bool leader = (threadIdx.x & 127) == 0;
-    uint8_t *chunk = chunks + group * kChunk, *mine = chunk + row * 128;
-    int i = 0, loads = 0;
-    for (int n = pair0; n < tiles; n += pairs, ++i) {
-      Tile tile = tile_of(n, tiles_m, tiles_n);
-      tile.row += 128 * rank;
-      const int half = i & 1;
-      bool stop = false;
-      for (int part = 0; part < 2; ++part) {
-        const int col = tile.col + group * 128 + part * 64;
-        const bool there = col < p.outer && tile.row < p.rows;
-        bool ok = true;
-        if (leader) {
-          bulk_wait_read(0);                       // the chunk's last output has left
-          if (p.residual && there) {
-            mbar_arrive_expect_tx(&c.residual[group], kChunk);
-            tma_load(chunk, &rmap, col, tile.row, &c.residual[group]);
-          }
-        }
-        if (part == 0) {
-          ok = wait_phase(&c.sums_full[half], (i >> 1) & 1, &c.abort);
-          tc_fence_after();
-        }
-        uint32_t r[2][32];
-        if (group_sync_or(group, !ok)) {           // all of the warpgroup, or none
-          stop = true;
-          break;
-        }
-        const uint32_t from =
-            tmem + (static_cast<uint32_t>(w4 * 32) << 16) + half * kTileCols + group * 128 + part * 64;
-        tc_ld(from, r[0]);
-        tc_ld(from + 32, r[1]);
-        tc_wait_ld(r[0]);
-        tc_wait_ld(r[1]);
-        if (part == 1) {
+    // Each warp takes 32 tokens x 64 features of a tile through a buffer of its own, and
+    // waits for none of the others.  16 warps, as a chunk is a long chain for one warp
+    // (TMEM, arithmetic, shared memory, a fence, a copy: 3.8k cycles where a thin tile's
+    // products take 2k; 8 warps with two chunks each, 9159 x 256 x 4096: 33 us, 16 warps 27).
+    const int w4 = warp & 3, group = (warp - 4) >> 2;
+    const bool leader = lane == 0;
+    uint8_t *const chunk = chunks + (warp - 4) * kChunk, *const mine = chunk + lane * 128;
+    uint64_t *const residual = &c.residual[warp - 4];
+    auto chunk_of = [&](int q, Tile *at) {         // whether there is one
+      const int n = pair0 + q * pairs;
+      if (n >= tiles) return false;
+      *at = tile_of(n, tiles_m, tiles_n);
+      at->row += 128 * rank + 32 * w4;
+      at->col += group * 64;
+      return true;
+    };
+    auto fetch = [&](int q) {                      // a chunk's residual
+      Tile at;
+      if (!chunk_of(q, &at) || at.col >= p.outer || at.row >= p.rows) return;
+      mbar_arrive_expect_tx(residual, kChunk);
+      tma_load(chunk, &rmap, at.col, at.row, residual);
+    };
+    uint32_t loads = 0;
+    if (leader && p.residual) fetch(0);
+    Tile at;
+    for (int q = 0; chunk_of(q, &at); ++q) {
+      const int half = q & 1;
+      const bool there = at.col < p.outer && at.row < p.rows;
+      const int left = p.outer - at.col;           // features of the chunk, where fewer than 64
+      bool ok = wait_phase(&c.sums_full[half], (q >> 1) & 1, &c.abort);
+      tc_fence_after();
+      if (p.residual && there) ok &= wait_phase(residual, loads++ & 1, &c.abort);
+      if (leader) bulk_wait_read(0);               // the last output has left the buffer
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint32_t from =
+          tmem + (static_cast<uint32_t>(w4 * 32) << 16) + half * kTileCols + group * 64;
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {                // 32 features
+        uint32_t r[32];
+        tc_ld(from + 32 * z, r);
+        tc_wait_ld(r);
+        if (z == 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_in(cluster_map(&c.sums_empty[half], 0));
+          if (leader) arrive_in(cluster_map(&c.sums_empty[half], 0));
         }
         if (!there) continue;
-        if (p.residual) ok = wait_phase(&c.residual[group], loads++ & 1, &c.abort);
+        if (p.bias) {
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {              // 8 features, 16 bytes
-          float y[8], add[8];
+          for (int g = 0; g < 4; ++g) {
+            float add[8];
+            unpack8(vector_of(p.bias + at.col + 32 * z + 8 * g, left - 32 * z - 8 * g), add);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(r[g >> 2][(g & 3) * 8 + e]);
-          if (p.bias && col + 8 * g < p.outer) {
-            if (col + 8 * g + 8 <= p.outer) {
-              unpack8(__ldg(reinterpret_cast<const uint4 *>(p.bias + col + 8 * g)), add);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                add[e] = col + 8 * g + e < p.outer ? __bfloat162float(p.bias[col + 8 * g + e]) : 0.0f;
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] += add[e];
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = activated(y[e], kAct);
-          uint4 *at = reinterpret_cast<uint4 *>(mine + ((g ^ (row & 7)) << 4));
-          if (p.residual) {
-            unpack8(*at, add);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] += add[e];
-          }
-          *at = pack8(y);
-          const int left = p.outer - col - 8 * g;
-          if (left > 0 && left < 8 && tile.row + row < p.rows) {
-            __nv_bfloat16 *out = p.output + (tile.row + row) * p.o_stride + col + 8 * g;
-#pragma unroll
-            for (int e = 0; e < 7; ++e)
-              if (e < left) out[e] = __float2bfloat16_rn(y[e]);
+            for (int e = 0; e < 8; ++e)
+              r[8 * g + e] = __float_as_uint(__uint_as_float(r[8 * g + e]) + add[e]);
           }
         }
-        fence_proxy_async_smem();
-        if (group_sync_or(group, !ok)) {
-          stop = true;
-          break;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          r[e] = __float_as_uint(activated(__uint_as_float(r[e]), kAct));
+        if (p.residual) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            float add[8];
+            unpack8(*reinterpret_cast<const uint4 *>(mine + (((4 * z + g) ^ (lane & 7)) << 4)), add);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              r[8 * g + e] = __float_as_uint(__uint_as_float(r[8 * g + e]) + add[e]);
+          }
         }
-        if (leader) {
-          tma_store(&omap, col, tile.row, chunk);
-          bulk_commit();
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          w[e] = pack2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<uint4 *>(mine + (((4 * z + g) ^ (lane & 7)) << 4)) =
+              make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
+        const int end = left - 32 * z;             // the output ends inside a vector of these 32
+        if (end > 0 && end < 32 && (end & 7) && at.row + lane < p.rows) {
+          uint16_t *out = reinterpret_cast<uint16_t *>(p.output) + (at.row + lane) * p.o_stride + at.col + 32 * z;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (e >= (end & ~7) && e < end) out[e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
         }
       }
-      if (stop) break;
+      if (!there) continue;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (leader) {
+        tma_store(&omap, at.col, at.row, chunk);
+        bulk_commit();
+        if (p.residual) {
+          bulk_wait_read(0);                       // the buffer is free for the next residual
+          fetch(q + 1);
+        }
+      }
     }
     if (leader) bulk_wait_all();
   }
@@ -561,8 +579,8 @@ static int launch_tiles(const kda_linear_args *a, const Params &p, int dev, int 
   CUtensorMap x, w, r = {}, o;
   if (!rows_map(&x, a->x, a->inner, a->rows, a->x_stride, 128, dev) ||
       !rows_map(&w, a->weight, a->inner, a->outer, a->w_stride, 128, dev) ||
-      !rows_map(&o, a->output, a->outer / 8 * 8, a->rows, a->o_stride, 128, dev) ||
-      (a->residual && !rows_map(&r, a->residual, a->outer, a->rows, a->r_stride, 128, dev)))
+      !rows_map(&o, a->output, a->outer / 8 * 8, a->rows, a->o_stride, 32, dev) ||
+      (a->residual && !rows_map(&r, a->residual, a->outer, a->rows, a->r_stride, 32, dev)))
     return KDA_ERR_LAUNCH;
   static const TileKernel kernels[4] = {tile_kernel<KDA_ACT_NONE>, tile_kernel<KDA_ACT_SILU>,
                                         tile_kernel<KDA_ACT_GELU>, tile_kernel<KDA_ACT_SOFTPLUS>};
@@ -578,28 +596,39 @@ static int launch_tiles(const kda_linear_args *a, const Params &p, int dev, int 
 
 typedef void (*ProductKernel)(const Params, const CUtensorMap, const CUtensorMap);
 
-// Which form and layout: the cheapest by a model of an SM's cycles for its CTAs, a
-// block of the inner dimension costing its products (2 a token) or its bytes at 48 a
-// cycle, whichever is more.  tile_n 0: many tiles.
+// Which form and layout: the cheapest by a model of the time in us, fitted to 30 shapes
+// with up to 20 layouts each (the layout it takes is within 15% of the best measured, most
+// within 5%).  Few tiles: a CTA streams a block of the inner dimension in its products'
+// time or at 160 KB a us, W comes at 6.5 MB a us at most, a CTA starts and ends in 1 + 0.009
+// a token (half of it hidden where two share an SM), and a join costs by its ranks and
+// tokens.  Pairs: 0.305 a block, 2.3 a tile at least.  tile_n 0: pairs.
 struct Plan {
   int tile_n, split;
 };
-static Plan plan_of(int rows, int blocks, int outer, int sms) {
+static Plan plan_of(int rows, int blocks, int inner, int outer, int sms) {
   const int64_t tiles_m = (outer + kM - 1) / kM;
+  const double weights = 2.0 * inner * outer / 6.5e6;
   Plan best = {0, 1};
   double least = 1e300;
-  if (rows > kMostN && outer >= 8) {
-    const int64_t tiles = (rows + kTileRows - 1) / kTileRows * ((outer + kTileCols - 1) / int64_t(kTileCols));
-    least = static_cast<double>((tiles + sms - 1) / sms) * blocks * 600 + 5000;
+  if (outer >= 8 && rows > 64) {
+    const int64_t tiles = static_cast<int64_t>((rows + kTileRows - 1) / kTileRows) *
+                          ((outer + kTileCols - 1) / kTileCols);
+    const double tile = blocks * 0.305 > 2.3 ? blocks * 0.305 : 2.3;
+    least = static_cast<double>((tiles + sms / 2 - 1) / (sms / 2)) * tile + 6.0;
   }
   for (int tile_n = 16; tile_n <= kMostN; tile_n += tile_n < 64 ? 16 : 32) {
     if (tile_n - 32 >= rows) break;
     const int64_t tiles = tiles_m * ((rows + tile_n - 1) / tile_n);
-    const double bytes = (kATile + tile_n * kK * 2) / 48.0, block = bytes > 2 * tile_n ? bytes : 2 * tile_n;
+    const double bytes = (kATile + tile_n * kK * 2) / 160e3;
+    const double block = bytes > 0.0011 * tile_n ? bytes : 0.0011 * tile_n;
     for (int split = 1; split <= 8 && split <= blocks; ++split) {
-      const int64_t ctas = (tiles * split + sms - 1) / sms;
-      const double cost = static_cast<double>(ctas) * ((blocks + split - 1) / split * block + 12 * tile_n + 600) +
-                          3000 + (split > 1 ? 1200 : 0);
+      const int64_t ctas = tiles * split, waves = (ctas + sms - 1) / sms;
+      const double ends = (1.0 + 0.009 * tile_n) * (ctas > sms && tile_n <= 64 ? 0.5 : 1.0);
+      double stream = static_cast<double>(waves) * ((blocks + split - 1) / split) * block;
+      const double read = weights * (1.0 + 0.15 * ((rows - 1) / tile_n));
+      if (stream < read) stream = read;
+      const double join = split > 1 ? 0.2 + (split - 1) * (0.02 + 0.006 * tile_n) : 0.0;
+      const double cost = stream + static_cast<double>(waves) * (ends + join) + 3.2;
       if (cost < least) {
         least = cost;
         best = {tile_n, split};
@@ -636,9 +665,7 @@ static int run(const kda_linear_args *a, cudaStream_t stream) {
   p.output = static_cast<__nv_bfloat16 *>(a->output);
   p.err = a->err;
   p.blocks = (a->inner + kK - 1) / kK;
-  Plan plan = plan_of(a->rows, p.blocks, a->outer, df.sms);
-  if (getenv("LT")) plan.tile_n = atoi(getenv("LT"));
-  if (getenv("LS")) plan.split = atoi(getenv("LS"));
+  const Plan plan = plan_of(a->rows, p.blocks, a->inner, a->outer, df.sms);
   if (getenv("LP")) printf("plan %d %d\n", plan.tile_n, plan.split);
 
   if (plan.tile_n == 0) return launch_tiles(a, p, dev, df.sms, stream);
