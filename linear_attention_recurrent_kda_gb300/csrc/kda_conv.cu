@@ -38,48 +38,39 @@ struct Params {
   int32_t *err;
 };
 
+// 8 channels, two to an operation.
 template <int kTaps>
 struct Channels {
-  float w[kTaps][8], bias[8];
-  float last[kTaps - 1][8];      // the inputs before this one, oldest first
+  f32x2 w[kTaps][4], bias[4];
+  f32x2 last[kTaps - 1][4];      // the inputs before this one, oldest first
 
   __device__ __forceinline__ void load_weights(const Params &p, int c) {
     const __nv_bfloat16 *at = p.weight + static_cast<int64_t>(c / p.part) * kTaps * p.part + c % p.part;
 #pragma unroll
     for (int j = 0; j < kTaps; ++j)
-      unpack8(__ldg(reinterpret_cast<const uint4 *>(at + static_cast<int64_t>(j) * p.part)), w[j]);
-    if (p.bias) {
-      unpack8(__ldg(reinterpret_cast<const uint4 *>(p.bias + c)), bias);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) bias[i] = 0.0f;
-    }
-  }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int j = 0; j < kTaps - 1; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) last[j][i] = 0.0f;
+      pairs8(__ldg(reinterpret_cast<const uint4 *>(at + static_cast<int64_t>(j) * p.part)), w[j]);
+    pairs8(p.bias ? __ldg(reinterpret_cast<const uint4 *>(p.bias + c)) : make_uint4(0, 0, 0, 0), bias);
   }
   // One token: its output, and the inputs move on.
   __device__ __forceinline__ uint4 token(const uint4 &raw, int silu) {
-    float x[8], y[8];
-    unpack8(raw, x);
+    f32x2 x[4];
+    uint32_t y[4];
+    pairs8(raw, x);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float acc = bias[i];
+    for (int i = 0; i < 4; ++i) {
+      f32x2 acc = bias[i];
 #pragma unroll
-      for (int j = 0; j < kTaps - 1; ++j) acc = __fmaf_rn(w[j][i], last[j][i], acc);
-      y[i] = __fmaf_rn(w[kTaps - 1][i], x[i], acc);
+      for (int j = 0; j < kTaps - 1; ++j) acc = fma2(w[j][i], last[j][i], acc);
+      acc = fma2(w[kTaps - 1][i], x[i], acc);
 #pragma unroll
       for (int j = 0; j < kTaps - 2; ++j) last[j][i] = last[j + 1][i];
       last[kTaps - 2][i] = x[i];
+      if (silu) acc = silu2(acc);
+      float lo, hi;
+      unpair(acc, lo, hi);
+      y[i] = pack2(lo, hi);
     }
-    if (silu) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = silu_approx(y[i]);
-    }
-    return pack8(y);
+    return make_uint4(y[0], y[1], y[2], y[3]);
   }
 };
 
@@ -88,7 +79,7 @@ struct Channels {
 // before the last.
 template <int kTaps, bool kF32>
 __device__ __forceinline__ void read_window(const Params &p, int slot, int c,
-                                            float (&last)[kTaps - 1][8]) {
+                                            f32x2 (&last)[kTaps - 1][4]) {
   constexpr int kN = kTaps - 1, kWords = kF32 ? 8 * kN : 4 * kN;
   const int64_t at = (static_cast<int64_t>(slot) * p.channels + c) * p.width;
   if (p.width == kN) {
@@ -101,28 +92,41 @@ __device__ __forceinline__ void read_window(const Params &p, int slot, int c,
       u[4 * i] = q.x, u[4 * i + 1] = q.y, u[4 * i + 2] = q.z, u[4 * i + 3] = q.w;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int j = 0; j < kN; ++j) {
+      float f[8];
 #pragma unroll
-      for (int j = 0; j < kN; ++j) {
+      for (int i = 0; i < 8; ++i) {
         const int e = i * kN + j;
-        last[j][i] = kF32 ? __uint_as_float(u[e])
-                          : __uint_as_float(e & 1 ? u[e / 2] & 0xFFFF0000u : u[e / 2] << 16);
+        f[i] = kF32 ? __uint_as_float(u[e])
+                    : __uint_as_float(e & 1 ? u[e / 2] & 0xFFFF0000u : u[e / 2] << 16);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) last[j][i] = pair(f[2 * i], f[2 * i + 1]);
+    }
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int j = 0; j < kN; ++j) {
+    float f[8];
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
+    for (int i = 0; i < 8; ++i) {
       const int64_t e = at + static_cast<int64_t>(i) * p.width + j;
-      last[j][i] = kF32 ? static_cast<const float *>(p.window)[e]
-                        : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.window)[e]);
+      f[i] = kF32 ? static_cast<const float *>(p.window)[e]
+                  : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.window)[e]);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) last[j][i] = pair(f[2 * i], f[2 * i + 1]);
+  }
 }
 template <int kTaps, bool kF32>
 __device__ __forceinline__ void write_window(const Params &p, int slot, int c,
-                                             const float (&last)[kTaps - 1][8]) {
+                                             const f32x2 (&pairs)[kTaps - 1][4]) {
   constexpr int kN = kTaps - 1, kWords = kF32 ? 8 * kN : 4 * kN;
+  float last[kN][8];
+#pragma unroll
+  for (int j = 0; j < kN; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpair(pairs[j][i], last[j][2 * i], last[j][2 * i + 1]);
   const int64_t at = (static_cast<int64_t>(slot) * p.channels + c) * p.width;
   if (p.width == kN) {
     uint32_t u[kWords];
@@ -173,22 +177,25 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const __grid_constant_
   if (piece > 0) {
 #pragma unroll
     for (int j = 0; j < kN; ++j)
-      unpack8(__ldg(reinterpret_cast<const uint4 *>(x + (begin - kN + j) * p.x_stride)), ch.last[j]);
+      pairs8(__ldg(reinterpret_cast<const uint4 *>(x + (begin - kN + j) * p.x_stride)), ch.last[j]);
   } else {
     if (seq.src)
       read_window<kTaps, kF32>(p, seq.src, c, ch.last);
     else
-      ch.clear();
+#pragma unroll
+      for (int j = 0; j < kN; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ch.last[j][i] = 0;
     if (seq.dst) {
-      float next[kN][8];
+      f32x2 next[kN][4];
 #pragma unroll
       for (int j = 0; j < kN; ++j) {
         const int at = seq.len - kN + j;             // of the sequence, or before it
         if (at >= 0) {
-          unpack8(__ldg(reinterpret_cast<const uint4 *>(x + at * p.x_stride)), next[j]);
+          pairs8(__ldg(reinterpret_cast<const uint4 *>(x + at * p.x_stride)), next[j]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 4; ++i) {
             next[j][i] = ch.last[j][i];              // len 0; else `len` further
             if (j + 1 < kN && seq.len == 1) next[j][i] = ch.last[(j + 1) % kN][i];
             if (j + 2 < kN && seq.len == 2) next[j][i] = ch.last[(j + 2) % kN][i];
@@ -201,16 +208,23 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const __grid_constant_
   ch.load_weights(p, c);
   x += begin * p.x_stride;
   __nv_bfloat16 *out = p.output + (seq.start + begin) * p.o_stride + c;
-  for (int t = 0; t < rows; t += kBatch) {
-    uint4 raw[kBatch];
+  // the next rows come while these are worked on
+  uint4 raw[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (t + i < rows) raw[i] = __ldg(reinterpret_cast<const uint4 *>(x + i * p.x_stride));
+  for (int i = 0; i < kBatch; ++i)
+    if (i < rows) raw[i] = __ldg(reinterpret_cast<const uint4 *>(x + i * p.x_stride));
+  for (int t = 0; t < rows; t += kBatch) {
+    uint4 now[kBatch];
+    x += kBatch * p.x_stride;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      now[i] = raw[i];
+      if (t + kBatch + i < rows) raw[i] = __ldg(reinterpret_cast<const uint4 *>(x + i * p.x_stride));
+    }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
       if (t + i < rows)
-        *reinterpret_cast<uint4 *>(out + i * p.o_stride) = ch.token(raw[i], p.silu);
-    x += kBatch * p.x_stride;
+        *reinterpret_cast<uint4 *>(out + i * p.o_stride) = ch.token(now[i], p.silu);
     out += kBatch * p.o_stride;
   }
 }

@@ -31,6 +31,25 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// The same in pairs, for operations on two.
+__device__ __forceinline__ f32x2 two(float v) { return pair(v, v); }
+__device__ __forceinline__ f32x2 unpack2(uint32_t u) {
+  return pair(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+__device__ __forceinline__ void pairs8(const uint4 &u, f32x2 (&f)[4]) {
+  f[0] = unpack2(u.x), f[1] = unpack2(u.y), f[2] = unpack2(u.z), f[3] = unpack2(u.w);
+}
+
+// silu() of two values.  The bits of silu_approx, whose division is this product for
+// all arguments from -87 on (all of FP32's compared); below, where both are under 2^-118,
+// 0 for some of what it leaves.
+__device__ __forceinline__ f32x2 silu2(f32x2 z) {
+  float lo, hi;
+  unpair(mul2(z, two(-kLog2e)), lo, hi);
+  unpair(add2(pair(exp2_approx(lo), exp2_approx(hi)), two(1.0f)), lo, hi);
+  return mul2(z, pair(rcp_approx(lo), rcp_approx(hi)));
+}
+
 // exp(x) for x <= 0, off by the approximate exp2 alone: the argument's rounding
 // goes in as a factor.
 __device__ __forceinline__ float exp_of(float x) {

@@ -16,8 +16,9 @@ constexpr int kThreads = 128;
 constexpr int kRequests = 4;     // of a thread: they share its part of a
 
 // A thread: 4 states of a channel, of kRequests requests, all loads in flight at
-// once.  Groups of channels are multiples of 8, so a warp's channels are of one
-// group, and all there or none.
+// once.  What is the same for all states of a channel (the step, the gate, the output) is
+// one lane's for each request.  Groups of channels are multiples of 8, so a warp's
+// channels are of one group, and all there or none.
 template <int kStates>
 __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ Params p,
                                                         int blocks) {
@@ -26,52 +27,75 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
   const int channel = (block * kThreads + threadIdx.x) / kLanes, quad = threadIdx.x % kLanes;
   if (channel >= p.channels) return;
   int slot[kRequests];
+#pragma unroll
+  for (int i = 0; i < kRequests; ++i) slot[i] = first + i < p.batch ? __ldg(p.slots + first + i) : 0;
+  // this lane's request
+  const int mine = quad % kRequests, row = min(first + mine, p.batch - 1);
+  const __nv_bfloat16 x_in = p.x[row * p.x_stride + channel];
+  const __nv_bfloat16 dt_in = p.dt[row * p.dt_stride + channel];
+  const __nv_bfloat16 z_in = p.z ? p.z[row * p.z_stride + channel] : __nv_bfloat16();
+  const int states = channel / p.span * kStates + 4 * quad;
+  uint2 b_in[kRequests], c_in[kRequests];
+#pragma unroll
+  for (int i = 0; i < kRequests; ++i) {
+    const int64_t r = min(first + i, p.batch - 1);
+    b_in[i] = __ldg(reinterpret_cast<const uint2 *>(p.b + r * p.b_stride + states));
+    c_in[i] = __ldg(reinterpret_cast<const uint2 *>(p.c + r * p.c_stride + states));
+  }
+  float4 a = __ldg(reinterpret_cast<const float4 *>(p.a + static_cast<int64_t>(channel) * kStates) + quad);
+  const float skip = p.d ? __ldg(p.d + channel) : 0.0f;
+  const float bias = p.dt_bias ? __ldg(p.dt_bias + channel) : 0.0f;
   float4 h[kRequests];
 #pragma unroll
   for (int i = 0; i < kRequests; ++i) {
-    slot[i] = first + i < p.batch ? __ldg(p.slots + first + i) : 0;
     if (slot[i] >= p.seqs.num_slots) {
       if (p.err && block == 0 && threadIdx.x == 0) atomicOr(p.err, KDA_DEVERR_SLOT);
       slot[i] = 0;
     }
+    h[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (slot[i] > 0)
       h[i] = __ldcs(reinterpret_cast<const float4 *>(state_of(p, slot[i], channel, kStates)) + quad);
   }
-  float4 a = __ldg(reinterpret_cast<const float4 *>(p.a + static_cast<int64_t>(channel) * kStates) + quad);
   a.x *= kLog2e, a.y *= kLog2e, a.z *= kLog2e, a.w *= kLog2e;
-  const float d = p.d ? __ldg(p.d + channel) : 0.0f;
-  const float bias = p.dt_bias ? __ldg(p.dt_bias + channel) : 0.0f;
-  const int states = channel / p.span * kStates + 4 * quad;
+  const float x = __bfloat162float(x_in);
+  float s = __bfloat162float(dt_in) + bias;
+  if (p.softplus) s = softplus(s);
+  const float sx = s * x;
+  float y[kRequests];
 #pragma unroll
   for (int i = 0; i < kRequests; ++i) {
-    const int64_t row = first + i;
-    if (row >= p.batch) continue;
-    __nv_bfloat16 *out = p.output + row * p.o_stride + channel;
-    if (slot[i] <= 0) {
-      if (quad == 0) *out = __float2bfloat16_rn(0.0f);
-      continue;
-    }
-    const float x = __bfloat162float(p.x[row * p.x_stride + channel]);
-    float s = __bfloat162float(p.dt[row * p.dt_stride + channel]) + bias;
-    if (p.softplus) s = softplus(s);
+    const float si = __shfl_sync(0xffffffffu, s, i, kRequests);
+    const float sxi = __shfl_sync(0xffffffffu, sx, i, kRequests);
     float bn[4], cn[4];
-    unpack4(__ldg(reinterpret_cast<const uint2 *>(p.b + row * p.b_stride + states)), bn);
-    unpack4(__ldg(reinterpret_cast<const uint2 *>(p.c + row * p.c_stride + states)), cn);
-    const float sx = s * x;
-    h[i].x = decayed(h[i].x, decay_of(s * a.x), sx * bn[0]);
-    h[i].y = decayed(h[i].y, decay_of(s * a.y), sx * bn[1]);
-    h[i].z = decayed(h[i].z, decay_of(s * a.z), sx * bn[2]);
-    h[i].w = decayed(h[i].w, decay_of(s * a.w), sx * bn[3]);
-    __stcs(reinterpret_cast<float4 *>(state_of(p, slot[i], channel, kStates)) + quad, h[i]);
-    float y = cn[0] * h[i].x + cn[1] * h[i].y + cn[2] * h[i].z + cn[3] * h[i].w;
-#pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (quad == 0) {
-      y = __fmaf_rn(d, x, y);
-      if (p.z) y *= silu_approx(__bfloat162float(p.z[row * p.z_stride + channel]));
-      *out = __float2bfloat16_rn(y);
-    }
+    unpack4(b_in[i], bn);
+    unpack4(c_in[i], cn);
+    h[i].x = decayed(h[i].x, decay_of(si * a.x), sxi * bn[0]);
+    h[i].y = decayed(h[i].y, decay_of(si * a.y), sxi * bn[1]);
+    h[i].z = decayed(h[i].z, decay_of(si * a.z), sxi * bn[2]);
+    h[i].w = decayed(h[i].w, decay_of(si * a.w), sxi * bn[3]);
+    if (slot[i] > 0)
+      __stcs(reinterpret_cast<float4 *>(state_of(p, slot[i], channel, kStates)) + quad, h[i]);
+    y[i] = __fmaf_rn(cn[3], h[i].w, __fmaf_rn(cn[2], h[i].z, __fmaf_rn(cn[1], h[i].y, cn[0] * h[i].x)));
   }
+#pragma unroll
+  for (int o = kLanes / 2; o >= kRequests; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < kRequests; ++i) y[i] += __shfl_xor_sync(0xffffffffu, y[i], o);
+  // request `mine`'s sum over four lanes
+  const bool high = quad & 2, odd = quad & 1;
+  float keep[2] = {high ? y[2] : y[0], high ? y[3] : y[1]};
+  const float send[2] = {high ? y[0] : y[2], high ? y[1] : y[3]};
+  keep[0] += __shfl_xor_sync(0xffffffffu, send[0], 2);
+  keep[1] += __shfl_xor_sync(0xffffffffu, send[1], 2);
+  float sum = odd ? keep[1] : keep[0];
+  sum += __shfl_xor_sync(0xffffffffu, odd ? keep[0] : keep[1], 1);
+  sum = __fmaf_rn(skip, x, sum);
+  if (p.z) sum *= silu_approx(__bfloat162float(z_in));
+  int at = slot[0];
+#pragma unroll
+  for (int i = 1; i < kRequests; ++i) at = mine == i ? slot[i] : at;
+  if (quad < kRequests && first + mine < p.batch)
+    p.output[row * p.o_stride + channel] = __float2bfloat16_rn(at > 0 ? sum : 0.0f);
 }
 
 template <int kStates>

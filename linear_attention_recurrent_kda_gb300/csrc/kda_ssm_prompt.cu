@@ -112,10 +112,6 @@ __device__ __forceinline__ f32x2 corrected(f32x2 h, f32x2 h0, f32x2 a, float s, 
   return pair(v[0], v[1]);
 }
 
-__device__ __forceinline__ f32x2 two(float v) { return pair(v, v); }
-__device__ __forceinline__ f32x2 unpack2(uint32_t u) {
-  return pair(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
-}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -147,14 +143,6 @@ __device__ __forceinline__ f32x2 softplus2(f32x2 v) {
   t = fma2(t, u, two(2.0f));
   return fma2(q, t, pair(max_nan(lo, 0.0f), max_nan(hi, 0.0f)));
 }
-// silu() of two values.
-__device__ __forceinline__ f32x2 silu2(f32x2 z) {
-  float lo, hi;
-  unpair(mul2(z, two(-kLog2e)), lo, hi);
-  unpair(add2(pair(exp2_approx(lo), exp2_approx(hi)), two(1.0f)), lo, hi);
-  return mul2(z, pair(rcp_approx(lo), rcp_approx(hi)));
-}
-
 template <int kStates, int kHeld, bool kOut>
 __global__ void __launch_bounds__(kThreads, kHeld == 16 ? 4 : 6) scan_kernel(const __grid_constant__ Params p) {
   using S = Stage<kStates, kHeld>;
