@@ -15,6 +15,22 @@ namespace ssm {
 constexpr int kThreads = 128;
 constexpr int kRequests = 4;     // of a thread: they share its part of a
 
+// h <- 2^x h + add, two states: where the decay is near 1 (down to 2^-1/4) as
+// h + h (2^x - 1) + add, for the reason at decay_of; 2^x - 1 there is x times a
+// polynomial (interpolated at the Chebyshev points, degree 3, off by 2^-24 of itself).
+__device__ __forceinline__ f32x2 decayed2(f32x2 h, f32x2 x, f32x2 add) {
+  f32x2 t = fma2(two(8.977169171e-03f), x, two(5.540518463e-02f));
+  t = fma2(t, x, two(2.402215898e-01f));
+  t = mul2(fma2(t, x, two(6.931471229e-01f)), x);
+  float lo, hi, tl, th;
+  unpair(x, lo, hi);
+  unpair(t, tl, th);
+  const bool sl = fabsf(lo + 0.125f) <= 0.125f, sh = fabsf(hi + 0.125f) <= 0.125f;
+  const f32x2 change = pair(sl ? tl : exp2_approx(lo), sh ? th : exp2_approx(hi));
+  const f32x2 keep = pair(sl ? 1.0f : 0.0f, sh ? 1.0f : 0.0f);
+  return fma2(h, keep, fma2(h, change, add));
+}
+
 // A thread: 4 states of a channel, of kRequests requests, all loads in flight at
 // once.  What is the same for all states of a channel (the step, the gate, the output) is
 // one lane's for each request.  Groups of channels are multiples of 8, so a warp's
@@ -45,18 +61,19 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
   float4 a = __ldg(reinterpret_cast<const float4 *>(p.a + static_cast<int64_t>(channel) * kStates) + quad);
   const float skip = p.d ? __ldg(p.d + channel) : 0.0f;
   const float bias = p.dt_bias ? __ldg(p.dt_bias + channel) : 0.0f;
-  float4 h[kRequests];
+  ulonglong2 h[kRequests];
+  const int64_t page = static_cast<int64_t>(p.channels) * kStates;       // floats of a slot
+  float *const pool = p.state + static_cast<int64_t>(channel) * kStates + 4 * quad;
 #pragma unroll
   for (int i = 0; i < kRequests; ++i) {
     if (slot[i] >= p.seqs.num_slots) {
       if (p.err && block == 0 && threadIdx.x == 0) atomicOr(p.err, KDA_DEVERR_SLOT);
       slot[i] = 0;
     }
-    h[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (slot[i] > 0)
-      h[i] = __ldcs(reinterpret_cast<const float4 *>(state_of(p, slot[i], channel, kStates)) + quad);
+    h[i] = make_ulonglong2(0, 0);
+    if (slot[i] > 0) h[i] = __ldcs(reinterpret_cast<const ulonglong2 *>(pool + slot[i] * page));
   }
-  a.x *= kLog2e, a.y *= kLog2e, a.z *= kLog2e, a.w *= kLog2e;
+  const f32x2 a01 = pair(a.x * kLog2e, a.y * kLog2e), a23 = pair(a.z * kLog2e, a.w * kLog2e);
   const float x = __bfloat162float(x_in);
   float s = __bfloat162float(dt_in) + bias;
   if (p.softplus) s = softplus(s);
@@ -64,18 +81,14 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
   float y[kRequests];
 #pragma unroll
   for (int i = 0; i < kRequests; ++i) {
-    const float si = __shfl_sync(0xffffffffu, s, i, kRequests);
-    const float sxi = __shfl_sync(0xffffffffu, sx, i, kRequests);
-    float bn[4], cn[4];
-    unpack4(b_in[i], bn);
-    unpack4(c_in[i], cn);
-    h[i].x = decayed(h[i].x, decay_of(si * a.x), sxi * bn[0]);
-    h[i].y = decayed(h[i].y, decay_of(si * a.y), sxi * bn[1]);
-    h[i].z = decayed(h[i].z, decay_of(si * a.z), sxi * bn[2]);
-    h[i].w = decayed(h[i].w, decay_of(si * a.w), sxi * bn[3]);
-    if (slot[i] > 0)
-      __stcs(reinterpret_cast<float4 *>(state_of(p, slot[i], channel, kStates)) + quad, h[i]);
-    y[i] = __fmaf_rn(cn[3], h[i].w, __fmaf_rn(cn[2], h[i].z, __fmaf_rn(cn[1], h[i].y, cn[0] * h[i].x)));
+    const f32x2 si = two(__shfl_sync(0xffffffffu, s, i, kRequests));
+    const f32x2 sxi = two(__shfl_sync(0xffffffffu, sx, i, kRequests));
+    h[i].x = decayed2(h[i].x, mul2(si, a01), mul2(sxi, unpack2(b_in[i].x)));
+    h[i].y = decayed2(h[i].y, mul2(si, a23), mul2(sxi, unpack2(b_in[i].y)));
+    if (slot[i] > 0) __stcs(reinterpret_cast<ulonglong2 *>(pool + slot[i] * page), h[i]);
+    float lo, hi;
+    unpair(fma2(unpack2(c_in[i].y), h[i].y, mul2(unpack2(c_in[i].x), h[i].x)), lo, hi);
+    y[i] = lo + hi;
   }
 #pragma unroll
   for (int o = kLanes / 2; o >= kRequests; o >>= 1)
