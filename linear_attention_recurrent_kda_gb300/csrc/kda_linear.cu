@@ -459,6 +459,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
       const int half = q & 1;
       const bool there = at.col < p.outer && at.row < p.rows;
       const int left = p.outer - at.col;           // features of the chunk, where fewer than 64
+      uint4 bias[4];                               // of the next 32 features
+      auto ahead = [&](int z) {
+        if (p.bias && there)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            bias[g] = vector_of(p.bias + at.col + 32 * z + 8 * g, left - 32 * z - 8 * g);
+      };
+      ahead(0);
       bool ok = wait_phase(&c.sums_full[half], (q >> 1) & 1, &c.abort);
       tc_fence_after();
       if (p.residual && there) ok &= wait_phase(residual, loads++ & 1, &c.abort);
@@ -481,11 +489,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             float add[8];
-            unpack8(vector_of(p.bias + at.col + 32 * z + 8 * g, left - 32 * z - 8 * g), add);
+            unpack8(bias[g], add);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               r[8 * g + e] = __float_as_uint(__uint_as_float(r[8 * g + e]) + add[e]);
           }
+          if (z == 0) ahead(1);
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e)
