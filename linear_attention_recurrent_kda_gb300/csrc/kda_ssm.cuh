@@ -40,17 +40,20 @@ struct Params {
 struct Decay {
   float keep, change;
 };
-__device__ __forceinline__ Decay decay_of(float x) {
-  // (2^x - 1) / x on [-1, 0]: interpolated at the Chebyshev points, degree 5, off by
-  // 2^-26 of it
+// 2^x - 1 on [-1, 0]: x times a polynomial, interpolated at the Chebyshev points, degree 5,
+// off by 2^-26 of itself.
+__device__ __forceinline__ float less_one(float x) {
   float t = 1.14919952e-4f;
   t = __fmaf_rn(t, x, 1.29163684e-3f);
   t = __fmaf_rn(t, x, 9.59703512e-3f);
   t = __fmaf_rn(t, x, 5.54992296e-2f);
   t = __fmaf_rn(t, x, 2.40226090e-1f);
   t = __fmaf_rn(t, x, 6.93147182e-1f);
+  return t * x;
+}
+__device__ __forceinline__ Decay decay_of(float x) {
   const bool slow = fabsf(x + 0.5f) <= 0.5f;
-  return Decay{slow ? 1.0f : 0.0f, slow ? t * x : exp2_approx(x)};
+  return Decay{slow ? 1.0f : 0.0f, slow ? less_one(x) : exp2_approx(x)};
 }
 __device__ __forceinline__ float decayed(float h, const Decay &d, float add) {
   return __fmaf_rn(h, d.keep, __fmaf_rn(h, d.change, add));
