@@ -40,7 +40,7 @@
  * Ownership and threading: the caller owns every buffer; every pointer is a
  * DEVICE pointer of the current device.  The library allocates nothing,
  * never synchronises, and enqueues exactly one kernel on `stream` per call
- * (kda_lin_prompt, kda_ssm_prompt: up to three).
+ * (kda_lin_prompt: up to three, kda_ssm_prompt: up to two).
  * Calls are reentrant and may come from several host threads at once (the
  * first call on a device reads its attributes and configures the kernel
  * under a lock); two calls that write the same pool regions must be ordered
@@ -546,7 +546,7 @@ int64_t kda_ssm_prompt_workspace(const kda_ssm_prompt_args *args);
  * (KDA_DEVERR_SEQ) writes nothing; where starts are out of order, the call's other
  * sequences may be incomplete.  Errors: KDA_ERR_NULL_ARGS, KDA_ERR_SHAPE,
  * KDA_ERR_PATH, KDA_ERR_NULL_POINTER, KDA_ERR_ALIGNMENT, KDA_ERR_WORKSPACE,
- * KDA_ERR_DEVICE, KDA_ERR_LAUNCH; nothing is launched on error.  Up to three
+ * KDA_ERR_DEVICE, KDA_ERR_LAUNCH; nothing is launched on error.  Up to two
  * kernels on `stream`, in order. */
 int kda_ssm_prompt(const kda_ssm_prompt_args *args, void *stream);
 

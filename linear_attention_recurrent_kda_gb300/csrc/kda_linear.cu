@@ -34,7 +34,7 @@ constexpr int kHalfRing = 96 * 1024, kRing = 192 * 1024;
 
 struct Params {
   int rows, inner, outer, act;
-  int tile_n, stages, ring, blocks, split;       // blocks: of kK along inner
+  int tile_n, tiles_m, stages, ring, blocks, split;      // blocks: of kK along inner
   int64_t r_stride, o_stride;
   const __nv_bfloat16 *bias, *residual;
   __nv_bfloat16 *output;
@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   Ctrl &c = *reinterpret_cast<Ctrl *>(ring + p.ring);
   const int warp = threadIdx.x >> 5;
-  const int rank = blockIdx.x % p.split, feature0 = blockIdx.x / p.split * kM;
-  const int row0 = blockIdx.y * p.tile_n;
+  const int rank = blockIdx.x % p.split, tile = blockIdx.x / p.split;
+  const int feature0 = tile % p.tiles_m * kM, row0 = tile / p.tiles_m * p.tile_n;
   const int stage_bytes = kATile + p.tile_n * kK * 2;
   const int begin = static_cast<int>(static_cast<int64_t>(p.blocks) * rank / p.split);
   const int end = static_cast<int>(static_cast<int64_t>(p.blocks) * (rank + 1) / p.split);
@@ -681,12 +681,13 @@ static int run(const kda_linear_args *a, cudaStream_t stream) {
   p.tile_n = plan.tile_n;
   p.split = plan.split;
   const int stage = kATile + p.tile_n * kK * 2;
-  const int tiles_m = (a->outer + kM - 1) / kM, tiles_n = (a->rows + p.tile_n - 1) / p.tile_n;
-  const bool few = static_cast<int64_t>(tiles_m) * tiles_n * p.split <= df.sms;
+  p.tiles_m = (a->outer + kM - 1) / kM;
+  const int64_t ctas = static_cast<int64_t>(p.tiles_m) * ((a->rows + p.tile_n - 1) / p.tile_n) * p.split;
+  if (ctas > 0x7fffffffll) return KDA_ERR_SHAPE;
+  const bool few = ctas <= df.sms;
   p.ring = !few && kHalfRing / stage >= 4 ? kHalfRing : kRing;
   p.stages = p.ring / stage;
   if (p.stages > kMostStages) p.stages = kMostStages;
-  if (tiles_n > 65535 || static_cast<int64_t>(tiles_m) * p.split > 0x7fffffffll) return KDA_ERR_SHAPE;
   CUtensorMap w, x;
   if (!rows_map(&w, a->weight, a->inner, a->outer, a->w_stride, kM, dev) ||
       !rows_map(&x, a->x, a->inner, a->rows, a->x_stride, p.tile_n, dev))
@@ -698,7 +699,7 @@ static int run(const kda_linear_args *a, cudaStream_t stream) {
   if (!set_smem_limit_once(done[p.act], dev, reinterpret_cast<const void *>(kernel), smem_of(kRing)))
     return KDA_ERR_LAUNCH;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles_m * p.split, tiles_n);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem_of(p.ring);
   cfg.stream = stream;

@@ -61,37 +61,43 @@ __device__ __forceinline__ void copies_done() {
   asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
 }
 
-// The piece's start: the sequence's first state, and over the pieces before it,
-// h <- exp(a s) h + u with their steps' sums s and contributions u.
-template <int kStates, int kHeld>
-__device__ __forceinline__ void start_of(const Params &p, const Seq &seq, int64_t first, int before,
-                                         int channel, int held, const f32x2 (&a)[kHeld / 2],
-                                         f32x2 (&h)[kHeld / 2]) {
+template <int kHeld>
+__device__ __forceinline__ void read_states(const float *from, f32x2 (&h)[kHeld / 2]) {
 #pragma unroll
-  for (int i = 0; i < kHeld / 2; ++i) h[i] = 0;
-  if (seq.src) {
-    const float4 *from = reinterpret_cast<const float4 *>(state_of(p, seq.src, channel, kStates) + held);
-#pragma unroll
-    for (int i = 0; i < kHeld / 4; ++i) {
-      const float4 v = from[i];
-      h[2 * i] = pair(v.x, v.y);
-      h[2 * i + 1] = pair(v.z, v.w);
-    }
+  for (int i = 0; i < kHeld / 4; ++i) {
+    const float4 v = reinterpret_cast<const float4 *>(from)[i];
+    h[2 * i] = pair(v.x, v.y);
+    h[2 * i + 1] = pair(v.z, v.w);
   }
+}
+template <int kHeld>
+__device__ __forceinline__ void write_states(float *to, const f32x2 (&h)[kHeld / 2]) {
+#pragma unroll
+  for (int i = 0; i < kHeld / 4; ++i) {
+    float4 v;
+    unpair(h[2 * i], v.x, v.y);
+    unpair(h[2 * i + 1], v.z, v.w);
+    reinterpret_cast<float4 *>(to)[i] = v;
+  }
+}
+
+// A piece's start from its sequence's: over the pieces before it, h <- exp(a s) h + u with
+// their steps' sums s and contributions u.
+template <int kStates, int kHeld>
+__device__ __forceinline__ void pass_pieces(const Params &p, int64_t first, int before, int channel,
+                                            int held, const f32x2 (&a)[kHeld / 2],
+                                            f32x2 (&h)[kHeld / 2]) {
   for (int j = 0; j < before; ++j) {
     const float s = p.ws_step[(first + j) * p.channels + channel];
-    const float4 *u = reinterpret_cast<const float4 *>(
-        p.ws_state + ((first + j) * p.channels + channel) * kStates + held);
+    f32x2 u[kHeld / 2];
+    read_states<kHeld>(p.ws_state + ((first + j) * p.channels + channel) * kStates + held, u);
 #pragma unroll
-    for (int i = 0; i < kHeld / 4; ++i) {
-      const float4 v = u[i];
-      float lo, hi, al, ah;
-      unpair(h[2 * i], lo, hi);
-      unpair(a[2 * i], al, ah);
-      h[2 * i] = pair(decayed(lo, decay_of(s * al), v.x), decayed(hi, decay_of(s * ah), v.y));
-      unpair(h[2 * i + 1], lo, hi);
-      unpair(a[2 * i + 1], al, ah);
-      h[2 * i + 1] = pair(decayed(lo, decay_of(s * al), v.z), decayed(hi, decay_of(s * ah), v.w));
+    for (int i = 0; i < kHeld / 2; ++i) {
+      float lo, hi, al, ah, ul, uh;
+      unpair(h[i], lo, hi);
+      unpair(a[i], al, ah);
+      unpair(u[i], ul, uh);
+      h[i] = pair(decayed(lo, decay_of(s * al), ul), decayed(hi, decay_of(s * ah), uh));
     }
   }
 }
@@ -265,11 +271,22 @@ __global__ void __launch_bounds__(kThreads, kHeld == 16 ? 4 : 6) scan_kernel(con
     if (p.d) skip = pair(__ldg(p.d + c), __ldg(p.d + c + 1));
     if (p.dt_bias) bias = pair(__ldg(p.dt_bias + c), __ldg(p.dt_bias + c + 1));
   }
-  if (kOut) {
-    start_of<kStates, kHeld>(p, seq, first, piece, channel, held, a, h);
-  } else {
 #pragma unroll
-    for (int i = 0; i < kHeld / 2; ++i) h[i] = 0;
+  for (int i = 0; i < kHeld / 2; ++i) h[i] = 0;
+  // A split sequence's last piece leaves no contribution: its place holds the first
+  // state for the pass with outputs, whose last piece may write over it in the pool.
+  const int last = p.piece > 0 && seq.len > 0 ? (seq.len - 1) / p.piece : 0;
+  float *const copy = p.ws_state + ((first + last) * p.channels + channel) * kStates + held;
+  if (kOut && last > 0) {
+    if (seq.src) read_states<kHeld>(copy, h);
+    pass_pieces<kStates, kHeld>(p, first, piece, channel, held, a, h);
+  } else if (seq.src && piece == 0) {
+    read_states<kHeld>(state_of(p, seq.src, channel, kStates) + held, h);
+    if (!kOut) {
+      if (live) write_states<kHeld>(copy, h);
+#pragma unroll
+      for (int i = 0; i < kHeld / 2; ++i) h[i] = 0;
+    }
   }
   float sum = 0.0f;                                // steps of two tiles, or of the piece
   f32x2 used[kHeld / 2];
@@ -448,15 +465,7 @@ __global__ void __launch_bounds__(kThreads, kHeld == 16 ? 4 : 6) scan_kernel(con
   } else if (seq.dst && row0 + rows == seq.start + seq.len) {
     to = state_of(p, seq.dst, channel, kStates) + held;
   }
-  if (to) {
-#pragma unroll
-    for (int i = 0; i < kHeld / 4; ++i) {
-      float4 v;
-      unpair(h[2 * i], v.x, v.y);
-      unpair(h[2 * i + 1], v.z, v.w);
-      reinterpret_cast<float4 *>(to)[i] = v;
-    }
-  }
+  if (to) write_states<kHeld>(to, h);
 }
 
 template <int kStates, int kHeld>

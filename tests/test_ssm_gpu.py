@@ -87,6 +87,25 @@ def test_state_in_place(lens, path):
     check(d, state, lens, slots, slots, path=path)
 
 
+def test_many_pieces_in_place():
+    """900 pieces, more than run at a time: a sequence's last piece writes the state that its
+    first ones start from, and all give the bits of separate slots."""
+    B, T, C = 300, 800, 64
+    d, _ = make(B * T, C, seed=13, extra=8)
+    state = torch.randn(2 * B + 1, C, 16, generator=torch.Generator().manual_seed(14)).cuda()
+    starts = torch.arange(0, B * T + 1, T, dtype=I32, device="cuda")
+    at = torch.arange(1, B + 1, dtype=I32, device="cuda")
+    apart, place = state.clone(), state.clone()
+    outs = [torch.empty(B * T, C, dtype=BF, device="cuda") for _ in range(2)]
+    kda_ssm_prompt(**d, seq_starts=starts, output=outs[0], state=apart, src_slots=at, dst_slots=at + B,
+                   path=2, max_seq=T)
+    for _ in range(5):
+        place.copy_(state)
+        kda_ssm_prompt(**d, seq_starts=starts, output=outs[1], state=place, src_slots=at, dst_slots=at,
+                       path=2, max_seq=T)
+        assert torch.equal(outs[0], outs[1]) and torch.equal(place[1:B + 1], apart[B + 1:])
+
+
 @pytest.mark.parametrize("path", [1, 2])
 def test_without_states_and_without_tokens(path):
     d, state = make(300, 16)
