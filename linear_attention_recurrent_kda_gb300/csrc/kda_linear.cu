@@ -1,6 +1,6 @@
 // output = BF16(act(x W^T + bias) + residual), on the 5th-generation tensor cores.
 //
-// Two forms.  Few tiles: a CTA takes 128 features (rows of W) and up to 256 tokens; the
+// Three forms.  One token: no tensor core, below.  Few tiles: a CTA takes 128 features (rows of W) and up to 256 tokens; the
 // product's M is the features and its N the tokens, so that few tokens cost few columns
 // and W is read once.  One warp loads 64-wide tiles of both with TMA through a ring, one
 // issues the products into TMEM.  A cluster of CTAs may share a tile: each sums a range
@@ -277,6 +277,101 @@ __global__ void __launch_bounds__(kThreads, 2)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns)
                  : "memory");
   }
+}
+
+// ------------------------------------------------------------------- one token
+//
+// A matrix times a vector, bound by W's bytes: a warp takes 2 features over a slice of the
+// inner dimension, 8 values a lane and load, 8 loads in flight, in FP32; the token waits
+// in shared memory.  The 8 warps of a CTA are slices of the same features where features
+// are few, joined in shared memory in order.  No barriers, tensor memory or tensor maps
+// have to be set up first: 4096 x 1024 3.8 us in a graph (the clusters above 5.7), 4096 x
+// 16384 22.4 (23.7), 7168 x 7168 18.3 (21.8).  With 2 tokens the same is no faster than
+// they are, with 4 slower (5.2 and 9.2 us, 4096 x 1024: the tokens' values are unpacked
+// for every feature).
+constexpr int kOneThreads = 256, kOneWarps = kOneThreads / 32, kOneMost = 32768;   // values
+
+template <int kAct>
+__global__ void __launch_bounds__(kOneThreads)
+    one_kernel(const __grid_constant__ Params p, const __nv_bfloat16 *x, const __nv_bfloat16 *w,
+               int64_t w_stride) {
+  constexpr int kFeatures = 2, kAhead = 4;
+  extern __shared__ __align__(16) uint8_t raw[];
+  uint4 *token = reinterpret_cast<uint4 *>(raw);
+  __shared__ float part[kOneWarps][kFeatures];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = kOneWarps / p.split;                   // pairs of features of a CTA
+  const int feature0 = (blockIdx.x * per + warp / p.split) * kFeatures, slice = warp % p.split;
+  // vectors of 8 of the slice
+  const int vectors = (p.inner + 7) / 8, begin = vectors * slice / p.split;
+  const int end = feature0 < p.outer ? vectors * (slice + 1) / p.split : 0;
+  const __nv_bfloat16 *row[kFeatures];
+#pragma unroll
+  for (int f = 0; f < kFeatures; ++f) row[f] = w + min(feature0 + f, p.outer - 1) * w_stride;
+  uint4 in[kAhead][kFeatures];
+  auto load = [&](int v0) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int v = v0 + 32 * u, left = v < end ? p.inner - 8 * v : 0;
+#pragma unroll
+      for (int f = 0; f < kFeatures; ++f)
+        in[u][f] = left >= 8 ? __ldcs(reinterpret_cast<const uint4 *>(row[f] + 8 * v))
+                             : vector_of(row[f] + 8 * v, left);
+    }
+  };
+  load(begin + lane);
+  for (int v = threadIdx.x; v < vectors; v += kOneThreads)
+    token[v] = vector_of(x + 8 * v, p.inner - 8 * v);
+  __syncthreads();
+  float sum[kFeatures] = {0.0f, 0.0f};
+  for (int v0 = begin + lane; v0 < end; v0 += 32 * kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (v0 + 32 * u >= end) break;
+      float a[kFeatures][8], b[8];
+      unpack8(token[v0 + 32 * u], b);
+#pragma unroll
+      for (int f = 0; f < kFeatures; ++f) {
+        unpack8(in[u][f], a[f]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[f] = __fmaf_rn(a[f][e], b[e], sum[f]);
+      }
+    }
+    if (v0 + 32 * kAhead < end) load(v0 + 32 * kAhead);
+  }
+#pragma unroll
+  for (int f = 0; f < kFeatures; ++f) sum[f] = warp_sum(sum[f]);
+  if (lane < kFeatures) part[warp][lane] = lane == 0 ? sum[0] : sum[1];
+  __syncthreads();
+  const int pair_of = threadIdx.x / kFeatures, i = threadIdx.x % kFeatures;
+  const int feature = (blockIdx.x * per + pair_of) * kFeatures + i;
+  if (pair_of < per && feature < p.outer) {
+    float y = 0.0f;
+    for (int q = 0; q < p.split; ++q) y += part[pair_of * p.split + q][i];
+    y = activated(y + (p.bias ? __bfloat162float(p.bias[feature]) : 0.0f), kAct);
+    if (p.residual) y += __bfloat162float(p.residual[feature]);
+    p.output[feature] = __float2bfloat16_rn(y);
+  }
+}
+
+typedef void (*OneKernel)(const Params, const __nv_bfloat16 *, const __nv_bfloat16 *, int64_t);
+
+static int launch_one(const kda_linear_args *a, Params &p, int dev, int sms, cudaStream_t stream) {
+  const int64_t pairs = (static_cast<int64_t>(a->outer) + 1) / 2;
+  // slices until every SM has two CTAs, of 256 values at least
+  p.split = 1;
+  while (p.split < kOneWarps && pairs * p.split < 2ll * sms * kOneWarps && a->inner >= 512 * p.split)
+    p.split *= 2;
+  static const OneKernel kernels[4] = {one_kernel<KDA_ACT_NONE>, one_kernel<KDA_ACT_SILU>,
+                                       one_kernel<KDA_ACT_GELU>, one_kernel<KDA_ACT_SOFTPLUS>};
+  static std::atomic<bool> done[4][kMaxDevices];
+  const OneKernel kernel = kernels[p.act];
+  if (!set_smem_limit_once(done[p.act], dev, reinterpret_cast<const void *>(kernel), 2 * kOneMost))
+    return KDA_ERR_LAUNCH;
+  const int64_t grid = (pairs * p.split + kOneWarps - 1) / kOneWarps;
+  kernel<<<static_cast<unsigned>(grid), kOneThreads, (a->inner + 7) / 8 * 16, stream>>>(
+      p, static_cast<const __nv_bfloat16 *>(a->x), static_cast<const __nv_bfloat16 *>(a->weight), a->w_stride);
+  return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
 }
 
 // ------------------------------------------------------------------ many tokens
@@ -673,6 +768,7 @@ static int run(const kda_linear_args *a, cudaStream_t stream) {
   p.residual = static_cast<const __nv_bfloat16 *>(a->residual);
   p.output = static_cast<__nv_bfloat16 *>(a->output);
   p.err = a->err;
+  if (a->rows == 1 && a->inner <= kOneMost) return launch_one(a, p, dev, df.sms, stream);
   p.blocks = (a->inner + kK - 1) / kK;
   const Plan plan = plan_of(a->rows, p.blocks, a->inner, a->outer, df.sms);
   if (getenv("LP")) printf("plan %d %d\n", plan.tile_n, plan.split);

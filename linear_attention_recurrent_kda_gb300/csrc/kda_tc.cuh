@@ -29,9 +29,9 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
 // share the instruction cache, and their code is what fills it).  Each try may
 // sleep for a microsecond.  After kWaitLimitNs of wall clock the wait gives up,
 // raises `abort` and returns false.  It does not look at `abort` itself, which cost
-// 2-5% of the time in the 30 waits of a chunk (210 us instead of 198 with 16 prompts
-// x 64 heads): a role that waits for one that left runs out by itself, so the kernel
-// ends after 2 s a role, 14 s, at the latest.  The clock's low word is enough: tries
+// 2-5% of the time in the 30 waits of a chunk of the chunked linear attention (210 us
+// instead of 198 with 16 prompts x 64 heads): a role that waits for one that left runs
+// out by itself, so the kernel ends after 2 s a role, 14 s there, at the latest.  The clock's low word is enough: tries
 // are microseconds apart and the limit is under half of what it holds.  Lanes may get
 // different answers, so the branches are not uniform ones.
 static_assert(kWaitLimitNs < (1ull << 31), "the clock's low word");

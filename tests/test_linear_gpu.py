@@ -25,7 +25,7 @@ def whole(g, *shape, top):
     return torch.randint(-top, top + 1, shape, generator=g).float()
 
 
-SIZES = [(1, 1, 1), (1, 8, 8), (3, 7, 5), (16, 64, 128), (17, 65, 129), (31, 4096, 1024), (33, 72, 257),
+SIZES = [(1, 1, 1), (1, 8, 8), (1, 4097, 1001), (1, 7168, 64), (1, 300, 9001), (1, 33000, 70), (3, 7, 5), (16, 64, 128), (17, 65, 129), (31, 4096, 1024), (33, 72, 257),
          (64, 1000, 640), (61, 4096, 2049), (128, 128, 128), (129, 200, 300), (255, 96, 1000),
          (256, 512, 256), (257, 520, 511), (300, 1, 40), (513, 2048, 1111), (1024, 256, 4096),
          (4099, 64, 136), (700, 4096, 770), (2, 16384, 16), (5, 40, 20000)]
@@ -48,7 +48,7 @@ def test_whole_numbers_are_exact(M, K, N):
 
 
 @pytest.mark.parametrize("act", [None, "silu", "gelu", "softplus"])
-@pytest.mark.parametrize("M,K,N", [(4, 4096, 129), (61, 321, 640), (300, 256, 1001), (1025, 520, 264)])
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 1025), (4, 4096, 129), (61, 321, 640), (300, 256, 1001), (1025, 520, 264)])
 def test_epilogue_within_its_bound(M, K, N, act):
     g = torch.Generator().manual_seed(M + K)
     x, w = torch.randn(M, K, generator=g), torch.randn(N, K, generator=g) * K ** -0.5
@@ -84,7 +84,7 @@ def test_activations_over_their_range(act):
     assert got[1] == v[-2] and got[2] == 0
 
 
-@pytest.mark.parametrize("M", [7, 600])
+@pytest.mark.parametrize("M", [1, 7, 600])
 def test_residual_in_place(M):
     g = torch.Generator().manual_seed(9)
     x, w, res = whole(g, M, 256, top=3), whole(g, 264, 256, top=3), whole(g, M, 264, top=50)
@@ -111,7 +111,7 @@ def test_infinities_and_nan_reach_their_own_sums(M, N):
 def test_views_reach_no_further_than_themselves():
     """NaN all around the operands: rows before and behind, columns beside."""
     g = torch.Generator().manual_seed(12)
-    for M, K, N in ((5, 24, 40), (270, 136, 200)):
+    for M, K, N in ((1, 24, 40), (5, 24, 40), (270, 136, 200)):
         big = torch.full((M + 9, K + 48), float("nan"), dtype=BF, device="cuda")
         bigw = torch.full((N + 9, K + 48), float("nan"), dtype=BF, device="cuda")
         x, w = big[3:3 + M, 8:8 + K], bigw[4:4 + N, 16:16 + K]
