@@ -10,7 +10,6 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 #include <type_traits>
-#include <stdio.h>
 
 #include "../../include/kda.h"
 #include "kda_device.cuh"
@@ -771,7 +770,6 @@ static int run(const kda_linear_args *a, cudaStream_t stream) {
   if (a->rows == 1 && a->inner <= kOneMost) return launch_one(a, p, dev, df.sms, stream);
   p.blocks = (a->inner + kK - 1) / kK;
   const Plan plan = plan_of(a->rows, p.blocks, a->inner, a->outer, df.sms);
-  if (getenv("LP")) printf("plan %d %d\n", plan.tile_n, plan.split);
 
   if (plan.tile_n == 0) return launch_tiles(a, p, dev, df.sms, stream);
   p.tile_n = plan.tile_n;
