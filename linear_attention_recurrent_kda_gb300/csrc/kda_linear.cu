@@ -699,39 +699,41 @@ static int launch_tiles(const kda_linear_args *a, const Params &p, int dev, int 
 
 typedef void (*ProductKernel)(const Params, const CUtensorMap, const CUtensorMap);
 
-// Which form and layout: the cheapest by a model of the time in us, fitted to 30 shapes
-// with up to 20 layouts each (the layout it takes is within 15% of the best measured, most
-// within 5%).  Few tiles: a CTA streams a block of the inner dimension in its products'
-// time or at 160 KB a us, W comes at 6.5 MB a us at most, a CTA starts and ends in 1 + 0.009
-// a token (half of it hidden where two share an SM), and a join costs by its ranks and
-// tokens.  Pairs: 0.305 a block, 2.3 a tile at least.  tile_n 0: pairs.
+// Which form and layout: the cheapest by a model of the time in us, fitted to 26 shapes
+// with up to 19 layouts each (what it takes is within 2% of the best of them).  Few
+// tiles: a CTA streams a block of the inner dimension at 152 KB a us or in its products'
+// time, W comes at 6.2 MB a us at most (a little less for every time it is read again), a
+// CTA starts and ends in 2 + 0.0164 a token (a third of it hidden where two share an SM),
+// and a join costs by its ranks and tokens (clusters of 3, 5, 6 and 7 leave SMs idle: 300 x
+// 8192 x 640 18.1 us with one, 11.8 with 4).  Pairs: 0.32 a block, 2 a tile at least.
+// tile_n 0: pairs.
 struct Plan {
   int tile_n, split;
 };
 static Plan plan_of(int rows, int blocks, int inner, int outer, int sms) {
   const int64_t tiles_m = (outer + kM - 1) / kM;
-  const double weights = 2.0 * inner * outer / 6.5e6;
+  const double weights = 2.0 * inner * outer / 6.2e6;
   Plan best = {0, 1};
   double least = 1e300;
   if (outer >= 8 && rows > 64) {
     const int64_t tiles = static_cast<int64_t>((rows + kTileRows - 1) / kTileRows) *
                           ((outer + kTileCols - 1) / kTileCols);
-    const double tile = blocks * 0.305 > 2.3 ? blocks * 0.305 : 2.3;
-    least = static_cast<double>((tiles + sms / 2 - 1) / (sms / 2)) * tile + 6.0;
+    const double tile = blocks * 0.32 > 2.0 ? blocks * 0.32 : 2.0;
+    least = static_cast<double>((tiles + sms / 2 - 1) / (sms / 2)) * tile + 5.85;
   }
   for (int tile_n = 16; tile_n <= kMostN; tile_n += tile_n < 64 ? 16 : 32) {
     if (tile_n - 32 >= rows) break;
     const int64_t tiles = tiles_m * ((rows + tile_n - 1) / tile_n);
-    const double bytes = (kATile + tile_n * kK * 2) / 160e3;
-    const double block = bytes > 0.0011 * tile_n ? bytes : 0.0011 * tile_n;
-    for (int split = 1; split <= 8 && split <= blocks; ++split) {
+    const double bytes = (kATile + tile_n * kK * 2) / 152e3;
+    const double block = bytes > 0.00154 * tile_n ? bytes : 0.00154 * tile_n;
+    for (int split = 1; split <= 8 && split <= blocks; split *= 2) {
       const int64_t ctas = tiles * split, waves = (ctas + sms - 1) / sms;
-      const double ends = (1.0 + 0.009 * tile_n) * (ctas > sms && tile_n <= 64 ? 0.5 : 1.0);
+      const double ends = (2.0 + 0.0164 * tile_n) * (ctas > sms && tile_n <= 64 ? 0.64 : 1.0);
       double stream = static_cast<double>(waves) * ((blocks + split - 1) / split) * block;
-      const double read = weights * (1.0 + 0.15 * ((rows - 1) / tile_n));
+      const double read = weights * (1.0 + 0.12 * ((rows - 1) / tile_n));
       if (stream < read) stream = read;
-      const double join = split > 1 ? 0.2 + (split - 1) * (0.02 + 0.006 * tile_n) : 0.0;
-      const double cost = stream + static_cast<double>(waves) * (ends + join) + 3.2;
+      const double join = split > 1 ? 0.93 + (split - 1) * 0.0042 * tile_n : 0.0;
+      const double cost = stream + static_cast<double>(waves) * (ends + join) + 1.5;
       if (cost < least) {
         least = cost;
         best = {tile_n, split};
