@@ -423,13 +423,14 @@ int kda_snapshot_load(const kda_snapshot_args *args, void *stream);
  *     output = BF16(silu(y)) or BF16(y),
  * summed in FP32 from the bias on, oldest input first, with the KDA step's
  * arithmetic: on a KDA layer's q, k and v (parts 3, taps 4, conv_state as the
- * window) a prompt leaves the bits that decoding it token by token would.
+ * window) a prompt leaves the bits that decoding it token by token would (but
+ * values below 2^-118 may be zeros).
  * A window pool [num_slots, channels, width] keeps a slot's last inputs, oldest
  * first, in columns 0 .. taps - 2; other columns are left alone.  Rows of x and
  * output are BF16 [channels] and may be slices of wider rows: strides are
  * multiples of 8 elements and at least the row's width.  x, output, weight, bias and
  * window are 16-byte aligned, the index arrays 4.  The output must not overlap
- * the inputs. */
+ * the inputs.  (Rows of this call and of those below: up to 2^31 - 256.) */
 
 /* Arguments of one prompt call (kda_conv_prompt). */
 typedef struct kda_conv_prompt_args {
@@ -500,7 +501,8 @@ int kda_conv_step(const kda_conv_step_args *args, void *stream);
  * no gate).  Rows of x, dt, b, c, z and output are BF16 and may be slices of wider
  * rows: strides are multiples of 8 elements and at least the row's own width.  They,
  * a and state are 16-byte aligned, the other arrays 4.  The output must not overlap
- * the inputs. */
+ * the inputs.  a is finite; where it grows (s a > 0), it has to stay below 2^64 over a
+ * sequence. */
 
 /* Arguments of one prompt call (kda_ssm_prompt). */
 typedef struct kda_ssm_prompt_args {

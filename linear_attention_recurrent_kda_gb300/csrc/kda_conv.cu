@@ -255,7 +255,7 @@ template <class Args>
 static int check(const Args *a, int64_t rows) {
   if (a->channels < 0 || a->parts < 1 || a->channels % (8 * int64_t(a->parts)) != 0)
     return KDA_ERR_SHAPE;
-  if (a->taps < 2 || a->taps > 4 || rows < 0) return KDA_ERR_SHAPE;
+  if (a->taps < 2 || a->taps > 4 || rows < 0 || rows > kMostRows) return KDA_ERR_SHAPE;
   if (!stride_ok(a->x_stride, a->channels) || !stride_ok(a->o_stride, a->channels))
     return KDA_ERR_SHAPE;
   return KDA_SUCCESS;

@@ -1,8 +1,8 @@
 // output = BF16(act(x W^T + bias) + residual), on the 5th-generation tensor cores.
 //
-// Three forms.  One token: no tensor core, below.  Few tiles: a CTA takes 128 features (rows of W) and up to 256 tokens; the
-// product's M is the features and its N the tokens, so that few tokens cost few columns
-// and W is read once.  One warp loads 64-wide tiles of both with TMA through a ring, one
+// Three forms.  One token: no tensor core, below.  Few tiles: a CTA takes 128 features
+// (rows of W) and up to 256 tokens; the product's M is the features and its N the
+// tokens, so that few tokens cost few columns.  One warp loads 64-wide tiles of both with TMA through a ring, one
 // issues the products into TMEM.  A cluster of CTAs may share a tile: each sums a range
 // of the inner dimension, and the sums are joined through distributed shared memory,
 // 8 features a thread, in the order of the ranges.  Many tiles: below.
@@ -745,7 +745,9 @@ static Plan plan_of(int rows, int blocks, int inner, int outer, int sms) {
 
 static int run(const kda_linear_args *a, cudaStream_t stream) {
   if (!a) return KDA_ERR_NULL_ARGS;
-  if (a->rows < 0 || a->inner < 1 || a->outer < 0) return KDA_ERR_SHAPE;
+  if (a->rows < 0 || a->inner < 1 || a->outer < 0 || a->rows > kMostRows || a->inner > kMostRows ||
+      a->outer > kMostRows)
+    return KDA_ERR_SHAPE;
   if (!stride_ok(a->x_stride, a->inner) || !stride_ok(a->w_stride, a->inner) ||
       !stride_ok(a->o_stride, a->outer) || (a->residual && !stride_ok(a->r_stride, a->outer)))
     return KDA_ERR_SHAPE;

@@ -121,6 +121,9 @@ __device__ __forceinline__ int seq_of(const Seqs &p, int64_t n, int piece) {
 
 inline int64_t pieces_of(int64_t tokens, int64_t seqs, int piece) { return tokens / piece + seqs; }
 
+// Sizes that leave room to be rounded up to tiles in 32 bits.
+constexpr int64_t kMostRows = 0x7fffff00ll;
+
 inline bool aligned(const void *q, uintptr_t to) {
   return (reinterpret_cast<uintptr_t>(q) & (to - 1)) == 0;
 }

@@ -80,13 +80,13 @@ SCAN = [(dict(channels=-16), S), (dict(groups=0), S), (dict(groups=5), S), (dict
         (dict(dt_bias=FAKE + 1), A), (dict(output=FAKE + 2), A), (dict(channels=0), 0)]
 CALLS = [("kda_conv_prompt", conv_prompt, CONV + [
             (dict(seqs=-1), S), (dict(tokens=-1), S), (dict(num_slots=0), S), (dict(seq_starts=None), P),
-            (dict(src_slots=FAKE + 2), A), (dict(dst_slots=FAKE + 2), A), (dict(seq_starts=FAKE + 1), A),
+            (dict(tokens=2 ** 31 - 255), S), (dict(src_slots=FAKE + 2), A), (dict(dst_slots=FAKE + 2), A), (dict(seq_starts=FAKE + 1), A),
             (dict(seqs=0), 0)]),
          ("kda_conv_step", conv_step, CONV + [
             (dict(batch=-1), S), (dict(num_slots=0), S), (dict(slots=None), P), (dict(slots=FAKE + 2), A),
             (dict(batch=0), 0)]),
          ("kda_ssm_prompt", ssm_prompt, SCAN + [
-            (dict(seqs=-1), S), (dict(tokens=-1), S), (dict(max_seq=-1), S), (dict(num_slots=0), S),
+            (dict(seqs=-1), S), (dict(tokens=-1), S), (dict(tokens=2 ** 31 - 1), S), (dict(max_seq=-1), S), (dict(num_slots=0), S),
             (dict(path=3), kl.KDA_ERR_PATH), (dict(path=-1), kl.KDA_ERR_PATH),
             (dict(seq_starts=None), P), (dict(seq_starts=FAKE + 2), A), (dict(src_slots=FAKE + 1), A),
             (dict(dst_slots=FAKE + 2), A), (dict(seqs=0), 0)]),
@@ -94,7 +94,8 @@ CALLS = [("kda_conv_prompt", conv_prompt, CONV + [
             (dict(batch=-1), S), (dict(num_slots=0), S), (dict(slots=None), P), (dict(slots=FAKE + 2), A),
             (dict(batch=0), 0)]),
          ("kda_linear", linear, [
-            (dict(rows=-1), S), (dict(inner=0), S), (dict(outer=-1), S), (dict(x_stride=64), S),
+            (dict(rows=-1), S), (dict(inner=0), S), (dict(outer=-1), S), (dict(rows=2 ** 31 - 1), S),
+            (dict(outer=2 ** 31 - 200, r_stride=1 << 32, o_stride=1 << 32), S), (dict(x_stride=64), S),
             (dict(w_stride=73), S), (dict(r_stride=32), S), (dict(o_stride=36), S),
             (dict(activation=-1), kl.KDA_ERR_ACTIVATION), (dict(activation=4), kl.KDA_ERR_ACTIVATION),
             (dict(x=None), P), (dict(weight=None), P), (dict(output=None), P), (dict(x=FAKE + 8), A),
