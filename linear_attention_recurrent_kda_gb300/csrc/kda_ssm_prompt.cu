@@ -22,6 +22,21 @@
 // end backwards (every exponent is a sum of steps, so nothing drifts there), and its
 // steps; scan_kernel<.., true> runs the pieces side by side, each from the state that
 // it sums up itself from the pieces before.
+//
+// What bounds it (GB300): the schedulers' slots.  With 16 warps an SM a token of 32
+// channels x 16 states takes a warp 190 cycles of its scheduler: 75 for the products and
+// sums of decays, states and outputs, 20 for the corrections' products, 12 for b and c, 6
+// more for exp2 (64 of another unit, beside them), 14 for the tile's loads, 30 for the
+// steps, 16 for the outputs, 7 for the corrections (each measured by leaving it out of a
+// copy).  One CTA alone on an SM: 320 cycles a token with 16 states a thread, 220 with 8.
+// 8 ragged sequences (9159 tokens x 4096 channels) 316 us, bound by the longest of 2047
+// tokens; 32749 tokens x 4096 1079 us in 19 pieces, 390 of them in the first pass; its
+// bytes would take 45 and 158.  What made it fast: 16 states a thread instead of 4 (1959
+// -> 488 us, the long one 38 -> 1.5 ms), steps and outputs once per token in pairs of
+// channels and without branches (488 -> 353), contributions summed backwards (1400 ->
+// 1098).  Not kept: scalar operations for pairs (1174 us), exponents not ahead (1107), 2 or
+// 8 tokens a walk (1124, 1127), tiles of 8 or 32 tokens (1136, 1217), 5 CTAs an SM in
+// fewer registers (1240), 256 threads (1088, and 148 us instead of 117 for 1024 tokens).
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
