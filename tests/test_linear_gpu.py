@@ -25,7 +25,7 @@ def whole(g, *shape, top):
     return torch.randint(-top, top + 1, shape, generator=g).float()
 
 
-SIZES = [(1, 1, 1), (1, 8, 8), (1, 4097, 1001), (1, 7168, 64), (1, 300, 9001), (1, 33000, 70), (3, 7, 5), (16, 64, 128), (17, 65, 129), (31, 4096, 1024), (33, 72, 257),
+SIZES = [(1, 1, 1), (1, 8, 8), (1, 4097, 1001), (1, 7168, 64), (1, 300, 9001), (1, 33000, 70), (3, 7, 5), (2, 40, 33), (8, 4100, 1000), (5, 24, 17), (8, 31, 16), (7, 20000, 100), (6, 64, 40000), (16, 64, 128), (17, 65, 129), (31, 4096, 1024), (33, 72, 257),
          (64, 1000, 640), (61, 4096, 2049), (128, 128, 128), (129, 200, 300), (255, 96, 1000),
          (256, 512, 256), (257, 520, 511), (300, 1, 40), (513, 2048, 1111), (1024, 256, 4096),
          (4099, 64, 136), (700, 4096, 770), (2, 16384, 16), (5, 40, 20000)]
@@ -48,7 +48,7 @@ def test_whole_numbers_are_exact(M, K, N):
 
 
 @pytest.mark.parametrize("act", [None, "silu", "gelu", "softplus"])
-@pytest.mark.parametrize("M,K,N", [(1, 4096, 1025), (4, 4096, 129), (61, 321, 640), (300, 256, 1001), (1025, 520, 264)])
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 1025), (4, 4096, 129), (8, 1000, 77), (61, 321, 640), (300, 256, 1001), (1025, 520, 264)])
 def test_epilogue_within_its_bound(M, K, N, act):
     g = torch.Generator().manual_seed(M + K)
     x, w = torch.randn(M, K, generator=g), torch.randn(N, K, generator=g) * K ** -0.5
@@ -84,7 +84,7 @@ def test_activations_over_their_range(act):
     assert got[1] == v[-2] and got[2] == 0
 
 
-@pytest.mark.parametrize("M", [1, 7, 600])
+@pytest.mark.parametrize("M", [1, 3, 7, 600])
 def test_residual_in_place(M):
     g = torch.Generator().manual_seed(9)
     x, w, res = whole(g, M, 256, top=3), whole(g, 264, 256, top=3), whole(g, M, 264, top=50)
