@@ -165,6 +165,7 @@ __device__ __forceinline__ void write_window(const Params &p, int slot, int c,
 template <int kTaps, bool kF32>
 __global__ void __launch_bounds__(kThreads) prompt_kernel(const __grid_constant__ Params p) {
   constexpr int kN = kTaps - 1;
+  follow();
   const int64_t index = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const int64_t n = index / p.vectors;
   if (n >= p.pieces) return;
@@ -238,6 +239,7 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const __grid_constant_
 // A thread: 8 channels of a request.
 template <int kTaps, bool kF32>
 __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ Params p) {
+  follow();
   const int64_t index = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const int64_t r = index / p.vectors;
   if (r >= p.batch) return;
@@ -309,8 +311,7 @@ static int launch(Kernel kernel, const Params &p, int64_t threads, cudaStream_t 
   int dev = 0;
   DeviceFacts df;
   if (!current_device(&dev, &df)) return KDA_ERR_DEVICE;
-  kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
+  return launch_following(kernel, blocks, kThreads, 0, 0, stream, p) ? KDA_SUCCESS : KDA_ERR_LAUNCH;
 }
 
 static int run_prompt(const kda_conv_prompt_args *a, cudaStream_t stream) {

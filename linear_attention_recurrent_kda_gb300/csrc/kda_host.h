@@ -5,6 +5,7 @@
 // std::call_once; later calls only read).
 #pragma once
 #include <cuda_runtime.h>
+#include <stdint.h>
 
 #include <atomic>
 #include <mutex>
@@ -65,6 +66,28 @@ inline bool set_smem_limit_once(std::atomic<bool> (&done)[kMaxDevices], int dev,
     return false;
   done[dev].store(true, std::memory_order_release);
   return true;
+}
+
+// Launches `kernel` so that it may start while the kernel before it in the stream ends
+// (programmatic dependent launch); `cluster` CTAs to a cluster, 0: as the kernel says.
+// Every thread of the kernel calls follow() before it reads or writes global memory.
+template <class... Types, class... Args>
+inline bool launch_following(void (*kernel)(Types...), int64_t grid, int threads, int smem,
+                             int cluster, cudaStream_t stream, const Args &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess && cudaGetLastError() == cudaSuccess;
 }
 
 }  // namespace kda

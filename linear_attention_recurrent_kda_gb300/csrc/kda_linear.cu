@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c.tmem;
+  follow();
 
   if (warp == 4) {
     if (elect_one()) {
@@ -318,6 +319,7 @@ __global__ void __launch_bounds__(kOneThreads)
                              : vector_of(row[f] + 8 * v, left);
     }
   };
+  follow();
   load(begin + lane);
   for (int v = threadIdx.x; v < vectors; v += kOneThreads)
     token[v] = vector_of(x + 8 * v, p.inner - 8 * v);
@@ -368,9 +370,11 @@ static int launch_one(const kda_linear_args *a, Params &p, int dev, int sms, cud
   if (!set_smem_limit_once(done[p.act], dev, reinterpret_cast<const void *>(kernel), 2 * kOneMost))
     return KDA_ERR_LAUNCH;
   const int64_t grid = (pairs * p.split + kOneWarps - 1) / kOneWarps;
-  kernel<<<static_cast<unsigned>(grid), kOneThreads, (a->inner + 7) / 8 * 16, stream>>>(
-      p, static_cast<const __nv_bfloat16 *>(a->x), static_cast<const __nv_bfloat16 *>(a->weight), a->w_stride);
-  return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
+  return launch_following(kernel, grid, kOneThreads, (a->inner + 7) / 8 * 16, 0, stream, p,
+                          static_cast<const __nv_bfloat16 *>(a->x),
+                          static_cast<const __nv_bfloat16 *>(a->weight), a->w_stride)
+             ? KDA_SUCCESS
+             : KDA_ERR_LAUNCH;
 }
 
 // ------------------------------------------------------------------ many tokens
@@ -476,6 +480,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
   cluster_sync_all();                              // both CTAs' barriers are there
   tc_fence_after();
   const uint32_t tmem = c.tmem;
+  follow();
 
   if (warp == 0) {
     if (elect_one()) {
@@ -693,8 +698,10 @@ static int launch_tiles(const kda_linear_args *a, const Params &p, int dev, int 
     return KDA_ERR_LAUNCH;
   const int pairs = pairs_of(dev, reinterpret_cast<const void *>(kernel));
   if (pairs < 1) return KDA_ERR_LAUNCH;
-  kernel<<<2 * static_cast<int>(tiles < pairs ? tiles : pairs), kTileThreads, kTileSmem, stream>>>(p, x, w, r, o);
-  return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
+  return launch_following(kernel, 2 * (tiles < pairs ? tiles : pairs), kTileThreads, kTileSmem, 0, stream,
+                          p, x, w, r, o)
+             ? KDA_SUCCESS
+             : KDA_ERR_LAUNCH;
 }
 
 typedef void (*ProductKernel)(const Params, const CUtensorMap, const CUtensorMap);
@@ -796,19 +803,8 @@ static int run(const kda_linear_args *a, cudaStream_t stream) {
   const ProductKernel kernel = kernels[p.act];
   if (!set_smem_limit_once(done[p.act], dev, reinterpret_cast<const void *>(kernel), smem_of(kRing)))
     return KDA_ERR_LAUNCH;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_of(p.ring);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.split;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, p, w, x) != cudaSuccess) return KDA_ERR_LAUNCH;
-  return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
+  return launch_following(kernel, ctas, kThreads, smem_of(p.ring), p.split, stream, p, w, x) ? KDA_SUCCESS
+                                                                                             : KDA_ERR_LAUNCH;
 }
 
 }  // namespace linear

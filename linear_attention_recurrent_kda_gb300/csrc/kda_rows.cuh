@@ -11,6 +11,15 @@
 namespace kda {
 namespace rows {
 
+// The kernels here may start while the one before them in the stream ends
+// (launch_following): each thread calls this before its first access to global memory.
+// The kernel behind may start from then on, and so not before the one ahead is complete:
+// what is two launches ahead is complete for a kernel that reads before its own wait.
+__device__ __forceinline__ void follow() {
+  griddep_wait();
+  griddep_launch_dependents();
+}
+
 // 8 BF16 values of a 16-byte vector.
 __device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};

@@ -46,6 +46,7 @@ template <int kStates>
 __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ Params p,
                                                         int blocks) {
   constexpr int kLanes = kStates / 4;
+  follow();
   const int block = blockIdx.x % blocks, first = blockIdx.x / blocks * kRequests;
   const int channel = (block * kThreads + threadIdx.x) / kLanes, quad = threadIdx.x % kLanes;
   if (channel >= p.channels) return;
@@ -123,8 +124,8 @@ static int launch_step(const Params &p, cudaStream_t stream) {
   const int per = kThreads / (kStates / 4), blocks = (p.channels + per - 1) / per;
   const int64_t grid = (static_cast<int64_t>(p.batch) + kRequests - 1) / kRequests * blocks;
   if (grid > 0x7fffffffll) return KDA_ERR_SHAPE;
-  step_kernel<kStates><<<static_cast<int>(grid), kThreads, 0, stream>>>(p, blocks);
-  return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
+  return launch_following(step_kernel<kStates>, grid, kThreads, 0, 0, stream, p, blocks) ? KDA_SUCCESS
+                                                                                         : KDA_ERR_LAUNCH;
 }
 
 template <class Args>

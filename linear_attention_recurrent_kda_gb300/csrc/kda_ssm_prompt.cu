@@ -484,6 +484,8 @@ __global__ void __launch_bounds__(kThreads, kHeld == 16 ? 4 : 6) scan_kernel(con
 }
 
 template <int kStates, int kHeld>
+// (Not launched to start ahead of the end of the kernel before, as the others: CTAs then go
+// where that one leaves room first, several long sequences to an SM: ragged 316 -> 438 us.)
 static int launch(Params &p, cudaStream_t stream, int dev) {
   using S = Stage<kStates, kHeld>;
   p.group_blocks = (p.span + S::kChannels - 1) / S::kChannels;
