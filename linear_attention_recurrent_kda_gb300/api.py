@@ -300,10 +300,13 @@ def kda_oproj(*, partials, prefix, output, out_norm, blocks=None, norm=None,
 # These calls are short, so their host side is too: one look at each tensor, and
 # the general checks (with their messages) only where that look fails.
 
+_Tensor, _BF16, _F32, _I32 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32
+
+
 def _want(name, t, dtype, shape, index):
     """The address of a contiguous CUDA tensor of this type, shape (None: any)
     and device."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous()
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.is_contiguous()
             and t.get_device() == index and (shape is None or t.shape == shape)):
         _check(name, t, dtype, shape)
         _same_device(torch.device("cuda", index), **{name: t})
@@ -316,6 +319,11 @@ def _count(name, n):
     if n >= 1 << 31:
         raise ValueError(f"{name}: {n} are more than the library counts (2^31 - 1)")
     return n
+
+
+def _counts(**sizes):
+    for name, n in sizes.items():
+        _count(name, n)
 
 
 def _maybe(name, t, dtype, shape, index):
@@ -335,7 +343,7 @@ def _rows(name, t, rows, width, index):
     """(address, row stride) of a BF16 CUDA tensor [rows, width] whose rows may be
     slices of wider rows: elements of a row adjacent, any row stride that the
     library takes."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16
+    if not (isinstance(t, _Tensor) and t.dtype is _BF16
             and t.get_device() == index and t.shape == (rows, width)):
         if _cuda_index(name, t) != index:
             raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
@@ -343,6 +351,8 @@ def _rows(name, t, rows, width, index):
             raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
         raise ValueError(f"{name} must have shape {(rows, width)}, got {tuple(t.shape)}")
     step, one = t.stride()
+    if one == 1 and rows > 1 and step >= width > 0 and not step & 7:
+        return t.data_ptr(), step
     if not width:
         return t.data_ptr(), 0
     if rows <= 1:
@@ -530,37 +540,37 @@ def kda_snapshot_load(*, codes, scales, snaps, state, slots, err=None,
 
 def _sequences(seq_starts, src_slots, dst_slots, index):
     """(count, addresses) of a prompt call's sequences."""
-    i32 = torch.int32
-    sp = _want("seq_starts", seq_starts, i32, None, index)
-    if seq_starts.dim() != 1 or seq_starts.shape[0] < 1:
+    sp, shape = _want("seq_starts", seq_starts, _I32, None, index), seq_starts.shape
+    if len(shape) != 1 or shape[0] < 1:
         raise ValueError("seq_starts must be [seqs + 1]")
-    B = _count("seq_starts", seq_starts.shape[0] - 1)
-    return (B, sp, _maybe("src_slots", src_slots, i32, (B,), index),
-            _maybe("dst_slots", dst_slots, i32, (B,), index))
+    B = _count("seq_starts", shape[0] - 1)
+    return (B, sp, None if src_slots is None else _want("src_slots", src_slots, _I32, (B,), index),
+            None if dst_slots is None else _want("dst_slots", dst_slots, _I32, (B,), index))
 
 
 def _conv_shape(x, weight):
     """(device index, rows, channels, parts, taps)"""
     index = _cuda_index("x", x)
     _cuda_index("weight", weight)
-    if x.dim() != 2 or weight.dim() not in (2, 3):
+    rows, of = x.shape, weight.shape
+    if len(rows) != 2 or len(of) not in (2, 3):
         raise ValueError("x must be [tokens, channels], weight [taps, channels] or "
                          "[parts, taps, channels / parts]")
-    parts, taps = (1, weight.shape[0]) if weight.dim() == 2 else weight.shape[:2]
-    if parts * weight.shape[-1] != x.shape[1]:
-        raise ValueError(f"weight {tuple(weight.shape)} is not of {x.shape[1]} channels")
-    return index, _count("x", x.shape[0]), _count("channels", x.shape[1]), parts, taps
+    parts, taps = (1, of[0]) if len(of) == 2 else of[:2]
+    if parts * of[-1] != rows[1]:
+        raise ValueError(f"weight {tuple(of)} is not of {rows[1]} channels")
+    return index, _count("x", rows[0]), _count("channels", rows[1]), parts, taps
 
 
 def _window(window, channels, index):
     """(address, slots, width, whether FP32) of a window pool."""
-    if not isinstance(window, torch.Tensor) or window.dtype not in (torch.bfloat16, torch.float32):
+    dtype = window.dtype if isinstance(window, _Tensor) else None
+    if dtype is not _BF16 and dtype is not _F32:
         raise TypeError("window must be a bfloat16 or float32 tensor")
-    ptr = _want("window", window, window.dtype, None, index)
-    if window.dim() != 3 or window.shape[1] != channels:
-        raise ValueError(f"window must be [num_slots, {channels}, width], got {tuple(window.shape)}")
-    return (ptr, _count("window", window.shape[0]), _count("window", window.shape[2]),
-            int(window.dtype is torch.float32))
+    ptr, shape = _want("window", window, dtype, None, index), window.shape
+    if len(shape) != 3 or shape[1] != channels:
+        raise ValueError(f"window must be [num_slots, {channels}, width], got {tuple(shape)}")
+    return ptr, _count("window", shape[0]), _count("window", shape[2]), int(dtype is _F32)
 
 
 def kda_conv_prompt(*, x, weight, seq_starts, output, bias=None, window=None, src_slots=None,
@@ -629,32 +639,33 @@ def kda_conv_step(stream: Optional[torch.cuda.Stream] = None, **kw) -> None:
 def _ssm_rows(x, dt, a, b, c, d, z, dt_bias, output):
     """What the scan's calls share: (device index, rows, channels, states, groups,
     strides and addresses in the structs' order)."""
-    f32 = torch.float32
     index = _cuda_index("x", x)
     _cuda_index("a", a)
     _cuda_index("b", b)
     if x.dim() != 2 or a.dim() != 2 or b.dim() != 2:
         raise ValueError("x must be [tokens, channels], a [channels, states], b and c "
                          "[tokens, groups * states]")
-    rows, C, N = _count("x", x.shape[0]), _count("channels", x.shape[1]), _count("a", a.shape[1])
-    ap = _want("a", a, f32, (C, N), index)
-    groups = _count("b", b.shape[1]) // N if N else 0
-    if not N or not groups or groups * N != b.shape[1]:
+    (rows, C), N, wide = x.shape, a.shape[1], b.shape[1]
+    if (rows | C | N | wide) >> 31:
+        _counts(x=rows, channels=C, a=N, b=wide)
+    ap = _want("a", a, _F32, (C, N), index)
+    groups = wide // N if N else 0
+    if not N or not groups or groups * N != wide:
         raise ValueError(f"b must be [tokens, groups * {N}], got {tuple(b.shape)}")
     (xp, xs), (tp, ts) = _rows("x", x, rows, C, index), _rows("dt", dt, rows, C, index)
-    (bp, bs), (cp, cs) = (_rows(n, t, rows, groups * N, index) for n, t in (("b", b), ("c", c)))
+    (bp, bs), (cp, cs) = _rows("b", b, rows, wide, index), _rows("c", c, rows, wide, index)
     zp, zs = (None, 0) if z is None else _rows("z", z, rows, C, index)
     op, os_ = _rows("output", output, rows, C, index)
     return (index, rows, C, N, groups, (xs, ts, bs, cs, zs, os_),
-            (xp, tp, ap, bp, cp, _maybe("d", d, f32, (C,), index), zp,
-             _maybe("dt_bias", dt_bias, f32, (C,), index)), op)
+            (xp, tp, ap, bp, cp, _maybe("d", d, _F32, (C,), index), zp,
+             _maybe("dt_bias", dt_bias, _F32, (C,), index)), op)
 
 
 def _ssm_state(state, C, N, index):
-    ptr = _want("state", state, torch.float32, None, index)
-    if state.dim() != 3 or state.shape[1:] != (C, N):
-        raise ValueError(f"state must be [num_slots, {C}, {N}], got {tuple(state.shape)}")
-    return ptr, _count("state", state.shape[0])
+    ptr, shape = _want("state", state, _F32, None, index), state.shape
+    if len(shape) != 3 or shape[1] != C or shape[2] != N:
+        raise ValueError(f"state must be [num_slots, {C}, {N}], got {tuple(shape)}")
+    return ptr, _count("state", shape[0])
 
 
 def kda_ssm_prompt(*, x, dt, a, b, c, seq_starts, output, d=None, z=None, dt_bias=None,
@@ -744,17 +755,19 @@ def kda_linear(*, x, weight, output, bias=None, residual=None, activation: Optio
     "silu", "gelu" (with erf) or "softplus"."""
     index = _cuda_index("x", x)
     _cuda_index("weight", weight)
-    if x.dim() != 2 or weight.dim() != 2:
+    if x.ndim != 2 or weight.ndim != 2:
         raise ValueError("x must be [rows, inner], weight [outer, inner]")
-    if activation not in ACTIVATIONS:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation must be one of {sorted(map(str, ACTIVATIONS))}, "
                          f"got {activation!r}")
-    rows, K = _count("x", x.shape[0]), _count("inner", x.shape[1])
-    N = _count("weight", weight.shape[0])
+    (rows, K), N = x.shape, weight.shape[0]
+    if (rows | K | N) >> 31:
+        _counts(x=rows, inner=K, weight=N)
     (xp, xs), (wp, ws) = _rows("x", x, rows, K, index), _rows("weight", weight, N, K, index)
     op, os_ = _rows("output", output, rows, N, index)
     rp, rs = (None, 0) if residual is None else _rows("residual", residual, rows, N, index)
     _run("kda_linear", _lib.KdaLinearArgs(
-        rows, K, N, ACTIVATIONS[activation], xs, ws, rs, os_, xp, wp,
-        _maybe("bias", bias, torch.bfloat16, (N,), index), rp, op,
-        _maybe("err", err, torch.int32, None, index)), index, stream)
+        rows, K, N, act, xs, ws, rs, os_, xp, wp,
+        None if bias is None else _want("bias", bias, _BF16, (N,), index), rp, op,
+        None if err is None else _want("err", err, _I32, None, index)), index, stream)
