@@ -427,8 +427,10 @@ __device__ __forceinline__ void pair_commit(uint64_t *bar) {
       "h"(static_cast<uint16_t>(3))
       : "memory");
 }
+// Relaxed: it says that TMEM was read, which tcgen05's fences order.  (A release waited for
+// the output's copy, too: 1500 cycles, 9159 x 256 x 4096 25.1 instead of 19.3 us.)
 __device__ __forceinline__ void arrive_in(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 struct Tile {
@@ -531,8 +533,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (warp >= 4) {
     // Each warp takes 32 tokens x 64 features of a tile through a buffer of its own, and
     // waits for none of the others.  16 warps, as a chunk is a long chain for one warp
-    // (TMEM, arithmetic, shared memory, a fence, a copy: 3.8k cycles where a thin tile's
-    // products take 2k; 8 warps with two chunks each, 9159 x 256 x 4096: 33 us, 16 warps 27).
+    // (TMEM, arithmetic, shared memory, a fence, a copy: 3.1k cycles where a thin tile's
+    // products take 2k); 8 warps with two chunks each took 33 us where 16 took 27.
     const int w4 = warp & 3, group = (warp - 4) >> 2;
     const bool leader = lane == 0;
     uint8_t *const chunk = chunks + (warp - 4) * kChunk, *const mine = chunk + lane * 128;
@@ -659,25 +661,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
 typedef void (*TileKernel)(const Params, const CUtensorMap, const CUtensorMap, const CUtensorMap,
                            const CUtensorMap);
 
-// Pairs of CTAs that run at a time (half the SMs, less where one has no partner).
-static int pairs_of(int dev, const void *kernel) {
-  static std::atomic<int> known[kMaxDevices];
-  int pairs = known[dev].load(std::memory_order_acquire);
-  if (pairs == 0) {
+// Clusters of `cluster` such CTAs that run at a time (fewer than the SMs' number over it,
+// where SMs have no partners left).
+static int clusters_of(std::atomic<int> (&known)[kMaxDevices], int dev, const void *kernel, int cluster,
+                       int threads, int smem) {
+  int n = known[dev].load(std::memory_order_acquire);
+  if (n == 0) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(kTileThreads);
-    cfg.dynamicSmemBytes = kTileSmem;
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess) return 0;
-    known[dev].store(pairs, std::memory_order_release);
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+    known[dev].store(n, std::memory_order_release);
   }
-  return pairs;
+  return n;
 }
 
 static int launch_tiles(const kda_linear_args *a, const Params &p, int dev, int sms, cudaStream_t stream) {
@@ -696,7 +699,8 @@ static int launch_tiles(const kda_linear_args *a, const Params &p, int dev, int 
   const TileKernel kernel = kernels[p.act];
   if (!set_smem_limit_once(done[p.act], dev, reinterpret_cast<const void *>(kernel), kTileSmem))
     return KDA_ERR_LAUNCH;
-  const int pairs = pairs_of(dev, reinterpret_cast<const void *>(kernel));
+  static std::atomic<int> known[kMaxDevices];
+  const int pairs = clusters_of(known, dev, reinterpret_cast<const void *>(kernel), 2, kTileThreads, kTileSmem);
   if (pairs < 1) return KDA_ERR_LAUNCH;
   return launch_following(kernel, 2 * (tiles < pairs ? tiles : pairs), kTileThreads, kTileSmem, 0, stream,
                           p, x, w, r, o)
@@ -706,41 +710,43 @@ static int launch_tiles(const kda_linear_args *a, const Params &p, int dev, int 
 
 typedef void (*ProductKernel)(const Params, const CUtensorMap, const CUtensorMap);
 
-// Which form and layout: the cheapest by a model of the time in us, fitted to 26 shapes
-// with up to 19 layouts each (what it takes is within 2% of the best of them).  Few
-// tiles: a CTA streams a block of the inner dimension at 152 KB a us or in its products'
-// time, W comes at 6.2 MB a us at most (a little less for every time it is read again), a
-// CTA starts and ends in 2 + 0.0164 a token (a third of it hidden where two share an SM),
-// and a join costs by its ranks and tokens (clusters of 3, 5, 6 and 7 leave SMs idle: 300 x
-// 8192 x 640 18.1 us with one, 11.8 with 4).  Pairs: 0.32 a block, 2 a tile at least.
-// tile_n 0: pairs.
+// Which form and layout: the cheapest by a model of the time in us, fitted to 36 shapes
+// with up to 13 layouts each (what it takes is within 3% of the best of them; a shape of
+// 2000 x 104 x 104 within 21%).  Few tiles: a CTA streams a block of the inner dimension at
+// 140 KB a us or in its products' time, W comes at 7.5 MB a us at most (a third more for
+// every time it is read again), a CTA starts and ends in 1.55 + 0.02 a token (a third of it
+// hidden where two share an SM), and a join costs by its ranks and tokens.  Ranks are powers
+// of two: clusters of 3, 5, 6 and 7 leave SMs idle (300 x 8192 x 640 18.1 us with one, 11.8
+// with 4), and 8 some (128 x 16384 x 512 with 16 clusters of 8, which do not all run at once,
+// 18.0 us, with 12 10.7).  Pairs: 0.3 a block, 1.4 a tile at least.  tile_n 0: pairs.
 struct Plan {
   int tile_n, split;
 };
-static Plan plan_of(int rows, int blocks, int inner, int outer, int sms) {
+static Plan plan_of(int rows, int blocks, int inner, int outer, int sms, int eights) {
   const int64_t tiles_m = (outer + kM - 1) / kM;
-  const double weights = 2.0 * inner * outer / 6.2e6;
+  const double weights = 2.0 * inner * outer / 7.5e6;
   Plan best = {0, 1};
   double least = 1e300;
   if (outer >= 8 && rows > 64) {
     const int64_t tiles = static_cast<int64_t>((rows + kTileRows - 1) / kTileRows) *
                           ((outer + kTileCols - 1) / kTileCols);
-    const double tile = blocks * 0.32 > 2.0 ? blocks * 0.32 : 2.0;
-    least = static_cast<double>((tiles + sms / 2 - 1) / (sms / 2)) * tile + 5.85;
+    const double tile = blocks * 0.3 > 1.4 ? blocks * 0.3 : 1.4;
+    least = static_cast<double>((tiles + sms / 2 - 1) / (sms / 2)) * tile + 4.9;
   }
   for (int tile_n = 16; tile_n <= kMostN; tile_n += tile_n < 64 ? 16 : 32) {
     if (tile_n - 32 >= rows) break;
     const int64_t tiles = tiles_m * ((rows + tile_n - 1) / tile_n);
-    const double bytes = (kATile + tile_n * kK * 2) / 152e3;
-    const double block = bytes > 0.00154 * tile_n ? bytes : 0.00154 * tile_n;
+    const double bytes = (kATile + tile_n * kK * 2) / 140e3;
+    const double block = bytes > 0.00087 * tile_n ? bytes : 0.00087 * tile_n;
     for (int split = 1; split <= 8 && split <= blocks; split *= 2) {
-      const int64_t ctas = tiles * split, waves = (ctas + sms - 1) / sms;
-      const double ends = (2.0 + 0.0164 * tile_n) * (ctas > sms && tile_n <= 64 ? 0.64 : 1.0);
+      const int64_t ctas = tiles * split, room = split == 8 ? 8 * eights : sms;
+      const int64_t waves = (ctas + room - 1) / room;
+      const double ends = (1.55 + 0.02 * tile_n) * (ctas > sms && tile_n <= 64 ? 0.68 : 1.0);
       double stream = static_cast<double>(waves) * ((blocks + split - 1) / split) * block;
-      const double read = weights * (1.0 + 0.12 * ((rows - 1) / tile_n));
+      const double read = weights * (1.0 + 0.32 * ((rows - 1) / tile_n));
       if (stream < read) stream = read;
-      const double join = split > 1 ? 0.93 + (split - 1) * 0.0042 * tile_n : 0.0;
-      const double cost = stream + static_cast<double>(waves) * (ends + join) + 1.5;
+      const double join = split > 1 ? 0.9 + (split - 1) * 0.005 * tile_n : 0.0;
+      const double cost = stream + static_cast<double>(waves) * (ends + join) + 0.3;
       if (cost < least) {
         least = cost;
         best = {tile_n, split};
@@ -780,8 +786,16 @@ static int run(const kda_linear_args *a, cudaStream_t stream) {
   p.err = a->err;
   if (a->rows == 1 && a->inner <= kOneMost) return launch_one(a, p, dev, df.sms, stream);
   p.blocks = (a->inner + kK - 1) / kK;
-  const Plan plan = plan_of(a->rows, p.blocks, a->inner, a->outer, df.sms);
-
+  static const ProductKernel kernels[4] = {product_kernel<KDA_ACT_NONE>, product_kernel<KDA_ACT_SILU>,
+                                           product_kernel<KDA_ACT_GELU>, product_kernel<KDA_ACT_SOFTPLUS>};
+  static std::atomic<bool> done[4][kMaxDevices];
+  const ProductKernel kernel = kernels[p.act];
+  if (!set_smem_limit_once(done[p.act], dev, reinterpret_cast<const void *>(kernel), smem_of(kRing)))
+    return KDA_ERR_LAUNCH;
+  static std::atomic<int> known[kMaxDevices];
+  const int eights = clusters_of(known, dev, reinterpret_cast<const void *>(kernel), 8, kThreads, smem_of(kRing));
+  if (eights < 1) return KDA_ERR_LAUNCH;
+  const Plan plan = plan_of(a->rows, p.blocks, a->inner, a->outer, df.sms, eights);
   if (plan.tile_n == 0) return launch_tiles(a, p, dev, df.sms, stream);
   p.tile_n = plan.tile_n;
   p.split = plan.split;
@@ -796,12 +810,6 @@ static int run(const kda_linear_args *a, cudaStream_t stream) {
   CUtensorMap w, x;
   if (!rows_map(&w, a->weight, a->inner, a->outer, a->w_stride, kM, dev) ||
       !rows_map(&x, a->x, a->inner, a->rows, a->x_stride, p.tile_n, dev))
-    return KDA_ERR_LAUNCH;
-  static const ProductKernel kernels[4] = {product_kernel<KDA_ACT_NONE>, product_kernel<KDA_ACT_SILU>,
-                                           product_kernel<KDA_ACT_GELU>, product_kernel<KDA_ACT_SOFTPLUS>};
-  static std::atomic<bool> done[4][kMaxDevices];
-  const ProductKernel kernel = kernels[p.act];
-  if (!set_smem_limit_once(done[p.act], dev, reinterpret_cast<const void *>(kernel), smem_of(kRing)))
     return KDA_ERR_LAUNCH;
   return launch_following(kernel, ctas, kThreads, smem_of(p.ring), p.split, stream, p, w, x) ? KDA_SUCCESS
                                                                                              : KDA_ERR_LAUNCH;
