@@ -11,6 +11,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "../../include/kda.h"
 #include "kda_device.cuh"
 #include "kda_host.h"
@@ -196,7 +198,7 @@ struct Plan {
   int held, piece;         // states of a thread; rows of a piece (0: sequences stay whole)
   int64_t workspace;       // bytes
 };
-constexpr int kSms = 152, kCtas = 4;     // that the work is shared among, with 16 states a thread
+constexpr int kSms = 152, kCtas = 6;     // pieces: two for each of the 3 CTAs that an SM holds
 constexpr int kShortestPiece = 256;      // rows
 
 static int plan_prompt(const kda_ssm_prompt_args *a, Plan *plan) {
@@ -207,21 +209,26 @@ static int plan_prompt(const kda_ssm_prompt_args *a, Plan *plan) {
   const int64_t longest = a->max_seq < a->tokens ? a->max_seq : a->tokens;
   const int64_t threads = static_cast<int64_t>(a->channels) * (a->states / 16);
   const int64_t blocks = (threads + 127) / 128;          // CTAs of a sequence or piece
-  // 8 states a thread make twice the warps, with a third more instructions in all: better
-  // where warps are few (one sequence of 4096 tokens x 4096 channels 461 us instead of
-  // 656, 8 of 1145 on average 319 instead of 345), worse where an SM has its four CTAs
-  // (32749 tokens in pieces 1250 instead of 1098).
-  plan->held = blocks * a->seqs <= 2 * kSms ? 8 : 16;
+  // us.  A call takes as long as its longest sequence alone or as all the work, and a little
+  // longer where the two are near.  8 states a thread are faster alone and slower in all (8
+  // sequences, 9159 tokens x 4096 channels: 242 us with 8, 297 with 16 where the longest has
+  // 2047, 249 and 231 where all have 1145).  Of 19 shapes, 10% more than the other's at most.
+  const double work = static_cast<double>(a->tokens) * blocks;
+  const double with8 = std::hypot(0.072 * longest, 0.78e-3 * work);
+  const double with16 = std::hypot(0.125 * longest, 0.66e-3 * work);
+  plan->held = with8 < with16 ? 8 : 16;
   plan->piece = 0;
   plan->workspace = 0;
-  if (a->path == 1 || longest <= kShortestPiece) return KDA_SUCCESS;
-  // Whole, the longest sequence takes 0.14 us a token; in pieces, all tokens go through
-  // two passes at 1.1 ns a CTA and token.  (1 x 2048 tokens x 4096 channels: 230 us whole,
-  // 104 in pieces; the 8 ragged ones 319 and 329.)
-  const int64_t work = a->tokens * blocks;
-  if (a->path == 0 && 140 * longest < 11 * work / 10 + 15000) return KDA_SUCCESS;
-  int64_t piece = (work / (kSms * kCtas) + 15) / 16 * 16;
+  if (a->path == 1 || blocks == 0 || longest <= kShortestPiece) return KDA_SUCCESS;
+  // As many pieces as run at a time (each sequence's last one may be short); two passes over
+  // all tokens, and each piece sums up those before it.  (One sequence of 2048 x 4096
+  // channels 150 us whole, 92 in pieces; of 512 43 and 61; the 8 ragged ones 242 and 336.)
+  int64_t pieces = kSms * kCtas / blocks - (a->seqs - 1);
+  if (pieces < 1) pieces = 1;
+  int64_t piece = (a->tokens / pieces + 16) / 16 * 16;
   if (piece < kShortestPiece || piece >= longest) piece = kShortestPiece;
+  const double split = std::fmax(1.02e-3 * work, 0.23 * piece) + 1.3 * (longest / piece);
+  if (a->path == 0 && (with8 < with16 ? with8 : with16) < split) return KDA_SUCCESS;
   plan->held = 16;
   plan->piece = static_cast<int>(piece);
   plan->workspace = pieces_of(a->tokens, a->seqs, plan->piece) * a->channels * (a->states + 1) * 4;

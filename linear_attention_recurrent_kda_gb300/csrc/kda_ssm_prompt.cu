@@ -1,12 +1,12 @@
 // Selective scan over ragged prompts.
 //
-// A thread holds kHeld states of a channel in registers (N / kHeld lanes a channel)
-// and walks the tokens; a CTA of 128 threads takes channels of one group.  Tiles of 16
-// tokens of x, dt and z come by asynchronous copies, two tiles in flight; b and c go
-// through registers into FP32 in shared memory, from where every lane of a warp reads
-// the same words.  What is the same for all states of a channel is computed once per
-// token, two channels to an instruction, by the warp that owns the channel: the steps
-// s and s x before the tile's walk, skip and gate behind it, through shared memory.
+// A CTA of 256 threads takes channels of one group.  128 of them walk the tokens, each
+// with kHeld states of a channel in registers (N / kHeld lanes a channel) and no more
+// than that; 128 helpers do for tiles of 16 tokens, one ahead and one behind the walk,
+// what is the same for all states of a channel: x, dt and z by asynchronous copies, two
+// tiles in flight, b and c through registers into FP32 in shared memory, from where every
+// lane of a warp reads the same words, the steps s and s x, skip and gate, two channels to
+// an instruction.  The walk waits for them 26 cycles a tile.
 //
 // Decays.  exp(s a) = ex2(s (a log2 e)) per token and state on the approximate exp2,
 // and FP32 holds a factor near 1 to 2^-25: a state that remembers 1000 tokens would
@@ -23,20 +23,21 @@
 // steps; scan_kernel<.., true> runs the pieces side by side, each from the state that
 // it sums up itself from the pieces before.
 //
-// What bounds it (GB300): the schedulers' slots.  With 16 warps an SM a token of 32
-// channels x 16 states takes a warp 190 cycles of its scheduler: 75 for the products and
-// sums of decays, states and outputs, 20 for the corrections' products, 12 for b and c, 6
-// more for exp2 (64 of another unit, beside them), 14 for the tile's loads, 30 for the
-// steps, 16 for the outputs, 7 for the corrections (each measured by leaving it out of a
-// copy).  One CTA alone on an SM: 320 cycles a token with 16 states a thread, 220 with 8.
-// 8 ragged sequences (9159 tokens x 4096 channels) 316 us, bound by the longest of 2047
-// tokens; 32749 tokens x 4096 1079 us in 19 pieces, 390 of them in the first pass; its
-// bytes would take 45 and 158.  What made it fast: 16 states a thread instead of 4 (1959
-// -> 488 us, the long one 38 -> 1.5 ms), steps and outputs once per token in pairs of
-// channels and without branches (488 -> 353), contributions summed backwards (1400 ->
-// 1098).  Not kept: scalar operations for pairs (1174 us), exponents not ahead (1107), 2 or
-// 8 tokens a walk (1124, 1127), tiles of 8 or 32 tokens (1136, 1217), 5 CTAs an SM in
-// fewer registers (1240), 256 threads (1088, and 148 us instead of 117 for 1024 tokens).
+// What bounds it (GB300): where SMs are full, the schedulers' slots and the FP32 pipe: a
+// token of 32 channels x 16 states takes 190 cycles of a scheduler, 134 of them
+// instructions: 75 for the products and sums of decays, states and outputs and exp2, 20 for
+// the corrections' products, 12 for b and c, and what the helpers do.  Where CTAs are few, a
+// CTA's own time: 135 cycles a token with 8 states a thread, 230 with 16.
+// 8 ragged sequences (9159 tokens x 4096 channels) 242 us, one of 1024 x 4096 62 us (76
+// whole), 32749 tokens x 4096 1075 us in 28 pieces, 400 of them in the first pass; the
+// ragged ones' bytes would take 45, the long one's 158.  What made it fast: 16 states a
+// thread instead of 4 (1959 -> 488 us, the long one 38 -> 1.5 ms), steps and outputs once per
+// token in pairs of channels and without branches (488 -> 353), contributions summed
+// backwards (1400 -> 1098), helpers (316 -> 250, 1024 tokens whole 115 -> 76; before, each
+// warp did its own channels' steps and outputs between the walks of its tiles), a whole
+// tile's walk unrolled with 8 states (250 -> 242).  Not kept: scalar operations for pairs
+// (1174 us; for some of them 1081 to 1110), exponents not ahead (1107), 2 or 8 tokens a walk
+// with 16 states (1124, 1127), tiles of 8 or 32 tokens (1136, 1217).
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -57,23 +58,32 @@ template <int kStates, int kHeld>
 struct Stage {
   static constexpr int kLanes = kStates / kHeld;             // of a channel
   static constexpr int kChannels = kThreads / kLanes;        // of a CTA
-  static constexpr int kOwn = 32 / kLanes;                   // of a warp
   static constexpr int kVectors = kChannels / 8;             // 16 bytes each, of a row
   static constexpr int kShared = kTile * 2 * kStates / 8;    // vectors of b and c
-  __nv_bfloat16 x[2][kTile][kChannels], dt[2][kTile][kChannels], z[2][kTile][kChannels];
+  __nv_bfloat16 x[3][kTile][kChannels], dt[2][kTile][kChannels], z[2][kTile][kChannels];
   float b[2][kTile][kStates], c[2][kTile][kStates];
-  float2 steps[kTile][kChannels];                            // s and s x, then y
+  float2 steps[2][kTile][kChannels];                         // s and s x, then y
   ulonglong2 before[kHeld / 4][kThreads];                    // the states before two tiles
-  // Channel c of token t of x, dt and z: odd tokens' halves of 128 bytes change places, so
-  // that lanes which read two tokens' 64 bytes meet no bank twice.
-  __device__ static int at(int t, int c) { return kChannels >= 64 ? c ^ ((t & 1) << 5) : c; }
 };
+
+// Named barriers of all threads: a tile's steps, b and c are there (the helpers arrive),
+// its outputs are (the walkers do); two of each in turn.  And one of the helpers.
+constexpr int kReady = 1, kDone = 3, kHelpers = 5;
+__device__ __forceinline__ void bar_arrive(int id) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(2 * kThreads) : "memory");
+}
+__device__ __forceinline__ void bar_helpers() {
+  asm volatile("bar.sync %0, %1;" ::"n"(kHelpers), "n"(kThreads) : "memory");
+}
+__device__ __forceinline__ void bar_wait(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(2 * kThreads) : "memory");
+}
 
 __device__ __forceinline__ void copy16(void *to, const void *from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copies_done() {
-  asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <int kHeld>
@@ -168,7 +178,7 @@ __device__ __forceinline__ f32x2 softplus2(f32x2 v) {
 }
 
 template <int kStates, int kHeld, bool kOut>
-__global__ void __launch_bounds__(kThreads, kHeld == 16 ? 4 : 6) scan_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(2 * kThreads, 3) scan_kernel(const __grid_constant__ Params p) {
   using S = Stage<kStates, kHeld>;
   extern __shared__ __align__(16) uint8_t raw[];
   S &st = *reinterpret_cast<S *>(raw);
@@ -177,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, kHeld == 16 ? 4 : 6) scan_kernel(con
   const int group = block / p.group_blocks;
   const int channel0 = group * p.span + (block - group * p.group_blocks) * S::kChannels;
   const int wide = min(S::kChannels, (group + 1) * p.span - channel0);   // channels, 8 at least
-  const int tid = threadIdx.x, mine = tid / S::kLanes, held = tid % S::kLanes * kHeld;
+  const int tid = threadIdx.x % kThreads, mine = tid / S::kLanes, held = tid % S::kLanes * kHeld;
   Seq seq;
   int64_t first = 0;
   int piece = 0, rows, b;
@@ -203,67 +213,165 @@ __global__ void __launch_bounds__(kThreads, kHeld == 16 ? 4 : 6) scan_kernel(con
     rows = seq.len;
   }
   const int64_t row0 = seq.start + static_cast<int64_t>(piece) * p.piece;
+  const int tiles = (rows + kTile - 1) / kTile;
+  // (launched with 80 registers a thread, 3 CTAs an SM: 104 + 56 for a walker and a helper)
+  if (threadIdx.x >= kThreads) {                   // a helper
+    regs_dec<56>();
+    // x, dt and z of a tile: this thread's vectors are kStep tokens apart
+    constexpr int kStep = kThreads / S::kVectors < kTile ? kThreads / S::kVectors : kTile;
+    constexpr int kCopies = kTile / kStep;
+    static_assert(kThreads % S::kVectors == 0 && kTile % kStep == 0, "whole rows");
+    const int copy_t = tid / S::kVectors, copy_c = tid % S::kVectors * 8;
+    const int copy_to = copy_c < wide && copy_t < kStep ? rows - copy_t : 0;   // tokens from there on are not
+    const __nv_bfloat16 *from_x = p.x + (row0 + copy_t) * p.x_stride + channel0 + copy_c;
+    const __nv_bfloat16 *from_dt = p.dt + (row0 + copy_t) * p.dt_stride + channel0 + copy_c;
+    const __nv_bfloat16 *from_z =
+        kOut && p.z ? p.z + (row0 + copy_t) * p.z_stride + channel0 + copy_c : nullptr;
+    auto load = [&](int tile, int stage, int buf) {
+      const int64_t rows_before = static_cast<int64_t>(tile) * kTile;
+#pragma unroll
+      for (int k = 0; k < kCopies; ++k) {
+        const int t = copy_t + k * kStep;
+        if (tile * kTile + k * kStep < copy_to) {
+          copy16(&st.x[stage][t][copy_c], from_x + (rows_before + k * kStep) * p.x_stride);
+          copy16(&st.dt[buf][t][copy_c], from_dt + (rows_before + k * kStep) * p.dt_stride);
+        }
+      }
+    };
+    auto load_gate = [&](int tile) {
+      if (!kOut || !from_z) return;
+      const int64_t rows_before = static_cast<int64_t>(tile) * kTile;
+#pragma unroll
+      for (int k = 0; k < kCopies; ++k)
+        if (tile * kTile + k * kStep < copy_to)
+          copy16(&st.z[tile & 1][copy_t + k * kStep][copy_c], from_z + (rows_before + k * kStep) * p.z_stride);
+    };
+    constexpr int kMine = (S::kShared + kThreads - 1) / kThreads;
+    uint4 shared[kMine];                             // this thread's part of b and c
+    auto fetch = [&](int tile) {
+#pragma unroll
+      for (int k = 0; k < kMine; ++k) {
+        const int i = tid + k * kThreads, t = i / (kStates / 4), v = i % (kStates / 4);
+        shared[k] = make_uint4(0, 0, 0, 0);
+        if (i < S::kShared && tile * kTile + t < rows) {
+          const int64_t row = row0 + tile * kTile + t;
+          shared[k] = __ldg(reinterpret_cast<const uint4 *>(
+              (v < kStates / 8 ? p.b + row * p.b_stride : p.c + row * p.c_stride) + group * kStates) +
+              v % (kStates / 8));
+        }
+      }
+    };
+    auto spread = [&](int buf) {
+#pragma unroll
+      for (int k = 0; k < kMine; ++k) {
+        const int i = tid + k * kThreads, t = i / (kStates / 4), v = i % (kStates / 4);
+        if (i < S::kShared) {
+          float f[8];
+          unpack8(shared[k], f);
+          float4 *to = reinterpret_cast<float4 *>(
+              (v < kStates / 8 ? st.b[buf][t] : st.c[buf][t]) + v % (kStates / 8) * 8);
+          to[0] = make_float4(f[0], f[1], f[2], f[3]);
+          to[1] = make_float4(f[4], f[5], f[6], f[7]);
+        }
+      }
+    };
+
+    // two channels of every kStride-th token
+    constexpr int kPairs = S::kChannels / 2, kStride = kThreads / kPairs;
+    const int at2 = tid % kPairs * 2, t2 = tid / kPairs;
+    const bool live2 = at2 < wide;
+    f32x2 skip = 0, bias = 0;
+    if (live2) {
+      const int c = channel0 + at2;
+      if (p.d) skip = pair(__ldg(p.d + c), __ldg(p.d + c + 1));
+      if (p.dt_bias) bias = pair(__ldg(p.dt_bias + c), __ldg(p.dt_bias + c + 1));
+    }
+    // (rows behind the piece's end and channels behind the group's: what is there is
+    // computed with, and goes nowhere)
+    auto steps = [&](int buf, int stage) {
+      auto steps_of = [&](auto soft) {
+#pragma unroll
+        for (int k = 0; k < kTile / kStride; ++k) {
+          const int t = t2 + k * kStride;
+          const f32x2 x = unpack2(*reinterpret_cast<const uint32_t *>(&st.x[stage][t][at2]));
+          f32x2 v = add2(unpack2(*reinterpret_cast<const uint32_t *>(&st.dt[buf][t][at2])), bias);
+          if (decltype(soft)::value) v = softplus2(v);
+          float4 w;
+          unpair(v, w.x, w.z);
+          unpair(mul2(v, x), w.y, w.w);
+          *reinterpret_cast<float4 *>(&st.steps[buf][t][at2]) = w;
+        }
+      };
+      if (p.softplus)
+        steps_of(std::true_type());
+      else
+        steps_of(std::false_type());
+    };
+    auto results = [&](int tile, int buf, int stage) {
+      const int count = min(kTile, rows - tile * kTile);
+      __nv_bfloat16 *const to =
+          p.output + (row0 + static_cast<int64_t>(tile) * kTile + t2) * p.o_stride + channel0 + at2;
+      const int ends = live2 ? count : 0;
+      const int64_t step = kStride * p.o_stride;
+      auto outputs = [&](auto gated) {
+#pragma unroll
+        for (int k = 0; k < kTile / kStride; ++k) {
+          const int t = t2 + k * kStride;
+          const float4 w = *reinterpret_cast<const float4 *>(&st.steps[buf][t][at2]);
+          const f32x2 x = unpack2(*reinterpret_cast<const uint32_t *>(&st.x[stage][t][at2]));
+          f32x2 y = fma2(skip, x, pair(w.x, w.z));
+          if (decltype(gated)::value)
+            y = mul2(y, silu2(unpack2(*reinterpret_cast<const uint32_t *>(&st.z[buf][t][at2]))));
+          float lo, hi;
+          unpair(y, lo, hi);
+          if (t < ends) *reinterpret_cast<uint32_t *>(to + k * step) = pack2(lo, hi);
+        }
+      };
+      if (p.z)
+        outputs(std::true_type());
+      else
+        outputs(std::false_type());
+    };
+    auto tile_of = [&](int i) { return kOut ? i : tiles - 1 - i; };   // contributions: from the end
+    if (tiles > 0) {
+      load(tile_of(0), 0, 0);
+      fetch(tile_of(0));
+      copies_done();
+      bar_helpers();
+      load_gate(0);
+      if (tiles > 1) load(tile_of(1), 1, 1);
+    }
+    for (int i = 0, stage = 0; i < tiles; ++i) {   // stage: i % 3
+      const int next = stage == 2 ? 0 : stage + 1, before = stage == 0 ? 2 : stage - 1;
+      spread(i & 1);
+      if (i + 1 < tiles) fetch(tile_of(i + 1));
+      steps(i & 1, stage);
+      bar_arrive(kReady + (i & 1));
+      if (i > 0) {
+        bar_wait(kDone + ((i - 1) & 1));
+        if (kOut) results(i - 1, (i - 1) & 1, before);
+      }
+      if (i + 1 < tiles) {
+        copies_done();
+        bar_helpers();                             // of tile i + 1, by all; tile i - 1 is read
+        load_gate(i + 1);
+        if (i + 2 < tiles) load(tile_of(i + 2), before, i & 1);
+      } else {
+        if (kOut) {
+          copies_done();                           // the last gate
+          bar_helpers();
+        }
+        bar_wait(kDone + (i & 1));
+        if (kOut) results(i, i & 1, stage);
+      }
+      stage = next;
+    }
+    return;
+  }
+  regs_inc<104>();
   const bool live = mine < wide;
   const int channel = channel0 + (live ? mine : 0);
 
-  // x, dt and z of a tile: this thread's vectors are kStep tokens apart
-  constexpr int kStep = kThreads / S::kVectors < kTile ? kThreads / S::kVectors : kTile;
-  constexpr int kCopies = kTile / kStep;
-  static_assert(kThreads % S::kVectors == 0 && kTile % kStep == 0, "whole rows");
-  const int copy_t = tid / S::kVectors, copy_c = tid % S::kVectors * 8;
-  const int copy_to = copy_c < wide && copy_t < kStep ? rows - copy_t : 0;        // the first token that is not there
-  const __nv_bfloat16 *from_x = p.x + (row0 + copy_t) * p.x_stride + channel0 + copy_c;
-  const __nv_bfloat16 *from_dt = p.dt + (row0 + copy_t) * p.dt_stride + channel0 + copy_c;
-  const __nv_bfloat16 *from_z =
-      kOut && p.z ? p.z + (row0 + copy_t) * p.z_stride + channel0 + copy_c : nullptr;
-  auto load = [&](int tile) {
-    const int buf = tile & 1;
-    const int64_t rows_before = static_cast<int64_t>(tile) * kTile;
-#pragma unroll
-    for (int k = 0; k < kCopies; ++k) {
-      const int t = copy_t + k * kStep, c = S::at(t, copy_c);
-      if (tile * kTile + k * kStep < copy_to) {
-        copy16(&st.x[buf][t][c], from_x + (rows_before + k * kStep) * p.x_stride);
-        copy16(&st.dt[buf][t][c], from_dt + (rows_before + k * kStep) * p.dt_stride);
-        if (kOut && from_z) copy16(&st.z[buf][t][c], from_z + (rows_before + k * kStep) * p.z_stride);
-      }
-    }
-  };
-  constexpr int kMine = (S::kShared + kThreads - 1) / kThreads;
-  uint4 shared[kMine];                             // this thread's part of b and c
-  auto fetch = [&](int tile) {
-#pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-      const int i = tid + k * kThreads, t = i / (kStates / 4), v = i % (kStates / 4);
-      shared[k] = make_uint4(0, 0, 0, 0);
-      if (i < S::kShared && tile * kTile + t < rows) {
-        const int64_t row = row0 + tile * kTile + t;
-        shared[k] = __ldg(reinterpret_cast<const uint4 *>(
-            (v < kStates / 8 ? p.b + row * p.b_stride : p.c + row * p.c_stride) + group * kStates) +
-            v % (kStates / 8));
-      }
-    }
-  };
-  auto spread = [&](int tile) {
-#pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-      const int i = tid + k * kThreads, t = i / (kStates / 4), v = i % (kStates / 4);
-      if (i < S::kShared) {
-        float f[8];
-        unpack8(shared[k], f);
-        float4 *to = reinterpret_cast<float4 *>(
-            (v < kStates / 8 ? st.b[tile & 1][t] : st.c[tile & 1][t]) + v % (kStates / 8) * 8);
-        to[0] = make_float4(f[0], f[1], f[2], f[3]);
-        to[1] = make_float4(f[4], f[5], f[6], f[7]);
-      }
-    }
-  };
-
-  const int tiles = (rows + kTile - 1) / kTile;
-  if (rows > 0) {                                  // contributions are summed from the end
-    load(kOut ? 0 : tiles - 1);
-    fetch(kOut ? 0 : tiles - 1);
-  }
   f32x2 a[kHeld / 2], h[kHeld / 2];
   {
     const float4 *from =
@@ -274,17 +382,6 @@ __global__ void __launch_bounds__(kThreads, kHeld == 16 ? 4 : 6) scan_kernel(con
       a[2 * i] = pair(v.x * kLog2e, v.y * kLog2e);
       a[2 * i + 1] = pair(v.z * kLog2e, v.w * kLog2e);
     }
-  }
-  // for what is once a token: two channels, every kStride-th token, of this lane
-  constexpr int kPairs = S::kOwn / 2, kStride = 32 / kPairs;
-  const int lane = tid & 31, own = (tid >> 5) * S::kOwn, at2 = own + lane % kPairs * 2;
-  const int t2 = lane / kPairs;
-  const bool live2 = at2 < wide;
-  f32x2 skip = 0, bias = 0;
-  if (live2) {
-    const int c = channel0 + at2;
-    if (p.d) skip = pair(__ldg(p.d + c), __ldg(p.d + c + 1));
-    if (p.dt_bias) bias = pair(__ldg(p.dt_bias + c), __ldg(p.dt_bias + c + 1));
   }
 #pragma unroll
   for (int i = 0; i < kHeld / 2; ++i) h[i] = 0;
@@ -305,18 +402,11 @@ __global__ void __launch_bounds__(kThreads, kHeld == 16 ? 4 : 6) scan_kernel(con
   }
   float sum = 0.0f;                                // steps of two tiles, or of the piece
   f32x2 used[kHeld / 2];
-  __nv_bfloat16 *out = kOut ? p.output + (row0 + t2) * p.o_stride + channel0 + at2 : nullptr;
 
   for (int i = 0; i < tiles; ++i) {
     const int tile = kOut ? i : tiles - 1 - i;
-    const int buf = tile & 1, count = min(kTile, rows - tile * kTile);
-    copies_done();
-    spread(tile);
-    __syncthreads();
-    if (i + 1 < tiles) {
-      load(kOut ? tile + 1 : tile - 1);
-      fetch(kOut ? tile + 1 : tile - 1);
-    }
+    const int buf = i & 1, count = min(kTile, rows - tile * kTile);
+    bar_wait(kReady + buf);
     if (kOut && (tile & 1) == 0) {
       sum = 0.0f;
 #pragma unroll
@@ -325,26 +415,6 @@ __global__ void __launch_bounds__(kThreads, kHeld == 16 ? 4 : 6) scan_kernel(con
         used[i] = used[i + 1] = 0;
       }
     }
-    // (rows behind the piece's end and channels behind the group's: what is there is
-    // computed with, and goes nowhere)
-    auto steps_of = [&](auto soft) {
-#pragma unroll
-      for (int k = 0; k < kTile / kStride; ++k) {
-        const int t = t2 + k * kStride;
-        const f32x2 x = unpack2(*reinterpret_cast<const uint32_t *>(&st.x[buf][t][S::at(t, at2)]));
-        f32x2 v = add2(unpack2(*reinterpret_cast<const uint32_t *>(&st.dt[buf][t][S::at(t, at2)])), bias);
-        if (decltype(soft)::value) v = softplus2(v);
-        float4 w;
-        unpair(v, w.x, w.z);
-        unpair(mul2(v, x), w.y, w.w);
-        *reinterpret_cast<float4 *>(&st.steps[t][at2]) = w;
-      }
-    };
-    if (p.softplus)
-      steps_of(std::true_type());
-    else
-      steps_of(std::false_type());
-    __syncwarp();
     // kMany tokens at a time: what they add up to leaves the registers behind them,
     // so that the next one's loads and exponents need not wait for a store
     auto walk = [&](int t0, auto many) {
@@ -352,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, kHeld == 16 ? 4 : 6) scan_kernel(con
       float2 w[kMany];
       float ys[kMany];
 #pragma unroll
-      for (int u = 0; u < kMany; ++u) w[u] = st.steps[t0 + u][mine];
+      for (int u = 0; u < kMany; ++u) w[u] = st.steps[buf][t0 + u][mine];
       auto decay = [&](float s, int i) {
         float lo, hi;
         unpair(mul2(two(s), a[i]), lo, hi);
@@ -399,14 +469,14 @@ __global__ void __launch_bounds__(kThreads, kHeld == 16 ? 4 : 6) scan_kernel(con
       if (S::kLanes > 1) __syncwarp();                 // all lanes of the channel have read w
 #pragma unroll
       for (int u = 0; u < kMany; ++u)
-        if (held == 0) st.steps[t0 + u][mine].x = ys[u];
+        if (held == 0) st.steps[buf][t0 + u][mine].x = ys[u];
     };
     // A piece's contribution: sum_t exp(a sum of the steps behind t) s_t x_t b_t.
     auto gather = [&](int t0, auto many) {
       constexpr int kMany = decltype(many)::value;
       float2 w[kMany];
 #pragma unroll
-      for (int u = 0; u < kMany; ++u) w[u] = st.steps[t0 - u][mine];
+      for (int u = 0; u < kMany; ++u) w[u] = st.steps[buf][t0 - u][mine];
 #pragma unroll
       for (int u = 0; u < kMany; ++u) {
         const ulonglong2 *bn = reinterpret_cast<const ulonglong2 *>(st.b[buf][t0 - u] + held);
@@ -426,6 +496,10 @@ __global__ void __launch_bounds__(kThreads, kHeld == 16 ? 4 : 6) scan_kernel(con
     };
     if (kOut) {
       int t = 0;
+      if (kHeld == 8 && count == kTile) {
+        walk(0, std::integral_constant<int, kTile>());
+        t = kTile;
+      }
 #pragma unroll 1
       for (; t + 4 <= count; t += 4) walk(t, std::integral_constant<int, 4>());
 #pragma unroll 1
@@ -436,33 +510,8 @@ __global__ void __launch_bounds__(kThreads, kHeld == 16 ? 4 : 6) scan_kernel(con
       for (; t >= 3; t -= 4) gather(t, std::integral_constant<int, 4>());
 #pragma unroll 1
       for (; t >= 0; --t) gather(t, std::integral_constant<int, 1>());
-      __syncwarp();
     }
-    if (kOut) {
-      __syncwarp();
-      const int ends = live2 ? count : 0;
-      const int64_t step = kStride * p.o_stride;
-      auto outputs = [&](auto gated) {
-#pragma unroll
-        for (int k = 0; k < kTile / kStride; ++k) {
-          const int t = t2 + k * kStride;
-          const float4 w = *reinterpret_cast<const float4 *>(&st.steps[t][at2]);
-          const f32x2 x = unpack2(*reinterpret_cast<const uint32_t *>(&st.x[buf][t][S::at(t, at2)]));
-          f32x2 y = fma2(skip, x, pair(w.x, w.z));
-          if (decltype(gated)::value)
-            y = mul2(y, silu2(unpack2(*reinterpret_cast<const uint32_t *>(&st.z[buf][t][S::at(t, at2)]))));
-          float lo, hi;
-          unpair(y, lo, hi);
-          if (t < ends) *reinterpret_cast<uint32_t *>(out + k * step) = pack2(lo, hi);
-        }
-      };
-      if (p.z)
-        outputs(std::true_type());
-      else
-        outputs(std::false_type());
-      out += kTile * p.o_stride;
-      __syncwarp();
-    }
+    bar_arrive(kDone + buf);
     if (kOut && ((tile & 1) || i + 1 == tiles)) {
 #pragma unroll
       for (int i = 0; i < kHeld / 2; i += 2) {
@@ -485,7 +534,8 @@ __global__ void __launch_bounds__(kThreads, kHeld == 16 ? 4 : 6) scan_kernel(con
 
 template <int kStates, int kHeld>
 // (Not launched to start ahead of the end of the kernel before, as the others: CTAs then go
-// where that one leaves room first, several long sequences to an SM: ragged 316 -> 438 us.)
+// where that one leaves room first, several long sequences to an SM: ragged 316 -> 438 us
+// before the helpers were.)
 static int launch(Params &p, cudaStream_t stream, int dev) {
   using S = Stage<kStates, kHeld>;
   p.group_blocks = (p.span + S::kChannels - 1) / S::kChannels;
@@ -503,11 +553,11 @@ static int launch(Params &p, cudaStream_t stream, int dev) {
       if (!set_smem_limit_once(sum_done, dev,
                                reinterpret_cast<const void *>(scan_kernel<kStates, kHeld, false>), sizeof(S)))
         return KDA_ERR_LAUNCH;
-      scan_kernel<kStates, kHeld, false><<<grid, kThreads, sizeof(S), stream>>>(p);
+      scan_kernel<kStates, kHeld, false><<<grid, 2 * kThreads, sizeof(S), stream>>>(p);
       if (cudaGetLastError() != cudaSuccess) return KDA_ERR_LAUNCH;
     }
   }
-  scan_kernel<kStates, kHeld, true><<<grid, kThreads, sizeof(S), stream>>>(p);
+  scan_kernel<kStates, kHeld, true><<<grid, 2 * kThreads, sizeof(S), stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
 }
 

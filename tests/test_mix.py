@@ -119,6 +119,10 @@ def test_workspace_of_refused_and_missing_arguments():
     assert kl.load().kda_ssm_prompt_workspace(None) == -1
     assert kl.ssm_workspace(ssm_prompt(states=17)) == 0
     assert kl.ssm_workspace(ssm_prompt(path=1)) == 0
+    assert kl.ssm_workspace(ssm_prompt(channels=0, tokens=4096, max_seq=4096)) == 0
+    assert kl.ssm_workspace(ssm_prompt(seqs=0, tokens=4096, max_seq=4096, path=2)) >= 0
+    most = ssm_prompt(seqs=(1 << 31) - 2, channels=8, tokens=1 << 20, max_seq=1 << 20, path=2)
+    assert kl.ssm_workspace(most) >= 0
 
 
 def test_error_text():
