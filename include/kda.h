@@ -41,6 +41,9 @@
  * DEVICE pointer of the current device.  The library allocates nothing,
  * never synchronises, and enqueues exactly one kernel on `stream` per call
  * (kda_lin_prompt: up to three, kda_ssm_prompt: up to two).
+ * The kernels of kda_conv_*, kda_ssm_step and kda_linear are launched so that
+ * they may start while the kernel before them on the stream ends; they read
+ * and write nothing before it has.
  * Calls are reentrant and may come from several host threads at once (the
  * first call on a device reads its attributes and configures the kernel
  * under a lock); two calls that write the same pool regions must be ordered

@@ -8,11 +8,11 @@
 // come while four are worked on.  The sum runs from the bias on, oldest input first,
 // and the SiLU is the KDA step's, so a prompt leaves the step's own bits.
 //
-// GB300: 9159 tokens x 12288 channels 84 us, 5.4 TB/s (0.79 of the copy's rate); one
+// GB300: 9159 tokens x 12288 channels 82 us, 5.5 TB/s (0.81 of the copy's rate); one
 // channel to an operation and no rows ahead 113 us.  Not kept: pieces of 16 rows 91 us,
 // of 64 82 (with half the threads for small calls), of 128 96; 2 rows ahead 99, 8 85; 4
 // channels a thread 79-85, and 16.8 instead of 12.3 us for the step of 256 requests x 8192
-// channels (4.2 TB/s, 3 us more than a launch alone).
+// channels (10.5 us, 4.9 TB/s, since it starts while the kernel before ends).
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>

@@ -2,10 +2,11 @@
 //
 // Three forms.  One token: no tensor core, below.  Few tiles: a CTA takes 128 features
 // (rows of W) and up to 256 tokens; the product's M is the features and its N the
-// tokens, so that few tokens cost few columns.  One warp loads 64-wide tiles of both with TMA through a ring, one
-// issues the products into TMEM.  A cluster of CTAs may share a tile: each sums a range
-// of the inner dimension, and the sums are joined through distributed shared memory,
-// 8 features a thread, in the order of the ranges.  Many tiles: below.
+// tokens, so that few tokens cost few columns.  One warp loads 64-wide tiles of both with
+// TMA through a ring, one issues the products into TMEM.  A cluster of CTAs may share a
+// tile: each sums a range of the inner dimension, and the sums are joined through
+// distributed shared memory, 8 features a thread, in the order of the ranges.  Many
+// tiles: below.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -285,10 +286,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 // inner dimension, 8 values a lane and load, 8 loads in flight, in FP32; the token waits
 // in shared memory.  The 8 warps of a CTA are slices of the same features where features
 // are few, joined in shared memory in order.  No barriers, tensor memory or tensor maps
-// have to be set up first: 4096 x 1024 3.8 us in a graph (the clusters above 5.7), 4096 x
-// 16384 22.4 (23.7), 7168 x 7168 18.3 (21.8).  With 2 tokens the same is no faster than
-// they are, with 4 slower (5.2 and 9.2 us, 4096 x 1024: the tokens' values are unpacked
-// for every feature).
+// have to be set up first: 4096 x 1024 3.3 us in a graph (the clusters above 4.8), 4096 x
+// 16384 22.1 (21.9), 7168 x 7168 18.1 (18.6).  With 2 tokens the same is no faster than
+// they are, with 4 slower (the tokens' values are unpacked for every feature).
 constexpr int kOneThreads = 256, kOneWarps = kOneThreads / 32, kOneMost = 32768;   // values
 
 template <int kAct>
@@ -384,7 +384,7 @@ static int launch_one(const kda_linear_args *a, Params &p, int dev, int sms, cud
 // takes the tokens of both and the features of both, so that a CTA loads 32 KiB where
 // one alone would load 48 for as many products (128 x 256 tiles of single CTAs: 323 us
 // where pairs take 283, 9159 x 4096 x 7168; their loads came in at 70 bytes a cycle and
-// SM).  One warp loads, one of the first CTA issues the products, two warpgroups take
+// SM).  One warp loads, one of the first CTA issues the products, 16 warps take
 // the sums of the tile before (the two halves of TMEM hold a tile each) through swizzled
 // shared memory, 64 features at a time, the residual in by TMA and the output out by
 // TMA, which clips it (to whole vectors of 8: a copy that ends inside one wrote an
