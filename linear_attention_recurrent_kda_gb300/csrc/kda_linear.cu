@@ -677,7 +677,10 @@ static int clusters_of(std::atomic<int> (&known)[kMaxDevices], int dev, const vo
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();                          // (not the launch's)
+      return 0;
+    }
     known[dev].store(n, std::memory_order_release);
   }
   return n;
@@ -738,7 +741,7 @@ static Plan plan_of(int rows, int blocks, int inner, int outer, int sms, int eig
     const int64_t tiles = tiles_m * ((rows + tile_n - 1) / tile_n);
     const double bytes = (kATile + tile_n * kK * 2) / 140e3;
     const double block = bytes > 0.00087 * tile_n ? bytes : 0.00087 * tile_n;
-    for (int split = 1; split <= 8 && split <= blocks; split *= 2) {
+    for (int split = 1; split <= (eights > 0 ? 8 : 4) && split <= blocks; split *= 2) {
       const int64_t ctas = tiles * split, room = split == 8 ? 8 * eights : sms;
       const int64_t waves = (ctas + room - 1) / room;
       const double ends = (1.55 + 0.02 * tile_n) * (ctas > sms && tile_n <= 64 ? 0.68 : 1.0);
@@ -794,7 +797,6 @@ static int run(const kda_linear_args *a, cudaStream_t stream) {
     return KDA_ERR_LAUNCH;
   static std::atomic<int> known[kMaxDevices];
   const int eights = clusters_of(known, dev, reinterpret_cast<const void *>(kernel), 8, kThreads, smem_of(kRing));
-  if (eights < 1) return KDA_ERR_LAUNCH;
   const Plan plan = plan_of(a->rows, p.blocks, a->inner, a->outer, df.sms, eights);
   if (plan.tile_n == 0) return launch_tiles(a, p, dev, df.sms, stream);
   p.tile_n = plan.tile_n;
