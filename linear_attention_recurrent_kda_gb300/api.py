@@ -405,6 +405,14 @@ def _run(entry, args, index, stream):
         raise _lib.KdaError(rc, _lib.strerror(rc))
 
 
+def _done(rc):
+    """Whether a call by the short way (csrc/kda_bind.cpp) was made; None leaves it, or
+    what is to be said about it, to the checks below."""
+    if rc:
+        raise _lib.KdaError(rc, _lib.strerror(rc))
+    return rc is not None
+
+
 def kda_lin_prompt(*, q, k, v, decay, seq_starts, output, scale: float, state=None,
                    src_slots=None, dst_slots=None, max_seq: Optional[int] = None, err=None,
                    path: int = 0, workspace=None,
@@ -585,6 +593,9 @@ def kda_conv_prompt(*, x, weight, seq_starts, output, bias=None, window=None, sr
     [seqs + 1]; ``window`` bf16 or f32 [num_slots, channels, width] (the KDA step's
     ``conv_state``) with ``src_slots`` (the windows the sequences continue from) and
     ``dst_slots`` (where their last inputs go), i32 [seqs] each or None."""
+    if _done((_lib._bind or _lib.bind()).conv_prompt(
+            x, weight, seq_starts, output, bias, window, src_slots, dst_slots, bool(silu), err, stream)):
+        return
     bf = torch.bfloat16
     index, rows, C, parts, taps = _conv_shape(x, weight)
     xp, xs = _rows("x", x, rows, C, index)
@@ -685,6 +696,10 @@ def kda_ssm_prompt(*, x, dt, a, b, c, seq_starts, output, d=None, z=None, dt_bia
     the work is laid out).  ``workspace``: a CUDA uint8 tensor of at least
     ``lib.ssm_workspace`` bytes; by default allocated for the call, on the stream it
     runs on."""
+    if workspace is None and _done((_lib._bind or _lib.bind()).ssm_prompt(
+            x, dt, a, b, c, seq_starts, output, d, z, dt_bias, bool(softplus), state, src_slots,
+            dst_slots, max_seq, err, path, stream)):
+        return
     index, rows, C, N, G, strides, ptrs, op = _ssm_rows(x, dt, a, b, c, d, z, dt_bias, output)
     B, sp, src, dst = _sequences(seq_starts, src_slots, dst_slots, index)
     if state is None:
@@ -753,11 +768,14 @@ def kda_linear(*, x, weight, output, bias=None, residual=None, activation: Optio
     ``output`` bf16 [rows, outer] (each may be a slice of wider rows; the residual may
     be the output itself); ``bias`` bf16 [outer]; ``activation`` None, "none",
     "silu", "gelu" (with erf) or "softplus"."""
+    act = ACTIVATIONS.get(activation)
+    if act is not None and _done((_lib._bind or _lib.bind()).linear(
+            x, weight, output, bias, residual, act, err, stream)):
+        return
     index = _cuda_index("x", x)
     _cuda_index("weight", weight)
     if x.ndim != 2 or weight.ndim != 2:
         raise ValueError("x must be [rows, inner], weight [outer, inner]")
-    act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation must be one of {sorted(map(str, ACTIVATIONS))}, "
                          f"got {activation!r}")

@@ -5,15 +5,20 @@
 convolution, scan, product and self-test kernels; the C ABI of include/kda.h).
 ``libkda_probe_gb300.so``: the measurement probe of include/kda_probe.h, a bench
 instrument kept out of the product library.
-Every translation unit is compiled by its own nvcc process, in parallel, with
-a single ``-gencode arch=compute_103a,code=sm_103a``; each library is linked
-by one more nvcc call and sits next to this file.
+``kda_bind-<python>-torch<version>.so``: the short way from Python to the calls whose
+host side is most of their time, against the headers of the installed PyTorch.
+Every translation unit is compiled by its own nvcc process (g++ for the binding), in
+parallel, with a single ``-gencode arch=compute_103a,code=sm_103a``; each library is
+linked by one more nvcc call and sits next to this file.
 """
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -33,6 +38,9 @@ HEADERS = [os.path.join(INCLUDE, "kda.h"), os.path.join(INCLUDE, "kda_probe.h"),
            os.path.join(CSRC, "kda_rows.cuh"), os.path.join(CSRC, "kda_tc.cuh"),
            os.path.join(CSRC, "kda_ssm.cuh"),
            os.path.join(CSRC, "kda_host.h")]
+BIND_PATH = os.path.join(HERE, "kda_bind-%s-torch%s.so" % (sysconfig.get_config_var("SOABI"),
+                                                            importlib.metadata.version("torch")))
+BIND_SOURCE = os.path.join(CSRC, "kda_bind.cpp")
 LIBS = ((LIB_PATH, SOURCES), (PROBE_LIB_PATH, PROBE_SOURCES))
 
 NVCC_FLAGS = [
@@ -56,7 +64,20 @@ def _stale(lib: str, sources) -> bool:
 
 
 def is_stale() -> bool:
-    return any(_stale(lib, srcs) for lib, srcs in LIBS)
+    return any(_stale(lib, srcs) for lib, srcs in LIBS + ((BIND_PATH, [BIND_SOURCE]),))
+
+
+def _bind_command(out: str):
+    """The compiler's call for the binding (PyTorch's headers, found without importing it)."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    includes = [os.path.join(torch, "include"),
+                os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_path("include"),
+                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")]
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared"]
+            + [a for path in includes for a in ("-isystem", path)]
+            + [BIND_SOURCE, "-o", out, "-L" + os.path.join(torch, "lib"),
+               "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -66,10 +87,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
     then one nvcc call per library links it.  Returns the product library's
     path."""
     todo = [(lib, srcs) for lib, srcs in LIBS if force or _stale(lib, srcs)]
-    if not todo:
+    bind = force or _stale(BIND_PATH, [BIND_SOURCE])
+    if not todo and not bind:
         return LIB_PATH
     with tempfile.TemporaryDirectory() as tmp:
         procs = []
+        if bind:
+            procs.append((BIND_SOURCE, subprocess.Popen(
+                _bind_command(os.path.join(tmp, "kda_bind.so")), stdout=subprocess.PIPE,
+                stderr=subprocess.STDOUT, text=True)))
         objs = {lib: [] for lib, _ in todo}
         for lib, srcs in todo:
             for src in srcs:
@@ -85,7 +111,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             out, _ = pr.communicate()
             logs.append(out)
             if pr.returncode != 0:
-                raise RuntimeError(f"nvcc failed on {src}:\n{out}")
+                raise RuntimeError(f"the compiler failed on {src}:\n{out}")
+        if bind:
+            shutil.copyfile(os.path.join(tmp, "kda_bind.so"), BIND_PATH + ".new")
+            os.replace(BIND_PATH + ".new", BIND_PATH)
         for lib, _ in todo:
             out = os.path.join(tmp, os.path.basename(lib))
             link = [nvcc(), "-gencode", "arch=compute_103a,code=sm_103a", "-shared",

@@ -7,6 +7,8 @@ no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 from . import build as _build
@@ -257,6 +259,28 @@ def strerror(code: int) -> str:
 def call(entry: str, args, stream_handle: int) -> int:
     """Raw call: returns the library's code without raising."""
     return getattr(_lib or load(), entry)(args, stream_handle or None)
+
+
+_bind = None
+
+
+def bind():
+    """The short way to kda_conv_prompt, kda_ssm_prompt and kda_linear (building first if
+    needed): functions that launch and return the library's code, or return None for
+    what they leave to the general checks."""
+    global _bind
+    if _bind is None:
+        if not os.path.exists(_build.BIND_PATH):
+            _build.build()
+        loader = importlib.machinery.ExtensionFileLoader("kda_bind", _build.BIND_PATH)
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_file_location("kda_bind", _build.BIND_PATH, loader=loader))
+        loader.exec_module(module)
+        lib = load()
+        module.setup(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+            "kda_conv_prompt", "kda_ssm_prompt_workspace", "kda_ssm_prompt", "kda_linear")))
+        _bind = module
+    return _bind
 
 
 def prompt_workspace(args) -> int:
