@@ -114,16 +114,21 @@ __device__ __forceinline__ int resolve(const Seqs &p, int b, Seq *s) {
 
 // Pieces of `piece` rows: sequence b's begin at number starts[b] / piece + b, so
 // there are tokens / piece + count numbers and none is taken twice, however the
-// lengths are spread.  Returns the sequence that number n falls to, by bisection
-// (in range also where starts are out of order: what it finds is checked).
+// lengths are spread.  Returns the sequence that number n falls to, by parts of an eighth
+// whose starts are read together, as a call of few tokens is such waits (in range also
+// where starts are out of order: what it finds is checked).
 __device__ __forceinline__ int seq_of(const Seqs &p, int64_t n, int piece) {
   int lo = 0, hi = p.count;                 // first(lo) <= n < first(hi)
   while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2;
-    if (static_cast<int64_t>(__ldg(p.starts + mid)) / piece + mid <= n)
-      lo = mid;
-    else
-      hi = mid;
+    const int step = (hi - lo + 7) / 8;
+    int below = 0;                          // of the seven between, how many begin by n
+#pragma unroll
+    for (int k = 1; k < 8; ++k) {
+      const int64_t mid = lo + static_cast<int64_t>(k) * step;
+      if (mid < hi && __ldg(p.starts + mid) / piece + mid <= n) ++below;
+    }
+    lo += below * step;
+    if (hi - lo > step) hi = lo + step;
   }
   return lo;
 }

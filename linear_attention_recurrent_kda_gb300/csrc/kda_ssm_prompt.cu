@@ -53,6 +53,10 @@ namespace ssm {
 
 constexpr int kThreads = 128;
 constexpr int kTile = 16;                        // tokens
+// Sequences up to here: the kernel may start while the one before it ends.  CTAs then go
+// where that one leaves room first, and long sequences meet on an SM (the ragged ones above
+// 316 -> 438 us, before the helpers were).
+constexpr int kAhead = 64;
 
 template <int kStates, int kHeld>
 struct Stage {
@@ -182,6 +186,7 @@ __global__ void __launch_bounds__(2 * kThreads, 3) scan_kernel(const __grid_cons
   using S = Stage<kStates, kHeld>;
   extern __shared__ __align__(16) uint8_t raw[];
   S &st = *reinterpret_cast<S *>(raw);
+  follow();
   const int block = blockIdx.x % p.blocks;
   const int64_t n = blockIdx.x / p.blocks;
   const int group = block / p.group_blocks;
@@ -533,9 +538,6 @@ __global__ void __launch_bounds__(2 * kThreads, 3) scan_kernel(const __grid_cons
 }
 
 template <int kStates, int kHeld>
-// (Not launched to start ahead of the end of the kernel before, as the others: CTAs then go
-// where that one leaves room first, several long sequences to an SM: ragged 316 -> 438 us
-// before the helpers were.)
 static int launch(Params &p, cudaStream_t stream, int dev) {
   using S = Stage<kStates, kHeld>;
   p.group_blocks = (p.span + S::kChannels - 1) / S::kChannels;
@@ -557,6 +559,10 @@ static int launch(Params &p, cudaStream_t stream, int dev) {
       if (cudaGetLastError() != cudaSuccess) return KDA_ERR_LAUNCH;
     }
   }
+  if (p.seqs.longest <= kAhead)
+    return launch_following(scan_kernel<kStates, kHeld, true>, grid, 2 * kThreads, sizeof(S), 0, stream, p)
+               ? KDA_SUCCESS
+               : KDA_ERR_LAUNCH;
   scan_kernel<kStates, kHeld, true><<<grid, 2 * kThreads, sizeof(S), stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? KDA_SUCCESS : KDA_ERR_LAUNCH;
 }
