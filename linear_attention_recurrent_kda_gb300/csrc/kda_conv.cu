@@ -8,8 +8,9 @@
 // come while four are worked on.  The sum runs from the bias on, oldest input first,
 // and the SiLU is the KDA step's, so a prompt leaves the step's own bits.
 //
-// GB300: 9159 tokens x 12288 channels 82 us, 5.5 TB/s (0.81 of the copy's rate); one
-// channel to an operation and no rows ahead 113 us.  Not kept: pieces of 16 rows 91 us,
+// GB300: 9159 tokens x 12288 channels 79 us, 5.7 TB/s (0.84 of the copy's rate); one
+// channel to an operation and no rows ahead 113 us, weights and the first rows behind the
+// windows 82 (4 x 9 tokens: 4.1 us, 3.7 so).  Not kept: pieces of 16 rows 91 us,
 // of 64 82 (with half the threads for small calls), of 128 96; 2 rows ahead 99, 8 85; 4
 // channels a thread 79-85, and 16.8 instead of 12.3 us for the step of 256 requests x 8192
 // channels (10.5 us, 4.9 TB/s, since it starts while the kernel before ends).
@@ -170,6 +171,8 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const __grid_constant_
   const int64_t n = index / p.vectors;
   if (n >= p.pieces) return;
   const int v = static_cast<int>(index - n * p.vectors), c = 8 * v;
+  Channels<kTaps> ch;
+  ch.load_weights(p, c);
   Seq seq;
   if (v == 0 && n < p.seqs.count && p.err) {         // each sequence's flags, once
     if (const int bad = resolve(p.seqs, static_cast<int>(n), &seq)) atomicOr(p.err, bad);
@@ -179,8 +182,12 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const __grid_constant_
   const int64_t piece = n - (seq.start / kPiece + b), begin = piece * kPiece;
   if (piece < 0 || (piece > 0 && begin >= seq.len)) return;
   const int rows = static_cast<int>(min(static_cast<int64_t>(kPiece), seq.len - begin));
-  Channels<kTaps> ch;
   const __nv_bfloat16 *x = p.x + seq.start * p.x_stride + c;      // the sequence's rows
+  // the next rows come while these are worked on
+  uint4 raw[kBatch];
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i)
+    if (i < rows) raw[i] = __ldg(reinterpret_cast<const uint4 *>(x + (begin + i) * p.x_stride));
   if (piece > 0) {
 #pragma unroll
     for (int j = 0; j < kN; ++j)
@@ -212,14 +219,8 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const __grid_constant_
       write_window<kTaps, kF32>(p, seq.dst, c, next);
     }
   }
-  ch.load_weights(p, c);
   x += begin * p.x_stride;
   __nv_bfloat16 *out = p.output + (seq.start + begin) * p.o_stride + c;
-  // the next rows come while these are worked on
-  uint4 raw[kBatch];
-#pragma unroll
-  for (int i = 0; i < kBatch; ++i)
-    if (i < rows) raw[i] = __ldg(reinterpret_cast<const uint4 *>(x + i * p.x_stride));
   for (int t = 0; t < rows; t += kBatch) {
     uint4 now[kBatch];
     x += kBatch * p.x_stride;
