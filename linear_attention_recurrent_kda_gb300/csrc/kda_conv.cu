@@ -246,16 +246,16 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
   if (r >= p.batch) return;
   const int v = static_cast<int>(index - r * p.vectors), c = 8 * v;
   const int slot = __ldg(p.slots + r);
+  const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(p.x + r * p.x_stride + c));
+  Channels<kTaps> ch;
+  ch.load_weights(p, c);
   uint4 *out = reinterpret_cast<uint4 *>(p.output + r * p.o_stride + c);
   if (slot <= 0 || slot >= p.seqs.num_slots) {
     *out = make_uint4(0, 0, 0, 0);
     if (slot >= p.seqs.num_slots && p.err && v == 0) atomicOr(p.err, KDA_DEVERR_SLOT);
     return;
   }
-  Channels<kTaps> ch;
   read_window<kTaps, kF32>(p, slot, c, ch.last);
-  const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(p.x + r * p.x_stride + c));
-  ch.load_weights(p, c);
   *out = ch.token(raw, p.silu);
   write_window<kTaps, kF32>(p, slot, c, ch.last);
 }
