@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(2 * kThreads, 3) scan_kernel(const __grid_cons
           const int t = t2 + k * kStride;
           const float4 w = *reinterpret_cast<const float4 *>(&st.steps[buf][t][at2]);
           const f32x2 x = unpack2(*reinterpret_cast<const uint32_t *>(&st.x[stage][t][at2]));
-          f32x2 y = fma2(skip, x, pair(w.x, w.z));
+          f32x2 y = fma2(skip, x, S::kLanes == 1 ? pair(w.x, w.z) : pair(w.x + w.y, w.z + w.w));
           if (decltype(gated)::value)
             y = mul2(y, silu2(unpack2(*reinterpret_cast<const uint32_t *>(&st.z[buf][t][at2]))));
           float lo, hi;
@@ -468,13 +468,16 @@ __global__ void __launch_bounds__(2 * kThreads, 3) scan_kernel(const __grid_cons
         ys[u] = lo + hi;
       }
 #pragma unroll
-      for (int o = 1; o < S::kLanes; o <<= 1)
+      for (int o = 2; o < S::kLanes; o <<= 1)
 #pragma unroll
         for (int u = 0; u < kMany; ++u) ys[u] += __shfl_xor_sync(0xffffffffu, ys[u], o);
       if (S::kLanes > 1) __syncwarp();                 // all lanes of the channel have read w
 #pragma unroll
       for (int u = 0; u < kMany; ++u)
-        if (held == 0) st.steps[buf][t0 + u][mine].x = ys[u];
+        if (S::kLanes == 1)
+          st.steps[buf][t0 + u][mine].x = ys[u];
+        else if (held < 2 * kHeld)                     // two lanes' sums, which a helper adds
+          (&st.steps[buf][t0 + u][mine].x)[held / kHeld] = ys[u];
     };
     // A piece's contribution: sum_t exp(a sum of the steps behind t) s_t x_t b_t.
     auto gather = [&](int t0, auto many) {
