@@ -28,14 +28,15 @@
 // instructions: 75 for the products and sums of decays, states and outputs and exp2, 20 for
 // the corrections' products, 12 for b and c, and what the helpers do.  Where CTAs are few, a
 // CTA's own time: 135 cycles a token with 8 states a thread, 230 with 16.
-// 8 ragged sequences (9159 tokens x 4096 channels) 242 us, one of 1024 x 4096 62 us (76
+// 8 ragged sequences (9159 tokens x 4096 channels) 236 us, one of 1024 x 4096 62 us (74
 // whole), 32749 tokens x 4096 1075 us in 28 pieces, 400 of them in the first pass; the
 // ragged ones' bytes would take 45, the long one's 158.  What made it fast: 16 states a
 // thread instead of 4 (1959 -> 488 us, the long one 38 -> 1.5 ms), steps and outputs once per
 // token in pairs of channels and without branches (488 -> 353), contributions summed
 // backwards (1400 -> 1098), helpers (316 -> 250, 1024 tokens whole 115 -> 76; before, each
 // warp did its own channels' steps and outputs between the walks of its tiles), a whole
-// tile's walk unrolled with 8 states (250 -> 242).  Not kept: scalar operations for pairs
+// tile's walk unrolled with 8 states (250 -> 242), its lanes' sums added by the helpers (242
+// -> 236).  Not kept: scalar operations for pairs
 // (1174 us; for some of them 1081 to 1110), exponents not ahead (1107), 2 or 8 tokens a walk
 // with 16 states (1124, 1127), tiles of 8 or 32 tokens (1136, 1217).
 #include <cuda_runtime.h>
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(2 * kThreads, 3) scan_kernel(const __grid_cons
         const f32x2 sx = two(w[u].y);
         const ulonglong2 *bn = reinterpret_cast<const ulonglong2 *>(st.b[buf][t] + held);
         const ulonglong2 *cn = reinterpret_cast<const ulonglong2 *>(st.c[buf][t] + held);
-        f32x2 y[2] = {0, 0};
+        f32x2 y = 0;
 #pragma unroll
         for (int i = 0; i < kHeld / 2; i += 2) {
           const ulonglong2 bb = bn[i / 2], cc = cn[i / 2];
@@ -460,11 +461,11 @@ __global__ void __launch_bounds__(2 * kThreads, 3) scan_kernel(const __grid_cons
               last[k] = now;
             }
             h[k] = fma2(h[k], now, mul2(sx, k == i ? bb.x : bb.y));
-            y[k - i] = fma2(h[k], k == i ? cc.x : cc.y, y[k - i]);
+            y = k == 0 ? mul2(h[k], cc.x) : fma2(h[k], k == i ? cc.x : cc.y, y);
           }
         }
         float lo, hi;
-        unpair(add2(y[0], y[1]), lo, hi);
+        unpair(y, lo, hi);
         ys[u] = lo + hi;
       }
 #pragma unroll
