@@ -201,3 +201,24 @@ def test_reference_product_against_the_library():
     for act, f in ((None, lambda v: v), ("silu", torch.nn.functional.silu),
                    ("gelu", torch.nn.functional.gelu), ("softplus", torch.nn.functional.softplus)):
         assert torch.allclose(mixref.linear(x, w, b, act=act)[0], f(y), rtol=1e-12, atol=1e-14)
+
+
+def test_the_short_way_leaves_what_it_does_not_take():
+    """The extension module returns None for what the general checks have to answer, and
+    they do."""
+    bind = kl.bind()
+    x, w = torch.zeros(2, 8, dtype=torch.bfloat16), torch.zeros(8, 8, dtype=torch.bfloat16)
+    assert bind.linear(x, w, x, None, None, 0, None, None) is None           # no CUDA tensors
+    assert bind.linear(None, w, x, None, None, 0, None, None) is None
+    assert bind.linear(3, "w", [], None, None, 0, None, None) is None
+    assert bind.conv_prompt(*[x] * 8, True, None, None) is None
+    assert bind.conv_prompt(*[None] * 11) is None
+    assert bind.ssm_prompt(*[x] * 14, None, None, 0, None) is None
+    assert bind.ssm_prompt(*[None] * 18) is None
+    for fn, n in ((bind.linear, 7), (bind.conv_prompt, 0), (bind.ssm_prompt, 19), (bind.setup, 3)):
+        with pytest.raises(TypeError):
+            fn(*[None] * n)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.kda_linear(x=x, weight=w, output=x)
+    with pytest.raises(TypeError):
+        api.kda_linear(x=None, weight=w, output=x)

@@ -14,6 +14,7 @@ from linear_attention_recurrent_kda_gb300 import lib as kl
 from linear_attention_recurrent_kda_gb300.api import (KdaConvStep, KdaSsmStep, kda_conv_prompt,
                                                       kda_linear, kda_ssm_prompt)
 from tests import mixref
+from tests.test_conv_gpu import make as make_conv
 from tests.test_ssm_gpu import i32
 from tests.test_ssm_gpu import make as make_ssm
 
@@ -226,3 +227,78 @@ def test_a_graph_of_the_whole_step_while_eager_calls_run():
         assert torch.equal(a, b)
     side.synchronize()
     assert torch.equal(other, clean)
+
+
+class Counted:
+    """The short way from Python, with what it took counted; or one that takes nothing."""
+
+    def __init__(self, inner):
+        self.inner, self.took = inner, 0
+
+    def __getattr__(self, name):
+        def call(*args):
+            rc = getattr(self.inner, name)(*args) if self.inner else None
+            self.took += rc is not None
+            return rc
+        return call
+
+
+def _three(stream, out):
+    """A product, a convolution and a scan on slices, with everything that may be there."""
+    g = torch.Generator().manual_seed(12)
+    x, w = (torch.randn(*s, generator=g).to(BF).cuda() for s in ((5, 48), (24, 48)))
+    torch.cuda.synchronize()
+    kda_linear(x=x[:, :40], weight=torch.nn.Parameter(w[:, :40]), output=out["product"][:, :24],
+               bias=w[0, :24].contiguous(), residual=x[:, 8:32], activation="gelu",
+               err=out["err"], stream=stream)
+    kda_linear(x=x[:1, :40], weight=w[:, :40], output=out["one"], stream=stream)
+    seq = dict(seq_starts=i32([0, 1, 30]), src_slots=i32([1, 2]), dst_slots=i32([3, 2]))
+    d, y = make_conv(30, 48, seed=3)
+    torch.cuda.synchronize()
+    kda_conv_prompt(**dict(d, output=out["conv"]), **seq, err=out["err"], stream=stream)
+    out["window"] = d["window"]
+    d, state = make_ssm(30, 64, seed=4)
+    torch.cuda.synchronize()
+    kda_ssm_prompt(**d, **seq, output=out["scan"], state=state, err=out["err"], max_seq=29, stream=stream)
+    out["state"] = state
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_the_short_way_and_the_general_one(monkeypatch, own_stream):
+    """The same bits by both, and the short way takes all of them."""
+    stream = torch.cuda.Stream() if own_stream else None
+    short, general = Counted(kl.bind()), Counted(None)
+    got = []
+    for way in (short, general):
+        monkeypatch.setattr(kl, "_bind", way)
+        out = dict(product=torch.zeros(5, 32, dtype=BF, device="cuda"), one=torch.zeros(1, 24, dtype=BF, device="cuda"),
+                   conv=torch.zeros(30, 48, dtype=BF, device="cuda"), scan=torch.zeros(30, 64, dtype=BF, device="cuda"),
+                   err=torch.zeros(1, dtype=torch.int32, device="cuda"))
+        _three(stream, out)
+        got.append(out)
+    assert short.took == 4 and general.took == 0
+    for k in got[0]:
+        assert torch.equal(got[0][k], got[1][k]), k
+    assert (got[0]["product"][:, :24] != 0).any() and (got[0]["product"][:, 24:] == 0).all()
+
+
+def test_the_short_way_leaves_rare_calls():
+    bind = kl.bind()
+    x, w = torch.zeros(4, 16, dtype=BF, device="cuda"), torch.zeros(8, 16, dtype=BF, device="cuda")
+    out = torch.zeros(4, 8, dtype=BF, device="cuda")
+    assert bind.linear(x, w, out, None, None, 0, None, None) == 0
+    for args in ((x.float(), w, out), (x, w.float(), out), (x, w, out.T), (x.T, w, out), (x, w[:, :8], out),
+                 (x, w, out[:, :7]), (x[0], w, out), (x, w, out.cpu()), (x, w, None), (x[:, ::2], w[:, :8], out)):
+        assert bind.linear(*args, None, None, 0, None, None) is None
+    for bias in (out[0, :7], out, out[0].float(), out[0].cpu()):
+        assert bind.linear(x, w, out, bias, None, 0, None, None) is None
+    assert bind.linear(x, w, out, None, None, 0, out, None) is None
+    assert bind.linear(x, w, out, None, None, 0, None, "a stream") is None
+    with pytest.raises(kl.KdaError):                  # it is the library that refuses this
+        kda_linear(x=torch.zeros(4, 24, dtype=BF, device="cuda")[:, 1:17], weight=w, output=out)
+    with pytest.raises(ValueError, match="shape"):
+        kda_linear(x=x, weight=w, output=out[:, :7])
+    with pytest.raises(ValueError, match="adjacent"):
+        kda_linear(x=torch.zeros(16, 4, dtype=BF, device="cuda").T, weight=w, output=out)
+    torch.cuda.synchronize()
