@@ -6,7 +6,8 @@
 // 5.1 TB/s (0.75 of the copy's rate), 65% of the issue slots taken.  Steps, gates and
 // outputs by every lane of a channel for itself 75.7 us, a polynomial for each state by
 // itself 55.3; 8 requests a thread 64 (134 registers), 64 or 256 threads a CTA 50 and 51,
-// requests along a second grid dimension 50.7.  4 x 1024: 3.0 us, a launch
+// requests along a second grid dimension 50.7, 8 to 32 requests one after another in a CTA
+// 52 to 56, 10 CTAs an SM in fewer registers 57.  4 x 1024: 3.0 us, a launch
 // (4.1, and 51 for the large one, where it does not start while the kernel before ends).
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
