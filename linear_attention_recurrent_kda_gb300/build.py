@@ -36,7 +36,7 @@ PROBE_SOURCES = [os.path.join(CSRC, "kda_probe.cu")]
 HEADERS = [os.path.join(INCLUDE, "kda.h"), os.path.join(INCLUDE, "kda_probe.h"),
            os.path.join(CSRC, "kda_device.cuh"), os.path.join(CSRC, "kda_lin.cuh"),
            os.path.join(CSRC, "kda_rows.cuh"), os.path.join(CSRC, "kda_tc.cuh"),
-           os.path.join(CSRC, "kda_ssm.cuh"),
+           os.path.join(CSRC, "kda_ssm.cuh"), os.path.join(CSRC, "kda_linear_tiles.h"),
            os.path.join(CSRC, "kda_host.h")]
 BIND_PATH = os.path.join(HERE, "kda_bind-%s-torch%s.so" % (sysconfig.get_config_var("SOABI"),
                                                             importlib.metadata.version("torch")))

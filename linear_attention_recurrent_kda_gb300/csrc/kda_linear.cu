@@ -15,6 +15,7 @@
 #include "../../include/kda.h"
 #include "kda_device.cuh"
 #include "kda_host.h"
+#include "kda_linear_tiles.h"
 #include "kda_rows.cuh"
 #include "kda_tc.cuh"
 
@@ -389,11 +390,10 @@ static int launch_one(const kda_linear_args *a, Params &p, int dev, int sms, cud
 // shared memory, 64 features at a time, the residual in by TMA and the output out by
 // TMA, which clips it (to whole vectors of 8: a copy that ends inside one wrote an
 // element behind; threads store the last few features).
-constexpr int kTileRows = 256, kTileCols = 256, kTileStages = 5;     // of a pair
+constexpr int kTileStages = 5;
 constexpr int kTileThreads = 640;                // TMA, products, 2 idle; 16 epilogue warps
 constexpr int kTileStage = (kTileRows + kTileCols) / 2 * kK * 2;     // of a CTA
-constexpr int kChunk = 32 * 64 * 2;              // bytes of a warp's 32 tokens, 64 features
-constexpr int kGroupRows = 8;                    // tiles along the tokens that run side by side
+constexpr int kChunk = kChunkRows * kChunkCols * 2;                  // bytes of a warp's part of a tile
 
 struct TileCtrl {
   uint64_t full[kTileStages], empty[kTileStages], sums_full[2], sums_empty[2], residual[16];
@@ -431,17 +431,6 @@ __device__ __forceinline__ void pair_commit(uint64_t *bar) {
 // the output's copy, too: 1500 cycles, 9159 x 256 x 4096 25.1 instead of 19.3 us.)
 __device__ __forceinline__ void arrive_in(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-struct Tile {
-  int row, col;
-};
-// Tiles in groups of kGroupRows along the tokens, so that those that run at a time
-// share their operands in L2.
-__device__ __forceinline__ Tile tile_of(int n, int tiles_m, int tiles_n) {
-  const int group = n / (kGroupRows * tiles_n), first = group * kGroupRows;
-  const int high = min(kGroupRows, tiles_m - first), at = n - first * tiles_n;
-  return Tile{(first + at % high) * kTileRows, at / high * kTileCols};
 }
 
 template <int kAct>
@@ -539,26 +528,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
     const bool leader = lane == 0;
     uint8_t *const chunk = chunks + (warp - 4) * kChunk, *const mine = chunk + lane * 128;
     uint64_t *const residual = &c.residual[warp - 4];
-    auto chunk_of = [&](int q, Tile *at) {         // whether there is one
-      const int n = pair0 + q * pairs;
-      if (n >= tiles) return false;
-      *at = tile_of(n, tiles_m, tiles_n);
-      at->row += 128 * rank + 32 * w4;
-      at->col += group * 64;
-      return true;
-    };
-    auto fetch = [&](int q) {                      // a chunk's residual
-      Tile at;
-      if (!chunk_of(q, &at) || at.col >= p.outer || at.row >= p.rows) return;
+    const Chunks chunks_of = {p.rows, p.outer, pair0, pairs, 128 * rank + kChunkRows * w4, group * kChunkCols};
+    uint32_t loads = 0;
+    auto fetch = [&](const Tile &at) {             // a chunk's residual
+      if (!leader || !p.residual) return;
+      bulk_wait_read(0);                           // the last output has left the buffer
       mbar_arrive_expect_tx(residual, kChunk);
       tma_load(chunk, &rmap, at.col, at.row, residual);
     };
-    uint32_t loads = 0;
-    if (leader && p.residual) fetch(0);
-    Tile at;
-    for (int q = 0; chunk_of(q, &at); ++q) {
+    auto work = [&](int q, const Tile &at, bool there) {
       const int half = q & 1;
-      const bool there = at.col < p.outer && at.row < p.rows;
       const int left = p.outer - at.col;           // features of the chunk, where fewer than 64
       uint4 bias[4];                               // of the next 32 features
       auto ahead = [&](int z) {
@@ -572,7 +551,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
       tc_fence_after();
       if (p.residual && there) ok &= wait_phase(residual, loads++ & 1, &c.abort);
       if (leader) bulk_wait_read(0);               // the last output has left the buffer
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (!__all_sync(0xffffffffu, ok)) return false;
       const uint32_t from =
           tmem + (static_cast<uint32_t>(w4 * 32) << 16) + half * kTileCols + group * 64;
 #pragma unroll
@@ -626,18 +605,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
             if (e >= (end & ~7) && e < end) out[e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
         }
       }
-      if (!there) continue;
+      if (!there) return true;
       fence_proxy_async_smem();
       __syncwarp();
       if (leader) {
         tma_store(&omap, at.col, at.row, chunk);
         bulk_commit();
-        if (p.residual) {
-          bulk_wait_read(0);                       // the buffer is free for the next residual
-          fetch(q + 1);
-        }
       }
-    }
+      return true;
+    };
+    walk_chunks(chunks_of, fetch, work);
     if (leader) bulk_wait_all();
   }
   __syncwarp();
