@@ -611,6 +611,12 @@ typedef struct kda_linear_args {
  * `stream`. */
 int kda_linear(const kda_linear_args *args, void *stream);
 
+/* The same in a form of the caller's choice.  path 0: kda_linear's own; 1: 128 columns of
+ * output and up to 256 rows to a block of threads or a cluster of them (few tiles); 2:
+ * 256 x 256 to a pair of them, which takes several in turn (many tiles; outer >= 8).
+ * Further errors: KDA_ERR_PATH, and KDA_ERR_SHAPE where a form does not take the sizes. */
+int kda_linear_path(const kda_linear_args *args, int32_t path, void *stream);
+
 /* Self-test of the bounded on-chip wait of the KDA step, the replay and the
  * output projection: one CTA waits on an mbarrier that nothing completes; the
  * wait gives up after its wall-clock limit (2 s), KDA_DEVERR_TIMEOUT is OR-ed

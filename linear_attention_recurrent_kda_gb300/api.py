@@ -388,7 +388,7 @@ def _state(state, H, index):
     return ptr, _count("state", state.shape[0])
 
 
-def _run(entry, args, index, stream):
+def _run(entry, args, index, stream, *more):
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(index)
     elif stream.device_index != index:
@@ -397,12 +397,17 @@ def _run(entry, args, index, stream):
         handle = stream.cuda_stream
     # the library launches on the current device: make it the tensors' one
     if torch._C._cuda_getDevice() == index:
-        rc = _lib.call(entry, args, handle)
+        rc = _lib.call(entry, args, handle, *more)
     else:
         with torch.cuda.device(index):
-            rc = _lib.call(entry, args, handle)
+            rc = _lib.call(entry, args, handle, *more)
     if rc != _lib.KDA_SUCCESS:
         raise _lib.KdaError(rc, _lib.strerror(rc))
+
+
+def _path(path):
+    """A form's number; -1, which the library refuses, for what its 32 bits do not hold."""
+    return path if 0 <= path < 1 << 31 else -1
 
 
 def _done(rc):
@@ -761,15 +766,16 @@ ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "gelu": 2, "softplus": 3}
 
 
 def kda_linear(*, x, weight, output, bias=None, residual=None, activation: Optional[str] = None,
-               err=None, stream: Optional[torch.cuda.Stream] = None) -> None:
+               err=None, path: int = 0, stream: Optional[torch.cuda.Stream] = None) -> None:
     """output = act(x weight^T + bias) + residual (include/kda.h ``kda_linear``).
 
     ``x`` bf16 [rows, inner], ``weight`` bf16 [outer, inner], ``residual`` and
     ``output`` bf16 [rows, outer] (each may be a slice of wider rows; the residual may
     be the output itself); ``bias`` bf16 [outer]; ``activation`` None, "none",
-    "silu", "gelu" (with erf) or "softplus"."""
+    "silu", "gelu" (with erf) or "softplus".  ``path``: 0 = automatic, 1 = the form for few
+    tiles, 2 = the form for many (``kda_linear_path``)."""
     act = ACTIVATIONS.get(activation)
-    if act is not None and _done((_lib._bind or _lib.bind()).linear(
+    if act is not None and path == 0 and _done((_lib._bind or _lib.bind()).linear(
             x, weight, output, bias, residual, act, err, stream)):
         return
     index = _cuda_index("x", x)
@@ -785,7 +791,7 @@ def kda_linear(*, x, weight, output, bias=None, residual=None, activation: Optio
     (xp, xs), (wp, ws) = _rows("x", x, rows, K, index), _rows("weight", weight, N, K, index)
     op, os_ = _rows("output", output, rows, N, index)
     rp, rs = (None, 0) if residual is None else _rows("residual", residual, rows, N, index)
-    _run("kda_linear", _lib.KdaLinearArgs(
+    _run("kda_linear_path", _lib.KdaLinearArgs(
         rows, K, N, act, xs, ws, rs, os_, xp, wp,
         None if bias is None else _want("bias", bias, _BF16, (N,), index), rp, op,
-        None if err is None else _want("err", err, _I32, None, index)), index, stream)
+        None if err is None else _want("err", err, _I32, None, index)), index, stream, _path(path))

@@ -702,12 +702,13 @@ typedef void (*ProductKernel)(const Params, const CUtensorMap, const CUtensorMap
 struct Plan {
   int tile_n, split;
 };
-static Plan plan_of(int rows, int blocks, int inner, int outer, int sms, int eights) {
+static Plan plan_of(int rows, int blocks, int inner, int outer, int sms, int eights, int path) {
   const int64_t tiles_m = (outer + kM - 1) / kM;
   const double weights = 2.0 * inner * outer / 7.5e6;
   Plan best = {0, 1};
   double least = 1e300;
-  if (outer >= 8 && rows > 64) {
+  if (path == 2) return best;
+  if (path == 0 && outer >= 8 && rows > 64) {
     const int64_t tiles = static_cast<int64_t>((rows + kTileRows - 1) / kTileRows) *
                           ((outer + kTileCols - 1) / kTileCols);
     const double tile = blocks * 0.3 > 1.4 ? blocks * 0.3 : 1.4;
@@ -736,7 +737,7 @@ static Plan plan_of(int rows, int blocks, int inner, int outer, int sms, int eig
   return best;
 }
 
-static int run(const kda_linear_args *a, cudaStream_t stream) {
+static int run(const kda_linear_args *a, int path, cudaStream_t stream) {
   if (!a) return KDA_ERR_NULL_ARGS;
   if (a->rows < 0 || a->inner < 1 || a->outer < 0 || a->rows > kMostRows || a->inner > kMostRows ||
       a->outer > kMostRows)
@@ -745,7 +746,9 @@ static int run(const kda_linear_args *a, cudaStream_t stream) {
       !stride_ok(a->o_stride, a->outer) || (a->residual && !stride_ok(a->r_stride, a->outer)))
     return KDA_ERR_SHAPE;
   if (a->activation < KDA_ACT_NONE || a->activation > KDA_ACT_SOFTPLUS) return KDA_ERR_ACTIVATION;
+  if (path < 0 || path > 2) return KDA_ERR_PATH;
   if (a->rows == 0 || a->outer == 0) return KDA_SUCCESS;
+  if (path == 2 && a->outer < 8) return KDA_ERR_SHAPE;   // (an output's tensor map of whole vectors)
   if (!a->x || !a->weight || !a->output) return KDA_ERR_NULL_POINTER;
   if (!aligned(a->x, 16) || !aligned(a->weight, 16) || !aligned(a->bias, 16) ||
       !aligned(a->residual, 16) || !aligned(a->output, 16) || !aligned(a->err, 4))
@@ -764,7 +767,7 @@ static int run(const kda_linear_args *a, cudaStream_t stream) {
   p.residual = static_cast<const __nv_bfloat16 *>(a->residual);
   p.output = static_cast<__nv_bfloat16 *>(a->output);
   p.err = a->err;
-  if (a->rows == 1 && a->inner <= kOneMost) return launch_one(a, p, dev, df.sms, stream);
+  if (path == 0 && a->rows == 1 && a->inner <= kOneMost) return launch_one(a, p, dev, df.sms, stream);
   p.blocks = (a->inner + kK - 1) / kK;
   static const ProductKernel kernels[4] = {product_kernel<KDA_ACT_NONE>, product_kernel<KDA_ACT_SILU>,
                                            product_kernel<KDA_ACT_GELU>, product_kernel<KDA_ACT_SOFTPLUS>};
@@ -774,7 +777,7 @@ static int run(const kda_linear_args *a, cudaStream_t stream) {
     return KDA_ERR_LAUNCH;
   static std::atomic<int> known[kMaxDevices];
   const int eights = clusters_of(known, dev, reinterpret_cast<const void *>(kernel), 8, kThreads, smem_of(kRing));
-  const Plan plan = plan_of(a->rows, p.blocks, a->inner, a->outer, df.sms, eights);
+  const Plan plan = plan_of(a->rows, p.blocks, a->inner, a->outer, df.sms, eights, path);
   if (plan.tile_n == 0) return launch_tiles(a, p, dev, df.sms, stream);
   p.tile_n = plan.tile_n;
   p.split = plan.split;
@@ -798,5 +801,9 @@ static int run(const kda_linear_args *a, cudaStream_t stream) {
 }  // namespace kda
 
 extern "C" int kda_linear(const kda_linear_args *args, void *stream) {
-  return kda::linear::run(args, static_cast<cudaStream_t>(stream));
+  return kda::linear::run(args, 0, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int kda_linear_path(const kda_linear_args *args, int32_t path, void *stream) {
+  return kda::linear::run(args, path, static_cast<cudaStream_t>(stream));
 }

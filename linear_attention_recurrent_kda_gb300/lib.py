@@ -40,7 +40,7 @@ EXPORTED = ("kda_decode", "kda_verify", "kda_step_noalloc", "kda_recover", "kda_
             "kda_lin_prompt_workspace", "kda_lin_prompt", "kda_lin_step",
             "kda_snapshot_save", "kda_snapshot_load",
             "kda_conv_prompt", "kda_conv_step", "kda_ssm_prompt_workspace", "kda_ssm_prompt",
-            "kda_ssm_step", "kda_linear",
+            "kda_ssm_step", "kda_linear", "kda_linear_path",
             "kda_selftest_wait_timeout", "kda_selftest_lin_wait_timeout",
             "kda_strerror", "kda_abi_version")
 
@@ -238,7 +238,9 @@ def load(path: str | None = None) -> ctypes.CDLL:
                             ("kda_ssm_prompt", [ctypes.POINTER(KdaSsmPromptArgs), _P],
                              ctypes.c_int),
                             ("kda_ssm_step", [ctypes.POINTER(KdaSsmStepArgs), _P], ctypes.c_int),
-                            ("kda_linear", [ctypes.POINTER(KdaLinearArgs), _P], ctypes.c_int)):
+                            ("kda_linear", [ctypes.POINTER(KdaLinearArgs), _P], ctypes.c_int),
+                            ("kda_linear_path", [ctypes.POINTER(KdaLinearArgs), ctypes.c_int32, _P],
+                             ctypes.c_int)):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, res
     for fn in (lib.kda_selftest_wait_timeout, lib.kda_selftest_lin_wait_timeout):
@@ -256,9 +258,10 @@ def strerror(code: int) -> str:
     return load().kda_strerror(int(code)).decode()
 
 
-def call(entry: str, args, stream_handle: int) -> int:
-    """Raw call: returns the library's code without raising."""
-    return getattr(_lib or load(), entry)(args, stream_handle or None)
+def call(entry: str, args, stream_handle: int, *more) -> int:
+    """Raw call: returns the library's code without raising (``more``: what an entry takes
+    between its struct and its stream)."""
+    return getattr(_lib or load(), entry)(args, *more, stream_handle or None)
 
 
 _bind = None
