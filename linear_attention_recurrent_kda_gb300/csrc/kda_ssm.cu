@@ -27,19 +27,23 @@ constexpr int kThreads = 128;
 constexpr int kRequests = 4;     // of a thread: they share its part of a
 
 // h <- 2^x h + add, two states: where the decay is near 1 (down to 2^-1/4) as
-// h + h (2^x - 1) + add, for the reason at decay_of; 2^x - 1 there is x times a
-// polynomial (interpolated at the Chebyshev points, degree 3, off by 2^-24 of itself).
+// h + h (2^x - 1) + add, for the reason at decayed; 2^x - 1 there is x times a
+// polynomial (interpolated at the Chebyshev points, degree 3, off by 2^-24 of itself).  An
+// infinite state stays (its parts would cancel to NaN), for 1% of the large step's time in
+// as many registers (70 without a bound of them: 52.3 us).
 __device__ __forceinline__ f32x2 decayed2(f32x2 h, f32x2 x, f32x2 add) {
   f32x2 t = fma2(two(8.977169171e-03f), x, two(5.540518463e-02f));
   t = fma2(t, x, two(2.402215898e-01f));
   t = mul2(fma2(t, x, two(6.931471229e-01f)), x);
-  float lo, hi, tl, th;
+  float lo, hi, tl, th, hl, hh;
   unpair(x, lo, hi);
   unpair(t, tl, th);
-  const bool sl = fabsf(lo + 0.125f) <= 0.125f, sh = fabsf(hi + 0.125f) <= 0.125f;
+  unpair(h, hl, hh);
+  const bool sl = fabsf(lo + 0.125f) <= 0.125f && fabsf(hl) < INFINITY;
+  const bool sh = fabsf(hi + 0.125f) <= 0.125f && fabsf(hh) < INFINITY;
   const f32x2 change = pair(sl ? tl : exp2_approx(lo), sh ? th : exp2_approx(hi));
-  const f32x2 keep = pair(sl ? 1.0f : 0.0f, sh ? 1.0f : 0.0f);
-  return fma2(h, keep, fma2(h, change, add));
+  const f32x2 keep = pair(sl ? hl : 0.0f, sh ? hh : 0.0f);
+  return add2(keep, fma2(h, change, add));
 }
 
 // A thread: 4 states of a channel, of kRequests requests, all loads in flight at
@@ -47,8 +51,8 @@ __device__ __forceinline__ f32x2 decayed2(f32x2 h, f32x2 x, f32x2 add) {
 // one lane's for each request.  Groups of channels are multiples of 8, so a warp's
 // channels are of one group, and all there or none.
 template <int kStates>
-__global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ Params p,
-                                                        int blocks) {
+__global__ void __launch_bounds__(kThreads, 8) step_kernel(const __grid_constant__ Params p,
+                                                           int blocks) {
   constexpr int kLanes = kStates / 4;
   follow();
   const int block = blockIdx.x % blocks, first = blockIdx.x / blocks * kRequests;

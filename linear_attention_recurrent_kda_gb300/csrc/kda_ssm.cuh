@@ -7,6 +7,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "../../include/kda.h"
 #include "kda_device.cuh"
 #include "kda_rows.cuh"
@@ -33,13 +35,6 @@ struct Params {
   float *ws_state, *ws_step;
 };
 
-// A token's decay 2^x as keep + change, keep 0 or 1: near 1 a factor rounded to
-// FP32 is off the same way at every token of a constant step, and a slow state
-// drifts (2^-25 a token); 2^x - 1 is off by 2^-23 of itself, which no number of
-// tokens adds up.
-struct Decay {
-  float keep, change;
-};
 // 2^x - 1 on [-1, 0]: x times a polynomial, interpolated at the Chebyshev points, degree 5,
 // off by 2^-26 of itself.
 __device__ __forceinline__ float less_one(float x) {
@@ -51,12 +46,13 @@ __device__ __forceinline__ float less_one(float x) {
   t = __fmaf_rn(t, x, 6.93147182e-1f);
   return t * x;
 }
-__device__ __forceinline__ Decay decay_of(float x) {
-  const bool slow = fabsf(x + 0.5f) <= 0.5f;
-  return Decay{slow ? 1.0f : 0.0f, slow ? less_one(x) : exp2_approx(x)};
-}
-__device__ __forceinline__ float decayed(float h, const Decay &d, float add) {
-  return __fmaf_rn(h, d.keep, __fmaf_rn(h, d.change, add));
+// 2^x h + add; where the decay is down to 1/2 as h + h (2^x - 1) + add: near 1 a factor
+// rounded to FP32 is off the same way at every token of a constant step, and a slow state
+// drifts (2^-25 a token); 2^x - 1 is off by 2^-23 of itself, which no number of tokens
+// adds up.  (Not so an infinite state, whose parts would cancel to NaN.)
+__device__ __forceinline__ float decayed(float h, float x, float add) {
+  const bool slow = fabsf(x + 0.5f) <= 0.5f && fabsf(h) < INFINITY;
+  return (slow ? h : 0.0f) + __fmaf_rn(h, slow ? less_one(x) : exp2_approx(x), add);
 }
 
 // 4 BF16 values of an 8-byte vector.

@@ -13,7 +13,7 @@
 // drift by 2e-5 of itself or more, to one side.  So over a tile the product of the
 // factors that were used is kept too, less 1 (m <- m + q + m q, with q = e e' - 1 of two
 // tokens in one operation), and at the end of two tiles the state is corrected by
-// (exp(a sum s) - 1 - m) h_0, with exp - 1 from a polynomial (decay_of): 1.5 operations
+// (exp(a sum s) - 1 - m) h_0, with exp - 1 from a polynomial (less_one): 1.5 operations
 // per token and state and 20 per two tiles and state, where a polynomial at every
 // token would take 8.
 //
@@ -127,13 +127,14 @@ __device__ __forceinline__ void pass_pieces(const Params &p, int64_t first, int 
       unpair(h[i], lo, hi);
       unpair(a[i], al, ah);
       unpair(u[i], ul, uh);
-      h[i] = pair(decayed(lo, decay_of(s * al), ul), decayed(hi, decay_of(s * ah), uh));
+      h[i] = pair(decayed(lo, s * al, ul), decayed(hi, s * ah, uh));
     }
   }
 }
 
 // h + h_0 (exp(a s) - 1 - used), for decays down to 1/2: `used` is off by 2^-24 of 1,
-// which a stronger decay's own state would show, and its states remember 50 tokens.
+// which a stronger decay's own state would show, and its states remember 50 tokens.  (An
+// infinite h_0 has nothing to correct.)
 __device__ __forceinline__ f32x2 corrected(f32x2 h, f32x2 h0, f32x2 a, float s, f32x2 product) {
   float v[2], v0[2], x[2], used[2];
   unpair(h, v[0], v[1]);
@@ -143,7 +144,7 @@ __device__ __forceinline__ f32x2 corrected(f32x2 h, f32x2 h0, f32x2 a, float s, 
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const float z = s * x[i];
-    v[i] = fabsf(z + 0.5f) <= 0.5f ? __fmaf_rn(v0[i], less_one(z) - used[i], v[i]) : v[i];
+    v[i] = fabsf(z + 0.5f) <= 0.5f && fabsf(v0[i]) < INFINITY ? __fmaf_rn(v0[i], less_one(z) - used[i], v[i]) : v[i];
   }
   return pair(v[0], v[1]);
 }
