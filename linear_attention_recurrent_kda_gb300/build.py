@@ -6,7 +6,8 @@ convolution, scan, product and self-test kernels; the C ABI of include/kda.h).
 ``libkda_probe_gb300.so``: the measurement probe of include/kda_probe.h, a bench
 instrument kept out of the product library.
 ``kda_bind-<python>-torch<version>.so``: the short way from Python to the calls whose
-host side is most of their time, against the headers of the installed PyTorch.
+host side is most of their time, against the headers of the installed PyTorch.  The
+library does not need it: where it cannot be built the calls take the general way.
 Every translation unit is compiled by its own nvcc process (g++ for the binding), in
 parallel, with a single ``-gencode arch=compute_103a,code=sm_103a``; each library is
 linked by one more nvcc call and sits next to this file.
@@ -20,6 +21,7 @@ import shutil
 import subprocess
 import sysconfig
 import tempfile
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -38,8 +40,19 @@ HEADERS = [os.path.join(INCLUDE, "kda.h"), os.path.join(INCLUDE, "kda_probe.h"),
            os.path.join(CSRC, "kda_rows.cuh"), os.path.join(CSRC, "kda_tc.cuh"),
            os.path.join(CSRC, "kda_ssm.cuh"), os.path.join(CSRC, "kda_linear_tiles.h"),
            os.path.join(CSRC, "kda_host.h")]
-BIND_PATH = os.path.join(HERE, "kda_bind-%s-torch%s.so" % (sysconfig.get_config_var("SOABI"),
-                                                            importlib.metadata.version("torch")))
+
+
+def _bind_path():
+    """Of the binding for this interpreter and PyTorch; None where PyTorch does not say its
+    version (a module for another one's headers must not be loaded)."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return None
+    return os.path.join(HERE, "kda_bind-%s-torch%s.so" % (sysconfig.get_config_var("SOABI"), version))
+
+
+BIND_PATH = _bind_path()
 BIND_SOURCE = os.path.join(CSRC, "kda_bind.cpp")
 LIBS = ((LIB_PATH, SOURCES), (PROBE_LIB_PATH, PROBE_SOURCES))
 
@@ -63,8 +76,12 @@ def _stale(lib: str, sources) -> bool:
     return any(os.path.getmtime(s) > t for s in list(sources) + HEADERS)
 
 
+def _bind_stale() -> bool:
+    return BIND_PATH is not None and _stale(BIND_PATH, [BIND_SOURCE])
+
+
 def is_stale() -> bool:
-    return any(_stale(lib, srcs) for lib, srcs in LIBS + ((BIND_PATH, [BIND_SOURCE]),))
+    return any(_stale(lib, srcs) for lib, srcs in LIBS) or _bind_stale()
 
 
 def _bind_command(out: str):
@@ -80,22 +97,41 @@ def _bind_command(out: str):
                "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
 
 
+def _publish(made: str, path: str) -> None:
+    """Puts a finished file in place at once (processes may build side by side)."""
+    fd, new = tempfile.mkstemp(dir=os.path.dirname(path), prefix=os.path.basename(path) + ".")
+    os.close(fd)
+    try:
+        shutil.copyfile(made, new)
+        shutil.copymode(made, new)
+        os.replace(new, path)
+    except BaseException:
+        os.unlink(new)
+        raise
+
+
+def _start(cmd):
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile the libraries that are missing or older than their sources.
 
     Each translation unit compiles in its own nvcc process (all in parallel),
-    then one nvcc call per library links it.  Returns the product library's
-    path."""
+    then one nvcc call per library links it.  A binding that cannot be built is a
+    warning.  Returns the product library's path."""
     todo = [(lib, srcs) for lib, srcs in LIBS if force or _stale(lib, srcs)]
-    bind = force or _stale(BIND_PATH, [BIND_SOURCE])
+    bind = BIND_PATH is not None and (force or _bind_stale())
     if not todo and not bind:
         return LIB_PATH
     with tempfile.TemporaryDirectory() as tmp:
-        procs = []
+        binding, trouble = None, ""
         if bind:
-            procs.append((BIND_SOURCE, subprocess.Popen(
-                _bind_command(os.path.join(tmp, "kda_bind.so")), stdout=subprocess.PIPE,
-                stderr=subprocess.STDOUT, text=True)))
+            try:
+                binding = _start(_bind_command(os.path.join(tmp, "kda_bind.so")))
+            except (OSError, RuntimeError, AttributeError) as e:     # no compiler, no PyTorch
+                trouble = repr(e)
+        procs = []
         objs = {lib: [] for lib, _ in todo}
         for lib, srcs in todo:
             for src in srcs:
@@ -103,8 +139,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 cmd = [nvcc()] + NVCC_FLAGS + ["-I", INCLUDE, "-c", src, "-o", obj]
                 if verbose:
                     cmd.insert(1, "-Xptxas=-v")
-                procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE,
-                                                    stderr=subprocess.STDOUT, text=True)))
+                procs.append((src, _start(cmd)))
                 objs[lib].append(obj)
         logs = []
         for src, pr in procs:
@@ -112,9 +147,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
             logs.append(out)
             if pr.returncode != 0:
                 raise RuntimeError(f"the compiler failed on {src}:\n{out}")
-        if bind:
-            shutil.copyfile(os.path.join(tmp, "kda_bind.so"), BIND_PATH + ".new")
-            os.replace(BIND_PATH + ".new", BIND_PATH)
         for lib, _ in todo:
             out = os.path.join(tmp, os.path.basename(lib))
             link = [nvcc(), "-gencode", "arch=compute_103a,code=sm_103a", "-shared",
@@ -122,7 +154,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
             res = subprocess.run(link, capture_output=True, text=True)
             if res.returncode != 0:
                 raise RuntimeError("nvcc link failed:\n" + res.stdout + res.stderr)
-            os.replace(out, lib)
+            _publish(out, lib)
+        if binding is not None:
+            out, _ = binding.communicate()
+            logs.append(out)
+            if binding.returncode == 0:
+                _publish(os.path.join(tmp, "kda_bind.so"), BIND_PATH)
+            else:
+                trouble = out
+        if trouble:
+            warnings.warn(f"the short way from Python was not built, calls take the general one:\n{trouble}",
+                          RuntimeWarning, stacklevel=2)
         if verbose:
             print("".join(logs))
     return LIB_PATH

@@ -10,6 +10,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 
 from . import build as _build
 
@@ -267,21 +268,46 @@ def call(entry: str, args, stream_handle: int, *more) -> int:
 _bind = None
 
 
+class _General:
+    """In the binding's place where there is none: leaves every call to the general checks."""
+
+    @staticmethod
+    def _leave(*args):
+        return None
+
+    conv_prompt = ssm_prompt = linear = _leave
+
+
+def _load_bind():
+    path = _build.BIND_PATH
+    if path is None:
+        raise ImportError("PyTorch's version is not known")
+    if not os.path.exists(path):
+        _build.build()
+    loader = importlib.machinery.ExtensionFileLoader("kda_bind", path)
+    module = importlib.util.module_from_spec(
+        importlib.util.spec_from_file_location("kda_bind", path, loader=loader))
+    loader.exec_module(module)
+    return module
+
+
 def bind():
     """The short way to kda_conv_prompt, kda_ssm_prompt and kda_linear (building first if
     needed): functions that launch and return the library's code, or return None for
-    what they leave to the general checks."""
+    what they leave to the general checks.  Where the binding cannot be built or loaded
+    they leave everything, after a warning."""
     global _bind
     if _bind is None:
-        if not os.path.exists(_build.BIND_PATH):
-            _build.build()
-        loader = importlib.machinery.ExtensionFileLoader("kda_bind", _build.BIND_PATH)
-        module = importlib.util.module_from_spec(
-            importlib.util.spec_from_file_location("kda_bind", _build.BIND_PATH, loader=loader))
-        loader.exec_module(module)
         lib = load()
-        module.setup(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
-            "kda_conv_prompt", "kda_ssm_prompt_workspace", "kda_ssm_prompt", "kda_linear")))
+        try:
+            module = _load_bind()
+        except (ImportError, OSError) as e:
+            warnings.warn(f"no short way from Python, calls take the general one: {e}", RuntimeWarning,
+                          stacklevel=3)
+            module = _General()
+        else:
+            module.setup(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+                "kda_conv_prompt", "kda_ssm_prompt_workspace", "kda_ssm_prompt", "kda_linear")))
         _bind = module
     return _bind
 
