@@ -433,7 +433,8 @@ int kda_snapshot_load(const kda_snapshot_args *args, void *stream);
  * output are BF16 [channels] and may be slices of wider rows: strides are
  * multiples of 8 elements and at least the row's width.  x, output, weight, bias and
  * window are 16-byte aligned, the index arrays 4.  The output must not overlap
- * the inputs.  (Rows of this call and of those below: up to 2^31 - 256.) */
+ * the inputs.  (Rows and sequences of this call and of those below: up
+ * to 2^31 - 256.) */
 
 /* Arguments of one prompt call (kda_conv_prompt). */
 typedef struct kda_conv_prompt_args {

@@ -319,7 +319,7 @@ static int run_prompt(const kda_conv_prompt_args *a, cudaStream_t stream) {
   if (!a) return KDA_ERR_NULL_ARGS;
   if (const int rc = check(a, a->tokens)) return rc;
   const bool pool = a->src_slots || a->dst_slots;
-  if (a->seqs < 0 || (pool && a->num_slots < 1)) return KDA_ERR_SHAPE;
+  if (a->seqs < 0 || a->seqs > kMostRows || (pool && a->num_slots < 1)) return KDA_ERR_SHAPE;
   if (pool && a->width < a->taps - 1) return KDA_ERR_CONV_WIDTH;
   if (a->seqs == 0 || a->channels == 0) return KDA_SUCCESS;
   if (!a->seq_starts || !a->weight || (pool && !a->window)) return KDA_ERR_NULL_POINTER;

@@ -210,7 +210,7 @@ constexpr int kShortestPiece = 256;      // rows
 static int plan_prompt(const kda_ssm_prompt_args *a, Plan *plan) {
   if (const int rc = check(a, a->tokens)) return rc;
   const bool pool = a->src_slots || a->dst_slots;
-  if (a->seqs < 0 || a->max_seq < 0 || (pool && a->num_slots < 1)) return KDA_ERR_SHAPE;
+  if (a->seqs < 0 || a->seqs > kMostRows || a->max_seq < 0 || (pool && a->num_slots < 1)) return KDA_ERR_SHAPE;
   if (a->path < 0 || a->path > 2) return KDA_ERR_PATH;
   const int64_t longest = a->max_seq < a->tokens ? a->max_seq : a->tokens;
   const int64_t threads = static_cast<int64_t>(a->channels) * (a->states / 16);
