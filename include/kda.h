@@ -505,10 +505,10 @@ int kda_conv_step(const kda_conv_step_args *args, void *stream);
  * no gate).  Rows of x, dt, b, c, z and output are BF16 and may be slices of wider
  * rows: strides are multiples of 8 elements and at least the row's own width.  They,
  * a and state are 16-byte aligned, the other arrays 4.  The output must not overlap
- * the inputs.  a is finite; where it grows (s a > 0), it has to stay below 2^64 over a
- * sequence.  An infinity or NaN reaches later tokens of its sequence and channel as an
- * infinity or NaN; an infinite state stays as it is while the decays since then are above
- * 2^-126. */
+ * the inputs.  A slot has up to 2^31 - 256 states (channels * states).  a is finite;
+ * where it grows (s a > 0), it has to stay below 2^64 over a sequence.  An infinity or NaN
+ * reaches later tokens of its sequence and channel as an infinity or NaN; an infinite
+ * state stays as it is while the decays since then are above 2^-126. */
 
 /* Arguments of one prompt call (kda_ssm_prompt). */
 typedef struct kda_ssm_prompt_args {

@@ -141,6 +141,7 @@ static int check(const Args *a, int64_t rows) {
   if (a->channels < 0 || a->groups < 1 || a->channels % (8 * int64_t(a->groups)) != 0)
     return KDA_ERR_SHAPE;
   if (rows < 0 || rows > kMostRows || (a->states != 16 && a->states != 32 && a->states != 64)) return KDA_ERR_SHAPE;
+  if (int64_t(a->channels) * a->states > kMostRows) return KDA_ERR_SHAPE;
   const int64_t shared = int64_t(a->groups) * a->states;
   if (!stride_ok(a->x_stride, a->channels) || !stride_ok(a->dt_stride, a->channels) ||
       !stride_ok(a->b_stride, shared) || !stride_ok(a->c_stride, shared) ||

@@ -5,7 +5,7 @@ from __future__ import annotations
 import pytest
 
 from linear_attention_recurrent_kda_gb300 import lib as kl
-from tests.test_mix import conv_prompt, ssm_prompt
+from tests.test_mix import conv_prompt, ssm_prompt, ssm_step
 
 
 @pytest.mark.parametrize("seqs", [2 ** 31 - 255, 2 ** 31 - 7, 2 ** 31 - 1])
@@ -16,3 +16,15 @@ def test_sequences_that_bisection_cannot_round_up(seqs):
         args = ssm_prompt(seqs=seqs, channels=16, tokens=1 << 20, max_seq=1 << 20, path=path)
         assert kl.call("kda_ssm_prompt", args, None) == kl.KDA_ERR_SHAPE
         assert kl.ssm_workspace(args) == 0
+
+
+@pytest.mark.parametrize("channels,states,groups", [(1 << 30, 16, 1), (1 << 28, 64, 1), (1 << 26, 64, 1 << 23),
+                                                    ((1 << 27) - 8, 16, 1)])
+def test_channels_times_states_that_32_bits_do_not_count(channels, states, groups):
+    """The kernels number the states of a slot's channels and groups."""
+    sizes = dict(channels=channels, states=states, groups=groups, batch=1)
+    sizes.update({f"{n}_stride": channels for n in ("x", "dt", "z", "o")})
+    sizes.update({f"{n}_stride": groups * states for n in "bc"})
+    assert kl.call("kda_ssm_step", ssm_step(**sizes), None) == kl.KDA_ERR_SHAPE
+    del sizes["batch"]
+    assert kl.call("kda_ssm_prompt", ssm_prompt(**sizes), None) == kl.KDA_ERR_SHAPE
