@@ -208,6 +208,13 @@ struct Plan {
 constexpr int kSms = 152, kCtas = 6;     // pieces: two for each of the 3 CTAs that an SM holds
 constexpr int kShortestPiece = 256;      // rows
 
+// Whether so many sequences or pieces are a grid that can be launched (CTAs are of one
+// group's channels: kda_ssm_prompt.cu).
+static bool launchable(const kda_ssm_prompt_args *a, int64_t units, int held) {
+  const int64_t per = 128 / (a->states / held), span = a->channels / a->groups;
+  return units * a->groups * ((span + per - 1) / per) <= 0x7fffffffll;
+}
+
 static int plan_prompt(const kda_ssm_prompt_args *a, Plan *plan) {
   if (const int rc = check(a, a->tokens)) return rc;
   const bool pool = a->src_slots || a->dst_slots;
@@ -226,7 +233,8 @@ static int plan_prompt(const kda_ssm_prompt_args *a, Plan *plan) {
   plan->held = with8 < with16 ? 8 : 16;
   plan->piece = 0;
   plan->workspace = 0;
-  if (a->path == 1 || blocks == 0 || longest <= kShortestPiece) return KDA_SUCCESS;
+  const int whole = launchable(a, a->seqs, plan->held) ? KDA_SUCCESS : KDA_ERR_SHAPE;
+  if (a->path == 1 || blocks == 0 || longest <= kShortestPiece) return whole;
   // As many pieces as run at a time (each sequence's last one may be short); two passes over
   // all tokens, and each piece sums up those before it.  (One sequence of 2048 x 4096
   // channels 150 us whole, 92 in pieces; of 512 43 and 61; the 8 ragged ones 236 and 336.)
@@ -235,10 +243,12 @@ static int plan_prompt(const kda_ssm_prompt_args *a, Plan *plan) {
   int64_t piece = (a->tokens / pieces + 16) / 16 * 16;
   if (piece < kShortestPiece || piece >= longest) piece = kShortestPiece;
   const double split = std::fmax(1.02e-3 * work, 0.23 * piece) + 1.3 * (longest / piece);
-  if (a->path == 0 && (with8 < with16 ? with8 : with16) < split) return KDA_SUCCESS;
+  if (a->path == 0 && (with8 < with16 ? with8 : with16) < split) return whole;
+  const int64_t units = pieces_of(a->tokens, a->seqs, static_cast<int>(piece));
+  if (!launchable(a, units, 16)) return a->path == 0 ? whole : KDA_ERR_SHAPE;
   plan->held = 16;
   plan->piece = static_cast<int>(piece);
-  plan->workspace = pieces_of(a->tokens, a->seqs, plan->piece) * a->channels * (a->states + 1) * 4;
+  plan->workspace = units * a->channels * (a->states + 1) * 4;
   return KDA_SUCCESS;
 }
 

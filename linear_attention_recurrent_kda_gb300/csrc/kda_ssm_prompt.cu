@@ -548,12 +548,11 @@ static int launch(Params &p, cudaStream_t stream, int dev) {
   p.group_blocks = (p.span + S::kChannels - 1) / S::kChannels;
   p.blocks = p.channels / p.span * p.group_blocks;
   const int64_t units = p.piece > 0 ? pieces_of(p.seqs.tokens, p.seqs.count, p.piece) : p.seqs.count;
-  if (units * p.blocks > 0x7fffffffll) return KDA_ERR_SHAPE;
   static std::atomic<bool> out_done[kMaxDevices];
   if (!set_smem_limit_once(out_done, dev, reinterpret_cast<const void *>(scan_kernel<kStates, kHeld, true>),
                            sizeof(S)))
     return KDA_ERR_LAUNCH;
-  const int grid = static_cast<int>(units * p.blocks);
+  const int grid = static_cast<int>(units * p.blocks);     // (that it is one: plan_prompt)
   if constexpr (kHeld == 16) {
     if (p.piece > 0) {
       static std::atomic<bool> sum_done[kMaxDevices];

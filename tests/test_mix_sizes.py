@@ -28,3 +28,15 @@ def test_channels_times_states_that_32_bits_do_not_count(channels, states, group
     assert kl.call("kda_ssm_step", ssm_step(**sizes), None) == kl.KDA_ERR_SHAPE
     del sizes["batch"]
     assert kl.call("kda_ssm_prompt", ssm_prompt(**sizes), None) == kl.KDA_ERR_SHAPE
+
+
+@pytest.mark.parametrize("path", [0, 1, 2])
+@pytest.mark.parametrize("seqs,channels,states,groups", [(1 << 24, 1 << 20, 16, 1), (1 << 22, 8 << 12, 64, 1 << 12),
+                                                         ((1 << 31) - 256, 1 << 26, 16, 1)])
+def test_no_workspace_for_grids_that_are_refused(seqs, channels, states, groups, path):
+    """More blocks of threads than a launch takes: refused before its workspace is asked for."""
+    sizes = dict(seqs=seqs, channels=channels, states=states, groups=groups, tokens=1 << 14, max_seq=1 << 14)
+    sizes.update({f"{n}_stride": channels for n in ("x", "dt", "z", "o")})
+    sizes.update({f"{n}_stride": groups * states for n in "bc"})
+    assert kl.ssm_workspace(ssm_prompt(path=path, **sizes)) == 0
+    assert kl.call("kda_ssm_prompt", ssm_prompt(path=path, **sizes), None) == kl.KDA_ERR_SHAPE
