@@ -410,6 +410,11 @@ def _path(path):
     return path if 0 <= path < 1 << 31 else -1
 
 
+def _most(max_seq, rows):
+    """The longest sequence's length (-1, which the library refuses, for all below 0)."""
+    return rows if max_seq is None else max(-1, min(int(max_seq), rows))
+
+
 def _done(rc):
     """Whether a call by the short way (csrc/kda_bind.cpp) was made; None leaves it, or
     what is to be said about it, to the checks below."""
@@ -454,8 +459,8 @@ def kda_lin_prompt(*, q, k, v, decay, seq_starts, output, scale: float, state=No
     else:
         state_p, num_slots = _state(state, H, index)
     a = _lib.KdaLinPromptArgs(
-        B, H, Hk, rows, rows if max_seq is None else min(int(max_seq), rows), num_slots, per_row,
-        int(path), qs, ks, vs, os_, qp, kp, vp, dp, sp, src, dst, state_p, op, float(scale),
+        B, H, Hk, rows, _most(max_seq, rows), num_slots, per_row,
+        _path(int(path)), qs, ks, vs, os_, qp, kp, vp, dp, sp, src, dst, state_p, op, float(scale),
         _maybe("err", err, i32, None, index))
     if workspace is not None:
         a.workspace = _want("workspace", workspace, torch.uint8, None, index)
@@ -714,8 +719,8 @@ def kda_ssm_prompt(*, x, dt, a, b, c, seq_starts, output, d=None, z=None, dt_bia
     else:
         state_p, num_slots = _ssm_state(state, C, N, index)
     args = _lib.KdaSsmPromptArgs(
-        B, C, N, G, rows, rows if max_seq is None else min(int(max_seq), rows), num_slots,
-        int(bool(softplus)), int(path), *strides, *ptrs, sp, src, dst, state_p, op,
+        B, C, N, G, rows, _most(max_seq, rows), num_slots,
+        int(bool(softplus)), _path(int(path)), *strides, *ptrs, sp, src, dst, state_p, op,
         _maybe("err", err, torch.int32, None, index))
     if workspace is not None:
         args.workspace = _want("workspace", workspace, torch.uint8, None, index)

@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import pytest
 
+from linear_attention_recurrent_kda_gb300 import api
 from linear_attention_recurrent_kda_gb300 import lib as kl
 from tests.test_mix import conv_prompt, ssm_prompt, ssm_step
 
@@ -40,3 +41,8 @@ def test_no_workspace_for_grids_that_are_refused(seqs, channels, states, groups,
     sizes.update({f"{n}_stride": groups * states for n in "bc"})
     assert kl.ssm_workspace(ssm_prompt(path=path, **sizes)) == 0
     assert kl.call("kda_ssm_prompt", ssm_prompt(path=path, **sizes), None) == kl.KDA_ERR_SHAPE
+
+
+def test_lengths_that_32_bits_do_not_hold():
+    most = [api._most(n, 9) for n in (None, 0, 5, 9, 10, 1 << 40, -1, -5, 5 - (1 << 32))]
+    assert most == [9, 0, 5, 9, 9, 9, -1, -1, -1]
