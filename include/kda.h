@@ -41,9 +41,10 @@
  * DEVICE pointer of the current device.  The library allocates nothing,
  * never synchronises, and enqueues exactly one kernel on `stream` per call
  * (kda_lin_prompt: up to three, kda_ssm_prompt: up to two).
- * The kernels of kda_conv_*, kda_ssm_step and kda_linear are launched so that
- * they may start while the kernel before them on the stream ends; they read
- * and write nothing before it has.
+ * The kernels of kda_conv_*, kda_ssm_step, kda_linear and, where no sequence
+ * is longer than 64, kda_ssm_prompt are launched so that they may start while
+ * the kernel before them on the stream ends; they read and write nothing
+ * before it has.
  * Calls are reentrant and may come from several host threads at once (the
  * first call on a device reads its attributes and configures the kernel
  * under a lock); two calls that write the same pool regions must be ordered
@@ -608,7 +609,10 @@ typedef struct kda_linear_args {
 } kda_linear_args;
 
 /* Columns behind `outer` in a wider row are left as they are.  An infinity or NaN
- * reaches the sums that it is part of only.  Errors: KDA_ERR_NULL_ARGS,
+ * reaches the sums that it is part of only.  Where a wait on the chip runs out (each has
+ * 2 s; only with more than one row or an inner dimension above 32768),
+ * KDA_DEVERR_TIMEOUT is set and the output is incomplete: without `err` nobody learns of
+ * it, as the call has returned by then.  Errors: KDA_ERR_NULL_ARGS,
  * KDA_ERR_SHAPE, KDA_ERR_ACTIVATION, KDA_ERR_NULL_POINTER, KDA_ERR_ALIGNMENT,
  * KDA_ERR_DEVICE, KDA_ERR_LAUNCH; nothing is launched on error.  One kernel on
  * `stream`. */

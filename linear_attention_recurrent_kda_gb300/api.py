@@ -778,7 +778,9 @@ def kda_linear(*, x, weight, output, bias=None, residual=None, activation: Optio
     ``output`` bf16 [rows, outer] (each may be a slice of wider rows; the residual may
     be the output itself); ``bias`` bf16 [outer]; ``activation`` None, "none",
     "silu", "gelu" (with erf) or "softplus".  ``path``: 0 = automatic, 1 = the form for few
-    tiles, 2 = the form for many (``kda_linear_path``)."""
+    tiles, 2 = the form for many (``kda_linear_path``).  ``err`` takes
+    ``lib.KDA_DEVERR_TIMEOUT`` where a wait on the chip ran out and the output is
+    incomplete, which nothing else tells."""
     act = ACTIVATIONS.get(activation)
     if act is not None and path == 0 and _done((_lib._bind or _lib.bind()).linear(
             x, weight, output, bias, residual, act, err, stream)):

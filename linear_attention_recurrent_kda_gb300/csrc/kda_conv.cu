@@ -13,7 +13,7 @@
 // windows 82 (4 x 9 tokens: 4.1 us, 3.7 so).  Not kept: pieces of 16 rows 91 us,
 // of 64 82 (with half the threads for small calls), of 128 96; 2 rows ahead 99, 8 85; 4
 // channels a thread 79-85 (before), and 16.8 instead of 12.3 us for the step of 256 requests x 8192
-// channels (10.5 us, 4.9 TB/s, since it starts while the kernel before ends).
+// channels (10.0 us, 5.1 TB/s, since it starts while the kernel before ends).
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>

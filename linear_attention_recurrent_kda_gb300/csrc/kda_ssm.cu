@@ -225,7 +225,7 @@ static int plan_prompt(const kda_ssm_prompt_args *a, Plan *plan) {
   const int64_t blocks = (threads + 127) / 128;          // CTAs of a sequence or piece
   // us.  A call takes as long as its longest sequence alone or as all the work, and a little
   // longer where the two are near.  8 states a thread are faster alone and slower in all (8
-  // sequences, 9159 tokens x 4096 channels: 236 us with 8, 297 with 16 where the longest has
+  // sequences, 9159 tokens x 4096 channels: 237 us with 8, 297 with 16 where the longest has
   // 2047, 249 and 231 where all have 1145).  Of 19 shapes, 10% more than the other's at most.
   const double work = static_cast<double>(a->tokens) * blocks;
   const double with8 = std::hypot(0.072 * longest, 0.78e-3 * work);
@@ -237,7 +237,8 @@ static int plan_prompt(const kda_ssm_prompt_args *a, Plan *plan) {
   if (a->path == 1 || blocks == 0 || longest <= kShortestPiece) return whole;
   // As many pieces as run at a time (each sequence's last one may be short); two passes over
   // all tokens, and each piece sums up those before it.  (One sequence of 2048 x 4096
-  // channels 150 us whole, 92 in pieces; of 512 43 and 61; the 8 ragged ones 236 and 336.)
+  // channels 150 us whole, 92 in pieces; of 512 43 and 61; the 8 ragged ones 237 and 336.  All of 16 states;
+  // with 32 and 64 the ragged ones take 389 and 1297 us, 8192 x 4096 485 and 1409.)
   int64_t pieces = kSms * kCtas / blocks - (a->seqs - 1);
   if (pieces < 1) pieces = 1;
   int64_t piece = (a->tokens / pieces + 16) / 16 * 16;

@@ -28,8 +28,8 @@
 // instructions: 75 for the products and sums of decays, states and outputs and exp2, 20 for
 // the corrections' products, 12 for b and c, and what the helpers do.  Where CTAs are few, a
 // CTA's own time: 135 cycles a token with 8 states a thread, 230 with 16.
-// 8 ragged sequences (9159 tokens x 4096 channels) 236 us, one of 1024 x 4096 62 us (74
-// whole), 32749 tokens x 4096 1075 us in 28 pieces, 400 of them in the first pass; the
+// 8 ragged sequences (9159 tokens x 4096 channels) 237 us, one of 1024 x 4096 62 us (74
+// whole), 32749 tokens x 4096 1081 us in 28 pieces, 400 of them in the first pass; the
 // ragged ones' bytes would take 45, the long one's 158.  What made it fast: 16 states a
 // thread instead of 4 (1959 -> 488 us, the long one 38 -> 1.5 ms), steps and outputs once per
 // token in pairs of channels and without branches (488 -> 353), contributions summed
