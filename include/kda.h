@@ -609,10 +609,10 @@ typedef struct kda_linear_args {
 } kda_linear_args;
 
 /* Columns behind `outer` in a wider row are left as they are.  An infinity or NaN
- * reaches the sums that it is part of only.  Where a wait on the chip runs out (each has
- * 2 s; only with more than one row or an inner dimension above 32768),
- * KDA_DEVERR_TIMEOUT is set and the output is incomplete: without `err` nobody learns of
- * it, as the call has returned by then.  Errors: KDA_ERR_NULL_ARGS,
+ * reaches the sums that it is part of only.  Where a wait on the chip runs out (2 s each;
+ * kda_linear has none for one row of up to 32768), KDA_DEVERR_TIMEOUT is set and the
+ * output is incomplete: without `err` nobody learns of it, as the call has returned by
+ * then.  Errors: KDA_ERR_NULL_ARGS,
  * KDA_ERR_SHAPE, KDA_ERR_ACTIVATION, KDA_ERR_NULL_POINTER, KDA_ERR_ALIGNMENT,
  * KDA_ERR_DEVICE, KDA_ERR_LAUNCH; nothing is launched on error.  One kernel on
  * `stream`. */

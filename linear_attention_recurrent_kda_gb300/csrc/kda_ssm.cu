@@ -3,7 +3,7 @@
 //
 // The step moves 8 bytes a state and has some 10 operations for it, 16 states a channel:
 // it is near both bounds.  256 requests x 8192 channels x 16, 32 of them padding: 49 us,
-// 5.1 TB/s (0.75 of the copy's rate), 65% of the issue slots taken.  Steps, gates and
+// 5.1 TB/s (0.75 of the copy's rate), 67% of the issue slots taken.  Steps, gates and
 // outputs by every lane of a channel for itself 75.7 us, a polynomial for each state by
 // itself 55.3; 8 requests a thread 64 (134 registers), 64 or 256 threads a CTA 50 and 51,
 // requests along a second grid dimension 50.7, 8 to 32 requests one after another in a CTA

@@ -31,3 +31,19 @@ def test_activations_of_infinities(act, below, rows, path):
         got = out[rows - 1].tolist()
         if want is not None:
             assert all(v == want or (math.isnan(v) and math.isnan(want)) for v in got), (pair, got)
+
+
+@pytest.mark.parametrize("rows,inner,outer", [(2000, 72, 3), (700, 520, 7), (65, 8200, 1), (4100, 16, 5)])
+def test_many_rows_of_fewer_than_8_columns(rows, inner, outer):
+    """Whole numbers: |sum| <= 4 inner + 50 is exact in FP32, so the output is its rounding."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+
+    def whole(n, width, top):
+        wide = torch.randint(-top, top + 1, (n, -(-width // 8) * 8 + 8), generator=g, device="cuda").to(BF)
+        return wide[:, :width]
+    x, w, res = whole(rows, inner, 2), whole(outer, inner, 2), whole(rows, outer, 50)
+    wide = torch.full((rows, 16), NAN, dtype=BF, device="cuda")
+    for path in (0, 1):
+        kda_linear(x=x, weight=w, residual=res, output=wide[:, :outer], path=path)
+        assert torch.equal(wide[:, :outer], (x.double() @ w.double().T + res.double()).to(BF))
+        assert torch.isnan(wide[:, outer:]).all()
